@@ -96,6 +96,10 @@ extern "C" {
 #define TRELLIS_MAX_N (1 << 22)
 #define TRELLIS_MAX_GROUPS 4096
 #define TRELLIS_MAX_GROUP_ROWS (1 << 20)
+/* Limits of the entry points for fine-tuned layers (trellis_adapters and below). */
+#define TRELLIS_MAX_ROWS (1 << 20)
+#define TRELLIS_MAX_ADAPTERS 4096
+#define TRELLIS_MAX_RANK 128
 /* Device memory of trellis_prefill_noalloc, per GPU: 1 MiB of tile counters
  * plus 31 MiB of float32 partial tiles. */
 #define TRELLIS_NOALLOC_SCRATCH_BYTES (32u << 20)
@@ -114,11 +118,12 @@ typedef struct trellis_geom {
 typedef enum trellis_status {
     TRELLIS_OK = 0,
     TRELLIS_E_GEOMETRY = -1, /* t, l, bits, n or k outside the accepted domain */
-    TRELLIS_E_M = -2,        /* m outside [5, 15] (prefill) or [1, 4] (matvec); bad packed group or row counts */
+    TRELLIS_E_M = -2,        /* m outside the entry point's range; bad packed group or row counts */
     TRELLIS_E_NULL = -3,     /* a required pointer is NULL */
     TRELLIS_E_ALIGN = -4,    /* a pointer is not aligned as documented */
     TRELLIS_E_HIP = -5,      /* the HIP runtime reported a launch error */
-    TRELLIS_E_SCRATCH = -6   /* trellis_prefill_noalloc: the call's workspace exceeds the fixed scratch */
+    TRELLIS_E_SCRATCH = -6,  /* trellis_prefill_noalloc: the call's workspace exceeds the fixed scratch */
+    TRELLIS_E_ADAPTERS = -7  /* the number of adapters or their rank outside the accepted range */
 } trellis_status;
 
 /* 1 if (g, m) is inside the accepted domain of trellis_prefill, else 0.
@@ -213,6 +218,70 @@ trellis_status trellis_gate_up(const uint16_t *x_bf16, int32_t m,
 trellis_status trellis_prefill_noalloc(const uint16_t *x_bf16, int32_t m,
                                        const uint32_t *codes, const uint16_t *scales_bf16,
                                        trellis_geom g, uint16_t *out_bf16, void *hip_stream);
+
+/* ---- Fine-tuned layers: any number of rows, 1 <= m <= TRELLIS_MAX_ROWS ------
+ *
+ * The packed weights are frozen; what is trained or swapped per request stands
+ * beside them. Formats, accepted geometries, execution and errors are those
+ * above; a stream's workspace of these entry points is a second one, under the
+ * same rules (allocated by the first call that needs it, kept, one per device
+ * and stream: call once before capturing, and order a captured graph's replays
+ * with every other use of the capture stream). All sums are float32; outputs
+ * are rounded to bf16 once. Results do not depend on timing: every sum has a
+ * fixed order. Inputs and outputs must not overlap. */
+
+/* Low-rank adapters of many requests beside one shared projection:
+ *   out[r] = W x[r] + gain[i] * B[i] (A[i] x[r]),   i = index[r],
+ * for the m rows r of x; a row whose index lies outside [0, count) has no
+ * adapter (out[r] = W x[r]). Rows of one adapter need not stand together.
+ *   x      bf16 [m, K]            out   bf16 [m, N]
+ *   a      bf16 [count, rank, K]  b     bf16 [count, N, rank]
+ *   gain   float32 [count]        index int32 [m]
+ * all row-major device memory; x, a, b and out 16-byte aligned, gain and index
+ * 4-byte aligned; 1 <= count <= TRELLIS_MAX_ADAPTERS, 1 <= rank <=
+ * TRELLIS_MAX_RANK (any value). An adapter's infinities and NaNs reach its own
+ * rows only. */
+trellis_status trellis_adapters(const uint16_t *x_bf16, int32_t m, const uint32_t *codes, const uint16_t *scales_bf16,
+                                trellis_geom g, const uint16_t *a_bf16, const uint16_t *b_bf16, const float *gain,
+                                const int32_t *index, int32_t count, int32_t rank, uint16_t *out_bf16,
+                                void *hip_stream);
+
+/* Gradients of trellis_adapters for the gradient dout [m, N] of its output:
+ *   u[r]  = gain[i] * B[i]^T dout[r],  t[r] = gain[i] * A[i] x[r],
+ *   dx[r] = W^T dout[r] + A[i]^T u[r],
+ *   da[i] = sum over the rows r of adapter i of u[r] x[r]^T,
+ *   db[i] = sum over the rows r of adapter i of dout[r] t[r]^T.
+ * dx bf16 [m, K], da bf16 [count, rank, K], db bf16 [count, N, rank], 16-byte
+ * aligned, all written (an adapter without rows gets zeros). W, gain and index
+ * get no gradient. */
+trellis_status trellis_adapters_backward(const uint16_t *dout_bf16, const uint16_t *x_bf16, int32_t m,
+                                         const uint32_t *codes, const uint16_t *scales_bf16, trellis_geom g,
+                                         const uint16_t *a_bf16, const uint16_t *b_bf16, const float *gain,
+                                         const int32_t *index, int32_t count, int32_t rank, uint16_t *dx_bf16,
+                                         uint16_t *da_bf16, uint16_t *db_bf16, void *hip_stream);
+
+/* The gated block at any number of rows:
+ *   h = silu(gate) * up,  gate = x . Wg^T,  up = x . Wu^T,
+ * evaluated in float32 from the two sums and rounded once (trellis_gate_up
+ * rounds every step as the page does). gate_bf16 and up_bf16 [m, N] receive
+ * the rounded projections, which trellis_gated_backward takes; either may be
+ * NULL where it is not wanted. */
+trellis_status trellis_gated(const uint16_t *x_bf16, int32_t m, const uint32_t *codes_gate,
+                             const uint16_t *scales_gate, const uint32_t *codes_up, const uint16_t *scales_up,
+                             trellis_geom g, uint16_t *h_bf16, uint16_t *gate_bf16, uint16_t *up_bf16,
+                             void *hip_stream);
+
+/* Gradients of trellis_gated for the gradient dh [m, N] of h and the
+ * projections that it kept:
+ *   s = sigmoid(gate),  dup = dh * gate * s,
+ *   dgate = dh * up * s * (1 + gate * (1 - s)),
+ *   dx = dgate . Wg + dup . Wu.
+ * dgate and dup bf16 [m, N] and dx bf16 [m, K] are written; dx is the product
+ * of the rounded dgate and dup. */
+trellis_status trellis_gated_backward(const uint16_t *dh_bf16, const uint16_t *gate_bf16, const uint16_t *up_bf16,
+                                      int32_t m, const uint32_t *codes_gate, const uint16_t *scales_gate,
+                                      const uint32_t *codes_up, const uint16_t *scales_up, trellis_geom g,
+                                      uint16_t *dx_bf16, uint16_t *dgate_bf16, uint16_t *dup_bf16, void *hip_stream);
 
 /* Static, NUL-terminated description of a status code. */
 const char *trellis_status_string(trellis_status s);

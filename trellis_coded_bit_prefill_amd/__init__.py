@@ -26,6 +26,9 @@ MAX_M = 15
 MATVEC_MAX_M = 4
 MAX_GROUPS = 4096
 MAX_GROUP_ROWS = 1 << 20
+MAX_ROWS = 1 << 20
+MAX_ADAPTERS = 4096
+MAX_RANK = 128
 
 OK = 0
 E_GEOMETRY = -1
@@ -34,11 +37,13 @@ E_NULL = -3
 E_ALIGN = -4
 E_HIP = -5
 E_SCRATCH = -6
+E_ADAPTERS = -7
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
 # Every symbol declared in include/trellis.h.
 EXPORTED = ("trellis_supported", "trellis_decode", "trellis_prefill", "trellis_matvec", "trellis_prefill_packed",
-            "trellis_gate_up", "trellis_prefill_noalloc", "trellis_status_string")
+            "trellis_gate_up", "trellis_prefill_noalloc", "trellis_adapters", "trellis_adapters_backward",
+            "trellis_gated", "trellis_gated_backward", "trellis_status_string")
 # Test and tuning hooks (include/trellis_testing.h).
 EXPORTED_TESTING = ("trellis_test_force_table",)
 TABLES = {"value": 0, "code": 1, "pair": 2}
@@ -104,6 +109,15 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     L.trellis_gate_up.restype = ctypes.c_int
     L.trellis_prefill_noalloc.argtypes = [vp, ctypes.c_int32, vp, vp, Geom, vp, vp]
     L.trellis_prefill_noalloc.restype = ctypes.c_int
+    i32 = ctypes.c_int32
+    L.trellis_adapters.argtypes = [vp, i32, vp, vp, Geom, vp, vp, vp, vp, i32, i32, vp, vp]
+    L.trellis_adapters.restype = ctypes.c_int
+    L.trellis_adapters_backward.argtypes = [vp, vp, i32, vp, vp, Geom, vp, vp, vp, vp, i32, i32, vp, vp, vp, vp]
+    L.trellis_adapters_backward.restype = ctypes.c_int
+    L.trellis_gated.argtypes = [vp, i32, vp, vp, vp, vp, Geom, vp, vp, vp, vp]
+    L.trellis_gated.restype = ctypes.c_int
+    L.trellis_gated_backward.argtypes = [vp, vp, vp, i32, vp, vp, vp, vp, Geom, vp, vp, vp, vp]
+    L.trellis_gated_backward.restype = ctypes.c_int
     L.trellis_test_force_table.argtypes = [ctypes.c_int]
     L.trellis_test_force_table.restype = ctypes.c_int
     _lib = L
@@ -212,6 +226,36 @@ def gate_up_raw(x_ptr: int, m: int, codes_gate_ptr: int, scales_gate_ptr: int, c
     """Direct C-ABI call with raw device addresses (1 <= m <= 15)."""
     _raise(load_library().trellis_gate_up(x_ptr, m, codes_gate_ptr, scales_gate_ptr, codes_up_ptr,
                                           scales_up_ptr, g, h_ptr, stream))
+
+
+def adapters_raw(x_ptr: int, m: int, codes_ptr: int, scales_ptr: int, g: Geom, a_ptr: int, b_ptr: int, gain_ptr: int,
+                 index_ptr: int, count: int, rank: int, out_ptr: int, stream: int) -> None:
+    """Direct C-ABI call with raw device addresses."""
+    _raise(load_library().trellis_adapters(x_ptr, m, codes_ptr, scales_ptr, g, a_ptr, b_ptr, gain_ptr, index_ptr,
+                                           count, rank, out_ptr, stream))
+
+
+def adapters_backward_raw(dout_ptr: int, x_ptr: int, m: int, codes_ptr: int, scales_ptr: int, g: Geom, a_ptr: int,
+                          b_ptr: int, gain_ptr: int, index_ptr: int, count: int, rank: int, dx_ptr: int, da_ptr: int,
+                          db_ptr: int, stream: int) -> None:
+    """Direct C-ABI call with raw device addresses."""
+    _raise(load_library().trellis_adapters_backward(dout_ptr, x_ptr, m, codes_ptr, scales_ptr, g, a_ptr, b_ptr,
+                                                    gain_ptr, index_ptr, count, rank, dx_ptr, da_ptr, db_ptr, stream))
+
+
+def gated_raw(x_ptr: int, m: int, codes_gate_ptr: int, scales_gate_ptr: int, codes_up_ptr: int, scales_up_ptr: int,
+              g: Geom, h_ptr: int, gate_ptr: int, up_ptr: int, stream: int) -> None:
+    """Direct C-ABI call with raw device addresses (gate_ptr and up_ptr may be 0)."""
+    _raise(load_library().trellis_gated(x_ptr, m, codes_gate_ptr, scales_gate_ptr, codes_up_ptr, scales_up_ptr, g,
+                                        h_ptr, gate_ptr, up_ptr, stream))
+
+
+def gated_backward_raw(dh_ptr: int, gate_ptr: int, up_ptr: int, m: int, codes_gate_ptr: int, scales_gate_ptr: int,
+                       codes_up_ptr: int, scales_up_ptr: int, g: Geom, dx_ptr: int, dgate_ptr: int, dup_ptr: int,
+                       stream: int) -> None:
+    """Direct C-ABI call with raw device addresses."""
+    _raise(load_library().trellis_gated_backward(dh_ptr, gate_ptr, up_ptr, m, codes_gate_ptr, scales_gate_ptr,
+                                                 codes_up_ptr, scales_up_ptr, g, dx_ptr, dgate_ptr, dup_ptr, stream))
 
 
 @dataclass
@@ -355,3 +399,141 @@ def gate_up(x, codes_gate, scales_gate, codes_up, scales_up, bits: int, out=None
     gate_up_raw(x.data_ptr(), m, codes_gate.data_ptr(), scales_gate.data_ptr(), codes_up.data_ptr(),
                 scales_up.data_ptr(), geom(n, k, bits), out.data_ptr(), _stream_handle(x.device))
     return out
+
+
+def _packed_k(codes, bits: int) -> int:
+    """Input columns of a packed matrix, from its words per row."""
+    if bits not in (2, 3, 4) or (codes.shape[1] * 32) % bits:
+        raise ValueError(f"codes has {codes.shape[1]} words per row, which is no row of {bits}-bit codes")
+    return codes.shape[1] * 32 // bits
+
+
+def _check_shape(name, t, shape):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _output(name, t, shape, device):
+    """`t`, checked, or a new bf16 tensor where it is None."""
+    import torch
+
+    if t is None:
+        return torch.empty(shape, dtype=torch.bfloat16, device=device)
+    _check_tensor(name, t, _dtypes()[0], len(shape), device)
+    _check_shape(name, t, shape)
+    return t
+
+
+def _check_packed(codes, scales, k: int, bits: int, device, suffix: str = "") -> int:
+    """Checks one packed matrix of k columns; returns its rows."""
+    bf, cw = _dtypes()
+    _check_tensor("codes" + suffix, codes, cw, 2, device)
+    _check_tensor("scales" + suffix, scales, bf, 1, device)
+    n = codes.shape[0]
+    if codes.shape[1] * 32 != k * bits:
+        raise ValueError(f"codes{suffix} has {codes.shape[1]} words per row, expected K*bits/32 = {k * bits // 32}")
+    _check_shape("scales" + suffix, scales, (n,))
+    return n
+
+
+def _check_adapters(a, b, gain, index, m: int, n: int, k: int, device):
+    """Checks an adapter set for m rows of a layer [n, k]; returns (count, rank)."""
+    import torch
+
+    bf, _ = _dtypes()
+    _check_tensor("a", a, bf, 3, device)
+    _check_tensor("b", b, bf, 3, device)
+    _check_tensor("gain", gain, (torch.float32,), 1, device)
+    _check_tensor("index", index, (torch.int32,), 1, device)
+    count, rank = a.shape[0], a.shape[1]
+    _check_shape("a", a, (count, rank, k))
+    _check_shape("b", b, (count, n, rank))
+    _check_shape("gain", gain, (count,))
+    _check_shape("index", index, (m,))
+    return count, rank
+
+
+def adapters(x, codes, scales, bits: int, a, b, gain, index, out=None):
+    """The shared projection with the low-rank adapter of each row's request
+    beside it, in one pass over W, on the current stream:
+
+        out[r] = W x[r] + gain[i] * B[i] (A[i] x[r]),  i = index[r]
+
+    x [M, K], a [count, rank, K], b [count, N, rank] and out [M, N] in bf16,
+    gain [count] in float32, index [M] in int32; any M from 1 to MAX_ROWS,
+    any rank from 1 to MAX_RANK. A row whose index is not in [0, count) has
+    no adapter."""
+    bf, _ = _dtypes()
+    _check_tensor("x", x, bf, 2)
+    m, k = x.shape
+    n = _check_packed(codes, scales, k, bits, x.device)
+    count, rank = _check_adapters(a, b, gain, index, m, n, k, x.device)
+    out = _output("out", out, (m, n), x.device)
+    adapters_raw(x.data_ptr(), m, codes.data_ptr(), scales.data_ptr(), geom(n, k, bits), a.data_ptr(), b.data_ptr(),
+                 gain.data_ptr(), index.data_ptr(), count, rank, out.data_ptr(), _stream_handle(x.device))
+    return out
+
+
+def adapters_backward(dout, x, codes, scales, bits: int, a, b, gain, index, dx=None, da=None, db=None):
+    """Gradients of adapters() for the gradient dout [M, N] of its output:
+    (dx [M, K], da [count, rank, K], db [count, N, rank]), bf16, each written
+    whole (an adapter without rows gets zeros)."""
+    bf, _ = _dtypes()
+    _check_tensor("x", x, bf, 2)
+    m, k = x.shape
+    n = _check_packed(codes, scales, k, bits, x.device)
+    _check_tensor("dout", dout, bf, 2, x.device)
+    _check_shape("dout", dout, (m, n))
+    count, rank = _check_adapters(a, b, gain, index, m, n, k, x.device)
+    dx = _output("dx", dx, (m, k), x.device)
+    da = _output("da", da, (count, rank, k), x.device)
+    db = _output("db", db, (count, n, rank), x.device)
+    adapters_backward_raw(dout.data_ptr(), x.data_ptr(), m, codes.data_ptr(), scales.data_ptr(), geom(n, k, bits),
+                          a.data_ptr(), b.data_ptr(), gain.data_ptr(), index.data_ptr(), count, rank, dx.data_ptr(),
+                          da.data_ptr(), db.data_ptr(), _stream_handle(x.device))
+    return dx, da, db
+
+
+def gated(x, codes_gate, scales_gate, codes_up, scales_up, bits: int, out=None, keep: bool = False):
+    """h[M, N] = silu(x . Wg^T) * (x . Wu^T) in one pass over both packed
+    matrices, any M from 1 to MAX_ROWS, evaluated in float32 and rounded once.
+    With keep, returns (h, gate, up): the projections that gated_backward()
+    takes."""
+    bf, _ = _dtypes()
+    _check_tensor("x", x, bf, 2)
+    m, k = x.shape
+    n = _check_packed(codes_gate, scales_gate, k, bits, x.device, "_gate")
+    _check_packed(codes_up, scales_up, k, bits, x.device, "_up")
+    _check_shape("codes_up", codes_up, codes_gate.shape)
+    h = _output("out", out, (m, n), x.device)
+    gate = _output("gate", None, (m, n), x.device) if keep else None
+    up = _output("up", None, (m, n), x.device) if keep else None
+    gated_raw(x.data_ptr(), m, codes_gate.data_ptr(), scales_gate.data_ptr(), codes_up.data_ptr(),
+              scales_up.data_ptr(), geom(n, k, bits), h.data_ptr(), gate.data_ptr() if keep else 0,
+              up.data_ptr() if keep else 0, _stream_handle(x.device))
+    return (h, gate, up) if keep else h
+
+
+def gated_backward(dh, gate, up, codes_gate, scales_gate, codes_up, scales_up, bits: int, dx=None, dgate=None,
+                   dup=None):
+    """Gradients of gated() for the gradient dh [M, N] of h and the kept
+    projections: (dx [M, K], dgate [M, N], dup [M, N]), bf16."""
+    bf, cw = _dtypes()
+    _check_tensor("dh", dh, bf, 2)
+    m, n = dh.shape
+    for name, t in (("gate", gate), ("up", up)):
+        _check_tensor(name, t, bf, 2, dh.device)
+        _check_shape(name, t, (m, n))
+    _check_tensor("codes_gate", codes_gate, cw, 2, dh.device)
+    k = _packed_k(codes_gate, bits)
+    for suffix, c, s in (("_gate", codes_gate, scales_gate), ("_up", codes_up, scales_up)):
+        rows = _check_packed(c, s, k, bits, dh.device, suffix)
+        if rows != n:
+            raise ValueError(f"codes{suffix} must have {n} rows, got {rows}")
+    dx = _output("dx", dx, (m, k), dh.device)
+    dgate = _output("dgate", dgate, (m, n), dh.device)
+    dup = _output("dup", dup, (m, n), dh.device)
+    gated_backward_raw(dh.data_ptr(), gate.data_ptr(), up.data_ptr(), m, codes_gate.data_ptr(),
+                       scales_gate.data_ptr(), codes_up.data_ptr(), scales_up.data_ptr(), geom(n, k, bits),
+                       dx.data_ptr(), dgate.data_ptr(), dup.data_ptr(), _stream_handle(dh.device))
+    return dx, dgate, dup

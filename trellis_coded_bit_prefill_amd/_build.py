@@ -1,14 +1,16 @@
 """Compile the HIP library ``libtrellis.so`` for gfx950 with hipcc."""
 from __future__ import annotations
 
-import glob
+import concurrent.futures
 import os
 import subprocess
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libtrellis.so")
-SOURCES = sorted(glob.glob(os.path.join(PKG, "csrc", "*.hip")))
+SOURCES = [os.path.join(PKG, "csrc", "trellis.hip")]       # the narrow-batch layer
+ROWS_SOURCES = [os.path.join(PKG, "csrc", "rows.hip")]     # fine-tuned layers, any number of rows
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",
@@ -30,12 +32,23 @@ def hipcc() -> str:
 
 
 def build(verbose: bool = False) -> str:
-    """Always recompiles; writes the library atomically next to this file."""
+    """Always recompiles (the sources side by side); writes the library
+    atomically next to this file."""
     tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = [hipcc(), *HIPCC_FLAGS, "-I", os.path.join(ROOT, "include"), "-o", tmp, *SOURCES]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.check_call(cmd)
+
+    def run(cmd):
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.check_call(cmd)
+
+    compile_flags = [f for f in HIPCC_FLAGS if f != "-shared"]
+    with tempfile.TemporaryDirectory() as d:
+        objects = [os.path.join(d, os.path.basename(s) + ".o") for s in SOURCES + ROWS_SOURCES]
+        cmds = [[hipcc(), *compile_flags, "-I", os.path.join(ROOT, "include"), "-c", "-o", o, s]
+                for o, s in zip(objects, SOURCES + ROWS_SOURCES)]
+        with concurrent.futures.ThreadPoolExecutor(len(cmds)) as pool:
+            list(pool.map(run, cmds))
+        run([hipcc(), *HIPCC_FLAGS, "-o", tmp, *objects])
     os.replace(tmp, LIB)
     return LIB
 

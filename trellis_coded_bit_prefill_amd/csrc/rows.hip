@@ -1,0 +1,1026 @@
+// Fine-tuned packed Trellis layers at any number of rows, gfx950: low-rank
+// adapters beside the shared projection, the gated block, and the backward
+// passes of both.
+//
+// Every entry point here contains one product of a dense bf16 matrix with a
+// packed matrix W[N, K], in one of two directions:
+//   forward     out[M, N] = P[M, K] . W^T   (contraction over K)
+//   transposed  out[M, K] = P[M, N] . W     (contraction over N)
+// and product_kernel computes both: a workgroup owns a tile of rows of P and a
+// group of output columns, stages P in LDS one step of the contraction at a
+// time, and its waves decode the weights straight into MFMA operand registers.
+// W is decoded once per tile of rows and never stored.
+//
+// The low-rank parts are sums of their own: t = x A^T and u = dout B
+// (shrink_kernel), added to the product before it is rounded, and the
+// gradients of A and B (outer_kernel).
+//
+// Build flags that matter for exactness: -ffp-contract=off.
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <map>
+#include <mutex>
+#include <thread>
+
+#include "decode.hpp"
+#include "trellis.h"
+
+namespace trellis {
+namespace {
+
+constexpr int kThreads = 512;       // product_kernel: 8 waves
+constexpr int kStep = 256;          // contraction columns staged per step
+constexpr int kStride = kStep * 2 + 16;  // bytes per staged row (16 B of padding spread the rows over the banks)
+constexpr int kHalf = 128;          // output columns reduced at a time
+constexpr int kRedStride = kHalf + 4;    // floats per row of the reduction tile
+constexpr int kTableBytes = 4096 * 4;
+constexpr int kRawBuffer = 0x00020000;  // gfx9 raw-buffer descriptor word 3
+constexpr int kSc1 = 16;                // cache policy: the level that is coherent across the XCDs' L2s
+static_assert(2 * 16 * kRedStride * 4 == 2 * 16 * kStride, "the reduction tile reuses the staged rows' space");
+
+__device__ __forceinline__ uint16_t bf16_of(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
+
+// The adapter term's operands. index[m] outside [0, count): the row has no
+// adapter. t is float32 [m, rank_p], rank_p = rank rounded up to 32, zero past
+// the rank, the gain already in it.
+struct LowRank {
+  const int32_t *index;
+  const uint16_t *factor;  // forward: B[count, N, rank]; transposed: A[count, rank, K]
+  const float *t;
+  int32_t count, rank, rank_p;
+};
+
+struct Product {
+  const uint16_t *p, *p2;         // [m, C]; transposed: p2 is the second matrix's rows, or null
+  const uint32_t *codes, *codes2;  // codes2: gated (up), or transposed with two matrices
+  const uint16_t *scales, *scales2;
+  uint16_t *out, *gate, *up;       // gate, up: gated only, null where they are not kept
+  float *partials;
+  uint32_t *counters;
+  int64_t units;     // tiles * steps
+  int32_t m, n, k;
+  int32_t groups;    // groups of output columns
+  int32_t steps;     // contraction steps of a tile (all matrices)
+  int32_t steps1;    // those of the first matrix
+  LowRank low;
+};
+
+// Adds the adapters' term to a wave's accumulators: for every adapter that a
+// 16-row tile names, the product of t's rows (as the sum of two bf16 numbers,
+// 2^-16 relative) with the factor, kept only in the rows that name it, so an
+// adapter's infinities and NaNs stay in its own rows.
+// load(a, r0, w): the NT operands for rank columns r0 + 8g .. +7.
+template <int MT, int NT, typename Load>
+__device__ __forceinline__ void add_low_rank(const LowRank &L, int m, int m0, int lane, f32x4 (&acc)[MT][NT], Load load) {
+  const int j = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    const int row = m0 + 16 * mt + j;
+    const int rowc = row < m ? row : m - 1;
+    int idx = row < m ? L.index[row] : -1;
+    if (idx >= L.count) idx = -1;
+    int of[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) of[e] = __shfl(idx, 4 * g + e);
+    uint64_t left = __ballot(idx >= 0) & 0xFFFFull;
+    while (left) {
+      const int a = __builtin_amdgcn_readlane(idx, __builtin_ctzll(left));
+      left &= ~__ballot(idx == a);
+      f32x4 d[NT];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) d[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int r0 = 0; r0 < L.rank_p; r0 += 32) {
+        const float *tp = L.t + (int64_t)rowc * L.rank_p + r0 + 8 * g;
+        const f32x4 t0 = *reinterpret_cast<const f32x4 *>(tp), t1 = *reinterpret_cast<const f32x4 *>(tp + 4);
+        bf16x8 hi, lo;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float v = e < 4 ? t0[e] : t1[e - 4];
+          hi[e] = (__bf16)v;
+          lo[e] = (__bf16)(v - (float)hi[e]);
+        }
+        bf16x8 w[NT];
+        load(a, r0 + 8 * g, w);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          d[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, w[i], d[i], 0, 0, 0);
+          d[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, w[i], d[i], 0, 0, 0);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[mt][i][e] += of[e] == a ? d[i][e] : 0.f;
+    }
+  }
+}
+
+// Weight E (0..31) of a forward lane's half block, through the value table.
+template <int BITS, int O>
+__device__ __forceinline__ float table_weight(const uint32_t (&d)[BITS + 1], const unsigned char *table, float s) {
+  return *reinterpret_cast<const float *>(table + win_xa<O, 2>(d)) * s;
+}
+template <int BITS, int U, int... S>
+__device__ __forceinline__ bf16x8 half_group(const uint32_t (&d)[BITS + 1], const unsigned char *table, float s,
+                                             std::integer_sequence<int, S...>) {
+  const float f[8] = {table_weight<BITS, (31 - 8 * U - S) * BITS>(d, table, s)...};
+  bf16x8 w;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = (__bf16)f[i];
+  return w;
+}
+template <int BITS>
+__device__ __forceinline__ bf16x8 half_group(const uint32_t (&d)[BITS + 1], const unsigned char *table, float s, int u) {
+  constexpr auto seq = std::make_integer_sequence<int, 8>{};
+  switch (u) {
+    case 0: return half_group<BITS, 0>(d, table, s, seq);
+    case 1: return half_group<BITS, 1>(d, table, s, seq);
+    case 2: return half_group<BITS, 2>(d, table, s, seq);
+    default: return half_group<BITS, 3>(d, table, s, seq);
+  }
+}
+
+enum Kind { kForward = 0, kGated = 1, kTransposed = 2 };
+
+// h = silu(gate) * up in float32, rounded once by the caller.
+__device__ __forceinline__ float silu_mul(float gate, float up) { return gate / (1.0f + expf(-gate)) * up; }
+
+// Four floats a time, four output columns: rounded and stored (N and K are
+// multiples of 4, rows start at multiples of 8 bytes).
+__device__ __forceinline__ void store4(uint16_t *p, f32x4 v) {
+  typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+  *reinterpret_cast<u16x4 *>(p) = u16x4{bf16_of(v[0]), bf16_of(v[1]), bf16_of(v[2]), bf16_of(v[3])};
+}
+
+// One tile: 16 MT rows of P by a group of output columns. 8 waves.
+//   forward     group = 128 rows of W; wave (wn, wk): rows 32 wn .. +31 (two
+//               16-row tiles), half wk of each 256-weight block
+//   gated       group = 64 rows of both matrices; wave (wn, wk): rows 16 wn .. +15
+//               of the gate (tile 0) and of the up matrix (tile 1)
+//   transposed  group = one 256-column block; wave (wn, wk): columns 64 wn .. +63
+//               as four 16-column tiles (tile e: columns 4 j + e), rows
+//               128 wk .. +127 of each 256-row step
+// The units (tile, step) are split evenly over the workgroups; a tile that
+// several share goes through `partials`, summed in a fixed order by the
+// workgroup that arrives last.
+template <int BITS, int KIND, int MT>
+__global__ __launch_bounds__(kThreads) void product_kernel(Product P) {
+  constexpr bool kT = KIND == kTransposed;
+  constexpr int NT = kT ? 4 : 2;
+  constexpr int BM = 16 * MT;
+  constexpr int BN = kT ? 256 : KIND == kGated ? 64 : 128;  // output columns of a group
+  constexpr int wpb = 8 * BITS;
+  constexpr int kRounds = kT ? 2 : 1;
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
+  unsigned char *const table = lds;
+  unsigned char *const xs = lds + kTableBytes;                       // two buffers of BM rows
+  float *const srow = reinterpret_cast<float *>(xs + 2 * BM * kStride);  // transposed: two buffers of 256 row scales
+  uint32_t *const arrived = reinterpret_cast<uint32_t *>(srow + 512);
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wn = wave & 3, wk = wave >> 2;
+  const int j = lane & 15, g = lane >> 4;
+  for (int i = tid; i < 4096; i += kThreads)
+    reinterpret_cast<uint32_t *>(table)[i] = __builtin_bit_cast(uint32_t, trellis_value(code_of((uint32_t)i)));
+
+  const uint32_t row_bytes = (uint32_t)(P.k >> 8) * wpb * 4;
+  const int cols = kT ? P.n : P.k;  // columns of P
+  const int64_t first = P.units * blockIdx.x / gridDim.x, end = P.units * (blockIdx.x + 1) / gridDim.x;
+  int64_t unit = first;
+  while (unit < end) {
+    const int64_t tile = unit / P.steps;
+    const int s0 = (int)(unit - tile * P.steps);
+    const int s1 = (int)(end - unit < P.steps - s0 ? s0 + (end - unit) : P.steps);
+    const int chunk = (int)(tile / P.groups), group = (int)(tile - (int64_t)chunk * P.groups);
+    const int m0 = chunk * BM;
+    f32x4 acc[MT][NT];
+#pragma unroll
+    for (int a = 0; a < MT; ++a)
+#pragma unroll
+      for (int b = 0; b < NT; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    // Staged rows of P: thread t takes 8 columns of row t / 32 + 16 r.
+    uint4 xv[MT];
+    float sv = 0.f;
+    auto fetch = [&](int s) {
+      const bool second = kT && s >= P.steps1;
+      const uint16_t *src = second ? P.p2 : P.p;
+      const int c0 = (second ? s - P.steps1 : s) * kStep + (tid & 31) * 8;
+#pragma unroll
+      for (int r = 0; r < MT; ++r) {
+        int row = m0 + r * 16 + (tid >> 5);
+        if (row >= P.m) row = P.m - 1;  // feeds output rows that are not stored
+        const uint16_t *q = src + (int64_t)row * cols + c0;
+        if constexpr (!kT) {
+          xv[r] = *reinterpret_cast<const uint4 *>(q);
+        } else {
+          // columns past N are zero; rows start at multiples of 8 bytes
+          const uint2 z = {0u, 0u};
+          const uint2 a = c0 < cols ? *reinterpret_cast<const uint2 *>(q) : z;
+          const uint2 b = c0 + 4 < cols ? *reinterpret_cast<const uint2 *>(q + 4) : z;
+          xv[r] = uint4{a.x, a.y, b.x, b.y};
+        }
+      }
+      if constexpr (kT) {
+        const int row = (second ? s - P.steps1 : s) * kStep + tid;
+        sv = tid < 256 && row < P.n ? bf16_bits_to_f32((second ? P.scales2 : P.scales)[row]) : 0.f;
+      }
+    };
+    auto put = [&](int s) {
+      unsigned char *dst = xs + (s & 1) * BM * kStride;
+#pragma unroll
+      for (int r = 0; r < MT; ++r)
+        *reinterpret_cast<uint4 *>(dst + (r * 16 + (tid >> 5)) * kStride + (tid & 31) * 16) = xv[r];
+      if constexpr (kT) {
+        if (tid < 256) srow[(s & 1) * 256 + tid] = sv;
+      }
+    };
+    __syncthreads();  // the previous tile's reduction is done with this space
+    fetch(s0);
+    put(s0);
+    __syncthreads();
+
+    if constexpr (!kT) {
+      float sc[NT];
+      const unsigned char *base[NT];
+      uint32_t size[NT];
+      const int wb = 2 * BITS * g + BITS * (1 - wk);
+      const uint32_t off = (uint32_t)j * row_bytes + 4 * wb, off_next = (uint32_t)j * row_bytes + 4 * ((wb + BITS) % wpb);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const int n0 = KIND == kGated ? group * BN + 16 * wn : group * BN + 32 * wn + 16 * i;
+        const uint32_t *c = KIND == kGated && i ? P.codes2 : P.codes;
+        const uint16_t *sp = KIND == kGated && i ? P.scales2 : P.scales;
+        const int rows = P.n - n0 < 0 ? 0 : P.n - n0 < 16 ? P.n - n0 : 16;
+        base[i] = reinterpret_cast<const unsigned char *>(c) + (int64_t)n0 * row_bytes;
+        size[i] = (uint32_t)rows * row_bytes;
+        sc[i] = j < rows ? bf16_bits_to_f32(sp[n0 + j]) : 0.f;
+      }
+      for (int s = s0; s < s1; ++s) {
+        if (s + 1 < s1) fetch(s + 1);
+        const unsigned char *xb = xs + (s & 1) * BM * kStride + j * kStride + (192 - 64 * g + 32 * wk) * 2;
+        uint32_t d[NT][BITS + 1];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          // rows past N lie outside the buffer and read as zero
+          const uint32_t blk = (uint32_t)s * (wpb * 4);
+          const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+              const_cast<unsigned char *>(base[i] + blk), (short)0, (int)(size[i] ? size[i] - blk : 0u), kRawBuffer);
+#pragma unroll
+          for (int b = 0; b < BITS; ++b) d[i][b] = __builtin_amdgcn_raw_buffer_load_b32(rs, off + 4 * b, 0, 0);
+          d[i][BITS] = __builtin_amdgcn_raw_buffer_load_b32(rs, off_next, 0, 0);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          bf16x8 w[NT];
+#pragma unroll
+          for (int i = 0; i < NT; ++i) w[i] = half_group<BITS>(d[i], table, sc[i], u);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            const bf16x8 x = *reinterpret_cast<const bf16x8 *>(xb + mt * 16 * kStride + 16 * u);
+#pragma unroll
+            for (int i = 0; i < NT; ++i) acc[mt][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w[i], acc[mt][i], 0, 0, 0);
+          }
+        }
+        if (s + 1 < s1) put(s + 1);
+        __syncthreads();
+      }
+      if (KIND == kForward && s1 == P.steps && wk == 0 && P.low.rank > 0) {
+        add_low_rank<MT, NT>(P.low, P.m, m0, lane, acc, [&](int a, int r0, bf16x8 (&w)[NT]) {
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            const int n = group * BN + 32 * wn + 16 * i + j;
+            const uint16_t *q = P.low.factor + ((int64_t)a * P.n + n) * P.low.rank + r0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              w[i][e] = __builtin_bit_cast(__bf16, n < P.n && r0 + e < P.low.rank ? q[e] : (uint16_t)0);
+          }
+        });
+      }
+    } else {
+      // Lane (j, g) decodes columns 64 wn + 4 j .. +3 of the block for rows
+      // 8 g .. 8 g + 7 of each 32-row MFMA step: the lowest of the four
+      // windows starts at stream bit (252 - 64 wn - 4 j) * BITS, the others
+      // BITS apart, 3 BITS + 12 <= 24 bits in all.
+      const int pos = (252 - 64 * wn - 4 * j) * BITS;
+      const uint32_t w0 = (uint32_t)(pos >> 5), sh = (uint32_t)(pos & 31);
+      const uint32_t o_lo = 4 * w0, o_hi = 4 * ((w0 + 1) % wpb);
+      for (int s = s0; s < s1; ++s) {
+        if (s + 1 < s1) fetch(s + 1);
+        const bool second = s >= P.steps1;
+        const int n0 = (second ? s - P.steps1 : s) * kStep;
+        const int rows = P.n - n0 < kStep ? P.n - n0 : kStep;
+        const unsigned char *base = reinterpret_cast<const unsigned char *>(second ? P.codes2 : P.codes) +
+                                    (int64_t)n0 * row_bytes + (int64_t)group * wpb * 4;
+        const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<unsigned char *>(base), (short)0, (int)((uint32_t)rows * row_bytes - (uint32_t)group * wpb * 4), kRawBuffer);
+        const unsigned char *xb = xs + (s & 1) * BM * kStride + j * kStride + (128 * wk + 8 * g) * 2;
+        const float *sr = srow + (s & 1) * 256 + 128 * wk + 8 * g;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          bf16x8 w[NT];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t ro = (uint32_t)(128 * wk + 32 * q + 8 * g + e) * row_bytes;
+            const uint32_t lo = __builtin_amdgcn_raw_buffer_load_b32(rs, ro + o_lo, 0, 0);
+            const uint32_t hi = __builtin_amdgcn_raw_buffer_load_b32(rs, ro + o_hi, 0, 0);
+            const uint32_t f = __builtin_amdgcn_alignbit(hi, lo, sh);
+            const float sc = sr[32 * q + e];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t win = (f >> ((3 - c) * BITS)) & 0xFFFu;
+              w[c][e] = (__bf16)(*reinterpret_cast<const float *>(table + 4 * win) * sc);
+            }
+          }
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            const bf16x8 x = *reinterpret_cast<const bf16x8 *>(xb + mt * 16 * kStride + 64 * q);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[mt][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w[c], acc[mt][c], 0, 0, 0);
+          }
+        }
+        if (s + 1 < s1) put(s + 1);
+        __syncthreads();
+      }
+      if (s1 == P.steps && wk == 0 && P.low.rank > 0) {
+        add_low_rank<MT, NT>(P.low, P.m, m0, lane, acc, [&](int a, int r0, bf16x8 (&w)[NT]) {
+          const int k0 = group * BN + 64 * wn + 4 * j;
+          typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            bf16x4 v = {};
+            if (r0 + e < P.low.rank)
+              v = *reinterpret_cast<const bf16x4 *>(P.low.factor + ((int64_t)a * P.low.rank + r0 + e) * P.k + k0);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) w[c][e] = v[c];
+          }
+        });
+      }
+    }
+
+    // The two wk halves meet in LDS, [wk][row][128 columns]; then each thread
+    // takes four columns of a row at a time.
+    const bool whole = s0 == 0 && s1 == P.steps;
+    float *const red = reinterpret_cast<float *>(xs);
+    // columns of P.out handled per round, and the store of four sums
+    auto finish = [&](int row, int c, f32x4 v, f32x4 v2) {
+      const int mrow = m0 + row;
+      if (mrow >= P.m) return;
+      if constexpr (KIND == kGated) {
+        const int n = group * BN + c;
+        if (n >= P.n) return;
+        const int64_t o = (int64_t)mrow * P.n + n;
+        f32x4 h;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[e] = silu_mul(v[e], v2[e]);
+        store4(P.out + o, h);
+        if (P.gate) store4(P.gate + o, v);
+        if (P.up) store4(P.up + o, v2);
+      } else {
+        const int width = kT ? P.k : P.n, n = group * BN + c;
+        if (n >= width) return;
+        store4(P.out + (int64_t)mrow * width + n, v);
+      }
+    };
+    constexpr int kPart = BM * kHalf * kRounds;  // floats of a tile's partial
+    const int64_t slot = 2 * (int64_t)blockIdx.x + (s0 == 0 ? 1 : 0);
+    for (int round = 0; round < kRounds; ++round) {
+      if (round) __syncthreads();
+      if (!kT || (wn >> 1) == round) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float *r = red + (wk * BM + mt * 16 + 4 * g + e) * kRedStride;
+            if constexpr (kT) {
+              *reinterpret_cast<f32x4 *>(r + 64 * (wn & 1) + 4 * j) =
+                  f32x4{acc[mt][0][e], acc[mt][1][e], acc[mt][2][e], acc[mt][3][e]};
+            } else {
+#pragma unroll
+              for (int i = 0; i < NT; ++i)
+                r[KIND == kGated ? 64 * i + 16 * wn + j : 32 * wn + 16 * i + j] = acc[mt][i][e];
+            }
+          }
+      }
+      __syncthreads();
+      if (whole && KIND == kGated) {
+        for (int q = tid; q < BM * 16; q += kThreads) {
+          const int row = q >> 4, c = (q & 15) * 4;
+          const f32x4 *r0 = reinterpret_cast<const f32x4 *>(red + row * kRedStride + c);
+          const f32x4 *r1 = reinterpret_cast<const f32x4 *>(red + (BM + row) * kRedStride + c);
+          finish(row, c, r0[0] + r1[0], r0[16] + r1[16]);
+        }
+      } else {
+        const __amdgpu_buffer_rsrc_t ws =
+            __builtin_amdgcn_make_buffer_rsrc(P.partials + slot * kPart, (short)0, kPart * 4, kRawBuffer);
+        for (int q = tid; q < BM * 32; q += kThreads) {
+          const int row = q >> 5, c = (q & 31) * 4;
+          const f32x4 v = *reinterpret_cast<const f32x4 *>(red + row * kRedStride + c) +
+                          *reinterpret_cast<const f32x4 *>(red + (BM + row) * kRedStride + c);
+          if (whole) finish(row, round * kHalf + c, v, v);
+          else
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(__attribute__((ext_vector_type(4))) uint32_t, v), ws,
+                                                   (uint32_t)((round * BM + row) * kHalf + c) * 4, 0, kSc1);
+        }
+      }
+    }
+    if (!whole) {
+      // The partial is complete at the coherent level before the counter moves.
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __syncthreads();
+      // workgroups that hold the tile's first and last unit
+      auto owner = [&](int64_t u) {
+        int64_t c = u * gridDim.x / P.units;
+        while (P.units * (c + 1) / gridDim.x <= u) ++c;
+        while (P.units * c / gridDim.x > u) --c;
+        return c;
+      };
+      const int64_t c0 = owner(tile * P.steps), c1 = owner(tile * P.steps + P.steps - 1);
+      if (tid == 0) *arrived = __hip_atomic_fetch_add(&P.counters[tile], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      __syncthreads();
+      const bool last = *arrived == (uint32_t)(c1 - c0);
+      if (last) {
+        if (tid == 0) __hip_atomic_store(&P.counters[tile], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        auto sum = [&](int at) {
+          f32x4 v = {0.f, 0.f, 0.f, 0.f};
+          for (int64_t c = c0; c <= c1; ++c) {
+            const int64_t sl = 2 * c + (P.units * c / gridDim.x <= tile * P.steps ? 1 : 0);
+            const __amdgpu_buffer_rsrc_t ws =
+                __builtin_amdgcn_make_buffer_rsrc(P.partials + sl * kPart, (short)0, kPart * 4, kRawBuffer);
+            v += __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(ws, (uint32_t)at * 4, 0, kSc1));
+          }
+          return v;
+        };
+        if constexpr (KIND == kGated) {
+          for (int q = tid; q < BM * 16; q += kThreads) {
+            const int row = q >> 4, c = (q & 15) * 4;
+            finish(row, c, sum(row * kHalf + c), sum(row * kHalf + 64 + c));
+          }
+        } else {
+          for (int q = tid; q < kRounds * BM * 32; q += kThreads) {
+            const int round = q / (BM * 32), row = (q >> 5) % BM, c = (q & 31) * 4;
+            finish(row, round * kHalf + c, sum((round * BM + row) * kHalf + c), f32x4{});
+          }
+        }
+      }
+    }
+    unit += s1 - s0;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// t[m, r] = gain[i] * sum_c P[m, c] F(i, r, c), i = index[m]: float32, zero
+// past the rank and in rows without an adapter.
+//   forward     P = x,    F(i, r, c) = A[i][r][c]   (c < K)
+//   transposed  P = dout, F(i, r, c) = B[i][c][r]   (c < N)
+// One workgroup (4 waves): 16 rows, 16 rank columns, one span of c; every
+// adapter that the 16 rows name is multiplied in turn and kept in its own
+// rows. The spans' sums meet in `partials`, added in order by the last to
+// arrive.
+// ---------------------------------------------------------------------------
+struct Shrink {
+  const uint16_t *p;
+  const uint16_t *factor;
+  const float *gain;
+  const int32_t *index;
+  float *t;
+  float *partials;
+  uint32_t *counters;
+  int32_t m, cols, count, rank, rank_p;
+  int32_t span, spans;
+};
+
+template <bool T>
+__global__ __launch_bounds__(256) void shrink_kernel(Shrink S) {
+  __shared__ f32x4 part[4][64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int j = lane & 15, g = lane >> 4;
+  const int span = blockIdx.y, rt = blockIdx.z;
+  const int64_t m0 = (int64_t)blockIdx.x * 16;
+  const int64_t row = m0 + j, rowc = row < S.m ? row : S.m - 1;
+  int idx = row < S.m ? S.index[row] : -1;
+  if (idx >= S.count) idx = -1;
+  int of[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) of[e] = __shfl(idx, 4 * g + e);
+  const int c_end = S.cols - span * S.span < S.span ? S.cols : (span + 1) * S.span;
+  const int r = rt * 16 + j;
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  uint64_t left = __ballot(idx >= 0) & 0xFFFFull;
+  while (left) {
+    const int a = __builtin_amdgcn_readlane(idx, __builtin_ctzll(left));
+    left &= ~__ballot(idx == a);
+    f32x4 d = {0.f, 0.f, 0.f, 0.f};
+    for (int c0 = span * S.span + wave * 32; c0 < c_end; c0 += 128) {
+      const int c = c0 + 8 * g;
+      bf16x8 x = {}, w = {};
+      const uint16_t *xp = S.p + rowc * S.cols + c;
+      typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (c + 4 * h < S.cols) {
+          const bf16x4 v = *reinterpret_cast<const bf16x4 *>(xp + 4 * h);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[4 * h + e] = v[e];
+        }
+      if (r < S.rank) {
+        if constexpr (!T) {
+          w = *reinterpret_cast<const bf16x8 *>(S.factor + ((int64_t)a * S.rank + r) * S.cols + c);
+        } else {
+          const uint16_t *q = S.factor + ((int64_t)a * S.cols + c) * S.rank + r;
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (c + e < S.cols) w[e] = __builtin_bit_cast(__bf16, q[(int64_t)e * S.rank]);
+        }
+      }
+      d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w, d, 0, 0, 0);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] += of[e] == a ? d[e] : 0.f;
+  }
+  part[wave][lane] = acc;
+  __syncthreads();
+  if (wave != 0) return;
+  acc = ((part[0][lane] + part[1][lane]) + part[2][lane]) + part[3][lane];
+  const int64_t cell = (int64_t)blockIdx.x * gridDim.z + rt;
+  if (S.spans > 1) {
+    float *const base = S.partials + cell * S.spans * 256;
+    const __amdgpu_buffer_rsrc_t ws = __builtin_amdgcn_make_buffer_rsrc(base, (short)0, S.spans * 1024, kRawBuffer);
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(__attribute__((ext_vector_type(4))) uint32_t, acc), ws,
+                                           (uint32_t)(span * 1024 + lane * 16), 0, kSc1);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    uint32_t old = 0;
+    if (lane == 0) old = __hip_atomic_fetch_add(&S.counters[cell], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    old = __builtin_amdgcn_readfirstlane(old);
+    asm volatile("" ::: "memory");
+    if ((int)old != S.spans - 1) return;
+    if (lane == 0) __hip_atomic_store(&S.counters[cell], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    acc = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < S.spans; ++s)
+      acc += __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(ws, (uint32_t)(s * 1024 + lane * 16), 0, kSc1));
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int64_t mrow = m0 + 4 * g + e;
+    if (mrow < S.m) S.t[mrow * S.rank_p + r] = of[e] >= 0 && r < S.rank ? acc[e] * S.gain[of[e]] : 0.f;
+  }
+}
+
+// The 32-row chunks that an adapter's rows lie in: range[a] = [first, last + 1).
+__global__ __launch_bounds__(256) void range_kernel(const int32_t *__restrict__ index, int m, int2 *__restrict__ range) {
+  __shared__ int lo[4], hi[4];
+  const int a = blockIdx.x, tid = threadIdx.x;
+  int first = 0x7fffffff, last = -1;
+  for (int i = tid; i < m; i += 256)
+    if (index[i] == a) {
+      if (first == 0x7fffffff) first = i;
+      last = i;
+    }
+  for (int o = 32; o > 0; o >>= 1) {
+    first = min(first, __shfl_xor(first, o));
+    last = max(last, __shfl_xor(last, o));
+  }
+  if ((tid & 63) == 0) {
+    lo[tid >> 6] = first;
+    hi[tid >> 6] = last;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    first = min(min(lo[0], lo[1]), min(lo[2], lo[3]));
+    last = max(max(hi[0], hi[1]), max(hi[2], hi[3]));
+    range[a] = last < 0 ? int2{0, 0} : int2{first >> 5, (last >> 5) + 1};
+  }
+}
+
+// Gradients of the factors: sum over an adapter's rows of P[m, c] V[m, r].
+//   dA[a][r][c]: P = x,    V = u    (c < K)
+//   dB[a][c][r]: P = dout, V = t    (c < N)
+// One wave: 16 columns c and 16 rank columns of one adapter, over the 32-row
+// chunks of its range; rows of other adapters enter as zeros on both sides
+// (a NaN in them must not count). V as the sum of two bf16 numbers.
+struct Outer {
+  const uint16_t *x, *dout;
+  const float *u, *t;
+  const int32_t *index;
+  const int2 *range;
+  uint16_t *da, *db;
+  int32_t m, n, k, rank, rank_p;
+  int32_t tiles_a, tiles;  // 16-column tiles of x, and of x and dout together
+};
+
+__global__ __launch_bounds__(256) void outer_kernel(Outer O) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int j = lane & 15, g = lane >> 4;
+  int tile = blockIdx.x * 4 + wave;
+  if (tile >= O.tiles) return;
+  const int a = blockIdx.y, r = blockIdx.z * 16 + j;
+  const bool is_a = tile < O.tiles_a;
+  if (!is_a) tile -= O.tiles_a;
+  const uint16_t *P = is_a ? O.x : O.dout;
+  const float *V = is_a ? O.u : O.t;
+  const int cols = is_a ? O.k : O.n;
+  const int c = tile * 16 + j;
+  const int2 range = O.range[a];
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  for (int ch = range.x; ch < range.y; ++ch) {
+    bf16x8 p, hi, lo;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int m = ch * 32 + 8 * g + e;
+      const bool mine = m < O.m && O.index[m < O.m ? m : 0] == a;
+      p[e] = __builtin_bit_cast(__bf16, mine && c < cols ? P[(int64_t)m * cols + c] : (uint16_t)0);
+      const float v = mine ? V[(int64_t)m * O.rank_p + r] : 0.f;
+      hi[e] = (__bf16)v;
+      lo[e] = (__bf16)(v - (float)hi[e]);
+    }
+    if (is_a) {  // rows r, columns c
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, p, acc, 0, 0, 0);
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, p, acc, 0, 0, 0);
+    } else {     // rows c, columns r
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(p, hi, acc, 0, 0, 0);
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(p, lo, acc, 0, 0, 0);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int other = 4 * g + e;
+    if (is_a) {
+      const int rr = blockIdx.z * 16 + other;
+      if (rr < O.rank) O.da[((int64_t)a * O.rank + rr) * O.k + c] = bf16_of(acc[e]);
+    } else {
+      const int cc = tile * 16 + other;
+      if (cc < O.n && r < O.rank) O.db[((int64_t)a * O.n + cc) * O.rank + r] = bf16_of(acc[e]);
+    }
+  }
+}
+
+// The gated block's elementwise gradients, four elements a thread:
+//   dup = dh silu(gate), dgate = dh up s (1 + gate (1 - s)), s = sigmoid(gate)
+__global__ __launch_bounds__(256) void gated_grad_kernel(const uint16_t *__restrict__ dh, const uint16_t *__restrict__ gate,
+                                                         const uint16_t *__restrict__ up, int64_t quads,
+                                                         uint16_t *__restrict__ dgate, uint16_t *__restrict__ dup) {
+  typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= quads) return;
+  const u16x4 d = reinterpret_cast<const u16x4 *>(dh)[i], gv = reinterpret_cast<const u16x4 *>(gate)[i],
+              uv = reinterpret_cast<const u16x4 *>(up)[i];
+  f32x4 og, ou;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float dd = bf16_bits_to_f32(d[e]), gg = bf16_bits_to_f32(gv[e]), uu = bf16_bits_to_f32(uv[e]);
+    const float s = 1.0f / (1.0f + expf(-gg));
+    ou[e] = dd * gg * s;
+    og[e] = dd * uu * s * (1.0f + gg * (1.0f - s));
+  }
+  store4(dgate + 4 * i, og);
+  store4(dup + 4 * i, ou);
+}
+
+__global__ __launch_bounds__(256) void clear_kernel(uint32_t *__restrict__ p, int64_t n) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i < n) p[i] = 0u;
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+constexpr int kMaxDevices = 64;
+
+struct Space {
+  unsigned char *bytes = nullptr;
+  size_t size = 0;
+  uint32_t *counters = nullptr;
+  size_t ncounters = 0;
+};
+struct Key {
+  int dev;
+  hipStream_t stream;
+  std::thread::id thread;  // the per-thread default stream is one handle for many streams
+  bool operator<(const Key &o) const {
+    if (dev != o.dev) return dev < o.dev;
+    if (stream != o.stream) return stream < o.stream;
+    return thread < o.thread;
+  }
+};
+std::mutex g_lock;
+std::map<Key, Space> g_space;
+int g_cus[kMaxDevices];
+
+bool geom_ok(const trellis_geom &g) {
+  return g.t == TRELLIS_T && g.l == TRELLIS_L && (g.bits == 2 || g.bits == 3 || g.bits == 4) && g.k >= TRELLIS_T &&
+         g.k <= TRELLIS_MAX_K && g.k % TRELLIS_T == 0 && g.n >= 4 && g.n <= TRELLIS_MAX_N && g.n % 4 == 0;
+}
+bool on(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
+
+trellis_status device(int &dev, int &cus) {
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices) return TRELLIS_E_HIP;
+  if (g_cus[dev] == 0 && (hipDeviceGetAttribute(&g_cus[dev], hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess ||
+                          g_cus[dev] <= 0))
+    return TRELLIS_E_HIP;
+  cus = g_cus[dev];
+  return TRELLIS_OK;
+}
+
+// The stream's workspace: grown on demand and kept (launches still queued and
+// captured graphs may hold an outgrown buffer's address, so none is freed).
+trellis_status space(int dev, hipStream_t stream, size_t size, size_t ncounters, Space *&out) {
+  const std::thread::id tid = stream == hipStreamPerThread ? std::this_thread::get_id() : std::thread::id();
+  Space &w = g_space[Key{dev, stream, tid}];
+  if (w.size < size) {
+    void *p = nullptr;
+    if (hipMalloc(&p, size) != hipSuccess) return TRELLIS_E_HIP;
+    w.bytes = static_cast<unsigned char *>(p);
+    w.size = size;
+  }
+  if (w.ncounters < ncounters) {
+    void *p = nullptr;
+    if (hipMalloc(&p, ncounters * 4) != hipSuccess) return TRELLIS_E_HIP;
+    hipLaunchKernelGGL(clear_kernel, dim3((unsigned)((ncounters + 255) / 256)), dim3(256), 0, stream,
+                       static_cast<uint32_t *>(p), (int64_t)ncounters);
+    if (hipGetLastError() != hipSuccess) return TRELLIS_E_HIP;
+    w.counters = static_cast<uint32_t *>(p);
+    w.ncounters = ncounters;
+  }
+  out = &w;
+  return TRELLIS_OK;
+}
+
+typedef void (*ProductFn)(Product);
+constexpr int kRowTiles[] = {1, 2, 4, 6, 8};
+constexpr int kMts = 5;
+template <int BITS, int KIND>
+ProductFn product_of(int i) {
+  switch (i) {
+    case 0: return &product_kernel<BITS, KIND, 1>;
+    case 1: return &product_kernel<BITS, KIND, 2>;
+    case 2: return &product_kernel<BITS, KIND, 4>;
+    case 3: return &product_kernel<BITS, KIND, 6>;
+    default: return &product_kernel<BITS, KIND, 8>;
+  }
+}
+template <int KIND>
+ProductFn product_of(int bits, int i) {
+  return bits == 2 ? product_of<2, KIND>(i) : bits == 3 ? product_of<3, KIND>(i) : product_of<4, KIND>(i);
+}
+ProductFn product_fn(int kind, int bits, int i) {
+  return kind == kForward ? product_of<kForward>(bits, i) : kind == kGated ? product_of<kGated>(bits, i)
+                                                                           : product_of<kTransposed>(bits, i);
+}
+
+// How a product is laid over the card.
+struct Shape {
+  int kind, bits, mt;  // mt: index into kRowTiles
+  int64_t tiles, units;
+  int groups, steps, steps1, grid;
+  size_t partial_bytes, lds;
+};
+Shape shape_of(int kind, trellis_geom g, int32_t m, int matrices, int cus) {
+  Shape s{};
+  s.kind = kind;
+  s.bits = g.bits;
+  const int64_t chunks = ((int64_t)m + 127) / 128;
+  const int need = (int)((((int64_t)m + chunks - 1) / chunks + 15) / 16);
+  while (kRowTiles[s.mt] < need) ++s.mt;
+  const int bm = 16 * kRowTiles[s.mt];
+  const int64_t rows = ((int64_t)m + bm - 1) / bm;
+  const int bn = kind == kTransposed ? 256 : kind == kGated ? 64 : 128;
+  s.groups = ((kind == kTransposed ? g.k : g.n) + bn - 1) / bn;
+  s.steps1 = ((kind == kTransposed ? g.n : g.k) + kStep - 1) / kStep;
+  s.steps = kind == kTransposed ? s.steps1 * matrices : s.steps1;
+  s.tiles = rows * s.groups;
+  s.units = s.tiles * s.steps;
+  s.grid = (int)(s.units < cus ? s.units : cus);
+  s.partial_bytes = (size_t)2 * s.grid * bm * (kind == kTransposed ? 256 : 128) * 4;
+  s.lds = kTableBytes + (size_t)2 * bm * kStride + 512 * 4 + 16;
+  return s;
+}
+
+trellis_status launch(const Shape &s, Product p, hipStream_t stream) {
+  const ProductFn fn = product_fn(s.kind, s.bits, s.mt);
+  static bool ready[kMaxDevices][3][3][kMts];
+  int dev = 0, cus = 0;
+  if (device(dev, cus) != TRELLIS_OK) return TRELLIS_E_HIP;
+  bool &done = ready[dev][s.kind][s.bits - 2][s.mt];
+  if (!done) {
+    if (hipFuncSetAttribute(reinterpret_cast<const void *>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, (int)s.lds) !=
+        hipSuccess)
+      return TRELLIS_E_HIP;
+    done = true;
+  }
+  p.units = s.units;
+  p.groups = s.groups;
+  p.steps = s.steps;
+  p.steps1 = s.steps1;
+  (void)hipGetLastError();
+  hipLaunchKernelGGL(fn, dim3((unsigned)s.grid), dim3(kThreads), s.lds, stream, p);
+  return hipGetLastError() == hipSuccess ? TRELLIS_OK : TRELLIS_E_HIP;
+}
+
+// Spans of a shrink product: enough workgroups to fill the card.
+int spans_of(int64_t cells, int cols, int cus) {
+  int64_t want = (4 * (int64_t)cus + cells - 1) / cells;
+  const int most = (cols + 127) / 128;
+  return (int)(want < 1 ? 1 : want > most ? most : want);
+}
+struct ShrinkShape {
+  int64_t cells;
+  int spans, span;
+  size_t partial_bytes;
+};
+ShrinkShape shrink_shape(int m, int cols, int rank, int cus) {
+  ShrinkShape s{};
+  s.cells = (((int64_t)m + 15) / 16) * ((rank + 31) / 32 * 2);
+  s.spans = spans_of(s.cells, cols, cus);
+  s.span = ((cols + s.spans - 1) / s.spans + 127) / 128 * 128;
+  s.spans = (cols + s.span - 1) / s.span;
+  s.partial_bytes = s.spans > 1 ? (size_t)s.cells * s.spans * 1024 : 0;
+  return s;
+}
+template <bool T>
+trellis_status launch_shrink(const ShrinkShape &h, Shrink s, hipStream_t stream) {
+  s.span = h.span;
+  s.spans = h.spans;
+  (void)hipGetLastError();
+  hipLaunchKernelGGL(shrink_kernel<T>, dim3((unsigned)((s.m + 15) / 16), (unsigned)h.spans, (unsigned)(s.rank_p / 16)),
+                     dim3(256), 0, stream, s);
+  return hipGetLastError() == hipSuccess ? TRELLIS_OK : TRELLIS_E_HIP;
+}
+
+}  // namespace
+}  // namespace trellis
+
+using namespace trellis;
+
+#define TRELLIS_TRY(e)                      \
+  do {                                      \
+    const trellis_status rc_ = (e);         \
+    if (rc_ != TRELLIS_OK) return rc_;      \
+  } while (0)
+
+extern "C" {
+
+trellis_status trellis_adapters(const uint16_t *x, int32_t m, const uint32_t *codes, const uint16_t *scales,
+                                trellis_geom g, const uint16_t *a, const uint16_t *b, const float *gain,
+                                const int32_t *index, int32_t count, int32_t rank, uint16_t *out, void *hip_stream) {
+  if (!geom_ok(g)) return TRELLIS_E_GEOMETRY;
+  if (m < 1 || m > TRELLIS_MAX_ROWS) return TRELLIS_E_M;
+  if (count < 1 || count > TRELLIS_MAX_ADAPTERS || rank < 1 || rank > TRELLIS_MAX_RANK) return TRELLIS_E_ADAPTERS;
+  if (!x || !codes || !scales || !a || !b || !gain || !index || !out) return TRELLIS_E_NULL;
+  if (!on(x, 16) || !on(codes, 16) || !on(scales, 2) || !on(a, 16) || !on(b, 16) || !on(gain, 4) || !on(index, 4) ||
+      !on(out, 16))
+    return TRELLIS_E_ALIGN;
+  hipStream_t stream = reinterpret_cast<hipStream_t>(hip_stream);
+  std::lock_guard<std::mutex> lock(g_lock);
+  int dev = 0, cus = 0;
+  TRELLIS_TRY(device(dev, cus));
+  const int rank_p = (rank + 31) / 32 * 32;
+  const Shape s = shape_of(kForward, g, m, 1, cus);
+  const ShrinkShape h = shrink_shape(m, g.k, rank, cus);
+  const size_t t_bytes = up256((size_t)m * rank_p * 4), hp = up256(h.partial_bytes);
+  Space *w = nullptr;
+  TRELLIS_TRY(space(dev, stream, t_bytes + hp + s.partial_bytes,
+                    (size_t)(s.tiles > h.cells ? s.tiles : h.cells), w));
+  float *const t = reinterpret_cast<float *>(w->bytes);
+  Shrink sh{x, a, gain, index, t, reinterpret_cast<float *>(w->bytes + t_bytes), w->counters, m, g.k, count, rank, rank_p, 0, 0};
+  TRELLIS_TRY(launch_shrink<false>(h, sh, stream));
+  Product p{};
+  p.p = x;
+  p.codes = codes;
+  p.scales = scales;
+  p.out = out;
+  p.partials = reinterpret_cast<float *>(w->bytes + t_bytes + hp);
+  p.counters = w->counters;
+  p.m = m;
+  p.n = g.n;
+  p.k = g.k;
+  p.low = LowRank{index, b, t, count, rank, rank_p};
+  return launch(s, p, stream);
+}
+
+trellis_status trellis_adapters_backward(const uint16_t *dout, const uint16_t *x, int32_t m, const uint32_t *codes,
+                                         const uint16_t *scales, trellis_geom g, const uint16_t *a, const uint16_t *b,
+                                         const float *gain, const int32_t *index, int32_t count, int32_t rank,
+                                         uint16_t *dx, uint16_t *da, uint16_t *db, void *hip_stream) {
+  if (!geom_ok(g)) return TRELLIS_E_GEOMETRY;
+  if (m < 1 || m > TRELLIS_MAX_ROWS) return TRELLIS_E_M;
+  if (count < 1 || count > TRELLIS_MAX_ADAPTERS || rank < 1 || rank > TRELLIS_MAX_RANK) return TRELLIS_E_ADAPTERS;
+  if (!dout || !x || !codes || !scales || !a || !b || !gain || !index || !dx || !da || !db) return TRELLIS_E_NULL;
+  if (!on(dout, 16) || !on(x, 16) || !on(codes, 16) || !on(scales, 2) || !on(a, 16) || !on(b, 16) || !on(gain, 4) ||
+      !on(index, 4) || !on(dx, 16) || !on(da, 16) || !on(db, 16))
+    return TRELLIS_E_ALIGN;
+  hipStream_t stream = reinterpret_cast<hipStream_t>(hip_stream);
+  std::lock_guard<std::mutex> lock(g_lock);
+  int dev = 0, cus = 0;
+  TRELLIS_TRY(device(dev, cus));
+  const int rank_p = (rank + 31) / 32 * 32;
+  const Shape s = shape_of(kTransposed, g, m, 1, cus);
+  const ShrinkShape hx = shrink_shape(m, g.k, rank, cus), hd = shrink_shape(m, g.n, rank, cus);
+  const size_t t_bytes = up256((size_t)m * rank_p * 4), r_bytes = up256((size_t)count * sizeof(int2));
+  size_t part = hx.partial_bytes > hd.partial_bytes ? hx.partial_bytes : hd.partial_bytes;
+  if (s.partial_bytes > part) part = s.partial_bytes;
+  int64_t counters = s.tiles > hx.cells ? s.tiles : hx.cells;
+  Space *w = nullptr;
+  TRELLIS_TRY(space(dev, stream, 2 * t_bytes + r_bytes + part, (size_t)counters, w));
+  float *const t = reinterpret_cast<float *>(w->bytes), *const u = reinterpret_cast<float *>(w->bytes + t_bytes);
+  int2 *const range = reinterpret_cast<int2 *>(w->bytes + 2 * t_bytes);
+  float *const partials = reinterpret_cast<float *>(w->bytes + 2 * t_bytes + r_bytes);
+  TRELLIS_TRY(launch_shrink<false>(
+      hx, Shrink{x, a, gain, index, t, partials, w->counters, m, g.k, count, rank, rank_p, 0, 0}, stream));
+  TRELLIS_TRY(launch_shrink<true>(
+      hd, Shrink{dout, b, gain, index, u, partials, w->counters, m, g.n, count, rank, rank_p, 0, 0}, stream));
+  hipLaunchKernelGGL(range_kernel, dim3((unsigned)count), dim3(256), 0, stream, index, m, range);
+  if (hipGetLastError() != hipSuccess) return TRELLIS_E_HIP;
+  Product p{};
+  p.p = dout;
+  p.codes = codes;
+  p.scales = scales;
+  p.out = dx;
+  p.partials = partials;
+  p.counters = w->counters;
+  p.m = m;
+  p.n = g.n;
+  p.k = g.k;
+  p.low = LowRank{index, a, u, count, rank, rank_p};
+  TRELLIS_TRY(launch(s, p, stream));
+  Outer o{x, dout, u, t, index, range, da, db, m, g.n, g.k, rank, rank_p, g.k / 16, g.k / 16 + (g.n + 15) / 16};
+  hipLaunchKernelGGL(outer_kernel, dim3((unsigned)((o.tiles + 3) / 4), (unsigned)count, (unsigned)((rank + 15) / 16)),
+                     dim3(256), 0, stream, o);
+  return hipGetLastError() == hipSuccess ? TRELLIS_OK : TRELLIS_E_HIP;
+}
+
+trellis_status trellis_gated(const uint16_t *x, int32_t m, const uint32_t *codes_gate, const uint16_t *scales_gate,
+                             const uint32_t *codes_up, const uint16_t *scales_up, trellis_geom g, uint16_t *h,
+                             uint16_t *gate, uint16_t *up, void *hip_stream) {
+  if (!geom_ok(g)) return TRELLIS_E_GEOMETRY;
+  if (m < 1 || m > TRELLIS_MAX_ROWS) return TRELLIS_E_M;
+  if (!x || !codes_gate || !scales_gate || !codes_up || !scales_up || !h) return TRELLIS_E_NULL;
+  if (!on(x, 16) || !on(codes_gate, 16) || !on(scales_gate, 2) || !on(codes_up, 16) || !on(scales_up, 2) || !on(h, 16) ||
+      !on(gate, 16) || !on(up, 16))
+    return TRELLIS_E_ALIGN;
+  hipStream_t stream = reinterpret_cast<hipStream_t>(hip_stream);
+  std::lock_guard<std::mutex> lock(g_lock);
+  int dev = 0, cus = 0;
+  TRELLIS_TRY(device(dev, cus));
+  const Shape s = shape_of(kGated, g, m, 1, cus);
+  Space *w = nullptr;
+  TRELLIS_TRY(space(dev, stream, s.partial_bytes, (size_t)s.tiles, w));
+  Product p{};
+  p.p = x;
+  p.codes = codes_gate;
+  p.codes2 = codes_up;
+  p.scales = scales_gate;
+  p.scales2 = scales_up;
+  p.out = h;
+  p.gate = gate;
+  p.up = up;
+  p.partials = reinterpret_cast<float *>(w->bytes);
+  p.counters = w->counters;
+  p.m = m;
+  p.n = g.n;
+  p.k = g.k;
+  return launch(s, p, stream);
+}
+
+trellis_status trellis_gated_backward(const uint16_t *dh, const uint16_t *gate, const uint16_t *up, int32_t m,
+                                      const uint32_t *codes_gate, const uint16_t *scales_gate,
+                                      const uint32_t *codes_up, const uint16_t *scales_up, trellis_geom g,
+                                      uint16_t *dx, uint16_t *dgate, uint16_t *dup, void *hip_stream) {
+  if (!geom_ok(g)) return TRELLIS_E_GEOMETRY;
+  if (m < 1 || m > TRELLIS_MAX_ROWS) return TRELLIS_E_M;
+  if (!dh || !gate || !up || !codes_gate || !scales_gate || !codes_up || !scales_up || !dx || !dgate || !dup)
+    return TRELLIS_E_NULL;
+  if (!on(dh, 16) || !on(gate, 16) || !on(up, 16) || !on(codes_gate, 16) || !on(scales_gate, 2) || !on(codes_up, 16) ||
+      !on(scales_up, 2) || !on(dx, 16) || !on(dgate, 16) || !on(dup, 16))
+    return TRELLIS_E_ALIGN;
+  hipStream_t stream = reinterpret_cast<hipStream_t>(hip_stream);
+  std::lock_guard<std::mutex> lock(g_lock);
+  int dev = 0, cus = 0;
+  TRELLIS_TRY(device(dev, cus));
+  const Shape s = shape_of(kTransposed, g, m, 2, cus);
+  Space *w = nullptr;
+  TRELLIS_TRY(space(dev, stream, s.partial_bytes, (size_t)s.tiles, w));
+  const int64_t quads = (int64_t)m * (g.n / 4);
+  (void)hipGetLastError();
+  hipLaunchKernelGGL(gated_grad_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream, dh, gate, up, quads,
+                     dgate, dup);
+  if (hipGetLastError() != hipSuccess) return TRELLIS_E_HIP;
+  Product p{};
+  p.p = dgate;
+  p.p2 = dup;
+  p.codes = codes_gate;
+  p.codes2 = codes_up;
+  p.scales = scales_gate;
+  p.scales2 = scales_up;
+  p.out = dx;
+  p.partials = reinterpret_cast<float *>(w->bytes);
+  p.counters = w->counters;
+  p.m = m;
+  p.n = g.n;
+  p.k = g.k;
+  return launch(s, p, stream);
+}
+
+}  // extern "C"

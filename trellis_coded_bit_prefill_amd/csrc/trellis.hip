@@ -1606,11 +1606,12 @@ const char *trellis_status_string(trellis_status s) {
   switch (s) {
     case TRELLIS_OK: return "ok";
     case TRELLIS_E_GEOMETRY: return "unsupported geometry (need t=256, l=12, bits 2/3/4, K%256==0, N%4==0)";
-    case TRELLIS_E_M: return "unsupported batch: m must be in [5, 15] (prefill) or [1, 4] (matvec)";
+    case TRELLIS_E_M: return "unsupported batch: m must be in [5, 15] (prefill), [1, 4] (matvec), [1, 15] (gate_up) or [1, 2^20] (adapters, gated)";
     case TRELLIS_E_NULL: return "null pointer argument";
     case TRELLIS_E_ALIGN: return "misaligned pointer argument";
     case TRELLIS_E_HIP: return "HIP runtime error";
     case TRELLIS_E_SCRATCH: return "the call needs more workspace than the no-allocation entry point's fixed scratch holds";
+    case TRELLIS_E_ADAPTERS: return "unsupported adapters: count must be in [1, 4096] and rank in [1, 128]";
   }
   return "unknown status";
 }
