@@ -154,6 +154,14 @@ __device__ __forceinline__ void store4(uint16_t *p, f32x4 v) {
   *reinterpret_cast<u16x4 *>(p) = u16x4{bf16_of(v[0]), bf16_of(v[1]), bf16_of(v[2]), bf16_of(v[3])};
 }
 
+}  // namespace
+}  // namespace trellis
+
+#include "dense.hpp"
+
+namespace trellis {
+namespace {
+
 // One tile: 16 MT rows of P by a group of output columns. 8 waves.
 //   forward     group = 128 rows of W; wave (wn, wk): rows 32 wn .. +31 (two
 //               16-row tiles), half wk of each 256-weight block
@@ -819,6 +827,164 @@ trellis_status launch(const Shape &s, Product p, hipStream_t stream) {
   return hipGetLastError() == hipSuccess ? TRELLIS_OK : TRELLIS_E_HIP;
 }
 
+// ---- many rows (dense.hpp) ---------------------------------------------------
+
+// Rows from which W is decoded once into the workspace.
+constexpr int kDenseFrom = 256;
+// Operand workspace of one launch; larger matrices go in slabs of columns.
+constexpr int64_t kOperandBytes = (int64_t)1 << 30;
+
+struct DenseShape {
+  int nt;              // accumulator tiles per wave
+  int matrices;        // gated: 2 in the tiles, transposed: in the contraction
+  int steps, steps1, cols;
+  int64_t tiles, slab;  // operand tiles in all and per launch
+  size_t operand_bytes, pad_bytes;
+};
+DenseShape dense_shape(int kind, trellis_geom g, int32_t m, int matrices, int cus) {
+  DenseShape s{};
+  s.matrices = matrices;
+  const bool t = kind == kTransposed;
+  s.cols = t ? (g.n + 63) / 64 * 64 : g.k;
+  s.steps1 = s.cols / kDenseStep;
+  s.steps = t ? s.steps1 * matrices : s.steps1;
+  const int64_t width = t ? g.k : g.n, one = (width + 15) / 16;
+  s.tiles = kind == kGated ? 2 * one : one;
+  // The column tile whose rounds over the card cost least.
+  const int64_t mt = (m + kDenseRows - 1) / kDenseRows;
+  double best = 0;
+  for (int nt = 8; nt >= 4; --nt) {
+    if (kind == kGated && nt % 2) continue;
+    const int64_t wg = mt * ((s.tiles + 2 * nt - 1) / (2 * nt));
+    const double cost = (double)((wg + cus - 1) / cus) * (nt + 1.0);
+    if (s.nt == 0 || cost < best) {
+      best = cost;
+      s.nt = nt;
+    }
+  }
+  const int64_t tile_bytes = (int64_t)s.steps * 2 * 1024;
+  int64_t slab = kOperandBytes / tile_bytes / (16 * s.nt) * (16 * s.nt);  // whole workgroup tiles, fours and pairs
+  if (slab < 16 * s.nt) slab = 16 * s.nt;
+  if (slab > s.tiles) slab = s.tiles;
+  s.slab = slab;
+  s.operand_bytes = (size_t)(slab * tile_bytes);
+  s.pad_bytes = t && s.cols != g.n ? up256((size_t)m * s.cols * 2) : 0;
+  return s;
+}
+
+typedef void (*DenseFn)(Dense);
+template <bool T>
+DenseFn dense_of(int nt) {
+  switch (nt) {
+    case 4: return &dense_kernel<4, false, T>;
+    case 5: return &dense_kernel<5, false, T>;
+    case 6: return &dense_kernel<6, false, T>;
+    case 7: return &dense_kernel<7, false, T>;
+    default: return &dense_kernel<8, false, T>;
+  }
+}
+DenseFn dense_fn(int kind, int nt) {
+  if (kind == kGated) return nt == 4 ? &dense_kernel<4, true, false> : nt == 6 ? &dense_kernel<6, true, false> : &dense_kernel<8, true, false>;
+  return kind == kTransposed ? dense_of<true>(nt) : dense_of<false>(nt);
+}
+
+trellis_status launch_dense(int kind, const DenseShape &s, trellis_geom g, const Product &p, unsigned char *operands,
+                            unsigned char *pads, hipStream_t stream) {
+  const DenseFn fn = dense_fn(kind, s.nt);
+  const size_t lds = 2 * ((size_t)kDenseRows * kDenseStep * 2 + (size_t)2 * s.nt * 2048);
+  static bool ready[kMaxDevices][3][9];
+  int dev = 0, cus = 0;
+  if (device(dev, cus) != TRELLIS_OK) return TRELLIS_E_HIP;
+  if (!ready[dev][kind][s.nt]) {
+    if (hipFuncSetAttribute(reinterpret_cast<const void *>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) !=
+        hipSuccess)
+      return TRELLIS_E_HIP;
+    ready[dev][kind][s.nt] = true;
+  }
+  Dense d{};
+  d.p = p.p;
+  d.p2 = p.p2;
+  d.w = reinterpret_cast<const uint16_t *>(operands);
+  d.out = p.out;
+  d.gate = p.gate;
+  d.up = p.up;
+  d.m = p.m;
+  d.cols = s.cols;
+  d.steps = s.steps;
+  d.steps1 = s.steps1;
+  d.width = kind == kTransposed ? g.k : g.n;
+  d.mtiles = (p.m + kDenseRows - 1) / kDenseRows;
+  d.low = p.low;
+  (void)hipGetLastError();
+  if (s.pad_bytes) {
+    const int64_t quads = (int64_t)p.m * (s.cols / 4);
+    for (int i = 0; i < s.matrices; ++i) {
+      uint16_t *dst = reinterpret_cast<uint16_t *>(pads + i * s.pad_bytes);
+      hipLaunchKernelGGL(pad_rows_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream, i ? p.p2 : p.p,
+                         (int64_t)p.m, g.n, s.cols, dst);
+      (i ? d.p2 : d.p) = dst;
+    }
+  }
+  for (int64_t first = 0; first < s.tiles; first += s.slab) {
+    const int tiles = (int)(s.tiles - first < s.slab ? s.tiles - first : s.slab);
+    Unpack u{{p.codes, p.codes2}, {p.scales, p.scales2}, reinterpret_cast<uint16_t *>(operands), g.n, g.k, 2 * s.steps, 0, 0, 1};
+    if (kind == kTransposed) {
+      u.first = (int)first;
+      u.tiles = tiles;
+      u.matrices = s.matrices;
+      const int64_t waves = (int64_t)(tiles / 4) * (2 * s.steps1);
+      const dim3 grid((unsigned)((waves + 3) / 4), (unsigned)s.matrices);
+      if (g.bits == 2) hipLaunchKernelGGL(unpack_columns_kernel<2>, grid, dim3(256), 0, stream, u);
+      else if (g.bits == 3) hipLaunchKernelGGL(unpack_columns_kernel<3>, grid, dim3(256), 0, stream, u);
+      else hipLaunchKernelGGL(unpack_columns_kernel<4>, grid, dim3(256), 0, stream, u);
+    } else {
+      const int mats = kind == kGated ? 2 : 1;
+      u.first = (int)(first / mats);
+      u.tiles = tiles / mats;
+      u.matrices = mats;
+      const int64_t waves = (int64_t)u.tiles * (g.k >> 8);
+      const dim3 grid((unsigned)((waves + 3) / 4), (unsigned)mats);
+      if (g.bits == 2) hipLaunchKernelGGL(unpack_rows_kernel<2>, grid, dim3(256), 0, stream, u);
+      else if (g.bits == 3) hipLaunchKernelGGL(unpack_rows_kernel<3>, grid, dim3(256), 0, stream, u);
+      else hipLaunchKernelGGL(unpack_rows_kernel<4>, grid, dim3(256), 0, stream, u);
+    }
+    if (hipGetLastError() != hipSuccess) return TRELLIS_E_HIP;
+    d.first = (int)(first * 16 / (kind == kGated ? 2 : 1));
+    d.tiles = tiles;
+    d.ntiles = (tiles + 2 * s.nt - 1) / (2 * s.nt);
+    hipLaunchKernelGGL(fn, dim3((unsigned)(d.mtiles * d.ntiles)), dim3(kDenseThreads), lds, stream, d);
+    if (hipGetLastError() != hipSuccess) return TRELLIS_E_HIP;
+  }
+  return TRELLIS_OK;
+}
+
+// Workspace of a product, and its launch with that workspace.
+struct Plan {
+  bool dense;
+  Shape fused;
+  DenseShape many;
+  size_t bytes;
+  int64_t counters;
+};
+Plan plan_of(int kind, trellis_geom g, int32_t m, int matrices, int cus) {
+  Plan p{};
+  p.dense = m >= kDenseFrom;
+  if (p.dense) {
+    p.many = dense_shape(kind, g, m, matrices, cus);
+    p.bytes = up256(p.many.operand_bytes) + p.many.pad_bytes * matrices;
+  } else {
+    p.fused = shape_of(kind, g, m, matrices, cus);
+    p.bytes = p.fused.partial_bytes;
+    p.counters = p.fused.tiles;
+  }
+  return p;
+}
+trellis_status run(const Plan &pl, int kind, trellis_geom g, Product p, unsigned char *ws, hipStream_t stream) {
+  if (pl.dense) return launch_dense(kind, pl.many, g, p, ws, ws + up256(pl.many.operand_bytes), stream);
+  p.partials = reinterpret_cast<float *>(ws);
+  return launch(pl.fused, p, stream);
+}
+
 // Spans of a shrink product: enough workgroups to fill the card.
 int spans_of(int64_t cells, int cols, int cus) {
   int64_t want = (4 * (int64_t)cus + cells - 1) / cells;
@@ -877,12 +1043,11 @@ trellis_status trellis_adapters(const uint16_t *x, int32_t m, const uint32_t *co
   int dev = 0, cus = 0;
   TRELLIS_TRY(device(dev, cus));
   const int rank_p = (rank + 31) / 32 * 32;
-  const Shape s = shape_of(kForward, g, m, 1, cus);
+  const Plan s = plan_of(kForward, g, m, 1, cus);
   const ShrinkShape h = shrink_shape(m, g.k, rank, cus);
   const size_t t_bytes = up256((size_t)m * rank_p * 4), hp = up256(h.partial_bytes);
   Space *w = nullptr;
-  TRELLIS_TRY(space(dev, stream, t_bytes + hp + s.partial_bytes,
-                    (size_t)(s.tiles > h.cells ? s.tiles : h.cells), w));
+  TRELLIS_TRY(space(dev, stream, t_bytes + hp + s.bytes, (size_t)(s.counters > h.cells ? s.counters : h.cells), w));
   float *const t = reinterpret_cast<float *>(w->bytes);
   Shrink sh{x, a, gain, index, t, reinterpret_cast<float *>(w->bytes + t_bytes), w->counters, m, g.k, count, rank, rank_p, 0, 0};
   TRELLIS_TRY(launch_shrink<false>(h, sh, stream));
@@ -891,13 +1056,12 @@ trellis_status trellis_adapters(const uint16_t *x, int32_t m, const uint32_t *co
   p.codes = codes;
   p.scales = scales;
   p.out = out;
-  p.partials = reinterpret_cast<float *>(w->bytes + t_bytes + hp);
   p.counters = w->counters;
   p.m = m;
   p.n = g.n;
   p.k = g.k;
   p.low = LowRank{index, b, t, count, rank, rank_p};
-  return launch(s, p, stream);
+  return run(s, kForward, g, p, w->bytes + t_bytes + hp, stream);
 }
 
 trellis_status trellis_adapters_backward(const uint16_t *dout, const uint16_t *x, int32_t m, const uint32_t *codes,
@@ -916,12 +1080,12 @@ trellis_status trellis_adapters_backward(const uint16_t *dout, const uint16_t *x
   int dev = 0, cus = 0;
   TRELLIS_TRY(device(dev, cus));
   const int rank_p = (rank + 31) / 32 * 32;
-  const Shape s = shape_of(kTransposed, g, m, 1, cus);
+  const Plan s = plan_of(kTransposed, g, m, 1, cus);
   const ShrinkShape hx = shrink_shape(m, g.k, rank, cus), hd = shrink_shape(m, g.n, rank, cus);
   const size_t t_bytes = up256((size_t)m * rank_p * 4), r_bytes = up256((size_t)count * sizeof(int2));
   size_t part = hx.partial_bytes > hd.partial_bytes ? hx.partial_bytes : hd.partial_bytes;
-  if (s.partial_bytes > part) part = s.partial_bytes;
-  int64_t counters = s.tiles > hx.cells ? s.tiles : hx.cells;
+  if (s.bytes > part) part = s.bytes;
+  const int64_t counters = s.counters > hx.cells ? s.counters : hx.cells;  // (hd has as many cells as hx)
   Space *w = nullptr;
   TRELLIS_TRY(space(dev, stream, 2 * t_bytes + r_bytes + part, (size_t)counters, w));
   float *const t = reinterpret_cast<float *>(w->bytes), *const u = reinterpret_cast<float *>(w->bytes + t_bytes);
@@ -938,13 +1102,12 @@ trellis_status trellis_adapters_backward(const uint16_t *dout, const uint16_t *x
   p.codes = codes;
   p.scales = scales;
   p.out = dx;
-  p.partials = partials;
   p.counters = w->counters;
   p.m = m;
   p.n = g.n;
   p.k = g.k;
   p.low = LowRank{index, a, u, count, rank, rank_p};
-  TRELLIS_TRY(launch(s, p, stream));
+  TRELLIS_TRY(run(s, kTransposed, g, p, reinterpret_cast<unsigned char *>(partials), stream));
   Outer o{x, dout, u, t, index, range, da, db, m, g.n, g.k, rank, rank_p, g.k / 16, g.k / 16 + (g.n + 15) / 16};
   hipLaunchKernelGGL(outer_kernel, dim3((unsigned)((o.tiles + 3) / 4), (unsigned)count, (unsigned)((rank + 15) / 16)),
                      dim3(256), 0, stream, o);
@@ -964,9 +1127,9 @@ trellis_status trellis_gated(const uint16_t *x, int32_t m, const uint32_t *codes
   std::lock_guard<std::mutex> lock(g_lock);
   int dev = 0, cus = 0;
   TRELLIS_TRY(device(dev, cus));
-  const Shape s = shape_of(kGated, g, m, 1, cus);
+  const Plan s = plan_of(kGated, g, m, 1, cus);
   Space *w = nullptr;
-  TRELLIS_TRY(space(dev, stream, s.partial_bytes, (size_t)s.tiles, w));
+  TRELLIS_TRY(space(dev, stream, s.bytes, (size_t)s.counters, w));
   Product p{};
   p.p = x;
   p.codes = codes_gate;
@@ -976,12 +1139,11 @@ trellis_status trellis_gated(const uint16_t *x, int32_t m, const uint32_t *codes
   p.out = h;
   p.gate = gate;
   p.up = up;
-  p.partials = reinterpret_cast<float *>(w->bytes);
   p.counters = w->counters;
   p.m = m;
   p.n = g.n;
   p.k = g.k;
-  return launch(s, p, stream);
+  return run(s, kGated, g, p, w->bytes, stream);
 }
 
 trellis_status trellis_gated_backward(const uint16_t *dh, const uint16_t *gate, const uint16_t *up, int32_t m,
@@ -999,9 +1161,9 @@ trellis_status trellis_gated_backward(const uint16_t *dh, const uint16_t *gate, 
   std::lock_guard<std::mutex> lock(g_lock);
   int dev = 0, cus = 0;
   TRELLIS_TRY(device(dev, cus));
-  const Shape s = shape_of(kTransposed, g, m, 2, cus);
+  const Plan s = plan_of(kTransposed, g, m, 2, cus);
   Space *w = nullptr;
-  TRELLIS_TRY(space(dev, stream, s.partial_bytes, (size_t)s.tiles, w));
+  TRELLIS_TRY(space(dev, stream, s.bytes, (size_t)s.counters, w));
   const int64_t quads = (int64_t)m * (g.n / 4);
   (void)hipGetLastError();
   hipLaunchKernelGGL(gated_grad_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream, dh, gate, up, quads,
@@ -1015,12 +1177,11 @@ trellis_status trellis_gated_backward(const uint16_t *dh, const uint16_t *gate, 
   p.scales = scales_gate;
   p.scales2 = scales_up;
   p.out = dx;
-  p.partials = reinterpret_cast<float *>(w->bytes);
   p.counters = w->counters;
   p.m = m;
   p.n = g.n;
   p.k = g.k;
-  return launch(s, p, stream);
+  return run(s, kTransposed, g, p, w->bytes, stream);
 }
 
 }  // extern "C"
