@@ -23,6 +23,7 @@
 #include <map>
 #include <mutex>
 #include <thread>
+#include <utility>
 
 #include "decode.hpp"
 #include "trellis.h"
@@ -33,12 +34,15 @@ namespace {
 constexpr int kThreads = 512;       // product_kernel: 8 waves
 constexpr int kStep = 256;          // contraction columns staged per step
 constexpr int kStride = kStep * 2 + 16;  // bytes per staged row (16 B of padding spread the rows over the banks)
-constexpr int kHalf = 128;          // output columns reduced at a time
-constexpr int kRedStride = kHalf + 4;    // floats per row of the reduction tile
-constexpr int kTableBytes = 4096 * 4;
+constexpr int kRedStride = 128 + 4;  // floats per row of the reduction tile (at most 128 columns at a time)
+constexpr int kTableBytes = 4096 * 2;
 constexpr int kRawBuffer = 0x00020000;  // gfx9 raw-buffer descriptor word 3
 constexpr int kSc1 = 16;                // cache policy: the level that is coherent across the XCDs' L2s
 static_assert(2 * 16 * kRedStride * 4 == 2 * 16 * kStride, "the reduction tile reuses the staged rows' space");
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ uint16_t bf16_of(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
 
@@ -67,80 +71,126 @@ struct Product {
   LowRank low;
 };
 
-// Adds the adapters' term to a wave's accumulators: for every adapter that a
-// 16-row tile names, the product of t's rows (as the sum of two bf16 numbers,
-// 2^-16 relative) with the factor, kept only in the rows that name it, so an
-// adapter's infinities and NaNs stay in its own rows.
-// load(a, r0, w): the NT operands for rank columns r0 + 8g .. +7.
-template <int MT, int NT, typename Load>
-__device__ __forceinline__ void add_low_rank(const LowRank &L, int m, int m0, int lane, f32x4 (&acc)[MT][NT], Load load) {
+// The adapters' term of one 16-row tile and a wave's NT column tiles: for every
+// adapter that the rows name, the product of t's rows (as the sum of two bf16
+// numbers, 2^-16 relative) with the factor, kept only in the rows that name
+// it, so an adapter's infinities and NaNs stay in its own rows.
+// load(a, r0, w): the NT operands for rank columns r0 .. +7.
+template <int NT, typename Load>
+__device__ __forceinline__ void low_rank_tile(const LowRank &L, int m, int m0, int lane, f32x4 (&sum)[NT], Load load) {
   const int j = lane & 15, g = lane >> 4;
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    const int row = m0 + 16 * mt + j;
-    const int rowc = row < m ? row : m - 1;
-    int idx = row < m ? L.index[row] : -1;
-    if (idx >= L.count) idx = -1;
-    int of[4];
+  for (int i = 0; i < NT; ++i) sum[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int row = m0 + j;
+  const int rowc = row < m ? row : m - 1;
+  int idx = row < m ? L.index[row] : -1;
+  if (idx >= L.count) idx = -1;
+  int of[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) of[e] = __shfl(idx, 4 * g + e);
-    uint64_t left = __ballot(idx >= 0) & 0xFFFFull;
-    while (left) {
-      const int a = __builtin_amdgcn_readlane(idx, __builtin_ctzll(left));
-      left &= ~__ballot(idx == a);
-      f32x4 d[NT];
+  for (int e = 0; e < 4; ++e) of[e] = __shfl(idx, 4 * g + e);
+  uint64_t left = __ballot(idx >= 0) & 0xFFFFull;
+  while (left) {
+    const int a = __builtin_amdgcn_readlane(idx, __builtin_ctzll(left));
+    left &= ~__ballot(idx == a);
+    f32x4 d[NT];
 #pragma unroll
-      for (int i = 0; i < NT; ++i) d[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-      for (int r0 = 0; r0 < L.rank_p; r0 += 32) {
-        const float *tp = L.t + (int64_t)rowc * L.rank_p + r0 + 8 * g;
-        const f32x4 t0 = *reinterpret_cast<const f32x4 *>(tp), t1 = *reinterpret_cast<const f32x4 *>(tp + 4);
-        bf16x8 hi, lo;
+    for (int i = 0; i < NT; ++i) d[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int r0 = 0; r0 < L.rank_p; r0 += 32) {
+      const float *tp = L.t + (int64_t)rowc * L.rank_p + r0 + 8 * g;
+      const f32x4 t0 = *reinterpret_cast<const f32x4 *>(tp), t1 = *reinterpret_cast<const f32x4 *>(tp + 4);
+      bf16x8 hi, lo;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float v = e < 4 ? t0[e] : t1[e - 4];
-          hi[e] = (__bf16)v;
-          lo[e] = (__bf16)(v - (float)hi[e]);
-        }
-        bf16x8 w[NT];
-        load(a, r0 + 8 * g, w);
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          d[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, w[i], d[i], 0, 0, 0);
-          d[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, w[i], d[i], 0, 0, 0);
-        }
+      for (int e = 0; e < 8; ++e) {
+        const float v = e < 4 ? t0[e] : t1[e - 4];
+        hi[e] = (__bf16)v;
+        lo[e] = (__bf16)(v - (float)hi[e]);
       }
+      bf16x8 w[NT];
+      load(a, r0 + 8 * g, w);
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[mt][i][e] += of[e] == a ? d[i][e] : 0.f;
+      for (int i = 0; i < NT; ++i) {
+        d[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, w[i], d[i], 0, 0, 0);
+        d[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, w[i], d[i], 0, 0, 0);
+      }
     }
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[i][e] += of[e] == a ? d[i][e] : 0.f;
   }
 }
 
-// Weight E (0..31) of a forward lane's half block, through the value table.
-template <int BITS, int O>
-__device__ __forceinline__ float table_weight(const uint32_t (&d)[BITS + 1], const unsigned char *table, float s) {
-  return *reinterpret_cast<const float *>(table + win_xa<O, 2>(d)) * s;
+// ---- decoding in the product kernel ------------------------------------------
+// Half of the weights go through an LDS table (window -> float16 code, one
+// gather and about 3 VALU operations a weight), half through the hash on the
+// ALU (about 5.5): gathers and VALU work then run side by side. A wave whose
+// rows' scales are not all in the range where code * q is exact takes the
+// page's chain for all of them.
+__device__ __forceinline__ uint32_t table_code(const unsigned char *table, uint32_t addr) {
+  return *reinterpret_cast<const uint16_t *>(table + addr);
+}
+
+// Forward lane: weights 8 u .. 8 u + 7 (u = 0 .. 3) of its 32, weight i at
+// local bit (31 - i) * BITS of d.
+template <int BITS, int U, int... S>
+__device__ __forceinline__ void group_addresses(const uint32_t (&d)[BITS + 1], uint32_t (&a)[8],
+                                                std::integer_sequence<int, S...>) {
+  ((a[S] = win_xa<(31 - 8 * U - S) * BITS, 1>(d)), ...);
 }
 template <int BITS, int U, int... S>
-__device__ __forceinline__ bf16x8 half_group(const uint32_t (&d)[BITS + 1], const unsigned char *table, float s,
-                                             std::integer_sequence<int, S...>) {
-  const float f[8] = {table_weight<BITS, (31 - 8 * U - S) * BITS>(d, table, s)...};
+__device__ __forceinline__ bf16x8 group_hashed(const uint32_t (&d)[BITS + 1], float q, float k, std::integer_sequence<int, S...>) {
+  const float f[8] = {__builtin_fmaf(code_plus_magic(win12<(31 - 8 * U - S) * BITS>(d)), q, k)...};
   bf16x8 w;
 #pragma unroll
   for (int i = 0; i < 8; ++i) w[i] = (__bf16)f[i];
   return w;
 }
-template <int BITS>
-__device__ __forceinline__ bf16x8 half_group(const uint32_t (&d)[BITS + 1], const unsigned char *table, float s, int u) {
-  constexpr auto seq = std::make_integer_sequence<int, 8>{};
-  switch (u) {
-    case 0: return half_group<BITS, 0>(d, table, s, seq);
-    case 1: return half_group<BITS, 1>(d, table, s, seq);
-    case 2: return half_group<BITS, 2>(d, table, s, seq);
-    default: return half_group<BITS, 3>(d, table, s, seq);
-  }
+template <int BITS, int U, int... S>
+__device__ __forceinline__ bf16x8 group_chain(const uint32_t (&d)[BITS + 1], float s, std::integer_sequence<int, S...>) {
+  const float f[8] = {(trellis_value(code_of(win12<(31 - 8 * U - S) * BITS>(d))) * s)...};
+  bf16x8 w;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = (__bf16)f[i];
+  return w;
 }
+using Eight = std::make_integer_sequence<int, 8>;
+
+// Codes of group U, gathered from the table. For k = 4 the windows of weights
+// i and i + 4 are 16 bits apart and come out of one shifted word.
+template <int O, int N>
+__device__ __forceinline__ void pair_addresses(const uint32_t (&d)[N], uint32_t mask, uint32_t &low, uint32_t &high) {
+  constexpr int sh = O - 1, w = sh < 0 ? 0 : sh >> 5, r = sh & 31;
+  uint32_t v;
+  if constexpr (sh < 0) v = d[0] << 1;
+  else if constexpr (r == 0) v = d[w];
+  else v = __builtin_amdgcn_alignbit(d[w + 1], d[w], r);
+  low = v & 0x1FFEu;
+  high = and_hi16(v, mask);
+}
+template <int BITS, int U>
+__device__ __forceinline__ void gather_codes(const uint32_t (&d)[BITS + 1], const unsigned char *table, uint32_t mask,
+                                             uint32_t (&r)[8]) {
+  uint32_t a[8];
+  if constexpr (BITS == 4) {
+    pair_addresses<(31 - 8 * U - 4) * 4>(d, mask, a[4], a[0]);
+    pair_addresses<(31 - 8 * U - 5) * 4>(d, mask, a[5], a[1]);
+    pair_addresses<(31 - 8 * U - 6) * 4>(d, mask, a[6], a[2]);
+    pair_addresses<(31 - 8 * U - 7) * 4>(d, mask, a[7], a[3]);
+  } else {
+    group_addresses<BITS, U>(d, a, Eight{});
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) r[e] = table_code(table, a[e]);
+}
+__device__ __forceinline__ bf16x8 gathered_weights(const uint32_t (&r)[8], float q) {
+  bf16x8 w;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) w[e] = (__bf16)mix_lo(r[e], q);
+  return w;
+}
+// A workgroup barrier for LDS data: global loads stay in flight across it
+// (the compiler's own barrier waits for them).
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 enum Kind { kForward = 0, kGated = 1, kTransposed = 2 };
 
@@ -163,8 +213,8 @@ namespace trellis {
 namespace {
 
 // One tile: 16 MT rows of P by a group of output columns. 8 waves.
-//   forward     group = 128 rows of W; wave (wn, wk): rows 32 wn .. +31 (two
-//               16-row tiles), half wk of each 256-weight block
+//   forward     group = 64 NT rows of W; wave (wn, wk): rows 16 NT wn .. (NT
+//               tiles of 16), half wk of each 256-weight block
 //   gated       group = 64 rows of both matrices; wave (wn, wk): rows 16 wn .. +15
 //               of the gate (tile 0) and of the up matrix (tile 1)
 //   transposed  group = one 256-column block; wave (wn, wk): columns 64 wn .. +63
@@ -172,26 +222,35 @@ namespace {
 //               128 wk .. +127 of each 256-row step
 // The units (tile, step) are split evenly over the workgroups; a tile that
 // several share goes through `partials`, summed in a fixed order by the
-// workgroup that arrives last.
-template <int BITS, int KIND, int MT>
-__global__ __launch_bounds__(kThreads) void product_kernel(Product P) {
+// workgroup that arrives last. Code words are loaded two steps ahead
+// (transposed: one 32-row part ahead), P's rows one step ahead.
+// OCC: waves per SIMD (4: two workgroups share a CU, so that one decodes while
+// the other waits at its barrier).
+template <int BITS, int KIND, int MT, int NT, int OCC>
+__global__ __launch_bounds__(kThreads, OCC) void product_kernel(Product P) {
   constexpr bool kT = KIND == kTransposed;
-  constexpr int NT = kT ? 4 : 2;
+  static_assert(kT ? NT == 4 : KIND == kGated ? NT == 2 : NT <= 2, "tiles per wave");
   constexpr int BM = 16 * MT;
-  constexpr int BN = kT ? 256 : KIND == kGated ? 64 : 128;  // output columns of a group
+  constexpr int BN = kT ? 256 : KIND == kGated ? 64 : 64 * NT;  // output columns of a group
+  constexpr int RC = kT ? 128 : 64 * NT;                        // columns reduced per round
   constexpr int wpb = 8 * BITS;
   constexpr int kRounds = kT ? 2 : 1;
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   unsigned char *const table = lds;
-  unsigned char *const xs = lds + kTableBytes;                       // two buffers of BM rows
-  float *const srow = reinterpret_cast<float *>(xs + 2 * BM * kStride);  // transposed: two buffers of 256 row scales
-  uint32_t *const arrived = reinterpret_cast<uint32_t *>(srow + 512);
+  unsigned char *const xs = lds + kTableBytes;  // two buffers of BM rows
+  // transposed: two buffers of 256 row constants (q, k) and scales, and the
+  // buffers' flags of scales outside the exact range, one per wave
+  f32x2 *const rowq = reinterpret_cast<f32x2 *>(xs + 2 * BM * kStride);
+  float *const rows_s = reinterpret_cast<float *>(rowq + 512);
+  uint32_t *const rowf = reinterpret_cast<uint32_t *>(rows_s + 512);
+  uint32_t *const arrived = kT ? rowf + 8 : reinterpret_cast<uint32_t *>(rowq);
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = wave & 3, wk = wave >> 2;
   const int j = lane & 15, g = lane >> 4;
-  for (int i = tid; i < 4096; i += kThreads)
-    reinterpret_cast<uint32_t *>(table)[i] = __builtin_bit_cast(uint32_t, trellis_value(code_of((uint32_t)i)));
+#pragma unroll
+  for (int i = 0; i < 2048 / kThreads; ++i)
+    reinterpret_cast<uint32_t *>(table)[i * kThreads + tid] = code_entry_pair((uint32_t)(i * kThreads + tid));
 
   const uint32_t row_bytes = (uint32_t)(P.k >> 8) * wpb * 4;
   const int cols = kT ? P.n : P.k;  // columns of P
@@ -210,29 +269,35 @@ __global__ __launch_bounds__(kThreads) void product_kernel(Product P) {
       for (int b = 0; b < NT; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     // Staged rows of P: thread t takes 8 columns of row t / 32 + 16 r.
-    uint4 xv[MT];
+    // (The last step stages itself again: straight-line code keeps xv in
+    // registers and the memory waits exact.)
+    u32x4 xv[MT];
     float sv = 0.f;
+    const uint32_t row_b = (uint32_t)cols * 2;
+    const uint32_t valid_b = (uint32_t)(P.m - m0 < BM ? P.m - m0 : BM) * row_b;
+    const uint32_t xoff = (uint32_t)(tid >> 5) * row_b + (uint32_t)(tid & 31) * 16;
     auto fetch = [&](int s) {
       const bool second = kT && s >= P.steps1;
-      const uint16_t *src = second ? P.p2 : P.p;
-      const int c0 = (second ? s - P.steps1 : s) * kStep + (tid & 31) * 8;
+      const int at = second ? s - P.steps1 : s;
+      // rows past m lie outside the buffer and read as zero
+      const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+          const_cast<uint16_t *>((second ? P.p2 : P.p) + (int64_t)m0 * cols + (int64_t)at * kStep), (short)0,
+          (int)(valid_b - (uint32_t)at * (kStep * 2)), kRawBuffer);
+      // transposed: so do columns past N (rows start at multiples of 8 bytes)
+      const int left = cols - at * kStep - (tid & 31) * 8;
 #pragma unroll
       for (int r = 0; r < MT; ++r) {
-        int row = m0 + r * 16 + (tid >> 5);
-        if (row >= P.m) row = P.m - 1;  // feeds output rows that are not stored
-        const uint16_t *q = src + (int64_t)row * cols + c0;
+        const uint32_t o = xoff + (uint32_t)(16 * r) * row_b;
         if constexpr (!kT) {
-          xv[r] = *reinterpret_cast<const uint4 *>(q);
+          xv[r] = __builtin_amdgcn_raw_buffer_load_b128(rs, o, 0, 0);
         } else {
-          // columns past N are zero; rows start at multiples of 8 bytes
-          const uint2 z = {0u, 0u};
-          const uint2 a = c0 < cols ? *reinterpret_cast<const uint2 *>(q) : z;
-          const uint2 b = c0 + 4 < cols ? *reinterpret_cast<const uint2 *>(q + 4) : z;
-          xv[r] = uint4{a.x, a.y, b.x, b.y};
+          const u32x2 a = __builtin_amdgcn_raw_buffer_load_b64(rs, left > 0 ? o : 0x80000000u, 0, 0);
+          const u32x2 b = __builtin_amdgcn_raw_buffer_load_b64(rs, left > 4 ? o + 8 : 0x80000000u, 0, 0);
+          xv[r] = u32x4{a[0], a[1], b[0], b[1]};
         }
       }
       if constexpr (kT) {
-        const int row = (second ? s - P.steps1 : s) * kStep + tid;
+        const int row = at * kStep + tid;
         sv = tid < 256 && row < P.n ? bf16_bits_to_f32((second ? P.scales2 : P.scales)[row]) : 0.f;
       }
     };
@@ -240,25 +305,31 @@ __global__ __launch_bounds__(kThreads) void product_kernel(Product P) {
       unsigned char *dst = xs + (s & 1) * BM * kStride;
 #pragma unroll
       for (int r = 0; r < MT; ++r)
-        *reinterpret_cast<uint4 *>(dst + (r * 16 + (tid >> 5)) * kStride + (tid & 31) * 16) = xv[r];
+        *reinterpret_cast<u32x4 *>(dst + (r * 16 + (tid >> 5)) * kStride + (tid & 31) * 16) = xv[r];
       if constexpr (kT) {
-        if (tid < 256) srow[(s & 1) * 256 + tid] = sv;
+        if (tid < 256) {
+          float q, k;
+          alu_row_constants(sv, q, k);
+          rowq[(s & 1) * 256 + tid] = f32x2{q, k};
+          rows_s[(s & 1) * 256 + tid] = sv;
+          const bool out = !__all(alu_scale_ok(sv));
+          if (lane == 0) rowf[(s & 1) * 4 + wave] = out;
+        }
       }
     };
     __syncthreads();  // the previous tile's reduction is done with this space
     fetch(s0);
-    put(s0);
-    __syncthreads();
 
     if constexpr (!kT) {
-      float sc[NT];
+      float sc[NT], q[NT], kq[NT];
+      bool exact = true;
       const unsigned char *base[NT];
       uint32_t size[NT];
       const int wb = 2 * BITS * g + BITS * (1 - wk);
       const uint32_t off = (uint32_t)j * row_bytes + 4 * wb, off_next = (uint32_t)j * row_bytes + 4 * ((wb + BITS) % wpb);
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
-        const int n0 = KIND == kGated ? group * BN + 16 * wn : group * BN + 32 * wn + 16 * i;
+        const int n0 = KIND == kGated ? group * BN + 16 * wn : group * BN + 16 * NT * wn + 16 * i;
         const uint32_t *c = KIND == kGated && i ? P.codes2 : P.codes;
         const uint16_t *sp = KIND == kGated && i ? P.scales2 : P.scales;
         const int rows = P.n - n0 < 0 ? 0 : P.n - n0 < 16 ? P.n - n0 : 16;
@@ -266,110 +337,195 @@ __global__ __launch_bounds__(kThreads) void product_kernel(Product P) {
         size[i] = (uint32_t)rows * row_bytes;
         sc[i] = j < rows ? bf16_bits_to_f32(sp[n0 + j]) : 0.f;
       }
-      for (int s = s0; s < s1; ++s) {
-        if (s + 1 < s1) fetch(s + 1);
-        const unsigned char *xb = xs + (s & 1) * BM * kStride + j * kStride + (192 - 64 * g + 32 * wk) * 2;
+      struct Words {
         uint32_t d[NT][BITS + 1];
+      };
+      auto load = [&](int s, Words &W) {
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
           // rows past N lie outside the buffer and read as zero
           const uint32_t blk = (uint32_t)s * (wpb * 4);
           const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
               const_cast<unsigned char *>(base[i] + blk), (short)0, (int)(size[i] ? size[i] - blk : 0u), kRawBuffer);
+          if constexpr (BITS == 4) {
+            const auto v = __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0);
 #pragma unroll
-          for (int b = 0; b < BITS; ++b) d[i][b] = __builtin_amdgcn_raw_buffer_load_b32(rs, off + 4 * b, 0, 0);
-          d[i][BITS] = __builtin_amdgcn_raw_buffer_load_b32(rs, off_next, 0, 0);
+            for (int b = 0; b < 4; ++b) W.d[i][b] = v[b];
+          } else if constexpr (BITS == 2) {
+            const auto v = __builtin_amdgcn_raw_buffer_load_b64(rs, off, 0, 0);
+            W.d[i][0] = v[0];
+            W.d[i][1] = v[1];
+          } else {
+#pragma unroll
+            for (int b = 0; b < BITS; ++b) W.d[i][b] = __builtin_amdgcn_raw_buffer_load_b32(rs, off + 4 * b, 0, 0);
+          }
+          W.d[i][BITS] = __builtin_amdgcn_raw_buffer_load_b32(rs, off_next, 0, 0);
         }
+      };
+      Words A, B;
+      load(s0, A);
+      load(s0 + 1 < s1 ? s0 + 1 : s0, B);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          bf16x8 w[NT];
-#pragma unroll
-          for (int i = 0; i < NT; ++i) w[i] = half_group<BITS>(d[i], table, sc[i], u);
+      for (int i = 0; i < NT; ++i) {
+        alu_row_constants(sc[i], q[i], kq[i]);
+        exact = exact && alu_scale_ok(sc[i]);
+      }
+      const bool chain = !__all(exact);
+      put(s0);
+      lds_barrier();
+      // Rows with scales outside the exact range take a loop of their own.
+      auto step = [&](int s, Words &W, auto chained) {
+        fetch(s + 1 < s1 ? s + 1 : s);
+        const unsigned char *xb = xs + (s & 1) * BM * kStride + j * kStride + (192 - 64 * g + 32 * wk) * 2;
+        auto multiply = [&](int u, const bf16x8 (&w)[NT]) {
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
             const bf16x8 x = *reinterpret_cast<const bf16x8 *>(xb + mt * 16 * kStride + 16 * u);
 #pragma unroll
             for (int i = 0; i < NT; ++i) acc[mt][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w[i], acc[mt][i], 0, 0, 0);
           }
+          // bounds the registers that operands read ahead take
+          __builtin_amdgcn_sched_barrier(0);
+        };
+        bf16x8 w[NT];
+        if constexpr (decltype(chained)::value) {
+#define TRELLIS_CHAIN(U)                                                                                  \
+  _Pragma("unroll") for (int i = 0; i < NT; ++i) w[i] = group_chain<BITS, U>(W.d[i], sc[i], Eight{});     \
+  multiply(U, w);
+          TRELLIS_CHAIN(0) TRELLIS_CHAIN(1) TRELLIS_CHAIN(2) TRELLIS_CHAIN(3)
+#undef TRELLIS_CHAIN
+          load(s + 2 < s1 ? s + 2 : s1 - 1, W);
+        } else {
+          // Two phases: the codes of one table group are gathered while one
+          // group goes through the ALU.
+          const uint32_t mask = 0x1FFEu;
+          uint32_t r[NT][8];
+#define TRELLIS_PHASE(TABLE, ALU, AFTER)                                                                      \
+  _Pragma("unroll") for (int i = 0; i < NT; ++i) gather_codes<BITS, TABLE>(W.d[i], table, mask, r[i]);        \
+  _Pragma("unroll") for (int i = 0; i < NT; ++i) w[i] = group_hashed<BITS, ALU>(W.d[i], q[i], kq[i], Eight{}); \
+  AFTER;                                                                                                      \
+  multiply(ALU, w);                                                                                           \
+  _Pragma("unroll") for (int i = 0; i < NT; ++i) w[i] = gathered_weights(r[i], q[i]);                         \
+  multiply(TABLE, w);
+          TRELLIS_PHASE(0, 2, (void)0)
+          TRELLIS_PHASE(1, 3, load(s + 2 < s1 ? s + 2 : s1 - 1, W))
+#undef TRELLIS_PHASE
         }
-        if (s + 1 < s1) put(s + 1);
-        __syncthreads();
-      }
-      if (KIND == kForward && s1 == P.steps && wk == 0 && P.low.rank > 0) {
-        add_low_rank<MT, NT>(P.low, P.m, m0, lane, acc, [&](int a, int r0, bf16x8 (&w)[NT]) {
-#pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            const int n = group * BN + 32 * wn + 16 * i + j;
-            const uint16_t *q = P.low.factor + ((int64_t)a * P.n + n) * P.low.rank + r0;
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              w[i][e] = __builtin_bit_cast(__bf16, n < P.n && r0 + e < P.low.rank ? q[e] : (uint16_t)0);
-          }
-        });
-      }
+        put(s + 1);
+        lds_barrier();
+      };
+      auto steps = [&](auto chained) {
+        for (int s = s0;;) {
+          step(s, A, chained);
+          if (++s == s1) break;
+          step(s, B, chained);
+          if (++s == s1) break;
+        }
+      };
+      if (chain) steps(std::true_type{});
+      else steps(std::false_type{});
     } else {
       // Lane (j, g) decodes columns 64 wn + 4 j .. +3 of the block for rows
-      // 8 g .. 8 g + 7 of each 32-row MFMA step: the lowest of the four
+      // 8 g .. 8 g + 7 of each 32-row MFMA part: the lowest of the four
       // windows starts at stream bit (252 - 64 wn - 4 j) * BITS, the others
       // BITS apart, 3 BITS + 12 <= 24 bits in all.
       const int pos = (252 - 64 * wn - 4 * j) * BITS;
       const uint32_t w0 = (uint32_t)(pos >> 5), sh = (uint32_t)(pos & 31);
-      const uint32_t o_lo = 4 * w0, o_hi = 4 * ((w0 + 1) % wpb);
-      for (int s = s0; s < s1; ++s) {
-        if (s + 1 < s1) fetch(s + 1);
+      const uint32_t row0 = (uint32_t)(128 * wk + 8 * g) * row_bytes;
+      const uint32_t o_lo = row0 + 4 * w0, o_hi = row0 + 4 * ((w0 + 1) % wpb);
+      struct Words {
+        uint32_t lo[8], hi[8];
+      };
+      const int parts = 4 * (s1 - s0);
+      auto load = [&](int part, Words &W) {
+        if (part >= parts) part = parts - 1;
+        const int s = s0 + (part >> 2);
         const bool second = s >= P.steps1;
         const int n0 = (second ? s - P.steps1 : s) * kStep;
         const int rows = P.n - n0 < kStep ? P.n - n0 : kStep;
         const unsigned char *base = reinterpret_cast<const unsigned char *>(second ? P.codes2 : P.codes) +
                                     (int64_t)n0 * row_bytes + (int64_t)group * wpb * 4;
+        // rows past N lie outside the buffer and read as zero
         const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
             const_cast<unsigned char *>(base), (short)0, (int)((uint32_t)rows * row_bytes - (uint32_t)group * wpb * 4), kRawBuffer);
-        const unsigned char *xb = xs + (s & 1) * BM * kStride + j * kStride + (128 * wk + 8 * g) * 2;
-        const float *sr = srow + (s & 1) * 256 + 128 * wk + 8 * g;
+        const uint32_t ro = (uint32_t)(32 * (part & 3)) * row_bytes;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          bf16x8 w[NT];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const uint32_t ro = (uint32_t)(128 * wk + 32 * q + 8 * g + e) * row_bytes;
-            const uint32_t lo = __builtin_amdgcn_raw_buffer_load_b32(rs, ro + o_lo, 0, 0);
-            const uint32_t hi = __builtin_amdgcn_raw_buffer_load_b32(rs, ro + o_hi, 0, 0);
-            const uint32_t f = __builtin_amdgcn_alignbit(hi, lo, sh);
-            const float sc = sr[32 * q + e];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const uint32_t win = (f >> ((3 - c) * BITS)) & 0xFFFu;
-              w[c][e] = (__bf16)(*reinterpret_cast<const float *>(table + 4 * win) * sc);
-            }
-          }
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            const bf16x8 x = *reinterpret_cast<const bf16x8 *>(xb + mt * 16 * kStride + 64 * q);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) acc[mt][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w[c], acc[mt][c], 0, 0, 0);
-          }
+        for (int e = 0; e < 8; ++e) {
+          W.lo[e] = __builtin_amdgcn_raw_buffer_load_b32(rs, o_lo + ro + (uint32_t)e * row_bytes, 0, 0);
+          W.hi[e] = __builtin_amdgcn_raw_buffer_load_b32(rs, o_hi + ro + (uint32_t)e * row_bytes, 0, 0);
         }
-        if (s + 1 < s1) put(s + 1);
-        __syncthreads();
-      }
-      if (s1 == P.steps && wk == 0 && P.low.rank > 0) {
-        add_low_rank<MT, NT>(P.low, P.m, m0, lane, acc, [&](int a, int r0, bf16x8 (&w)[NT]) {
-          const int k0 = group * BN + 64 * wn + 4 * j;
-          typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+      };
+      Words W;
+      load(0, W);
+      put(s0);
+      lds_barrier();
+      auto compute = [&](int part, bool chain) {
+        const int s = s0 + (part >> 2), p = part & 3;
+        const int at = (s & 1) * 256 + 128 * wk + 32 * p + 8 * g;
+        uint32_t fields[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            bf16x4 v = {};
-            if (r0 + e < P.low.rank)
-              v = *reinterpret_cast<const bf16x4 *>(P.low.factor + ((int64_t)a * P.low.rank + r0 + e) * P.k + k0);
+        for (int e = 0; e < 8; ++e) fields[e] = __builtin_amdgcn_alignbit(W.hi[e], W.lo[e], sh);
+        load(part + 1, W);
+        bf16x8 w[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) w[c][e] = v[c];
+        for (int h = 0; h < 8; h += 4) {  // four rows at a time
+          const uint32_t(&f)[4] = *reinterpret_cast<uint32_t(*)[4]>(fields + h);
+          if (chain) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float sc = rows_s[at + h + e];
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                w[c][h + e] = (__bf16)(trellis_value(code_of(__builtin_amdgcn_ubfe(f[e], (3 - c) * BITS, 12))) * sc);
+            }
+          } else {
+            uint32_t r[2][4];
+            f32x2 qk[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              r[0][e] = table_code(table, (f[e] >> (3 * BITS - 1)) & 0x1FFEu);
+              r[1][e] = table_code(table, (f[e] >> (2 * BITS - 1)) & 0x1FFEu);
+              qk[e] = rowq[at + h + e];
+            }
+#pragma unroll
+            for (int c = 2; c < 4; ++c)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[c][h + e] = (__bf16)__builtin_fmaf(code_plus_magic(__builtin_amdgcn_ubfe(f[e], (3 - c) * BITS, 12)), qk[e][0], qk[e][1]);
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) w[c][h + e] = (__bf16)mix_lo(r[c][e], qk[e][0]);
           }
-        });
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        const unsigned char *xb = xs + (s & 1) * BM * kStride + j * kStride + (128 * wk + 32 * p + 8 * g) * 2;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          const bf16x8 x = *reinterpret_cast<const bf16x8 *>(xb + mt * 16 * kStride);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) acc[mt][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w[c], acc[mt][c], 0, 0, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      };
+      for (int s = s0; s < s1; ++s) {
+        const int part = 4 * (s - s0);
+        fetch(s + 1 < s1 ? s + 1 : s);
+        const uint32_t *fl = rowf + (s & 1) * 4;
+        const bool chain = __builtin_amdgcn_readfirstlane(fl[0] | fl[1] | fl[2] | fl[3]) != 0;
+        for (int p = 0; p < 4; ++p) compute(part + p, chain);
+        put(s + 1);
+        lds_barrier();
       }
     }
 
     // The two wk halves meet in LDS, [wk][row][128 columns]; then each thread
     // takes four columns of a row at a time.
+    // (The thread's number goes through an empty asm here, so that nothing of
+    // this part is computed ahead and kept in registers through the steps.)
+    int et = tid;
+    asm volatile("" : "+v"(et));
+    const int ej = et & 15, eg = (et >> 4) & 3;
     const bool whole = s0 == 0 && s1 == P.steps;
     float *const red = reinterpret_cast<float *>(xs);
     // columns of P.out handled per round, and the store of four sums
@@ -392,7 +548,7 @@ __global__ __launch_bounds__(kThreads) void product_kernel(Product P) {
         store4(P.out + (int64_t)mrow * width + n, v);
       }
     };
-    constexpr int kPart = BM * kHalf * kRounds;  // floats of a tile's partial
+    constexpr int kPart = BM * RC * kRounds;  // floats of a tile's partial
     const int64_t slot = 2 * (int64_t)blockIdx.x + (s0 == 0 ? 1 : 0);
     for (int round = 0; round < kRounds; ++round) {
       if (round) __syncthreads();
@@ -401,20 +557,66 @@ __global__ __launch_bounds__(kThreads) void product_kernel(Product P) {
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            float *r = red + (wk * BM + mt * 16 + 4 * g + e) * kRedStride;
+            float *r = red + (wk * BM + mt * 16 + 4 * eg + e) * kRedStride;
             if constexpr (kT) {
-              *reinterpret_cast<f32x4 *>(r + 64 * (wn & 1) + 4 * j) =
+              *reinterpret_cast<f32x4 *>(r + 64 * (wn & 1) + 4 * ej) =
                   f32x4{acc[mt][0][e], acc[mt][1][e], acc[mt][2][e], acc[mt][3][e]};
             } else {
 #pragma unroll
               for (int i = 0; i < NT; ++i)
-                r[KIND == kGated ? 64 * i + 16 * wn + j : 32 * wn + 16 * i + j] = acc[mt][i][e];
+                r[KIND == kGated ? 64 * i + 16 * wn + ej : 16 * NT * wn + 16 * i + ej] = acc[mt][i][e];
             }
           }
+        // The adapters' term joins the sums of the wave that holds the tile's
+        // last step, half of the row tiles in each wk.
+        if (KIND != kGated && s1 == P.steps && P.low.rank > 0) {
+          for (int mt = wk; mt < MT && m0 + 16 * mt < P.m; mt += 2) {
+            f32x4 term[NT];
+            low_rank_tile<NT>(P.low, P.m, m0 + 16 * mt, et & 63, term, [&](int a, int r0, bf16x8 (&w)[NT]) {
+              if constexpr (kT) {
+                const int k0 = group * BN + 64 * wn + 4 * ej;
+                typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  bf16x4 v = {};
+                  if (r0 + e < P.low.rank)
+                    v = *reinterpret_cast<const bf16x4 *>(P.low.factor + ((int64_t)a * P.low.rank + r0 + e) * P.k + k0);
+#pragma unroll
+                  for (int c = 0; c < 4; ++c) w[c][e] = v[c];
+                }
+              } else {
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                  const int n = group * BN + 16 * NT * wn + 16 * i + ej;
+                  const uint16_t *q = P.low.factor + ((int64_t)a * P.n + n) * P.low.rank + r0;
+                  if ((P.low.rank & 7) == 0) {
+                    w[i] = bf16x8{};
+                    if (n < P.n && r0 < P.low.rank) w[i] = *reinterpret_cast<const bf16x8 *>(q);
+                  } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                      w[i][e] = __builtin_bit_cast(__bf16, n < P.n && r0 + e < P.low.rank ? q[e] : (uint16_t)0);
+                  }
+                }
+              }
+            });
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float *r = red + (wk * BM + mt * 16 + 4 * eg + e) * kRedStride;
+              if constexpr (kT) {
+                f32x4 *v = reinterpret_cast<f32x4 *>(r + 64 * (wn & 1) + 4 * ej);
+                *v += f32x4{term[0][e], term[1][e], term[2][e], term[3][e]};
+              } else {
+#pragma unroll
+                for (int i = 0; i < NT; ++i) r[16 * NT * wn + 16 * i + ej] += term[i][e];
+              }
+            }
+          }
+        }
       }
       __syncthreads();
       if (whole && KIND == kGated) {
-        for (int q = tid; q < BM * 16; q += kThreads) {
+        for (int q = et; q < BM * 16; q += kThreads) {
           const int row = q >> 4, c = (q & 15) * 4;
           const f32x4 *r0 = reinterpret_cast<const f32x4 *>(red + row * kRedStride + c);
           const f32x4 *r1 = reinterpret_cast<const f32x4 *>(red + (BM + row) * kRedStride + c);
@@ -423,14 +625,14 @@ __global__ __launch_bounds__(kThreads) void product_kernel(Product P) {
       } else {
         const __amdgpu_buffer_rsrc_t ws =
             __builtin_amdgcn_make_buffer_rsrc(P.partials + slot * kPart, (short)0, kPart * 4, kRawBuffer);
-        for (int q = tid; q < BM * 32; q += kThreads) {
-          const int row = q >> 5, c = (q & 31) * 4;
+        for (int q = et; q < BM * (RC / 4); q += kThreads) {
+          const int row = q / (RC / 4), c = (q % (RC / 4)) * 4;
           const f32x4 v = *reinterpret_cast<const f32x4 *>(red + row * kRedStride + c) +
                           *reinterpret_cast<const f32x4 *>(red + (BM + row) * kRedStride + c);
-          if (whole) finish(row, round * kHalf + c, v, v);
+          if (whole) finish(row, round * RC + c, v, v);
           else
-            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(__attribute__((ext_vector_type(4))) uint32_t, v), ws,
-                                                   (uint32_t)((round * BM + row) * kHalf + c) * 4, 0, kSc1);
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), ws,
+                                                   (uint32_t)((round * BM + row) * RC + c) * 4, 0, kSc1);
         }
       }
     }
@@ -446,11 +648,11 @@ __global__ __launch_bounds__(kThreads) void product_kernel(Product P) {
         return c;
       };
       const int64_t c0 = owner(tile * P.steps), c1 = owner(tile * P.steps + P.steps - 1);
-      if (tid == 0) *arrived = __hip_atomic_fetch_add(&P.counters[tile], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      if (et == 0) *arrived = __hip_atomic_fetch_add(&P.counters[tile], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       __syncthreads();
       const bool last = *arrived == (uint32_t)(c1 - c0);
       if (last) {
-        if (tid == 0) __hip_atomic_store(&P.counters[tile], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (et == 0) __hip_atomic_store(&P.counters[tile], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         auto sum = [&](int at) {
           f32x4 v = {0.f, 0.f, 0.f, 0.f};
           for (int64_t c = c0; c <= c1; ++c) {
@@ -462,14 +664,14 @@ __global__ __launch_bounds__(kThreads) void product_kernel(Product P) {
           return v;
         };
         if constexpr (KIND == kGated) {
-          for (int q = tid; q < BM * 16; q += kThreads) {
+          for (int q = et; q < BM * 16; q += kThreads) {
             const int row = q >> 4, c = (q & 15) * 4;
-            finish(row, c, sum(row * kHalf + c), sum(row * kHalf + 64 + c));
+            finish(row, c, sum(row * RC + c), sum(row * RC + 64 + c));
           }
         } else {
-          for (int q = tid; q < kRounds * BM * 32; q += kThreads) {
-            const int round = q / (BM * 32), row = (q >> 5) % BM, c = (q & 31) * 4;
-            finish(row, round * kHalf + c, sum((round * BM + row) * kHalf + c), f32x4{});
+          for (int q = et; q < kRounds * BM * (RC / 4); q += kThreads) {
+            const int round = q / (BM * (RC / 4)), row = q / (RC / 4) % BM, c = (q % (RC / 4)) * 4;
+            finish(row, round * RC + c, sum((round * BM + row) * RC + c), f32x4{});
           }
         }
       }
@@ -556,7 +758,7 @@ __global__ __launch_bounds__(256) void shrink_kernel(Shrink S) {
   if (S.spans > 1) {
     float *const base = S.partials + cell * S.spans * 256;
     const __amdgpu_buffer_rsrc_t ws = __builtin_amdgcn_make_buffer_rsrc(base, (short)0, S.spans * 1024, kRawBuffer);
-    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(__attribute__((ext_vector_type(4))) uint32_t, acc), ws,
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc), ws,
                                            (uint32_t)(span * 1024 + lane * 16), 0, kSc1);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     uint32_t old = 0;
@@ -759,14 +961,22 @@ trellis_status space(int dev, hipStream_t stream, size_t size, size_t ncounters,
 typedef void (*ProductFn)(Product);
 constexpr int kRowTiles[] = {1, 2, 4, 6, 8};
 constexpr int kMts = 5;
+// Tiles per wave and waves per SIMD for each number of row tiles. Forward up
+// to two row tiles: one tile per wave, whose finer units split more evenly.
+constexpr int wave_tiles(int kind, int mt) { return kind == kTransposed ? 4 : kind == kGated || mt > 2 ? 2 : 1; }
+constexpr int waves_per_simd(int kind, int mt) { return kind != kTransposed && mt <= (kind == kGated ? 4 : 2) ? 4 : 2; }
+template <int BITS, int KIND, int MT>
+constexpr ProductFn product_one() {
+  return &product_kernel<BITS, KIND, MT, wave_tiles(KIND, MT), waves_per_simd(KIND, MT)>;
+}
 template <int BITS, int KIND>
 ProductFn product_of(int i) {
   switch (i) {
-    case 0: return &product_kernel<BITS, KIND, 1>;
-    case 1: return &product_kernel<BITS, KIND, 2>;
-    case 2: return &product_kernel<BITS, KIND, 4>;
-    case 3: return &product_kernel<BITS, KIND, 6>;
-    default: return &product_kernel<BITS, KIND, 8>;
+    case 0: return product_one<BITS, KIND, 1>();
+    case 1: return product_one<BITS, KIND, 2>();
+    case 2: return product_one<BITS, KIND, 4>();
+    case 3: return product_one<BITS, KIND, KIND == kTransposed ? 4 : 6>();
+    default: return product_one<BITS, KIND, KIND == kTransposed ? 4 : 8>();
   }
 }
 template <int KIND>
@@ -789,20 +999,24 @@ Shape shape_of(int kind, trellis_geom g, int32_t m, int matrices, int cus) {
   Shape s{};
   s.kind = kind;
   s.bits = g.bits;
-  const int64_t chunks = ((int64_t)m + 127) / 128;
+  // at most 128 rows a tile, transposed 64 (its waves hold four column tiles)
+  const int most_rows = kind == kTransposed ? 64 : 128;
+  const int64_t chunks = ((int64_t)m + most_rows - 1) / most_rows;
   const int need = (int)((((int64_t)m + chunks - 1) / chunks + 15) / 16);
   while (kRowTiles[s.mt] < need) ++s.mt;
   const int bm = 16 * kRowTiles[s.mt];
   const int64_t rows = ((int64_t)m + bm - 1) / bm;
-  const int bn = kind == kTransposed ? 256 : kind == kGated ? 64 : 128;
+  const int mt = kRowTiles[s.mt];
+  const int bn = kind == kTransposed ? 256 : kind == kGated ? 64 : 64 * wave_tiles(kind, mt);
   s.groups = ((kind == kTransposed ? g.k : g.n) + bn - 1) / bn;
   s.steps1 = ((kind == kTransposed ? g.n : g.k) + kStep - 1) / kStep;
   s.steps = kind == kTransposed ? s.steps1 * matrices : s.steps1;
   s.tiles = rows * s.groups;
   s.units = s.tiles * s.steps;
-  s.grid = (int)(s.units < cus ? s.units : cus);
-  s.partial_bytes = (size_t)2 * s.grid * bm * (kind == kTransposed ? 256 : 128) * 4;
-  s.lds = kTableBytes + (size_t)2 * bm * kStride + 512 * 4 + 16;
+  const int64_t room = (int64_t)cus * waves_per_simd(kind, mt) / 2;  // workgroups the card holds at once
+  s.grid = (int)(s.units < room ? s.units : room);
+  s.partial_bytes = (size_t)2 * s.grid * bm * (kind == kGated ? 128 : bn) * 4;
+  s.lds = kTableBytes + (size_t)2 * bm * kStride + (kind == kTransposed ? 512 * 12 + 8 * 4 : 0) + 16;
   return s;
 }
 
