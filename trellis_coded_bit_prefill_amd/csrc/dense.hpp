@@ -74,9 +74,10 @@ __global__ __launch_bounds__(256) void unpack_rows_kernel(Unpack U) {
 
 // Transposed: one wave per kstep (32 rows of W) and 64 columns; lane (j, g)
 // decodes columns 4 j .. +3 of rows 8 g .. +7 and so holds, for each of the
-// four columns, one lane's whole operand: 64 bytes in a row.
+// four columns, one lane's whole operand.
 template <int BITS>
 __global__ __launch_bounds__(256) void unpack_columns_kernel(Unpack U) {
+  __shared__ bf16x8 turn[4][4 * 64];
   constexpr int wpb = 8 * BITS;
   const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
   const int per = U.ksteps / U.matrices;  // ksteps of one matrix
@@ -108,10 +109,14 @@ __global__ __launch_bounds__(256) void unpack_columns_kernel(Unpack U) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) v[c][e] = (__bf16)window_weight((f[e] >> ((3 - c) * BITS)) & 0xFFFu, s[e], q, kq, exact);
   }
-  bf16x8 *out = reinterpret_cast<bf16x8 *>(U.w) +
-                ((int64_t)(4 * grp + (j >> 2)) * U.ksteps + (int64_t)which * per + ks) * 64 + g * 16 + 4 * (j & 3);
+  // Through the wave's own LDS, so that each store writes 1 KB in a row: lane
+  // (j, g) holds slots 16 g + 4 (j mod 4) .. +3 of tile j / 4.
+  bf16x8 *const mine = turn[threadIdx.x >> 6];
 #pragma unroll
-  for (int c = 0; c < 4; ++c) out[c] = v[c];
+  for (int c = 0; c < 4; ++c) mine[(j >> 2) * 64 + g * 16 + 4 * (j & 3) + c] = v[c];
+  bf16x8 *out = reinterpret_cast<bf16x8 *>(U.w) + ((int64_t)(4 * grp) * U.ksteps + (int64_t)which * per + ks) * 64 + lane;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) out[(int64_t)i * U.ksteps * 64] = mine[i * 64 + lane];
 }
 
 // Rows padded with zeros to whole contraction steps, four elements a thread.

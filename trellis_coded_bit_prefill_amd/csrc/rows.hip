@@ -42,6 +42,7 @@ static_assert(2 * 16 * kRedStride * 4 == 2 * 16 * kStride, "the reduction tile r
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef int32_t i32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ uint16_t bf16_of(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
@@ -685,10 +686,11 @@ __global__ __launch_bounds__(kThreads, OCC) void product_kernel(Product P) {
 // past the rank and in rows without an adapter.
 //   forward     P = x,    F(i, r, c) = A[i][r][c]   (c < K)
 //   transposed  P = dout, F(i, r, c) = B[i][c][r]   (c < N)
-// One workgroup (4 waves): 16 rows, 16 rank columns, one span of c; every
-// adapter that the 16 rows name is multiplied in turn and kept in its own
-// rows. The spans' sums meet in `partials`, added in order by the last to
-// arrive.
+// One workgroup: 16 MS rows, 32 rank columns, one span of c. Its waves share
+// out the adapters that the rows name and, where there are fewer adapters than
+// waves, the columns; an adapter's product is kept in its own rows only. The
+// waves' sums meet in LDS, the spans' in `partials`, added in order by the
+// workgroup that arrives last.
 // ---------------------------------------------------------------------------
 struct Shrink {
   const uint16_t *p;
@@ -701,85 +703,181 @@ struct Shrink {
   int32_t m, cols, count, rank, rank_p;
   int32_t span, spans;
 };
+constexpr int kMaxSpans = 16;      // one batch of loads
+constexpr int kFactorStride = 40;  // elements per staged row of B: 32 and padding
 
-template <bool T>
-__global__ __launch_bounds__(256) void shrink_kernel(Shrink S) {
-  __shared__ f32x4 part[4][64];
+template <bool T, int MS, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void shrink_kernel(Shrink S) {
+  constexpr int kPart = MS * 2 * 64;  // vectors of four sums: [row tile][rank tile][lane]
+  __shared__ f32x4 part[WAVES][kPart];
+  __shared__ __attribute__((aligned(16))) uint16_t staged[T ? WAVES : 1][T ? 32 * kFactorStride : 1];
+  __shared__ uint32_t arrived;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int j = lane & 15, g = lane >> 4;
-  const int span = blockIdx.y, rt = blockIdx.z;
-  const int64_t m0 = (int64_t)blockIdx.x * 16;
-  const int64_t row = m0 + j, rowc = row < S.m ? row : S.m - 1;
-  int idx = row < S.m ? S.index[row] : -1;
+  const int span = blockIdx.y, z = blockIdx.z;
+  const int64_t m0 = (int64_t)blockIdx.x * (16 * MS);
+  // lane l: the adapter of row m0 + l
+  int idx = lane < 16 * MS && m0 + lane < S.m ? S.index[m0 + lane] : -1;
   if (idx >= S.count) idx = -1;
-  int of[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) of[e] = __shfl(idx, 4 * g + e);
+  const uint64_t named = __ballot(idx >= 0);
+  int distinct = 0;
+  for (uint64_t left = named; left; ++distinct) left &= ~__ballot(idx == __builtin_amdgcn_readlane(idx, __builtin_ctzll(left)));
   const int c_end = S.cols - span * S.span < S.span ? S.cols : (span + 1) * S.span;
-  const int r = rt * 16 + j;
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  uint64_t left = __ballot(idx >= 0) & 0xFFFFull;
-  while (left) {
+  f32x4 acc[MS][2];
+#pragma unroll
+  for (int i = 0; i < MS; ++i) acc[i][0] = acc[i][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+  // Fewer adapters than waves: wave w takes adapter w mod distinct and one of
+  // the parts of its columns; else adapters w, w + WAVES, ...
+  const int share = distinct < WAVES ? distinct : WAVES;
+  const int mine = share > 0 ? wave % share : 0, part_i = share > 0 ? wave / share : 0;
+  const int parts = share > 0 ? (WAVES - mine + share - 1) / share : 1;
+  int at = 0;
+  for (uint64_t left = named; left; ++at) {
     const int a = __builtin_amdgcn_readlane(idx, __builtin_ctzll(left));
-    left &= ~__ballot(idx == a);
-    f32x4 d = {0.f, 0.f, 0.f, 0.f};
-    for (int c0 = span * S.span + wave * 32; c0 < c_end; c0 += 128) {
-      const int c = c0 + 8 * g;
-      bf16x8 x = {}, w = {};
-      const uint16_t *xp = S.p + rowc * S.cols + c;
-      typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+    const uint64_t rows = __ballot(idx == a);
+    left &= ~rows;
+    if (at % share != mine) continue;
+    f32x4 d[MS][2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        if (c + 4 * h < S.cols) {
-          const bf16x4 v = *reinterpret_cast<const bf16x4 *>(xp + 4 * h);
+    for (int i = 0; i < MS; ++i) d[i][0] = d[i][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // U steps of 32 columns are loaded before the first is multiplied.
+    constexpr int U = MS == 1 ? 4 : 2;
+    const bool vectors = T && (S.rank & 7) == 0;
+    for (int c0 = span * S.span + 32 * part_i; c0 < c_end; c0 += 32 * parts * U) {
+      bf16x8 w[U][2];
+      u32x4 b[U][2], x[U][MS];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[4 * h + e] = v[e];
+      for (int u = 0; u < U; ++u) {
+        const int cu = c0 + 32 * parts * u, c = cu + 8 * g;
+        const bool in = cu < c_end;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          w[u][h] = bf16x8{};
+          b[u][h] = u32x4{0u, 0u, 0u, 0u};
         }
-      if (r < S.rank) {
         if constexpr (!T) {
-          w = *reinterpret_cast<const bf16x8 *>(S.factor + ((int64_t)a * S.rank + r) * S.cols + c);
-        } else {
-          const uint16_t *q = S.factor + ((int64_t)a * S.cols + c) * S.rank + r;
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (c + e < S.cols) w[e] = __builtin_bit_cast(__bf16, q[(int64_t)e * S.rank]);
+          for (int h = 0; h < 2; ++h) {
+            const int r = 32 * z + 16 * h + j;
+            if (in && r < S.rank) w[u][h] = *reinterpret_cast<const bf16x8 *>(S.factor + ((int64_t)a * S.rank + r) * S.cols + c);
+          }
+        } else if (vectors) {
+          // 32 rows of B by 32 rank columns: lane l takes the 16 bytes at
+          // column 8 (l mod 4) of rows l / 4 and 16 + l / 4
+          const int r = 32 * z + 8 * (lane & 3);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int n = cu + 16 * h + (lane >> 2);
+            if (in && n < S.cols && r < S.rank)
+              b[u][h] = *reinterpret_cast<const u32x4 *>(S.factor + ((int64_t)a * S.cols + n) * S.rank + r);
+          }
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int r = 32 * z + 16 * h + j;
+            const uint16_t *q = S.factor + ((int64_t)a * S.cols + c) * S.rank + r;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (in && r < S.rank && c + e < S.cols) w[u][h][e] = __builtin_bit_cast(__bf16, q[(int64_t)e * S.rank]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < MS; ++i) {
+          const int64_t row = m0 + 16 * i + j, rowc = row < S.m ? row : S.m - 1;
+          const uint16_t *xp = S.p + rowc * S.cols + c;
+          x[u][i] = u32x4{0u, 0u, 0u, 0u};
+          if constexpr (!T) {
+            if (in) x[u][i] = *reinterpret_cast<const u32x4 *>(xp);
+          } else {  // rows start at multiples of 8 bytes, columns past N are zero
+            u32x2 v[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              v[h] = u32x2{0u, 0u};
+              if (in && c + 4 * h < S.cols) v[h] = *reinterpret_cast<const u32x2 *>(xp + 4 * h);
+            }
+            x[u][i] = u32x4{v[0][0], v[0][1], v[1][0], v[1][1]};
+          }
         }
       }
-      d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w, d, 0, 0, 0);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (vectors) {  // turned in the wave's own LDS
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            *reinterpret_cast<u32x4 *>(&staged[wave][(16 * h + (lane >> 2)) * kFactorStride + 8 * (lane & 3)]) = b[u][h];
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              w[u][h][e] = __builtin_bit_cast(__bf16, staged[wave][(8 * g + e) * kFactorStride + 16 * h + j]);
+        }
+#pragma unroll
+        for (int i = 0; i < MS; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            d[i][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[u][i]), w[u][h], d[i][h], 0, 0, 0);
+      }
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[e] += of[e] == a ? d[e] : 0.f;
-  }
-  part[wave][lane] = acc;
-  __syncthreads();
-  if (wave != 0) return;
-  acc = ((part[0][lane] + part[1][lane]) + part[2][lane]) + part[3][lane];
-  const int64_t cell = (int64_t)blockIdx.x * gridDim.z + rt;
-  if (S.spans > 1) {
-    float *const base = S.partials + cell * S.spans * 256;
-    const __amdgpu_buffer_rsrc_t ws = __builtin_amdgcn_make_buffer_rsrc(base, (short)0, S.spans * 1024, kRawBuffer);
-    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc), ws,
-                                           (uint32_t)(span * 1024 + lane * 16), 0, kSc1);
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    uint32_t old = 0;
-    if (lane == 0) old = __hip_atomic_fetch_add(&S.counters[cell], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    old = __builtin_amdgcn_readfirstlane(old);
-    asm volatile("" ::: "memory");
-    if ((int)old != S.spans - 1) return;
-    if (lane == 0) __hip_atomic_store(&S.counters[cell], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    acc = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < S.spans; ++s)
-      acc += __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(ws, (uint32_t)(s * 1024 + lane * 16), 0, kSc1));
+    for (int i = 0; i < MS; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if ((rows >> (16 * i + 4 * g + e)) & 1) {
+          acc[i][0][e] += d[i][0][e];
+          acc[i][1][e] += d[i][1][e];
+        }
   }
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int64_t mrow = m0 + 4 * g + e;
-    if (mrow < S.m) S.t[mrow * S.rank_p + r] = of[e] >= 0 && r < S.rank ? acc[e] * S.gain[of[e]] : 0.f;
+  for (int i = 0; i < MS; ++i) {
+    part[wave][(2 * i) * 64 + lane] = acc[i][0];
+    part[wave][(2 * i + 1) * 64 + lane] = acc[i][1];
+  }
+  __syncthreads();
+  const int64_t cell = (int64_t)blockIdx.x * gridDim.z + z;
+  float *const base = S.partials + cell * S.spans * (kPart * 4);
+  const __amdgpu_buffer_rsrc_t ws = __builtin_amdgcn_make_buffer_rsrc(base, (short)0, S.spans * kPart * 16, kRawBuffer);
+  auto sum_waves = [&](int v) {
+    f32x4 s = part[0][v];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) s += part[w][v];
+    return s;
+  };
+  if (S.spans > 1) {
+    for (int v = tid; v < kPart; v += 64 * WAVES)
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, sum_waves(v)), ws, (uint32_t)((span * kPart + v) * 16), 0, kSc1);
+    // The partial is complete at the coherent level before the counter moves.
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (tid == 0) arrived = __hip_atomic_fetch_add(&S.counters[cell], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    if (arrived != (uint32_t)S.spans - 1) return;
+    if (tid == 0) __hip_atomic_store(&S.counters[cell], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  for (int v = tid; v < kPart; v += 64 * WAVES) {
+    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+    if (S.spans > 1) {
+      f32x4 p[kMaxSpans];
+#pragma unroll
+      for (int s = 0; s < kMaxSpans; ++s)  // past the last span: outside the buffer, zero
+        p[s] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(ws, (uint32_t)((s * kPart + v) * 16), 0, kSc1));
+#pragma unroll
+      for (int s = 0; s < kMaxSpans; ++s) sum += p[s];
+    } else {
+      sum = sum_waves(v);
+    }
+    const int l = v & 63, r = 32 * z + 16 * ((v >> 6) & 1) + (l & 15);
+    const int64_t row0 = m0 + 16 * (v >> 7) + 4 * (l >> 4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (row0 + e < S.m) {
+        const int i = S.index[row0 + e];
+        S.t[(row0 + e) * S.rank_p + r] = i >= 0 && i < S.count ? sum[e] * S.gain[i] : 0.f;
+      }
   }
 }
 
 // The 32-row chunks that an adapter's rows lie in: range[a] = [first, last + 1).
-__global__ __launch_bounds__(256) void range_kernel(const int32_t *__restrict__ index, int m, int2 *__restrict__ range) {
+__global__ __launch_bounds__(256) void range_kernel(const int32_t *__restrict__ index, int m, i32x2 *__restrict__ range) {
   __shared__ int lo[4], hi[4];
   const int a = blockIdx.x, tid = threadIdx.x;
   int first = 0x7fffffff, last = -1;
@@ -800,68 +898,145 @@ __global__ __launch_bounds__(256) void range_kernel(const int32_t *__restrict__ 
   if (tid == 0) {
     first = min(min(lo[0], lo[1]), min(lo[2], lo[3]));
     last = max(max(hi[0], hi[1]), max(hi[2], hi[3]));
-    range[a] = last < 0 ? int2{0, 0} : int2{first >> 5, (last >> 5) + 1};
+    range[a] = last < 0 ? i32x2{0, 0} : i32x2{first >> 5, (last >> 5) + 1};
   }
 }
 
 // Gradients of the factors: sum over an adapter's rows of P[m, c] V[m, r].
 //   dA[a][r][c]: P = x,    V = u    (c < K)
 //   dB[a][c][r]: P = dout, V = t    (c < N)
-// One wave: 16 columns c and 16 rank columns of one adapter, over the 32-row
-// chunks of its range; rows of other adapters enter as zeros on both sides
-// (a NaN in them must not count). V as the sum of two bf16 numbers.
+// One workgroup (4 waves): 64 columns c and 32 rank columns of one adapter;
+// wave w takes the 32-row chunks w, w + 4, ... of the adapter's range and the
+// waves' sums meet in LDS in order. A chunk of P goes through the wave's own
+// LDS, which turns it (contraction is over rows); rows of other adapters enter
+// as zeros on both sides (a NaN in them must not count). V as the sum of two
+// bf16 numbers (2^-16 relative). The next chunk is loaded ahead.
 struct Outer {
   const uint16_t *x, *dout;
   const float *u, *t;
   const int32_t *index;
-  const int2 *range;
+  const i32x2 *range;
   uint16_t *da, *db;
   int32_t m, n, k, rank, rank_p;
-  int32_t tiles_a, tiles;  // 16-column tiles of x, and of x and dout together
+  int32_t tiles_a;  // 64-column tiles of x; those of dout follow
 };
+constexpr int kTurnStride = 72;  // elements per staged row: 64 and padding
 
 __global__ __launch_bounds__(256) void outer_kernel(Outer O) {
+  __shared__ __attribute__((aligned(16))) uint16_t turn[4][32 * kTurnStride];
+  __shared__ f32x4 part[4][8 * 64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int j = lane & 15, g = lane >> 4;
-  int tile = blockIdx.x * 4 + wave;
-  if (tile >= O.tiles) return;
-  const int a = blockIdx.y, r = blockIdx.z * 16 + j;
-  const bool is_a = tile < O.tiles_a;
-  if (!is_a) tile -= O.tiles_a;
-  const uint16_t *P = is_a ? O.x : O.dout;
-  const float *V = is_a ? O.u : O.t;
+  const int a = blockIdx.y, r0 = blockIdx.z * 32;
+  const bool is_a = (int)blockIdx.x < O.tiles_a;
+  const int tile = is_a ? blockIdx.x : blockIdx.x - O.tiles_a;
+  const uint16_t *const P = is_a ? O.x : O.dout;
+  const float *const V = is_a ? O.u : O.t;
   const int cols = is_a ? O.k : O.n;
-  const int c = tile * 16 + j;
-  const int2 range = O.range[a];
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  for (int ch = range.x; ch < range.y; ++ch) {
-    bf16x8 p, hi, lo;
+  const int c0 = tile * 64;
+  const i32x2 range = O.range[a];
+  f32x4 acc[4][2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i][0] = acc[i][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+  struct Chunk {
+    u32x2 p[8];     // rows 8 i + lane / 8 (i < 4), 8 columns as two halves
+    float v[2][8];  // rows 8 g + e, rank columns 16 h + j
+    uint32_t rows;  // which of the 32 rows are the adapter's
+  };
+  const int pc = c0 + 8 * (lane & 7);
+  auto load = [&](int ch, Chunk &C) {
+    const int m0 = ch * 32;
+    const int mi = m0 + (lane & 31);
+    C.rows = (uint32_t)__ballot(mi < O.m && O.index[mi < O.m ? mi : 0] == a);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int m = m0 + 8 * i + (lane >> 3);
+      const uint16_t *q = P + (int64_t)(m < O.m ? m : O.m - 1) * cols + pc;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        C.p[2 * i + h] = u32x2{0u, 0u};
+        if (pc + 4 * h < cols) C.p[2 * i + h] = *reinterpret_cast<const u32x2 *>(q + 4 * h);
+      }
+    }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int m = ch * 32 + 8 * g + e;
-      const bool mine = m < O.m && O.index[m < O.m ? m : 0] == a;
-      p[e] = __builtin_bit_cast(__bf16, mine && c < cols ? P[(int64_t)m * cols + c] : (uint16_t)0);
-      const float v = mine ? V[(int64_t)m * O.rank_p + r] : 0.f;
-      hi[e] = (__bf16)v;
-      lo[e] = (__bf16)(v - (float)hi[e]);
+      const int m = m0 + 8 * g + e;
+      const float *q = V + (int64_t)(m < O.m ? m : O.m - 1) * O.rank_p + r0 + j;
+      C.v[0][e] = q[0];
+      C.v[1][e] = q[16];
     }
-    if (is_a) {  // rows r, columns c
-      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, p, acc, 0, 0, 0);
-      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, p, acc, 0, 0, 0);
-    } else {     // rows c, columns r
-      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(p, hi, acc, 0, 0, 0);
-      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(p, lo, acc, 0, 0, 0);
+  };
+  auto use = [&](const Chunk &C) {
+    uint16_t *const mine = turn[wave];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = 8 * i + (lane >> 3);
+      u32x4 v = u32x4{C.p[2 * i][0], C.p[2 * i][1], C.p[2 * i + 1][0], C.p[2 * i + 1][1]};
+      if (!((C.rows >> row) & 1)) v = u32x4{0u, 0u, 0u, 0u};
+      *reinterpret_cast<u32x4 *>(mine + row * kTurnStride + 8 * (lane & 7)) = v;
+    }
+    bf16x8 hi[2], lo[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float v = (C.rows >> (8 * g + e)) & 1 ? C.v[h][e] : 0.f;
+        hi[h][e] = (__bf16)v;
+        lo[h][e] = (__bf16)(v - (float)hi[h][e]);
+      }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      bf16x8 p;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) p[e] = __builtin_bit_cast(__bf16, mine[(8 * g + e) * kTurnStride + 16 * i + j]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (is_a) {  // rows r, columns c
+          acc[i][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi[h], p, acc[i][h], 0, 0, 0);
+          acc[i][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo[h], p, acc[i][h], 0, 0, 0);
+        } else {     // rows c, columns r
+          acc[i][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(p, hi[h], acc[i][h], 0, 0, 0);
+          acc[i][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(p, lo[h], acc[i][h], 0, 0, 0);
+        }
+    }
+  };
+  const int first = range[0] + wave, last = range[1];
+  if (first < last) {
+    Chunk A, B;
+    load(first, A);
+    for (int ch = first;;) {
+      load(ch + 4 < last ? ch + 4 : ch, B);
+      use(A);
+      if ((ch += 4) >= last) break;
+      load(ch + 4 < last ? ch + 4 : ch, A);
+      use(B);
+      if ((ch += 4) >= last) break;
     }
   }
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int other = 4 * g + e;
+  for (int i = 0; i < 4; ++i) {
+    part[wave][(2 * i) * 64 + lane] = acc[i][0];
+    part[wave][(2 * i + 1) * 64 + lane] = acc[i][1];
+  }
+  __syncthreads();
+  for (int v = threadIdx.x; v < 8 * 64; v += 256) {
+    const f32x4 s = ((part[0][v] + part[1][v]) + part[2][v]) + part[3][v];
+    const int l = v & 63, h = (v >> 6) & 1, i = v >> 7;
+    const int lj = l & 15, lg = l >> 4;
     if (is_a) {
-      const int rr = blockIdx.z * 16 + other;
-      if (rr < O.rank) O.da[((int64_t)a * O.rank + rr) * O.k + c] = bf16_of(acc[e]);
+      const int c = c0 + 16 * i + lj;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = r0 + 16 * h + 4 * lg + e;
+        if (r < O.rank) O.da[((int64_t)a * O.rank + r) * O.k + c] = bf16_of(s[e]);
+      }
     } else {
-      const int cc = tile * 16 + other;
-      if (cc < O.n && r < O.rank) O.db[((int64_t)a * O.n + cc) * O.rank + r] = bf16_of(acc[e]);
+      const int r = r0 + 16 * h + lj;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int c = c0 + 16 * i + 4 * lg + e;
+        if (c < O.n && r < O.rank) O.db[((int64_t)a * O.n + c) * O.rank + r] = bf16_of(s[e]);
+      }
     }
   }
 }
@@ -1199,24 +1374,25 @@ trellis_status run(const Plan &pl, int kind, trellis_geom g, Product p, unsigned
   return launch(pl.fused, p, stream);
 }
 
-// Spans of a shrink product: enough workgroups to fill the card.
-int spans_of(int64_t cells, int cols, int cus) {
-  int64_t want = (4 * (int64_t)cus + cells - 1) / cells;
-  const int most = (cols + 127) / 128;
-  return (int)(want < 1 ? 1 : want > most ? most : want);
-}
+// A shrink product: 64 rows a workgroup where there are enough to fill the
+// card that way, else 16; spans of columns until the card is full.
 struct ShrinkShape {
-  int64_t cells;
-  int spans, span;
+  int64_t groups, cells;  // of rows; with the rank's
+  int ms, spans, span;
   size_t partial_bytes;
 };
 ShrinkShape shrink_shape(int m, int cols, int rank, int cus) {
   ShrinkShape s{};
-  s.cells = (((int64_t)m + 15) / 16) * ((rank + 31) / 32 * 2);
-  s.spans = spans_of(s.cells, cols, cus);
-  s.span = ((cols + s.spans - 1) / s.spans + 127) / 128 * 128;
+  s.ms = m >= 512 ? 4 : 1;
+  s.groups = ((int64_t)m + 16 * s.ms - 1) / (16 * s.ms);
+  s.cells = s.groups * ((rank + 31) / 32);
+  int64_t spans = (2 * (int64_t)cus + s.cells - 1) / s.cells;
+  const int most = (cols + 255) / 256;
+  if (spans > most) spans = most;
+  if (spans > kMaxSpans) spans = kMaxSpans;
+  s.span = (int)((cols + spans - 1) / spans + 31) / 32 * 32;
   s.spans = (cols + s.span - 1) / s.span;
-  s.partial_bytes = s.spans > 1 ? (size_t)s.cells * s.spans * 1024 : 0;
+  s.partial_bytes = s.spans > 1 ? (size_t)s.cells * s.spans * s.ms * 2 * 1024 : 0;
   return s;
 }
 template <bool T>
@@ -1224,8 +1400,9 @@ trellis_status launch_shrink(const ShrinkShape &h, Shrink s, hipStream_t stream)
   s.span = h.span;
   s.spans = h.spans;
   (void)hipGetLastError();
-  hipLaunchKernelGGL(shrink_kernel<T>, dim3((unsigned)((s.m + 15) / 16), (unsigned)h.spans, (unsigned)(s.rank_p / 16)),
-                     dim3(256), 0, stream, s);
+  const dim3 grid((unsigned)h.groups, (unsigned)h.spans, (unsigned)(s.rank_p / 32));
+  if (h.ms == 4) hipLaunchKernelGGL((shrink_kernel<T, 4, 4>), grid, dim3(256), 0, stream, s);
+  else hipLaunchKernelGGL((shrink_kernel<T, 1, 8>), grid, dim3(512), 0, stream, s);
   return hipGetLastError() == hipSuccess ? TRELLIS_OK : TRELLIS_E_HIP;
 }
 
@@ -1296,14 +1473,14 @@ trellis_status trellis_adapters_backward(const uint16_t *dout, const uint16_t *x
   const int rank_p = (rank + 31) / 32 * 32;
   const Plan s = plan_of(kTransposed, g, m, 1, cus);
   const ShrinkShape hx = shrink_shape(m, g.k, rank, cus), hd = shrink_shape(m, g.n, rank, cus);
-  const size_t t_bytes = up256((size_t)m * rank_p * 4), r_bytes = up256((size_t)count * sizeof(int2));
+  const size_t t_bytes = up256((size_t)m * rank_p * 4), r_bytes = up256((size_t)count * sizeof(i32x2));
   size_t part = hx.partial_bytes > hd.partial_bytes ? hx.partial_bytes : hd.partial_bytes;
   if (s.bytes > part) part = s.bytes;
   const int64_t counters = s.counters > hx.cells ? s.counters : hx.cells;  // (hd has as many cells as hx)
   Space *w = nullptr;
   TRELLIS_TRY(space(dev, stream, 2 * t_bytes + r_bytes + part, (size_t)counters, w));
   float *const t = reinterpret_cast<float *>(w->bytes), *const u = reinterpret_cast<float *>(w->bytes + t_bytes);
-  int2 *const range = reinterpret_cast<int2 *>(w->bytes + 2 * t_bytes);
+  i32x2 *const range = reinterpret_cast<i32x2 *>(w->bytes + 2 * t_bytes);
   float *const partials = reinterpret_cast<float *>(w->bytes + 2 * t_bytes + r_bytes);
   TRELLIS_TRY(launch_shrink<false>(
       hx, Shrink{x, a, gain, index, t, partials, w->counters, m, g.k, count, rank, rank_p, 0, 0}, stream));
@@ -1322,8 +1499,8 @@ trellis_status trellis_adapters_backward(const uint16_t *dout, const uint16_t *x
   p.k = g.k;
   p.low = LowRank{index, a, u, count, rank, rank_p};
   TRELLIS_TRY(run(s, kTransposed, g, p, reinterpret_cast<unsigned char *>(partials), stream));
-  Outer o{x, dout, u, t, index, range, da, db, m, g.n, g.k, rank, rank_p, g.k / 16, g.k / 16 + (g.n + 15) / 16};
-  hipLaunchKernelGGL(outer_kernel, dim3((unsigned)((o.tiles + 3) / 4), (unsigned)count, (unsigned)((rank + 15) / 16)),
+  Outer o{x, dout, u, t, index, range, da, db, m, g.n, g.k, rank, rank_p, g.k / 64};
+  hipLaunchKernelGGL(outer_kernel, dim3((unsigned)(o.tiles_a + (g.n + 63) / 64), (unsigned)count, (unsigned)(rank_p / 32)),
                      dim3(256), 0, stream, o);
   return hipGetLastError() == hipSuccess ? TRELLIS_OK : TRELLIS_E_HIP;
 }
