@@ -1,15 +1,19 @@
-// Many rows: W is decoded once into a workspace of MFMA operands, and a dense
-// product reads it from there (rows.hip decides from how many rows on).
+// Many rows: W is decoded once into a workspace of MFMA operands, P's rows are
+// copied into the same form, and a dense product reads both from there
+// (rows.hip decides from how many rows on).
 //
-// Workspace layout. A "tile" is 16 output columns of the product, a "kstep" 32
-// columns of its contraction; [tile][kstep][lane][8] bf16 holds lane (j, g)'s
-// MFMA operand, W at output column 16 tile + j and contraction columns
-// 32 kstep + 8 g .. +7, so a wave's operand is 1 KB in a row: it reaches LDS
-// by linear copies and is read from there without bank conflicts.
+// Workspace layout of either side. A "tile" is 16 rows of P or 16 output
+// columns, a "step" 32 columns of the contraction; [step][tile][lane][8] bf16
+// holds lane (j, g)'s MFMA operand: row or output column 16 tile + j,
+// contraction columns 32 step + 8 g .. +7. What a workgroup
+// stages per step is then one run of memory on each side: it spreads evenly
+// over the memory channels (rows of P as they come are a multiple of 2 KB
+// apart for most widths, and a step's bytes of each lie in a few channels), reaches LDS by linear copies and is read
+// from there without bank conflicts.
 //   forward     output columns = rows of W, contraction = K (gated: the tiles
 //               of the gate and of the up matrix alternate)
 //   transposed  output columns = columns of W, contraction = N, padded with
-//               zeros to whole steps of 64 (two matrices one after the other)
+//               zeros to a multiple of 64 (two matrices one after the other)
 #pragma once
 
 #include "decode.hpp"
@@ -18,7 +22,7 @@ namespace trellis {
 namespace {
 
 constexpr int kDenseRows = 256;   // rows of a workgroup's tile
-constexpr int kDenseStep = 64;    // contraction columns per step
+constexpr int kDenseStep = 32;    // contraction columns per step
 constexpr int kDenseThreads = 512;
 
 // bf16 weight of a window: code * q where the row's scale allows it, else the
@@ -32,7 +36,7 @@ struct Unpack {
   const uint16_t *scales[2];
   uint16_t *w;
   int32_t n, k;
-  int32_t ksteps;   // of the whole contraction
+  int32_t steps;         // of the whole contraction
   int32_t first, tiles;  // tiles of this launch: first, number (per matrix)
   int32_t matrices;
 };
@@ -60,19 +64,19 @@ __global__ __launch_bounds__(256) void unpack_rows_kernel(Unpack U) {
     const int w = w0 - st * BITS, next = w + 1 == wpb ? 0 : w + 1;
     f[st] = (((uint64_t)bw[next] << 32) | bw[w]) >> off;
   }
-  bf16x8 *out = reinterpret_cast<bf16x8 *>(U.w) +
-                (((int64_t)tile * U.matrices + which) * U.ksteps + b * 8) * 64 + lane;
+  const int64_t stride = (int64_t)U.tiles * U.matrices * 64;  // of a step
+  bf16x8 *out = reinterpret_cast<bf16x8 *>(U.w) + 8 * b * stride + ((int64_t)tile * U.matrices + which) * 64 + lane;
 #pragma unroll
   for (int st = 0; st < 8; ++st) {
     bf16x8 v;
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       v[e] = (__bf16)window_weight((uint32_t)(f[st] >> ((7 - e) * BITS)) & 0xFFFu, s, q, kq, exact);
-    out[st * 64] = v;
+    out[st * stride] = v;
   }
 }
 
-// Transposed: one wave per kstep (32 rows of W) and 64 columns; lane (j, g)
+// Transposed: one wave per step (32 rows of W) and 64 columns; lane (j, g)
 // decodes columns 4 j .. +3 of rows 8 g .. +7 and so holds, for each of the
 // four columns, one lane's whole operand.
 template <int BITS>
@@ -80,7 +84,7 @@ __global__ __launch_bounds__(256) void unpack_columns_kernel(Unpack U) {
   __shared__ bf16x8 turn[4][4 * 64];
   constexpr int wpb = 8 * BITS;
   const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
-  const int per = U.ksteps / U.matrices;  // ksteps of one matrix
+  const int per = U.steps / U.matrices;  // steps of one matrix
   const int groups = U.tiles >> 2;        // of 64 columns
   const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (id >= (int64_t)groups * per) return;
@@ -114,31 +118,81 @@ __global__ __launch_bounds__(256) void unpack_columns_kernel(Unpack U) {
   bf16x8 *const mine = turn[threadIdx.x >> 6];
 #pragma unroll
   for (int c = 0; c < 4; ++c) mine[(j >> 2) * 64 + g * 16 + 4 * (j & 3) + c] = v[c];
-  bf16x8 *out = reinterpret_cast<bf16x8 *>(U.w) + ((int64_t)(4 * grp) * U.ksteps + (int64_t)which * per + ks) * 64 + lane;
+  bf16x8 *out = reinterpret_cast<bf16x8 *>(U.w) + (((int64_t)which * per + ks) * U.tiles + 4 * grp) * 64 + lane;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) out[(int64_t)i * U.ksteps * 64] = mine[i * 64 + lane];
+  for (int i = 0; i < 4; ++i) out[i * 64] = mine[i * 64 + lane];
 }
 
-// Rows padded with zeros to whole contraction steps, four elements a thread.
-__global__ __launch_bounds__(256) void pad_rows_kernel(const uint16_t *__restrict__ src, int64_t rows, int cols,
-                                                       int padded, uint16_t *__restrict__ dst) {
-  const int quads = padded >> 2;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= rows * quads) return;
-  const int64_t row = i / quads;
-  const int c = (int)(i - row * quads) * 4;
-  const uint2 z = {0u, 0u};
-  reinterpret_cast<uint2 *>(dst)[i] = c < cols ? *reinterpret_cast<const uint2 *>(src + row * cols + c) : z;
+// Rows of P as operands: one wave per two steps and 16-row tile. Rows past m and
+// columns past `cols` are zero (rows start at multiples of 8 bytes).
+__device__ __forceinline__ u32x4 row_vector(const uint16_t *src, int64_t row, int64_t m, int cols, int c) {
+  u32x2 v[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    v[h] = u32x2{0u, 0u};
+    if (row < m && c + 4 * h < cols) v[h] = *reinterpret_cast<const u32x2 *>(src + row * cols + c + 4 * h);
+  }
+  return u32x4{v[0][0], v[0][1], v[1][0], v[1][1]};
+}
+__global__ __launch_bounds__(256) void pack_rows_kernel(const uint16_t *__restrict__ src, int m, int cols, int tiles,
+                                                        int steps, uint16_t *__restrict__ dst) {
+  const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
+  const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int pairs = steps >> 1;
+  if (id >= (int64_t)tiles * pairs) return;
+  const int tile = (int)(id / pairs), step = 2 * (int)(id - (int64_t)tile * pairs);
+  u32x4 *out = reinterpret_cast<u32x4 *>(dst) + ((int64_t)step * tiles + tile) * 64 + lane;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    out[(int64_t)h * tiles * 64] = row_vector(src, (int64_t)tile * 16 + j, m, cols, (step + h) * 32 + 8 * g);
+}
+
+// The gated block's elementwise gradients (see gated_grad_kernel) as rows and
+// as operands: steps 0 .. steps - 1 hold dgate, the next `steps` dup.
+__global__ __launch_bounds__(256) void gated_grad_pack_kernel(const uint16_t *__restrict__ dh,
+                                                              const uint16_t *__restrict__ gate,
+                                                              const uint16_t *__restrict__ up, int m, int cols, int tiles,
+                                                              int steps, uint16_t *__restrict__ dgate,
+                                                              uint16_t *__restrict__ dup, uint16_t *__restrict__ dst) {
+  const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
+  const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int pairs = steps >> 1;
+  if (id >= (int64_t)tiles * pairs) return;
+  const int tile = (int)(id / pairs), step = 2 * (int)(id - (int64_t)tile * pairs);
+  u32x4 *out = reinterpret_cast<u32x4 *>(dst) + ((int64_t)step * tiles + tile) * 64 + lane;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int64_t row = (int64_t)tile * 16 + j;
+    const int c = (step + h) * 32 + 8 * g;
+    const u32x4 d = row_vector(dh, row, m, cols, c), gv = row_vector(gate, row, m, cols, c), uv = row_vector(up, row, m, cols, c);
+    u32x4 pg, pu;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float og[2], ou[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        gated_gradients(bf16_half(d[e], k), bf16_half(gv[e], k), bf16_half(uv[e], k), og[k], ou[k]);
+      pg[e] = (uint32_t)bf16_of(og[0]) | ((uint32_t)bf16_of(og[1]) << 16);
+      pu[e] = (uint32_t)bf16_of(ou[0]) | ((uint32_t)bf16_of(ou[1]) << 16);
+    }
+    out[(int64_t)h * tiles * 64] = pg;
+    out[(int64_t)(steps + h) * tiles * 64] = pu;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (row < m && c + 4 * k < cols) {
+        *reinterpret_cast<u32x2 *>(dgate + row * cols + c + 4 * k) = u32x2{pg[2 * k], pg[2 * k + 1]};
+        *reinterpret_cast<u32x2 *>(dup + row * cols + c + 4 * k) = u32x2{pu[2 * k], pu[2 * k + 1]};
+      }
+  }
 }
 
 struct Dense {
-  const uint16_t *p, *p2;  // [m, cols], cols a multiple of 64; p2 from step steps1 on
-  const uint16_t *w;       // operands, from tile 0 of this launch on
+  const uint16_t *p, *w;   // operands of the rows, and of the columns of this launch
   uint16_t *out, *gate, *up;
-  int32_t m, cols, steps, steps1;
+  int32_t m, steps;
   int32_t width;           // row length of the outputs
   int32_t first;           // first output column of this launch (gated: of one matrix)
-  int32_t tiles;           // operand tiles of this launch
+  int32_t ptiles, wtiles;  // operand tiles
   int32_t mtiles, ntiles;  // workgroup tiles
   LowRank low;
 };
@@ -154,23 +208,30 @@ __device__ __forceinline__ void copy_to_lds(uint32_t lds, uint32_t off, const vo
       : "s"(lds), "v"(off), "s"(base)
       : "memory");
 }
+// Waits until at most N of the wave's copies are on their way and its LDS
+// reads are done, then for the workgroup.
+template <int N>
 __device__ __forceinline__ void step_barrier() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
+// LDS buffers of a step: as many as fit in 160 KB, at most 6.
+constexpr int dense_step_bytes(int nt) { return (kDenseRows / 16 + 2 * nt) * 1024; }
+constexpr int dense_buffers(int nt) { return 160 * 1024 / dense_step_bytes(nt) < 6 ? 160 * 1024 / dense_step_bytes(nt) : 6; }
+
 // One workgroup (8 waves, 4 by rows x 2 by columns): 256 rows by 32 NT
-// columns. Wave: 64 rows by 16 NT columns, 4 x NT accumulators. Each step
-// stages 64 contraction columns of both operands in one of two LDS buffers
-// while the other is multiplied. A row's eight 16-byte vectors are stored
-// permuted by (row / 2) mod 8, which spreads the sixteen rows that a wave
-// reads together over all banks (the copies can only write in lane order, so
-// the permutation is made in the addresses they read from). The operands'
-// roles are W then P, so a lane holds four consecutive output columns of one
-// row and stores 8 bytes at a time.
+// columns. Wave: 64 rows by 16 NT columns, 4 x NT accumulators. A step's
+// operands (32 contraction columns of both sides) are copied into one of S LDS
+// buffers, S steps ahead; a wave reads the operands of step s + 1 into
+// registers while it multiplies step s. One barrier a step: it says that step
+// s + 1 has landed and that step s has been read, so its buffer takes step
+// s + S. The operands' roles are W then P, so a lane holds four consecutive
+// output columns of one row and stores 8 bytes at a time.
 template <int NT, bool GATED, bool T>
 __global__ __launch_bounds__(kDenseThreads) void dense_kernel(Dense D) {
-  constexpr int kA = kDenseRows * kDenseStep * 2, kB = 2 * NT * 2048, kBuffer = kA + kB;
-  constexpr int kCopies = kB / 1024;  // of 1 KB
+  constexpr int kA = kDenseRows / 16 * 1024, kBuffer = dense_step_bytes(NT), S = dense_buffers(NT);
+  constexpr int kCopies = kBuffer / 1024;  // of 1 KB
+  constexpr int kMost = (kCopies + 7) / 8, kFull = kCopies % 8 == 0 ? 8 : kCopies % 8;  // waves 0 .. kFull - 1 copy kMost, the others one less
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -182,37 +243,31 @@ __global__ __launch_bounds__(kDenseThreads) void dense_kernel(Dense D) {
   const int xcd = blockIdx.x & 7, seq = blockIdx.x >> 3;
   const int id = xcd * each + (xcd < rest ? xcd : rest) + seq;
   const int tn = id / D.mtiles, tm = id - tn * D.mtiles;
-  const int m0 = tm * kDenseRows;
-  const int ksteps = 2 * D.steps;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char *)lds;
 
-  // P: copy i of a wave (of 4) takes rows 8 (4 wave + i) .. +7.
-  uint32_t aoff[4];
+  // Copy c of a step (1 KB): the first kA / 1024 are P's. Tiles past the last
+  // repeat it (what they feed is not stored).
+  const int atiles = D.ptiles - tm * (kDenseRows / 16), btiles = D.wtiles - tn * 2 * NT;
+  const unsigned char *const pa = reinterpret_cast<const unsigned char *>(D.p) + (int64_t)tm * (kDenseRows / 16) * 1024;
+  const unsigned char *const pb = reinterpret_cast<const unsigned char *>(D.w) + (int64_t)tn * 2 * NT * 1024;
+  const int64_t astride = (int64_t)D.ptiles * 1024, bstride = (int64_t)D.wtiles * 1024;
+  auto stage = [&](int s, uint32_t buffer) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = 8 * (4 * wave + i) + (lane >> 3);
-    const int row = m0 + r < D.m ? r : D.m - 1 - m0;  // rows past m feed outputs that are not stored
-    aoff[i] = (uint32_t)row * (uint32_t)(D.cols * 2) + (uint32_t)(((lane & 7) ^ ((r >> 1) & 7)) * 16);
-  }
-  const unsigned char *const pa = reinterpret_cast<const unsigned char *>(D.p + (int64_t)m0 * D.cols);
-  const unsigned char *const pa2 = reinterpret_cast<const unsigned char *>(D.p2 + (int64_t)m0 * D.cols);
-  const unsigned char *const pb = reinterpret_cast<const unsigned char *>(D.w) + (int64_t)tn * 2 * NT * ksteps * 1024;
-  const int btiles = D.tiles - tn * 2 * NT;  // of this workgroup, at least 1
-  auto stage = [&](int s) {
-    const uint32_t at = lds0 + (uint32_t)((s & 1) * kBuffer);
-    const unsigned char *a = s < D.steps1 ? pa + (int64_t)s * 128 : pa2 + (int64_t)(s - D.steps1) * 128;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) copy_to_lds(at + (uint32_t)((4 * wave + i) * 1024), aoff[i], a);
-#pragma unroll
-    for (int i = 0; i < (kCopies + 7) / 8; ++i) {
+    for (int i = 0; i < kMost; ++i) {
       const int c = wave + 8 * i;
-      if (kCopies % 8 == 0 || c < kCopies) {
-        // tiles past the last repeat it (their columns are not stored)
-        const int t = (c >> 1) < btiles ? c >> 1 : btiles - 1;
-        copy_to_lds(at + kA + (uint32_t)(c * 1024), (uint32_t)lane * 16,
-                    pb + ((int64_t)t * ksteps + 2 * s + (c & 1)) * 1024);
+      if (kFull == 8 || i < kMost - 1 || wave < kFull) {
+        const bool is_a = i < kA / 8192;
+        const int t = is_a ? c : c - kA / 1024, have = is_a ? atiles : btiles;
+        const unsigned char *src = is_a ? pa + s * astride : pb + s * bstride;
+        copy_to_lds(lds0 + buffer + (uint32_t)(c * 1024), (uint32_t)lane * 16, src + (t < have ? t : have - 1) * 1024);
       }
     }
+  };
+  // All but the last N steps' copies of this wave have landed, workgroup-wide.
+  auto landed = [&](auto n) {
+    constexpr int N = decltype(n)::value;
+    if (kFull == 8 || wave < kFull) step_barrier<N * kMost>();
+    else step_barrier<N *(kMost - 1)>();
   };
 
   f32x4 acc[4][NT];
@@ -220,72 +275,127 @@ __global__ __launch_bounds__(kDenseThreads) void dense_kernel(Dense D) {
   for (int a = 0; a < 4; ++a)
 #pragma unroll
     for (int b = 0; b < NT; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const uint32_t arow = (uint32_t)((64 * wm + j) * 128), sw = (uint32_t)((j >> 1) & 7);
-  stage(0);
-  step_barrier();
-  for (int s = 0; s < D.steps; ++s) {
-    if (s + 1 < D.steps) stage(s + 1);
-    const unsigned char *const buf = lds + (s & 1) * kBuffer;
+  // Lane (j, g), accumulator (r, i): row row0 + 16 r + j, operand tile
+  // tile0 + i, its columns 4 g .. +3.
+  const int row0 = tm * kDenseRows + 64 * wm, tile0 = tn * 2 * NT + wn * NT;
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      bf16x8 a[4], b[NT];
+  for (int b = 0; b < S; ++b)
+    if (b < D.steps) stage(b, b * kBuffer);
+  if constexpr (!GATED) {
+    // The adapters' term first, while the first steps are on their way: lane l
+    // looks up row row0 + l; for every adapter that the wave's rows name, the
+    // products are kept only in the rows that name it (see low_rank_tile).
+    if (D.low.rank > 0) {
+      int idx = row0 + lane < D.m ? D.low.index[row0 + lane] : -1;
+      if (idx >= D.low.count) idx = -1;
+      uint64_t left = __ballot(idx >= 0);
+      while (left) {
+        const int a = __builtin_amdgcn_readlane(idx, __builtin_ctzll(left));
+        const uint64_t rows = __ballot(idx == a);
+        left &= ~rows;
+        for (int r0 = 8 * g; r0 < D.low.rank_p + 8 * g; r0 += 32) {
+          // The factor's operands, each loaded while the one before it is
+          // multiplied (the barriers keep the loads in flight to two tiles').
+          // Offsets past the adapter's block, and those of rank columns past
+          // the rank, read as zero.
+          const uint32_t block = (uint32_t)D.low.rank * (uint32_t)D.width * 2;
+          const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+              const_cast<uint16_t *>(D.low.factor + (int64_t)a * D.low.rank * D.width), (short)0, (int)block, kRawBuffer);
+          const uint32_t col0 = (uint32_t)(D.first + tile0 * 16 + j);
+          auto fetch = [&](int i) {
+            if constexpr (T) {
+              bf16x8 f;
+              const uint32_t o = ((uint32_t)r0 * (uint32_t)D.width + col0) * 2 + 32u * (uint32_t)i;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        a[i] = *reinterpret_cast<const bf16x8 *>(buf + arow + i * 2048 + ((uint32_t)(4 * kk + g) ^ sw) * 16);
+              for (int e = 0; e < 8; ++e)
+                f[e] = __builtin_bit_cast(__bf16, (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(
+                                                      rs, o + (uint32_t)e * (uint32_t)D.width * 2, 0, 0));
+              return f;
+            } else {
+              const uint32_t o = ((col0 + 16u * (uint32_t)i) * (uint32_t)D.low.rank + (uint32_t)r0) * 2;
+              if ((D.low.rank & 7) == 0)
+                return __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(rs, r0 < D.low.rank ? o : 0x80000000u, 0, 0));
+              bf16x8 f;
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
-        b[i] = *reinterpret_cast<const bf16x8 *>(buf + kA + ((wn * NT + i) * 2 + kk) * 1024 + lane * 16);
+              for (int e = 0; e < 8; ++e)
+                f[e] = __builtin_bit_cast(__bf16, (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(
+                                                      rs, r0 + e < D.low.rank ? o + 2u * (uint32_t)e : 0x80000000u, 0, 0));
+              return f;
+            }
+          };
+          // (two row tiles at a time: t's operands for four take too many registers)
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
+          for (int rp = 0; rp < 4; rp += 2) {
+            bf16x8 hi[2], lo[2];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[r][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[i], a[r], acc[r][i], 0, 0, 0);
-    }
-    step_barrier();
-  }
-
-  // Lane (j, g), accumulator (r, i): row m0 + 64 wm + 16 r + j, operand tile
-  // tn 2 NT + wn NT + i, its columns 4 g .. +3.
-  const int tile0 = tn * 2 * NT + wn * NT;
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int row = m0 + 64 * wm + 16 * r + j;
-    if constexpr (!GATED) {
-      if (D.low.rank > 0) {
-        const int rowc = row < D.m ? row : D.m - 1;
-        int idx = row < D.m ? D.low.index[row] : -1;
-        if (idx >= D.low.count) idx = -1;
-        uint64_t left = __ballot(idx >= 0) & 0xFFFFull;
-        while (left) {
-          const int a = __builtin_amdgcn_readlane(idx, __builtin_ctzll(left));
-          left &= ~__ballot(idx == a);
-          for (int i = 0; i < NT; ++i) {
-            const int col = D.first + (tile0 + i) * 16 + j;
-            f32x4 d = {0.f, 0.f, 0.f, 0.f};
-            for (int r0 = 8 * g; r0 < D.low.rank_p + 8 * g; r0 += 32) {
-              const float *tp = D.low.t + (int64_t)rowc * D.low.rank_p + r0;
-              bf16x8 hi, lo, f;
+            for (int r = 0; r < 2; ++r) {
+              const int row = row0 + 16 * (rp + r) + j;
+              const f32x4 *tp = reinterpret_cast<const f32x4 *>(D.low.t + (int64_t)(row < D.m ? row : D.m - 1) * D.low.rank_p + r0);
+              const f32x4 t0 = tp[0], t1 = tp[1];
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
-                hi[e] = (__bf16)tp[e];
-                lo[e] = (__bf16)(tp[e] - (float)hi[e]);
-                uint16_t v = 0;
-                if (col < D.width && r0 + e < D.low.rank)
-                  v = T ? D.low.factor[((int64_t)a * D.low.rank + r0 + e) * D.width + col]
-                        : D.low.factor[((int64_t)a * D.width + col) * D.low.rank + r0 + e];
-                f[e] = __builtin_bit_cast(__bf16, v);
+                const float v = e < 4 ? t0[e] : t1[e - 4];
+                hi[r][e] = (__bf16)v;
+                lo[r][e] = (__bf16)(v - (float)hi[r][e]);
               }
-              d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, hi, d, 0, 0, 0);
-              d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, lo, d, 0, 0, 0);
             }
+            bf16x8 next = fetch(0);
 #pragma unroll
-            for (int q = 0; q < NT; ++q)
-              if (q == i)
+            for (int i = 0; i < NT; ++i) {
+              const bf16x8 f = next;
+              __builtin_amdgcn_sched_barrier(0);
+              if (i + 1 < NT) next = fetch(i + 1);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[r][q][e] += idx == a ? d[e] : 0.f;
+              for (int r = 0; r < 2; ++r) {
+                f32x4 d = {0.f, 0.f, 0.f, 0.f};
+                d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, hi[r], d, 0, 0, 0);
+                d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, lo[r], d, 0, 0, 0);
+                const bool mine = (rows >> (16 * (rp + r) + j)) & 1;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[rp + r][i][e] += mine ? d[e] : 0.f;
+              }
+            }
           }
         }
       }
     }
+  }
+  struct Operands {
+    bf16x8 a[4], b[NT];
+  };
+  auto read = [&](Operands &O, uint32_t buffer) {
+    const unsigned char *const buf = lds + buffer + lane * 16;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) O.b[i] = *reinterpret_cast<const bf16x8 *>(buf + kA + (wn * NT + i) * 1024);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) O.a[i] = *reinterpret_cast<const bf16x8 *>(buf + (4 * wm + i) * 1024);
+  };
+  auto multiply = [&](const Operands &O) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[r][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(O.b[i], O.a[r], acc[r][i], 0, 0, 0);
+  };
+  Operands X, Y;
+  uint32_t now = 0;  // buffer of step s
+  step_barrier<0>();
+  read(X, 0);
+  auto step = [&](int s, const Operands &A, Operands &B) {
+    if (s + S - 1 < D.steps) landed(std::integral_constant<int, S - 2>{});
+    else step_barrier<0>();
+    if (s + S < D.steps) stage(s + S, now);
+    now = now == (S - 1) * kBuffer ? 0 : now + kBuffer;
+    read(B, now);  // (past the last step: a buffer's old operands, not used)
+    multiply(A);
+  };
+  for (int s = 0; s < D.steps; s += 2) {  // an even number of steps
+    step(s, X, Y);
+    step(s + 1, Y, X);
+  }
+
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int row = row0 + 16 * r + j;
     if (row >= D.m) continue;
     if constexpr (GATED) {
 #pragma unroll

@@ -23,6 +23,7 @@
 #include <map>
 #include <mutex>
 #include <thread>
+#include <type_traits>
 #include <utility>
 
 #include "decode.hpp"
@@ -197,6 +198,15 @@ enum Kind { kForward = 0, kGated = 1, kTransposed = 2 };
 
 // h = silu(gate) * up in float32, rounded once by the caller.
 __device__ __forceinline__ float silu_mul(float gate, float up) { return gate / (1.0f + expf(-gate)) * up; }
+
+// Its gradients: dup = dh silu(gate), dgate = dh up s (1 + gate (1 - s)), s = sigmoid(gate).
+__device__ __forceinline__ void gated_gradients(float dh, float gate, float up, float &dgate, float &dup) {
+  const float s = 1.0f / (1.0f + expf(-gate));
+  dup = dh * gate * s;
+  dgate = dh * up * s * (1.0f + gate * (1.0f - s));
+}
+// The low (k = 0) or high bf16 of a word.
+__device__ __forceinline__ float bf16_half(uint32_t v, int k) { return __uint_as_float(k ? v & 0xFFFF0000u : v << 16); }
 
 // Four floats a time, four output columns: rounded and stored (N and K are
 // multiples of 4, rows start at multiples of 8 bytes).
@@ -1041,8 +1051,7 @@ __global__ __launch_bounds__(256) void outer_kernel(Outer O) {
   }
 }
 
-// The gated block's elementwise gradients, four elements a thread:
-//   dup = dh silu(gate), dgate = dh up s (1 + gate (1 - s)), s = sigmoid(gate)
+// The gated block's elementwise gradients as rows, four elements a thread.
 __global__ __launch_bounds__(256) void gated_grad_kernel(const uint16_t *__restrict__ dh, const uint16_t *__restrict__ gate,
                                                          const uint16_t *__restrict__ up, int64_t quads,
                                                          uint16_t *__restrict__ dgate, uint16_t *__restrict__ dup) {
@@ -1054,10 +1063,10 @@ __global__ __launch_bounds__(256) void gated_grad_kernel(const uint16_t *__restr
   f32x4 og, ou;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const float dd = bf16_bits_to_f32(d[e]), gg = bf16_bits_to_f32(gv[e]), uu = bf16_bits_to_f32(uv[e]);
-    const float s = 1.0f / (1.0f + expf(-gg));
-    ou[e] = dd * gg * s;
-    og[e] = dd * uu * s * (1.0f + gg * (1.0f - s));
+    float a, b;
+    gated_gradients(bf16_bits_to_f32(d[e]), bf16_bits_to_f32(gv[e]), bf16_bits_to_f32(uv[e]), a, b);
+    og[e] = a;
+    ou[e] = b;
   }
   store4(dgate + 4 * i, og);
   store4(dup + 4 * i, ou);
@@ -1226,16 +1235,16 @@ constexpr int64_t kOperandBytes = (int64_t)1 << 30;
 struct DenseShape {
   int nt;              // accumulator tiles per wave
   int matrices;        // gated: 2 in the tiles, transposed: in the contraction
-  int steps, steps1, cols;
+  int steps, steps1;
   int64_t tiles, slab;  // operand tiles in all and per launch
-  size_t operand_bytes, pad_bytes;
+  int ptiles;
+  size_t operand_bytes, row_bytes;
 };
 DenseShape dense_shape(int kind, trellis_geom g, int32_t m, int matrices, int cus) {
   DenseShape s{};
   s.matrices = matrices;
   const bool t = kind == kTransposed;
-  s.cols = t ? (g.n + 63) / 64 * 64 : g.k;
-  s.steps1 = s.cols / kDenseStep;
+  s.steps1 = ((t ? g.n : g.k) + 63) / 64 * 2;  // an even number
   s.steps = t ? s.steps1 * matrices : s.steps1;
   const int64_t width = t ? g.k : g.n, one = (width + 15) / 16;
   s.tiles = kind == kGated ? 2 * one : one;
@@ -1251,13 +1260,14 @@ DenseShape dense_shape(int kind, trellis_geom g, int32_t m, int matrices, int cu
       s.nt = nt;
     }
   }
-  const int64_t tile_bytes = (int64_t)s.steps * 2 * 1024;
+  const int64_t tile_bytes = (int64_t)s.steps * 1024;
   int64_t slab = kOperandBytes / tile_bytes / (16 * s.nt) * (16 * s.nt);  // whole workgroup tiles, fours and pairs
   if (slab < 16 * s.nt) slab = 16 * s.nt;
   if (slab > s.tiles) slab = s.tiles;
   s.slab = slab;
   s.operand_bytes = (size_t)(slab * tile_bytes);
-  s.pad_bytes = t && s.cols != g.n ? up256((size_t)m * s.cols * 2) : 0;
+  s.ptiles = (int)(((int64_t)m + 15) / 16);
+  s.row_bytes = (size_t)s.ptiles * s.steps * 1024;
   return s;
 }
 
@@ -1277,10 +1287,16 @@ DenseFn dense_fn(int kind, int nt) {
   return kind == kTransposed ? dense_of<true>(nt) : dense_of<false>(nt);
 }
 
-trellis_status launch_dense(int kind, const DenseShape &s, trellis_geom g, const Product &p, unsigned char *operands,
-                            unsigned char *pads, hipStream_t stream) {
+// What the elementwise gradients are computed from (transposed with two matrices).
+struct GatedGrads {
+  const uint16_t *dh, *gate, *up;
+  uint16_t *dgate, *dup;
+};
+
+trellis_status launch_dense(int kind, const DenseShape &s, trellis_geom g, const Product &p, const GatedGrads *grads,
+                            unsigned char *operands, unsigned char *rows, hipStream_t stream) {
   const DenseFn fn = dense_fn(kind, s.nt);
-  const size_t lds = 2 * ((size_t)kDenseRows * kDenseStep * 2 + (size_t)2 * s.nt * 2048);
+  const size_t lds = (size_t)dense_buffers(s.nt) * dense_step_bytes(s.nt);
   static bool ready[kMaxDevices][3][9];
   int dev = 0, cus = 0;
   if (device(dev, cus) != TRELLIS_OK) return TRELLIS_E_HIP;
@@ -1291,37 +1307,34 @@ trellis_status launch_dense(int kind, const DenseShape &s, trellis_geom g, const
     ready[dev][kind][s.nt] = true;
   }
   Dense d{};
-  d.p = p.p;
-  d.p2 = p.p2;
+  d.p = reinterpret_cast<const uint16_t *>(rows);
   d.w = reinterpret_cast<const uint16_t *>(operands);
   d.out = p.out;
   d.gate = p.gate;
   d.up = p.up;
   d.m = p.m;
-  d.cols = s.cols;
   d.steps = s.steps;
-  d.steps1 = s.steps1;
+  d.ptiles = s.ptiles;
   d.width = kind == kTransposed ? g.k : g.n;
   d.mtiles = (p.m + kDenseRows - 1) / kDenseRows;
   d.low = p.low;
   (void)hipGetLastError();
-  if (s.pad_bytes) {
-    const int64_t quads = (int64_t)p.m * (s.cols / 4);
-    for (int i = 0; i < s.matrices; ++i) {
-      uint16_t *dst = reinterpret_cast<uint16_t *>(pads + i * s.pad_bytes);
-      hipLaunchKernelGGL(pad_rows_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream, i ? p.p2 : p.p,
-                         (int64_t)p.m, g.n, s.cols, dst);
-      (i ? d.p2 : d.p) = dst;
-    }
-  }
+  const dim3 pack((unsigned)(((int64_t)s.ptiles * (s.steps1 / 2) + 3) / 4));
+  if (grads)
+    hipLaunchKernelGGL(gated_grad_pack_kernel, pack, dim3(256), 0, stream, grads->dh, grads->gate, grads->up, p.m, g.n,
+                       s.ptiles, s.steps1, grads->dgate, grads->dup, reinterpret_cast<uint16_t *>(rows));
+  else
+    hipLaunchKernelGGL(pack_rows_kernel, pack, dim3(256), 0, stream, p.p, p.m, kind == kTransposed ? g.n : g.k, s.ptiles,
+                       s.steps1, reinterpret_cast<uint16_t *>(rows));
+  if (hipGetLastError() != hipSuccess) return TRELLIS_E_HIP;
   for (int64_t first = 0; first < s.tiles; first += s.slab) {
     const int tiles = (int)(s.tiles - first < s.slab ? s.tiles - first : s.slab);
-    Unpack u{{p.codes, p.codes2}, {p.scales, p.scales2}, reinterpret_cast<uint16_t *>(operands), g.n, g.k, 2 * s.steps, 0, 0, 1};
+    Unpack u{{p.codes, p.codes2}, {p.scales, p.scales2}, reinterpret_cast<uint16_t *>(operands), g.n, g.k, s.steps, 0, 0, 1};
     if (kind == kTransposed) {
       u.first = (int)first;
       u.tiles = tiles;
       u.matrices = s.matrices;
-      const int64_t waves = (int64_t)(tiles / 4) * (2 * s.steps1);
+      const int64_t waves = (int64_t)(tiles / 4) * s.steps1;
       const dim3 grid((unsigned)((waves + 3) / 4), (unsigned)s.matrices);
       if (g.bits == 2) hipLaunchKernelGGL(unpack_columns_kernel<2>, grid, dim3(256), 0, stream, u);
       else if (g.bits == 3) hipLaunchKernelGGL(unpack_columns_kernel<3>, grid, dim3(256), 0, stream, u);
@@ -1339,7 +1352,7 @@ trellis_status launch_dense(int kind, const DenseShape &s, trellis_geom g, const
     }
     if (hipGetLastError() != hipSuccess) return TRELLIS_E_HIP;
     d.first = (int)(first * 16 / (kind == kGated ? 2 : 1));
-    d.tiles = tiles;
+    d.wtiles = tiles;
     d.ntiles = (tiles + 2 * s.nt - 1) / (2 * s.nt);
     hipLaunchKernelGGL(fn, dim3((unsigned)(d.mtiles * d.ntiles)), dim3(kDenseThreads), lds, stream, d);
     if (hipGetLastError() != hipSuccess) return TRELLIS_E_HIP;
@@ -1360,7 +1373,7 @@ Plan plan_of(int kind, trellis_geom g, int32_t m, int matrices, int cus) {
   p.dense = m >= kDenseFrom;
   if (p.dense) {
     p.many = dense_shape(kind, g, m, matrices, cus);
-    p.bytes = up256(p.many.operand_bytes) + p.many.pad_bytes * matrices;
+    p.bytes = up256(p.many.operand_bytes) + p.many.row_bytes;
   } else {
     p.fused = shape_of(kind, g, m, matrices, cus);
     p.bytes = p.fused.partial_bytes;
@@ -1368,8 +1381,16 @@ Plan plan_of(int kind, trellis_geom g, int32_t m, int matrices, int cus) {
   }
   return p;
 }
-trellis_status run(const Plan &pl, int kind, trellis_geom g, Product p, unsigned char *ws, hipStream_t stream) {
-  if (pl.dense) return launch_dense(kind, pl.many, g, p, ws, ws + up256(pl.many.operand_bytes), stream);
+trellis_status run(const Plan &pl, int kind, trellis_geom g, Product p, const GatedGrads *grads, unsigned char *ws,
+                   hipStream_t stream) {
+  if (pl.dense) return launch_dense(kind, pl.many, g, p, grads, ws, ws + up256(pl.many.operand_bytes), stream);
+  if (grads) {
+    const int64_t quads = (int64_t)p.m * (g.n / 4);
+    (void)hipGetLastError();
+    hipLaunchKernelGGL(gated_grad_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream, grads->dh,
+                       grads->gate, grads->up, quads, grads->dgate, grads->dup);
+    if (hipGetLastError() != hipSuccess) return TRELLIS_E_HIP;
+  }
   p.partials = reinterpret_cast<float *>(ws);
   return launch(pl.fused, p, stream);
 }
@@ -1452,7 +1473,7 @@ trellis_status trellis_adapters(const uint16_t *x, int32_t m, const uint32_t *co
   p.n = g.n;
   p.k = g.k;
   p.low = LowRank{index, b, t, count, rank, rank_p};
-  return run(s, kForward, g, p, w->bytes + t_bytes + hp, stream);
+  return run(s, kForward, g, p, nullptr, w->bytes + t_bytes + hp, stream);
 }
 
 trellis_status trellis_adapters_backward(const uint16_t *dout, const uint16_t *x, int32_t m, const uint32_t *codes,
@@ -1498,7 +1519,7 @@ trellis_status trellis_adapters_backward(const uint16_t *dout, const uint16_t *x
   p.n = g.n;
   p.k = g.k;
   p.low = LowRank{index, a, u, count, rank, rank_p};
-  TRELLIS_TRY(run(s, kTransposed, g, p, reinterpret_cast<unsigned char *>(partials), stream));
+  TRELLIS_TRY(run(s, kTransposed, g, p, nullptr, reinterpret_cast<unsigned char *>(partials), stream));
   Outer o{x, dout, u, t, index, range, da, db, m, g.n, g.k, rank, rank_p, g.k / 64};
   hipLaunchKernelGGL(outer_kernel, dim3((unsigned)(o.tiles_a + (g.n + 63) / 64), (unsigned)count, (unsigned)(rank_p / 32)),
                      dim3(256), 0, stream, o);
@@ -1534,7 +1555,7 @@ trellis_status trellis_gated(const uint16_t *x, int32_t m, const uint32_t *codes
   p.m = m;
   p.n = g.n;
   p.k = g.k;
-  return run(s, kGated, g, p, w->bytes, stream);
+  return run(s, kGated, g, p, nullptr, w->bytes, stream);
 }
 
 trellis_status trellis_gated_backward(const uint16_t *dh, const uint16_t *gate, const uint16_t *up, int32_t m,
@@ -1555,11 +1576,7 @@ trellis_status trellis_gated_backward(const uint16_t *dh, const uint16_t *gate, 
   const Plan s = plan_of(kTransposed, g, m, 2, cus);
   Space *w = nullptr;
   TRELLIS_TRY(space(dev, stream, s.bytes, (size_t)s.counters, w));
-  const int64_t quads = (int64_t)m * (g.n / 4);
-  (void)hipGetLastError();
-  hipLaunchKernelGGL(gated_grad_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream, dh, gate, up, quads,
-                     dgate, dup);
-  if (hipGetLastError() != hipSuccess) return TRELLIS_E_HIP;
+  const GatedGrads grads{dh, gate, up, dgate, dup};
   Product p{};
   p.p = dgate;
   p.p2 = dup;
@@ -1572,7 +1589,7 @@ trellis_status trellis_gated_backward(const uint16_t *dh, const uint16_t *gate, 
   p.m = m;
   p.n = g.n;
   p.k = g.k;
-  return run(s, kTransposed, g, p, w->bytes, stream);
+  return run(s, kTransposed, g, p, &grads, w->bytes, stream);
 }
 
 }  // extern "C"
