@@ -65,7 +65,7 @@ struct Product {
   uint16_t *out, *gate, *up;       // gate, up: gated only, null where they are not kept
   float *partials;
   uint32_t *counters;
-  int64_t units;     // tiles * steps
+  int32_t units_q, units_r;  // units (tiles * steps) of a workgroup: units_q, the first units_r one more
   int32_t m, n, k;
   int32_t groups;    // groups of output columns
   int32_t steps;     // contraction steps of a tile (all matrices)
@@ -76,10 +76,13 @@ struct Product {
 // The adapters' term of one 16-row tile and a wave's NT column tiles: for every
 // adapter that the rows name, the product of t's rows (as the sum of two bf16
 // numbers, 2^-16 relative) with the factor, kept only in the rows that name
-// it, so an adapter's infinities and NaNs stay in its own rows.
+// it, so an adapter's infinities and NaNs stay in its own rows. Several
+// adapters' operands are loaded before the first is multiplied: one at a time
+// cost about a microsecond each.
 // load(a, r0, w): the NT operands for rank columns r0 .. +7.
 template <int NT, typename Load>
 __device__ __forceinline__ void low_rank_tile(const LowRank &L, int m, int m0, int lane, f32x4 (&sum)[NT], Load load) {
+  constexpr int B = NT == 4 ? 2 : 4;  // adapters at a time
   const int j = lane & 15, g = lane >> 4;
 #pragma unroll
   for (int i = 0; i < NT; ++i) sum[i] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -87,38 +90,42 @@ __device__ __forceinline__ void low_rank_tile(const LowRank &L, int m, int m0, i
   const int rowc = row < m ? row : m - 1;
   int idx = row < m ? L.index[row] : -1;
   if (idx >= L.count) idx = -1;
-  int of[4];
+  const uint64_t named = __ballot(idx >= 0) & 0xFFFFull;
+  for (int r0 = 0; r0 < L.rank_p; r0 += 32) {
+    const float *tp = L.t + (int64_t)rowc * L.rank_p + r0 + 8 * g;
+    const f32x4 t0 = *reinterpret_cast<const f32x4 *>(tp), t1 = *reinterpret_cast<const f32x4 *>(tp + 4);
+    bf16x8 hi, lo;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) of[e] = __shfl(idx, 4 * g + e);
-  uint64_t left = __ballot(idx >= 0) & 0xFFFFull;
-  while (left) {
-    const int a = __builtin_amdgcn_readlane(idx, __builtin_ctzll(left));
-    left &= ~__ballot(idx == a);
-    f32x4 d[NT];
-#pragma unroll
-    for (int i = 0; i < NT; ++i) d[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int r0 = 0; r0 < L.rank_p; r0 += 32) {
-      const float *tp = L.t + (int64_t)rowc * L.rank_p + r0 + 8 * g;
-      const f32x4 t0 = *reinterpret_cast<const f32x4 *>(tp), t1 = *reinterpret_cast<const f32x4 *>(tp + 4);
-      bf16x8 hi, lo;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float v = e < 4 ? t0[e] : t1[e - 4];
-        hi[e] = (__bf16)v;
-        lo[e] = (__bf16)(v - (float)hi[e]);
-      }
-      bf16x8 w[NT];
-      load(a, r0 + 8 * g, w);
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        d[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, w[i], d[i], 0, 0, 0);
-        d[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, w[i], d[i], 0, 0, 0);
-      }
+    for (int e = 0; e < 8; ++e) {
+      const float v = e < 4 ? t0[e] : t1[e - 4];
+      hi[e] = (__bf16)v;
+      lo[e] = (__bf16)(v - (float)hi[e]);
     }
+    for (uint64_t left = named; left;) {
+      uint32_t rows[B];
+      bf16x8 w[B][NT];
+      int a = 0;
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+      for (int b = 0; b < B; ++b) {
+        rows[b] = 0;  // none left: the operands again, for no row
+        if (left) {
+          a = __builtin_amdgcn_readlane(idx, __builtin_ctzll(left));
+          rows[b] = (uint32_t)__ballot(idx == a) & 0xFFFFu;
+          left &= ~(uint64_t)rows[b];
+        }
+        load(a, r0 + 8 * g, w[b]);
+      }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sum[i][e] += of[e] == a ? d[i][e] : 0.f;
+      for (int b = 0; b < B; ++b)
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          f32x4 d = {0.f, 0.f, 0.f, 0.f};
+          d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, w[b][i], d, 0, 0, 0);
+          d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, w[b][i], d, 0, 0, 0);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum[i][e] += (rows[b] >> (4 * g + e)) & 1 ? d[e] : 0.f;
+        }
+    }
   }
 }
 
@@ -246,98 +253,237 @@ __global__ __launch_bounds__(kThreads, OCC) void product_kernel(Product P) {
   constexpr int RC = kT ? 128 : 64 * NT;                        // columns reduced per round
   constexpr int wpb = 8 * BITS;
   constexpr int kRounds = kT ? 2 : 1;
-  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
-  unsigned char *const table = lds;
-  unsigned char *const xs = lds + kTableBytes;  // two buffers of BM rows
+  // The table is static LDS, so its reads carry the base in the instruction.
+  __shared__ __attribute__((aligned(16))) uint32_t s_table[kTableBytes / 4];
+  __shared__ uint32_t arrived[2];
+  extern __shared__ __attribute__((aligned(16))) unsigned char xs[];  // two buffers of BM rows
+  const unsigned char *const table = reinterpret_cast<const unsigned char *>(s_table);
   // transposed: two buffers of 256 row constants (q, k) and scales, and the
   // buffers' flags of scales outside the exact range, one per wave
   f32x2 *const rowq = reinterpret_cast<f32x2 *>(xs + 2 * BM * kStride);
   float *const rows_s = reinterpret_cast<float *>(rowq + 512);
   uint32_t *const rowf = reinterpret_cast<uint32_t *>(rows_s + 512);
-  uint32_t *const arrived = kT ? rowf + 8 : reinterpret_cast<uint32_t *>(rowq);
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = wave & 3, wk = wave >> 2;
   const int j = lane & 15, g = lane >> 4;
-#pragma unroll
-  for (int i = 0; i < 2048 / kThreads; ++i)
-    reinterpret_cast<uint32_t *>(table)[i * kThreads + tid] = code_entry_pair((uint32_t)(i * kThreads + tid));
 
   const uint32_t row_bytes = (uint32_t)(P.k >> 8) * wpb * 4;
   const int cols = kT ? P.n : P.k;  // columns of P
-  const int64_t first = P.units * blockIdx.x / gridDim.x, end = P.units * (blockIdx.x + 1) / gridDim.x;
-  int64_t unit = first;
-  while (unit < end) {
-    const int64_t tile = unit / P.steps;
-    const int s0 = (int)(unit - tile * P.steps);
-    const int s1 = (int)(end - unit < P.steps - s0 ? s0 + (end - unit) : P.steps);
-    const int chunk = (int)(tile / P.groups), group = (int)(tile - (int64_t)chunk * P.groups);
-    const int m0 = chunk * BM;
-    f32x4 acc[MT][NT];
-#pragma unroll
-    for (int a = 0; a < MT; ++a)
-#pragma unroll
-      for (int b = 0; b < NT; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto start_of = [&](int c) { return c * P.units_q + (c < P.units_r ? c : P.units_r); };
+  int unit = start_of(blockIdx.x);
+  const int end = start_of(blockIdx.x + 1);
+  // The current segment: steps s0 .. s1 - 1 of a tile.
+  int tile = unit / P.steps, s0 = unit - tile * P.steps, s1 = end - unit < P.steps - s0 ? s0 + (end - unit) : P.steps;
+  int m0 = tile / P.groups * BM, group = tile % P.groups;
 
-    // Staged rows of P: thread t takes 8 columns of row t / 32 + 16 r.
-    // (The last step stages itself again: straight-line code keeps xv in
-    // registers and the memory waits exact.)
-    u32x4 xv[MT];
-    float sv = 0.f;
-    const uint32_t row_b = (uint32_t)cols * 2;
+  // Staged rows of P: thread t takes 8 columns of row t / 32 + 16 r.
+  // (The last step stages itself again: straight-line code keeps xv in
+  // registers and the memory waits exact.)
+  u32x4 xv[MT];
+  float sv = 0.f;
+  const uint32_t row_b = (uint32_t)cols * 2;
+  const uint32_t xoff = (uint32_t)(tid >> 5) * row_b + (uint32_t)(tid & 31) * 16;
+  auto fetch = [&](int s) {
+    const bool second = kT && s >= P.steps1;
+    const int at = second ? s - P.steps1 : s;
     const uint32_t valid_b = (uint32_t)(P.m - m0 < BM ? P.m - m0 : BM) * row_b;
-    const uint32_t xoff = (uint32_t)(tid >> 5) * row_b + (uint32_t)(tid & 31) * 16;
-    auto fetch = [&](int s) {
-      const bool second = kT && s >= P.steps1;
-      const int at = second ? s - P.steps1 : s;
-      // rows past m lie outside the buffer and read as zero
-      const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-          const_cast<uint16_t *>((second ? P.p2 : P.p) + (int64_t)m0 * cols + (int64_t)at * kStep), (short)0,
-          (int)(valid_b - (uint32_t)at * (kStep * 2)), kRawBuffer);
-      // transposed: so do columns past N (rows start at multiples of 8 bytes)
-      const int left = cols - at * kStep - (tid & 31) * 8;
+    // rows past m lie outside the buffer and read as zero
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint16_t *>((second ? P.p2 : P.p) + (int64_t)m0 * cols + (int64_t)at * kStep), (short)0,
+        (int)(valid_b - (uint32_t)at * (kStep * 2)), kRawBuffer);
+    // transposed: so do columns past N (rows start at multiples of 8 bytes)
+    const int left = cols - at * kStep - (tid & 31) * 8;
 #pragma unroll
-      for (int r = 0; r < MT; ++r) {
-        const uint32_t o = xoff + (uint32_t)(16 * r) * row_b;
-        if constexpr (!kT) {
-          xv[r] = __builtin_amdgcn_raw_buffer_load_b128(rs, o, 0, 0);
+    for (int r = 0; r < MT; ++r) {
+      const uint32_t o = xoff + (uint32_t)(16 * r) * row_b;
+      if constexpr (!kT) {
+        xv[r] = __builtin_amdgcn_raw_buffer_load_b128(rs, o, 0, 0);
+      } else {
+        const u32x2 a = __builtin_amdgcn_raw_buffer_load_b64(rs, left > 0 ? o : 0x80000000u, 0, 0);
+        const u32x2 b = __builtin_amdgcn_raw_buffer_load_b64(rs, left > 4 ? o + 8 : 0x80000000u, 0, 0);
+        xv[r] = u32x4{a[0], a[1], b[0], b[1]};
+      }
+    }
+    if constexpr (kT) {
+      const int row = at * kStep + tid;
+      sv = tid < 256 && row < P.n ? bf16_bits_to_f32((second ? P.scales2 : P.scales)[row]) : 0.f;
+    }
+  };
+  auto put = [&](int s) {
+    unsigned char *dst = xs + (s & 1) * BM * kStride;
+#pragma unroll
+    for (int r = 0; r < MT; ++r)
+      *reinterpret_cast<u32x4 *>(dst + (r * 16 + (tid >> 5)) * kStride + (tid & 31) * 16) = xv[r];
+    if constexpr (kT) {
+      if (tid < 256) {
+        float q, k;
+        alu_row_constants(sv, q, k);
+        rowq[(s & 1) * 256 + tid] = f32x2{q, k};
+        rows_s[(s & 1) * 256 + tid] = sv;
+        const bool out = !__all(alu_scale_ok(sv));
+        if (lane == 0) rowf[(s & 1) * 4 + wave] = out;
+      }
+    }
+  };
+  // Reduction of a finished segment (tile, steps a0 .. a1 - 1), and its store.
+  constexpr int kPart = BM * RC * kRounds;  // floats of a tile's partial
+  float *const red = reinterpret_cast<float *>(xs);
+  // columns of P.out handled per round, and the store of four sums
+  auto finish = [&](int am0, int agroup, int row, int c, f32x4 v, f32x4 v2) {
+    const int mrow = am0 + row;
+    if (mrow >= P.m) return;
+    if constexpr (KIND == kGated) {
+      const int n = agroup * BN + c;
+      if (n >= P.n) return;
+      const int64_t o = (int64_t)mrow * P.n + n;
+      f32x4 h;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) h[e] = silu_mul(v[e], v2[e]);
+      store4(P.out + o, h);
+      if (P.gate) store4(P.gate + o, v);
+      if (P.up) store4(P.up + o, v2);
+    } else {
+      const int width = kT ? P.k : P.n, n = agroup * BN + c;
+      if (n >= width) return;
+      store4(P.out + (int64_t)mrow * width + n, v);
+    }
+  };
+  f32x4 acc[MT][NT];
+  auto reduce = [&](int a0, int a1, int am0, int agroup) {
+    // The two wk halves meet in LDS, [wk][row][128 columns]; then each thread
+    // takes four columns of a row at a time.
+    // (The thread's number goes through an empty asm here, so that nothing of
+    // this part is computed ahead and kept in registers through the steps.)
+    int et = tid;
+    asm volatile("" : "+v"(et));
+    const int ej = et & 15, eg = (et >> 4) & 3;
+    const bool whole = a0 == 0 && a1 == P.steps;
+    const int64_t slot = 2 * (int64_t)blockIdx.x + (a0 == 0 ? 1 : 0);
+    for (int round = 0; round < kRounds; ++round) {
+      if (round) lds_barrier();
+      if (!kT || (wn >> 1) == round) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float *r = red + (wk * BM + mt * 16 + 4 * eg + e) * kRedStride;
+            if constexpr (kT) {
+              *reinterpret_cast<f32x4 *>(r + 64 * (wn & 1) + 4 * ej) =
+                  f32x4{acc[mt][0][e], acc[mt][1][e], acc[mt][2][e], acc[mt][3][e]};
+            } else {
+#pragma unroll
+              for (int i = 0; i < NT; ++i)
+                r[KIND == kGated ? 64 * i + 16 * wn + ej : 16 * NT * wn + 16 * i + ej] = acc[mt][i][e];
+            }
+          }
+        // The adapters' term joins the sums of the wave that holds the tile's
+        // last step, half of the row tiles in each wk.
+        if (KIND != kGated && a1 == P.steps && P.low.rank > 0) {
+          for (int mt = wk; mt < MT && am0 + 16 * mt < P.m; mt += 2) {
+            f32x4 term[NT];
+            low_rank_tile<NT>(P.low, P.m, am0 + 16 * mt, et & 63, term, [&](int a, int r0, bf16x8 (&w)[NT]) {
+              if constexpr (kT) {
+                const int k0 = agroup * BN + 64 * wn + 4 * ej;
+                typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  bf16x4 v = {};
+                  if (r0 + e < P.low.rank)
+                    v = *reinterpret_cast<const bf16x4 *>(P.low.factor + ((int64_t)a * P.low.rank + r0 + e) * P.k + k0);
+#pragma unroll
+                  for (int c = 0; c < 4; ++c) w[c][e] = v[c];
+                }
+              } else {
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                  const int n = agroup * BN + 16 * NT * wn + 16 * i + ej;
+                  const uint16_t *q = P.low.factor + ((int64_t)a * P.n + n) * P.low.rank + r0;
+                  if ((P.low.rank & 7) == 0) {
+                    w[i] = bf16x8{};
+                    if (n < P.n && r0 < P.low.rank) w[i] = *reinterpret_cast<const bf16x8 *>(q);
+                  } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                      w[i][e] = __builtin_bit_cast(__bf16, n < P.n && r0 + e < P.low.rank ? q[e] : (uint16_t)0);
+                  }
+                }
+              }
+            });
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float *r = red + (wk * BM + mt * 16 + 4 * eg + e) * kRedStride;
+              if constexpr (kT) {
+                f32x4 *v = reinterpret_cast<f32x4 *>(r + 64 * (wn & 1) + 4 * ej);
+                *v += f32x4{term[0][e], term[1][e], term[2][e], term[3][e]};
+              } else {
+#pragma unroll
+                for (int i = 0; i < NT; ++i) r[16 * NT * wn + 16 * i + ej] += term[i][e];
+              }
+            }
+          }
+        }
+      }
+      lds_barrier();
+      if (whole && KIND == kGated) {
+        for (int q = et; q < BM * 16; q += kThreads) {
+          const int row = q >> 4, c = (q & 15) * 4;
+          const f32x4 *r0 = reinterpret_cast<const f32x4 *>(red + row * kRedStride + c);
+          const f32x4 *r1 = reinterpret_cast<const f32x4 *>(red + (BM + row) * kRedStride + c);
+          finish(am0, agroup, row, c, r0[0] + r1[0], r0[16] + r1[16]);
+        }
+      } else {
+        const __amdgpu_buffer_rsrc_t ws =
+            __builtin_amdgcn_make_buffer_rsrc(P.partials + slot * kPart, (short)0, kPart * 4, kRawBuffer);
+        for (int q = et; q < BM * (RC / 4); q += kThreads) {
+          const int row = q / (RC / 4), c = (q % (RC / 4)) * 4;
+          const f32x4 v = *reinterpret_cast<const f32x4 *>(red + row * kRedStride + c) +
+                          *reinterpret_cast<const f32x4 *>(red + (BM + row) * kRedStride + c);
+          if (whole) finish(am0, agroup, row, round * RC + c, v, v);
+          else
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), ws,
+                                                   (uint32_t)((round * BM + row) * RC + c) * 4, 0, kSc1);
+        }
+      }
+    }
+  };
+  // Tiles shared with other workgroups: at most a range's first and its last.
+  int shared0 = -1, shared1 = -1;
+  if constexpr (!kT) {
+    float sc[NT];
+    uint16_t sb[NT];  // the rows' scales as loaded
+    const unsigned char *base[NT];
+    uint32_t size[NT];
+    const int wb = 2 * BITS * g + BITS * (1 - wk);
+    const uint32_t off = (uint32_t)j * row_bytes + 4 * wb, off_next = (uint32_t)j * row_bytes + 4 * ((wb + BITS) % wpb);
+    struct Words {
+      uint32_t d[NT][BITS + 1];
+    };
+    auto load = [&](int s, Words &W) {
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        // rows past N lie outside the buffer and read as zero
+        const uint32_t blk = (uint32_t)s * (wpb * 4);
+        const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<unsigned char *>(base[i] + blk), (short)0, (int)(size[i] ? size[i] - blk : 0u), kRawBuffer);
+        if constexpr (BITS == 4) {
+          const auto v = __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0);
+#pragma unroll
+          for (int b = 0; b < 4; ++b) W.d[i][b] = v[b];
+        } else if constexpr (BITS == 2) {
+          const auto v = __builtin_amdgcn_raw_buffer_load_b64(rs, off, 0, 0);
+          W.d[i][0] = v[0];
+          W.d[i][1] = v[1];
         } else {
-          const u32x2 a = __builtin_amdgcn_raw_buffer_load_b64(rs, left > 0 ? o : 0x80000000u, 0, 0);
-          const u32x2 b = __builtin_amdgcn_raw_buffer_load_b64(rs, left > 4 ? o + 8 : 0x80000000u, 0, 0);
-          xv[r] = u32x4{a[0], a[1], b[0], b[1]};
-        }
-      }
-      if constexpr (kT) {
-        const int row = at * kStep + tid;
-        sv = tid < 256 && row < P.n ? bf16_bits_to_f32((second ? P.scales2 : P.scales)[row]) : 0.f;
-      }
-    };
-    auto put = [&](int s) {
-      unsigned char *dst = xs + (s & 1) * BM * kStride;
 #pragma unroll
-      for (int r = 0; r < MT; ++r)
-        *reinterpret_cast<u32x4 *>(dst + (r * 16 + (tid >> 5)) * kStride + (tid & 31) * 16) = xv[r];
-      if constexpr (kT) {
-        if (tid < 256) {
-          float q, k;
-          alu_row_constants(sv, q, k);
-          rowq[(s & 1) * 256 + tid] = f32x2{q, k};
-          rows_s[(s & 1) * 256 + tid] = sv;
-          const bool out = !__all(alu_scale_ok(sv));
-          if (lane == 0) rowf[(s & 1) * 4 + wave] = out;
+          for (int b = 0; b < BITS; ++b) W.d[i][b] = __builtin_amdgcn_raw_buffer_load_b32(rs, off + 4 * b, 0, 0);
         }
+        W.d[i][BITS] = __builtin_amdgcn_raw_buffer_load_b32(rs, off_next, 0, 0);
       }
     };
-    __syncthreads();  // the previous tile's reduction is done with this space
-    fetch(s0);
-
-    if constexpr (!kT) {
-      float sc[NT], q[NT], kq[NT];
-      bool exact = true;
-      const unsigned char *base[NT];
-      uint32_t size[NT];
-      const int wb = 2 * BITS * g + BITS * (1 - wk);
-      const uint32_t off = (uint32_t)j * row_bytes + 4 * wb, off_next = (uint32_t)j * row_bytes + 4 * ((wb + BITS) % wpb);
+    Words A, B;
+    auto request = [&]() {
+      fetch(s0);
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
         const int n0 = KIND == kGated ? group * BN + 16 * wn : group * BN + 16 * NT * wn + 16 * i;
@@ -346,38 +492,26 @@ __global__ __launch_bounds__(kThreads, OCC) void product_kernel(Product P) {
         const int rows = P.n - n0 < 0 ? 0 : P.n - n0 < 16 ? P.n - n0 : 16;
         base[i] = reinterpret_cast<const unsigned char *>(c) + (int64_t)n0 * row_bytes;
         size[i] = (uint32_t)rows * row_bytes;
-        sc[i] = j < rows ? bf16_bits_to_f32(sp[n0 + j]) : 0.f;
+        const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t *>(sp + n0), (short)0, rows * 2, kRawBuffer);
+        sb[i] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, (uint32_t)j * 2, 0, 0);
       }
-      struct Words {
-        uint32_t d[NT][BITS + 1];
-      };
-      auto load = [&](int s, Words &W) {
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          // rows past N lie outside the buffer and read as zero
-          const uint32_t blk = (uint32_t)s * (wpb * 4);
-          const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-              const_cast<unsigned char *>(base[i] + blk), (short)0, (int)(size[i] ? size[i] - blk : 0u), kRawBuffer);
-          if constexpr (BITS == 4) {
-            const auto v = __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0);
-#pragma unroll
-            for (int b = 0; b < 4; ++b) W.d[i][b] = v[b];
-          } else if constexpr (BITS == 2) {
-            const auto v = __builtin_amdgcn_raw_buffer_load_b64(rs, off, 0, 0);
-            W.d[i][0] = v[0];
-            W.d[i][1] = v[1];
-          } else {
-#pragma unroll
-            for (int b = 0; b < BITS; ++b) W.d[i][b] = __builtin_amdgcn_raw_buffer_load_b32(rs, off + 4 * b, 0, 0);
-          }
-          W.d[i][BITS] = __builtin_amdgcn_raw_buffer_load_b32(rs, off_next, 0, 0);
-        }
-      };
-      Words A, B;
       load(s0, A);
       load(s0 + 1 < s1 ? s0 + 1 : s0, B);
+    };
+    request();
+    // The table, while the first loads are on their way.
+  #pragma unroll
+    for (int i = 0; i < 2048 / kThreads; ++i) s_table[i * kThreads + tid] = code_entry_pair((uint32_t)(i * kThreads + tid));
+      for (;;) {
+#pragma unroll
+      for (int a = 0; a < MT; ++a)
+#pragma unroll
+        for (int b = 0; b < NT; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+      float q[NT], kq[NT];
+      bool exact = true;
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
+        sc[i] = bf16_bits_to_f32(sb[i]);
         alu_row_constants(sc[i], q[i], kq[i]);
         exact = exact && alu_scale_ok(sc[i]);
       }
@@ -435,39 +569,71 @@ __global__ __launch_bounds__(kThreads, OCC) void product_kernel(Product P) {
       };
       if (chain) steps(std::true_type{});
       else steps(std::false_type{});
-    } else {
-      // Lane (j, g) decodes columns 64 wn + 4 j .. +3 of the block for rows
-      // 8 g .. 8 g + 7 of each 32-row MFMA part: the lowest of the four
-      // windows starts at stream bit (252 - 64 wn - 4 j) * BITS, the others
-      // BITS apart, 3 BITS + 12 <= 24 bits in all.
-      const int pos = (252 - 64 * wn - 4 * j) * BITS;
-      const uint32_t w0 = (uint32_t)(pos >> 5), sh = (uint32_t)(pos & 31);
-      const uint32_t row0 = (uint32_t)(128 * wk + 8 * g) * row_bytes;
-      const uint32_t o_lo = row0 + 4 * w0, o_hi = row0 + 4 * ((w0 + 1) % wpb);
-      struct Words {
-        uint32_t lo[8], hi[8];
-      };
+      // The next segment is requested before this one is reduced.
+      const int a0 = s0, a1 = s1, am0 = m0, agroup = group, at = tile;
+      unit += s1 - s0;
+      const bool more = unit < end;
+      if (more) {
+        tile = unit / P.steps;
+        s0 = unit - tile * P.steps;
+        s1 = end - unit < P.steps - s0 ? s0 + (end - unit) : P.steps;
+        m0 = tile / P.groups * BM;
+        group = tile % P.groups;
+        request();
+      }
+      if (a0 > 0 || a1 < P.steps) {
+        if (shared0 < 0) shared0 = at;
+        else shared1 = at;
+      }
+      reduce(a0, a1, am0, agroup);
+      if (!more) break;
+      lds_barrier();  // the reduction is done with P's space
+    }
+  } else {
+    // Lane (j, g) decodes columns 64 wn + 4 j .. +3 of the block for rows
+    // 8 g .. 8 g + 7 of each 32-row MFMA part: the lowest of the four
+    // windows starts at stream bit (252 - 64 wn - 4 j) * BITS, the others
+    // BITS apart, 3 BITS + 12 <= 24 bits in all.
+    const int pos = (252 - 64 * wn - 4 * j) * BITS;
+    const uint32_t w0 = (uint32_t)(pos >> 5), sh = (uint32_t)(pos & 31);
+    const uint32_t row0 = (uint32_t)(128 * wk + 8 * g) * row_bytes;
+    const uint32_t o_lo = row0 + 4 * w0, o_hi = row0 + 4 * ((w0 + 1) % wpb);
+    struct Words {
+      uint32_t lo[8], hi[8];
+    };
+    auto load = [&](int part, Words &W) {
       const int parts = 4 * (s1 - s0);
-      auto load = [&](int part, Words &W) {
-        if (part >= parts) part = parts - 1;
-        const int s = s0 + (part >> 2);
-        const bool second = s >= P.steps1;
-        const int n0 = (second ? s - P.steps1 : s) * kStep;
-        const int rows = P.n - n0 < kStep ? P.n - n0 : kStep;
-        const unsigned char *base = reinterpret_cast<const unsigned char *>(second ? P.codes2 : P.codes) +
-                                    (int64_t)n0 * row_bytes + (int64_t)group * wpb * 4;
-        // rows past N lie outside the buffer and read as zero
-        const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<unsigned char *>(base), (short)0, (int)((uint32_t)rows * row_bytes - (uint32_t)group * wpb * 4), kRawBuffer);
-        const uint32_t ro = (uint32_t)(32 * (part & 3)) * row_bytes;
+      if (part >= parts) part = parts - 1;
+      const int s = s0 + (part >> 2);
+      const bool second = s >= P.steps1;
+      const int n0 = (second ? s - P.steps1 : s) * kStep;
+      const int rows = P.n - n0 < kStep ? P.n - n0 : kStep;
+      const unsigned char *base = reinterpret_cast<const unsigned char *>(second ? P.codes2 : P.codes) +
+                                  (int64_t)n0 * row_bytes + (int64_t)group * wpb * 4;
+      // rows past N lie outside the buffer and read as zero
+      const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+          const_cast<unsigned char *>(base), (short)0, (int)((uint32_t)rows * row_bytes - (uint32_t)group * wpb * 4), kRawBuffer);
+      const uint32_t ro = (uint32_t)(32 * (part & 3)) * row_bytes;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          W.lo[e] = __builtin_amdgcn_raw_buffer_load_b32(rs, o_lo + ro + (uint32_t)e * row_bytes, 0, 0);
-          W.hi[e] = __builtin_amdgcn_raw_buffer_load_b32(rs, o_hi + ro + (uint32_t)e * row_bytes, 0, 0);
-        }
-      };
-      Words W;
+      for (int e = 0; e < 8; ++e) {
+        W.lo[e] = __builtin_amdgcn_raw_buffer_load_b32(rs, o_lo + ro + (uint32_t)e * row_bytes, 0, 0);
+        W.hi[e] = __builtin_amdgcn_raw_buffer_load_b32(rs, o_hi + ro + (uint32_t)e * row_bytes, 0, 0);
+      }
+    };
+    Words W;
+    auto request = [&]() {
+      fetch(s0);
       load(0, W);
+    };
+    request();
+    // The table, while the first loads are on their way.
+#pragma unroll
+    for (int i = 0; i < 2048 / kThreads; ++i) s_table[i * kThreads + tid] = code_entry_pair((uint32_t)(i * kThreads + tid));
+      for (;;) {
+#pragma unroll
+      for (int a = 0; a < MT; ++a)
+#pragma unroll
+        for (int b = 0; b < NT; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
       put(s0);
       lds_barrier();
       auto compute = [&](int part, bool chain) {
@@ -528,166 +694,82 @@ __global__ __launch_bounds__(kThreads, OCC) void product_kernel(Product P) {
         put(s + 1);
         lds_barrier();
       }
+      // The next segment is requested before this one is reduced.
+      const int a0 = s0, a1 = s1, am0 = m0, agroup = group, at = tile;
+      unit += s1 - s0;
+      const bool more = unit < end;
+      if (more) {
+        tile = unit / P.steps;
+        s0 = unit - tile * P.steps;
+        s1 = end - unit < P.steps - s0 ? s0 + (end - unit) : P.steps;
+        m0 = tile / P.groups * BM;
+        group = tile % P.groups;
+        request();
+      }
+      if (a0 > 0 || a1 < P.steps) {
+        if (shared0 < 0) shared0 = at;
+        else shared1 = at;
+      }
+      reduce(a0, a1, am0, agroup);
+      if (!more) break;
+      lds_barrier();  // the reduction is done with P's space
     }
+  }
 
-    // The two wk halves meet in LDS, [wk][row][128 columns]; then each thread
-    // takes four columns of a row at a time.
-    // (The thread's number goes through an empty asm here, so that nothing of
-    // this part is computed ahead and kept in registers through the steps.)
-    int et = tid;
-    asm volatile("" : "+v"(et));
-    const int ej = et & 15, eg = (et >> 4) & 3;
-    const bool whole = s0 == 0 && s1 == P.steps;
-    float *const red = reinterpret_cast<float *>(xs);
-    // columns of P.out handled per round, and the store of four sums
-    auto finish = [&](int row, int c, f32x4 v, f32x4 v2) {
-      const int mrow = m0 + row;
-      if (mrow >= P.m) return;
-      if constexpr (KIND == kGated) {
-        const int n = group * BN + c;
-        if (n >= P.n) return;
-        const int64_t o = (int64_t)mrow * P.n + n;
-        f32x4 h;
+  // Shared tiles: once this workgroup's partials are complete at the coherent
+  // level its tiles' counters move; the workgroup that arrives last at a tile
+  // adds the partials in order and stores the tile.
+  if (shared0 < 0) return;
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  if (tid < 2) {
+    const int t = tid ? shared1 : shared0;
+    if (t >= 0) arrived[tid] = __hip_atomic_fetch_add(&P.counters[t], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  // the workgroup that holds unit u
+  auto owner = [&](int u) {
+    const int cut = P.units_r * (P.units_q + 1);
+    return u < cut ? u / (P.units_q + 1) : P.units_r + (u - cut) / P.units_q;
+  };
+  for (int i = 0; i < 2; ++i) {
+    const int t = i ? shared1 : shared0;
+    if (t < 0) continue;
+    const int c0 = owner(t * P.steps), c1 = owner(t * P.steps + P.steps - 1);
+    if (arrived[i] != (uint32_t)(c1 - c0)) continue;
+    if (tid == 0) __hip_atomic_store(&P.counters[t], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const int tm0 = t / P.groups * BM, tgroup = t % P.groups;
+    // The tile's first workgroup keeps its partial in its second slot (the
+    // tile is where its range ends), the others in their first. Four loads at
+    // a time; those past the last lie outside the buffer and give zero.
+    const __amdgpu_buffer_rsrc_t ws = __builtin_amdgcn_make_buffer_rsrc(
+        P.partials + (int64_t)(2 * c0 + 1) * kPart, (short)0, (2 * (c1 - c0) + 1) * kPart * 4, kRawBuffer);
+    auto sum = [&](int at) {
+      f32x4 v = {0.f, 0.f, 0.f, 0.f};
+      for (int c = c0; c <= c1; c += 4) {
+        f32x4 p[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) h[e] = silu_mul(v[e], v2[e]);
-        store4(P.out + o, h);
-        if (P.gate) store4(P.gate + o, v);
-        if (P.up) store4(P.up + o, v2);
-      } else {
-        const int width = kT ? P.k : P.n, n = group * BN + c;
-        if (n >= width) return;
-        store4(P.out + (int64_t)mrow * width + n, v);
+        for (int u = 0; u < 4; ++u) {
+          const uint32_t slot = c + u == c0 ? 0u : (uint32_t)(2 * (c + u - c0) - 1);
+          p[u] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                               ws, c + u <= c1 ? (slot * kPart + (uint32_t)at) * 4 : 0x80000000u, 0, kSc1));
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) v += p[u];
       }
+      return v;
     };
-    constexpr int kPart = BM * RC * kRounds;  // floats of a tile's partial
-    const int64_t slot = 2 * (int64_t)blockIdx.x + (s0 == 0 ? 1 : 0);
-    for (int round = 0; round < kRounds; ++round) {
-      if (round) __syncthreads();
-      if (!kT || (wn >> 1) == round) {
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float *r = red + (wk * BM + mt * 16 + 4 * eg + e) * kRedStride;
-            if constexpr (kT) {
-              *reinterpret_cast<f32x4 *>(r + 64 * (wn & 1) + 4 * ej) =
-                  f32x4{acc[mt][0][e], acc[mt][1][e], acc[mt][2][e], acc[mt][3][e]};
-            } else {
-#pragma unroll
-              for (int i = 0; i < NT; ++i)
-                r[KIND == kGated ? 64 * i + 16 * wn + ej : 16 * NT * wn + 16 * i + ej] = acc[mt][i][e];
-            }
-          }
-        // The adapters' term joins the sums of the wave that holds the tile's
-        // last step, half of the row tiles in each wk.
-        if (KIND != kGated && s1 == P.steps && P.low.rank > 0) {
-          for (int mt = wk; mt < MT && m0 + 16 * mt < P.m; mt += 2) {
-            f32x4 term[NT];
-            low_rank_tile<NT>(P.low, P.m, m0 + 16 * mt, et & 63, term, [&](int a, int r0, bf16x8 (&w)[NT]) {
-              if constexpr (kT) {
-                const int k0 = group * BN + 64 * wn + 4 * ej;
-                typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  bf16x4 v = {};
-                  if (r0 + e < P.low.rank)
-                    v = *reinterpret_cast<const bf16x4 *>(P.low.factor + ((int64_t)a * P.low.rank + r0 + e) * P.k + k0);
-#pragma unroll
-                  for (int c = 0; c < 4; ++c) w[c][e] = v[c];
-                }
-              } else {
-#pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                  const int n = group * BN + 16 * NT * wn + 16 * i + ej;
-                  const uint16_t *q = P.low.factor + ((int64_t)a * P.n + n) * P.low.rank + r0;
-                  if ((P.low.rank & 7) == 0) {
-                    w[i] = bf16x8{};
-                    if (n < P.n && r0 < P.low.rank) w[i] = *reinterpret_cast<const bf16x8 *>(q);
-                  } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                      w[i][e] = __builtin_bit_cast(__bf16, n < P.n && r0 + e < P.low.rank ? q[e] : (uint16_t)0);
-                  }
-                }
-              }
-            });
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float *r = red + (wk * BM + mt * 16 + 4 * eg + e) * kRedStride;
-              if constexpr (kT) {
-                f32x4 *v = reinterpret_cast<f32x4 *>(r + 64 * (wn & 1) + 4 * ej);
-                *v += f32x4{term[0][e], term[1][e], term[2][e], term[3][e]};
-              } else {
-#pragma unroll
-                for (int i = 0; i < NT; ++i) r[16 * NT * wn + 16 * i + ej] += term[i][e];
-              }
-            }
-          }
-        }
+    if constexpr (KIND == kGated) {
+      for (int q = tid; q < BM * 16; q += kThreads) {
+        const int row = q >> 4, c = (q & 15) * 4;
+        finish(tm0, tgroup, row, c, sum(row * RC + c), sum(row * RC + 64 + c));
       }
-      __syncthreads();
-      if (whole && KIND == kGated) {
-        for (int q = et; q < BM * 16; q += kThreads) {
-          const int row = q >> 4, c = (q & 15) * 4;
-          const f32x4 *r0 = reinterpret_cast<const f32x4 *>(red + row * kRedStride + c);
-          const f32x4 *r1 = reinterpret_cast<const f32x4 *>(red + (BM + row) * kRedStride + c);
-          finish(row, c, r0[0] + r1[0], r0[16] + r1[16]);
-        }
-      } else {
-        const __amdgpu_buffer_rsrc_t ws =
-            __builtin_amdgcn_make_buffer_rsrc(P.partials + slot * kPart, (short)0, kPart * 4, kRawBuffer);
-        for (int q = et; q < BM * (RC / 4); q += kThreads) {
-          const int row = q / (RC / 4), c = (q % (RC / 4)) * 4;
-          const f32x4 v = *reinterpret_cast<const f32x4 *>(red + row * kRedStride + c) +
-                          *reinterpret_cast<const f32x4 *>(red + (BM + row) * kRedStride + c);
-          if (whole) finish(row, round * RC + c, v, v);
-          else
-            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), ws,
-                                                   (uint32_t)((round * BM + row) * RC + c) * 4, 0, kSc1);
-        }
+    } else {
+      for (int q = tid; q < kRounds * BM * (RC / 4); q += kThreads) {
+        const int round = q / (BM * (RC / 4)), row = q / (RC / 4) % BM, c = (q % (RC / 4)) * 4;
+        finish(tm0, tgroup, row, round * RC + c, sum((round * BM + row) * RC + c), f32x4{});
       }
     }
-    if (!whole) {
-      // The partial is complete at the coherent level before the counter moves.
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      __syncthreads();
-      // workgroups that hold the tile's first and last unit
-      auto owner = [&](int64_t u) {
-        int64_t c = u * gridDim.x / P.units;
-        while (P.units * (c + 1) / gridDim.x <= u) ++c;
-        while (P.units * c / gridDim.x > u) --c;
-        return c;
-      };
-      const int64_t c0 = owner(tile * P.steps), c1 = owner(tile * P.steps + P.steps - 1);
-      if (et == 0) *arrived = __hip_atomic_fetch_add(&P.counters[tile], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      __syncthreads();
-      const bool last = *arrived == (uint32_t)(c1 - c0);
-      if (last) {
-        if (et == 0) __hip_atomic_store(&P.counters[tile], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        auto sum = [&](int at) {
-          f32x4 v = {0.f, 0.f, 0.f, 0.f};
-          for (int64_t c = c0; c <= c1; ++c) {
-            const int64_t sl = 2 * c + (P.units * c / gridDim.x <= tile * P.steps ? 1 : 0);
-            const __amdgpu_buffer_rsrc_t ws =
-                __builtin_amdgcn_make_buffer_rsrc(P.partials + sl * kPart, (short)0, kPart * 4, kRawBuffer);
-            v += __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(ws, (uint32_t)at * 4, 0, kSc1));
-          }
-          return v;
-        };
-        if constexpr (KIND == kGated) {
-          for (int q = et; q < BM * 16; q += kThreads) {
-            const int row = q >> 4, c = (q & 15) * 4;
-            finish(row, c, sum(row * RC + c), sum(row * RC + 64 + c));
-          }
-        } else {
-          for (int q = et; q < kRounds * BM * (RC / 4); q += kThreads) {
-            const int round = q / (BM * (RC / 4)), row = q / (RC / 4) % BM, c = (q % (RC / 4)) * 4;
-            finish(row, round * RC + c, sum((round * BM + row) * RC + c), f32x4{});
-          }
-        }
-      }
-    }
-    unit += s1 - s0;
   }
 }
 
@@ -1200,7 +1282,7 @@ Shape shape_of(int kind, trellis_geom g, int32_t m, int matrices, int cus) {
   const int64_t room = (int64_t)cus * waves_per_simd(kind, mt) / 2;  // workgroups the card holds at once
   s.grid = (int)(s.units < room ? s.units : room);
   s.partial_bytes = (size_t)2 * s.grid * bm * (kind == kGated ? 128 : bn) * 4;
-  s.lds = kTableBytes + (size_t)2 * bm * kStride + (kind == kTransposed ? 512 * 12 + 8 * 4 : 0) + 16;
+  s.lds = (size_t)2 * bm * kStride + (kind == kTransposed ? 512 * 12 + 8 * 4 : 0);
   return s;
 }
 
@@ -1216,7 +1298,8 @@ trellis_status launch(const Shape &s, Product p, hipStream_t stream) {
       return TRELLIS_E_HIP;
     done = true;
   }
-  p.units = s.units;
+  p.units_q = (int)(s.units / s.grid);
+  p.units_r = (int)(s.units % s.grid);
   p.groups = s.groups;
   p.steps = s.steps;
   p.steps1 = s.steps1;
