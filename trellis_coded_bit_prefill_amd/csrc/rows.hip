@@ -73,36 +73,37 @@ struct Product {
   LowRank low;
 };
 
-// The adapters' term of one 16-row tile and a wave's NT column tiles: for every
-// adapter that the rows name, the product of t's rows (as the sum of two bf16
-// numbers, 2^-16 relative) with the factor, kept only in the rows that name
-// it, so an adapter's infinities and NaNs stay in its own rows. Several
-// adapters' operands are loaded before the first is multiplied: one at a time
-// cost about a microsecond each.
+// The adapters' term of TILES 16-row tiles (every second one from m0 on) and a
+// wave's NT column tiles: for every adapter that the rows name, the product of
+// t's rows (as the sum of two bf16 numbers, 2^-16 relative) with the factor,
+// kept only in the rows that name it, so an adapter's infinities and NaNs stay
+// in its own rows. Several adapters' operands are loaded before the first is
+// multiplied: one at a time cost about a microsecond each.
 // load(a, r0, w): the NT operands for rank columns r0 .. +7.
-template <int NT, typename Load>
-__device__ __forceinline__ void low_rank_tile(const LowRank &L, int m, int m0, int lane, f32x4 (&sum)[NT], Load load) {
+template <int TILES, int NT, typename Load>
+__device__ __forceinline__ void low_rank_tiles(const LowRank &L, int m, int m0, int lane, f32x4 (&sum)[TILES][NT], Load load) {
   constexpr int B = NT == 4 ? 2 : 4;  // adapters at a time
   const int j = lane & 15, g = lane >> 4;
-#pragma unroll
-  for (int i = 0; i < NT; ++i) sum[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int row = m0 + j;
-  const int rowc = row < m ? row : m - 1;
-  int idx = row < m ? L.index[row] : -1;
+  // lane l: the adapter of row l mod 16 of tile l / 16 (of the wave's)
+  const int look = m0 + 32 * (lane >> 4) + j;
+  int idx = lane < 16 * TILES && look < m ? L.index[look] : -1;
   if (idx >= L.count) idx = -1;
-  const uint64_t named = __ballot(idx >= 0) & 0xFFFFull;
-  for (int r0 = 0; r0 < L.rank_p; r0 += 32) {
-    const float *tp = L.t + (int64_t)rowc * L.rank_p + r0 + 8 * g;
-    const f32x4 t0 = *reinterpret_cast<const f32x4 *>(tp), t1 = *reinterpret_cast<const f32x4 *>(tp + 4);
-    bf16x8 hi, lo;
+  const uint64_t named = __ballot(idx >= 0);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float v = e < 4 ? t0[e] : t1[e - 4];
-      hi[e] = (__bf16)v;
-      lo[e] = (__bf16)(v - (float)hi[e]);
+  for (int t = 0; t < TILES; ++t)
+#pragma unroll
+    for (int i = 0; i < NT; ++i) sum[t][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int r0 = 0; r0 < L.rank_p; r0 += 32) {
+    f32x4 tv[TILES][2];
+#pragma unroll
+    for (int t = 0; t < TILES; ++t) {
+      const int row = m0 + 32 * t + j;
+      const float *tp = L.t + (int64_t)(row < m ? row : m - 1) * L.rank_p + r0 + 8 * g;
+      tv[t][0] = *reinterpret_cast<const f32x4 *>(tp);
+      tv[t][1] = *reinterpret_cast<const f32x4 *>(tp + 4);
     }
     for (uint64_t left = named; left;) {
-      uint32_t rows[B];
+      uint64_t rows[B];
       bf16x8 w[B][NT];
       int a = 0;
 #pragma unroll
@@ -110,21 +111,34 @@ __device__ __forceinline__ void low_rank_tile(const LowRank &L, int m, int m0, i
         rows[b] = 0;  // none left: the operands again, for no row
         if (left) {
           a = __builtin_amdgcn_readlane(idx, __builtin_ctzll(left));
-          rows[b] = (uint32_t)__ballot(idx == a) & 0xFFFFu;
-          left &= ~(uint64_t)rows[b];
+          rows[b] = __ballot(idx == a);
+          left &= ~rows[b];
         }
         load(a, r0 + 8 * g, w[b]);
       }
 #pragma unroll
-      for (int b = 0; b < B; ++b)
+      for (int t = 0; t < TILES; ++t) {
+        bf16x8 hi, lo;
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          f32x4 d = {0.f, 0.f, 0.f, 0.f};
-          d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, w[b][i], d, 0, 0, 0);
-          d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, w[b][i], d, 0, 0, 0);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sum[i][e] += (rows[b] >> (4 * g + e)) & 1 ? d[e] : 0.f;
+        for (int e = 0; e < 8; ++e) {
+          const float v = tv[t][e >> 2][e & 3];
+          hi[e] = (__bf16)v;
+          lo[e] = (__bf16)(v - (float)hi[e]);
         }
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+          const uint32_t of = (uint32_t)(rows[b] >> (16 * t)) & 0xFFFFu;
+          if (of == 0) continue;
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            f32x4 d = {0.f, 0.f, 0.f, 0.f};
+            d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, w[b][i], d, 0, 0, 0);
+            d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, w[b][i], d, 0, 0, 0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[t][i][e] += (of >> (4 * g + e)) & 1 ? d[e] : 0.f;
+          }
+        }
+      }
     }
   }
 }
@@ -240,8 +254,8 @@ namespace {
 //               128 wk .. +127 of each 256-row step
 // The units (tile, step) are split evenly over the workgroups; a tile that
 // several share goes through `partials`, summed in a fixed order by the
-// workgroup that arrives last. Code words are loaded two steps ahead
-// (transposed: one 32-row part ahead), P's rows one step ahead.
+// workgroup that arrives last. Code words and P's rows are loaded two steps
+// ahead (transposed: code words one 32-row part, P's rows one step ahead).
 // OCC: waves per SIMD (4: two workgroups share a CU, so that one decodes while
 // the other waits at its barrier).
 template <int BITS, int KIND, int MT, int NT, int OCC>
@@ -278,13 +292,15 @@ __global__ __launch_bounds__(kThreads, OCC) void product_kernel(Product P) {
   int m0 = tile / P.groups * BM, group = tile % P.groups;
 
   // Staged rows of P: thread t takes 8 columns of row t / 32 + 16 r.
-  // (The last step stages itself again: straight-line code keeps xv in
-  // registers and the memory waits exact.)
-  u32x4 xv[MT];
-  float sv = 0.f;
+  // (Past the last step it is staged again: straight-line code keeps the rows
+  // in registers and the memory waits exact.)
+  struct Rows {
+    u32x4 x[MT];
+    float s;
+  };
   const uint32_t row_b = (uint32_t)cols * 2;
   const uint32_t xoff = (uint32_t)(tid >> 5) * row_b + (uint32_t)(tid & 31) * 16;
-  auto fetch = [&](int s) {
+  auto fetch = [&](int s, Rows &R) {
     const bool second = kT && s >= P.steps1;
     const int at = second ? s - P.steps1 : s;
     const uint32_t valid_b = (uint32_t)(P.m - m0 < BM ? P.m - m0 : BM) * row_b;
@@ -298,30 +314,30 @@ __global__ __launch_bounds__(kThreads, OCC) void product_kernel(Product P) {
     for (int r = 0; r < MT; ++r) {
       const uint32_t o = xoff + (uint32_t)(16 * r) * row_b;
       if constexpr (!kT) {
-        xv[r] = __builtin_amdgcn_raw_buffer_load_b128(rs, o, 0, 0);
+        R.x[r] = __builtin_amdgcn_raw_buffer_load_b128(rs, o, 0, 0);
       } else {
         const u32x2 a = __builtin_amdgcn_raw_buffer_load_b64(rs, left > 0 ? o : 0x80000000u, 0, 0);
         const u32x2 b = __builtin_amdgcn_raw_buffer_load_b64(rs, left > 4 ? o + 8 : 0x80000000u, 0, 0);
-        xv[r] = u32x4{a[0], a[1], b[0], b[1]};
+        R.x[r] = u32x4{a[0], a[1], b[0], b[1]};
       }
     }
     if constexpr (kT) {
       const int row = at * kStep + tid;
-      sv = tid < 256 && row < P.n ? bf16_bits_to_f32((second ? P.scales2 : P.scales)[row]) : 0.f;
+      R.s = tid < 256 && row < P.n ? bf16_bits_to_f32((second ? P.scales2 : P.scales)[row]) : 0.f;
     }
   };
-  auto put = [&](int s) {
+  auto put = [&](int s, const Rows &R) {
     unsigned char *dst = xs + (s & 1) * BM * kStride;
 #pragma unroll
     for (int r = 0; r < MT; ++r)
-      *reinterpret_cast<u32x4 *>(dst + (r * 16 + (tid >> 5)) * kStride + (tid & 31) * 16) = xv[r];
+      *reinterpret_cast<u32x4 *>(dst + (r * 16 + (tid >> 5)) * kStride + (tid & 31) * 16) = R.x[r];
     if constexpr (kT) {
       if (tid < 256) {
         float q, k;
-        alu_row_constants(sv, q, k);
+        alu_row_constants(R.s, q, k);
         rowq[(s & 1) * 256 + tid] = f32x2{q, k};
-        rows_s[(s & 1) * 256 + tid] = sv;
-        const bool out = !__all(alu_scale_ok(sv));
+        rows_s[(s & 1) * 256 + tid] = R.s;
+        const bool out = !__all(alu_scale_ok(R.s));
         if (lane == 0) rowf[(s & 1) * 4 + wave] = out;
       }
     }
@@ -380,9 +396,11 @@ __global__ __launch_bounds__(kThreads, OCC) void product_kernel(Product P) {
         // The adapters' term joins the sums of the wave that holds the tile's
         // last step, half of the row tiles in each wk.
         if (KIND != kGated && a1 == P.steps && P.low.rank > 0) {
-          for (int mt = wk; mt < MT && am0 + 16 * mt < P.m; mt += 2) {
-            f32x4 term[NT];
-            low_rank_tile<NT>(P.low, P.m, am0 + 16 * mt, et & 63, term, [&](int a, int r0, bf16x8 (&w)[NT]) {
+          // (one row tile: the first wk alone)
+          if (MT > 1 || wk == 0) {
+            constexpr int TILES = (MT + 1) / 2;
+            f32x4 term[TILES][NT];
+            low_rank_tiles<TILES, NT>(P.low, P.m, am0 + 16 * wk, et & 63, term, [&](int a, int r0, bf16x8 (&w)[NT]) {
               if constexpr (kT) {
                 const int k0 = agroup * BN + 64 * wn + 4 * ej;
                 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
@@ -411,16 +429,18 @@ __global__ __launch_bounds__(kThreads, OCC) void product_kernel(Product P) {
               }
             });
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float *r = red + (wk * BM + mt * 16 + 4 * eg + e) * kRedStride;
-              if constexpr (kT) {
-                f32x4 *v = reinterpret_cast<f32x4 *>(r + 64 * (wn & 1) + 4 * ej);
-                *v += f32x4{term[0][e], term[1][e], term[2][e], term[3][e]};
-              } else {
+            for (int t = 0; t < TILES; ++t)
 #pragma unroll
-                for (int i = 0; i < NT; ++i) r[16 * NT * wn + 16 * i + ej] += term[i][e];
+              for (int e = 0; e < 4; ++e) {
+                float *r = red + (wk * BM + (2 * t + wk) * 16 + 4 * eg + e) * kRedStride;
+                if constexpr (kT) {
+                  f32x4 *v = reinterpret_cast<f32x4 *>(r + 64 * (wn & 1) + 4 * ej);
+                  *v += f32x4{term[t][0][e], term[t][1][e], term[t][2][e], term[t][3][e]};
+                } else {
+#pragma unroll
+                  for (int i = 0; i < NT; ++i) r[16 * NT * wn + 16 * i + ej] += term[t][i][e];
+                }
               }
-            }
           }
         }
       }
@@ -482,8 +502,13 @@ __global__ __launch_bounds__(kThreads, OCC) void product_kernel(Product P) {
       }
     };
     Words A, B;
+    // P's rows of the steps that A and B belong to; with eight row tiles there
+    // are no registers for two steps, and they are loaded one step ahead.
+    constexpr bool kFar = MT <= 6;
+    Rows X, Y;
     auto request = [&]() {
-      fetch(s0);
+      fetch(s0, X);
+      if constexpr (kFar) fetch(s0 + 1 < s1 ? s0 + 1 : s0, Y);
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
         const int n0 = KIND == kGated ? group * BN + 16 * wn : group * BN + 16 * NT * wn + 16 * i;
@@ -516,11 +541,12 @@ __global__ __launch_bounds__(kThreads, OCC) void product_kernel(Product P) {
         exact = exact && alu_scale_ok(sc[i]);
       }
       const bool chain = !__all(exact);
-      put(s0);
+      put(s0, X);
       lds_barrier();
       // Rows with scales outside the exact range take a loop of their own.
-      auto step = [&](int s, Words &W, auto chained) {
-        fetch(s + 1 < s1 ? s + 1 : s);
+      auto step = [&](int s, Words &W, Rows &mine, const Rows &next, auto chained) {
+        if constexpr (kFar) fetch(s + 2 < s1 ? s + 2 : s1 - 1, mine);  // (its rows are in LDS)
+        else fetch(s + 1 < s1 ? s + 1 : s, X);
         const unsigned char *xb = xs + (s & 1) * BM * kStride + j * kStride + (192 - 64 * g + 32 * wk) * 2;
         auto multiply = [&](int u, const bf16x8 (&w)[NT]) {
 #pragma unroll
@@ -556,14 +582,14 @@ __global__ __launch_bounds__(kThreads, OCC) void product_kernel(Product P) {
           TRELLIS_PHASE(1, 3, load(s + 2 < s1 ? s + 2 : s1 - 1, W))
 #undef TRELLIS_PHASE
         }
-        put(s + 1);
+        put(s + 1, kFar ? next : X);
         lds_barrier();
       };
       auto steps = [&](auto chained) {
         for (int s = s0;;) {
-          step(s, A, chained);
+          step(s, A, X, Y, chained);
           if (++s == s1) break;
-          step(s, B, chained);
+          step(s, B, Y, X, chained);
           if (++s == s1) break;
         }
       };
@@ -621,8 +647,9 @@ __global__ __launch_bounds__(kThreads, OCC) void product_kernel(Product P) {
       }
     };
     Words W;
+    Rows X;
     auto request = [&]() {
-      fetch(s0);
+      fetch(s0, X);
       load(0, W);
     };
     request();
@@ -634,7 +661,7 @@ __global__ __launch_bounds__(kThreads, OCC) void product_kernel(Product P) {
       for (int a = 0; a < MT; ++a)
 #pragma unroll
         for (int b = 0; b < NT; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-      put(s0);
+      put(s0, X);
       lds_barrier();
       auto compute = [&](int part, bool chain) {
         const int s = s0 + (part >> 2), p = part & 3;
@@ -687,11 +714,11 @@ __global__ __launch_bounds__(kThreads, OCC) void product_kernel(Product P) {
       };
       for (int s = s0; s < s1; ++s) {
         const int part = 4 * (s - s0);
-        fetch(s + 1 < s1 ? s + 1 : s);
+        fetch(s + 1 < s1 ? s + 1 : s, X);
         const uint32_t *fl = rowf + (s & 1) * 4;
         const bool chain = __builtin_amdgcn_readfirstlane(fl[0] | fl[1] | fl[2] | fl[3]) != 0;
         for (int p = 0; p < 4; ++p) compute(part + p, chain);
-        put(s + 1);
+        put(s + 1, X);
         lds_barrier();
       }
       // The next segment is requested before this one is reduced.
@@ -744,30 +771,46 @@ __global__ __launch_bounds__(kThreads, OCC) void product_kernel(Product P) {
     // a time; those past the last lie outside the buffer and give zero.
     const __amdgpu_buffer_rsrc_t ws = __builtin_amdgcn_make_buffer_rsrc(
         P.partials + (int64_t)(2 * c0 + 1) * kPart, (short)0, (2 * (c1 - c0) + 1) * kPart * 4, kRawBuffer);
-    auto sum = [&](int at) {
-      f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    constexpr int kQuads = KIND == kGated ? BM * 16 : kRounds * BM * (RC / 4);  // of outputs
+    constexpr int kSums = KIND == kGated ? 2 : 1;                             // sums behind each output
+    constexpr int kBatch = kQuads / kThreads >= 4 && !kT ? 4 : kQuads / kThreads >= 2 ? 2 : 1;  // quads of a thread at a time
+    for (int q0 = tid; q0 < kQuads; q0 += kBatch * kThreads) {
+      f32x4 v[kBatch][kSums];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+        for (int h = 0; h < kSums; ++h) v[b][h] = f32x4{0.f, 0.f, 0.f, 0.f};
       for (int c = c0; c <= c1; c += 4) {
-        f32x4 p[4];
+        f32x4 part[4][kBatch][kSums];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const uint32_t slot = c + u == c0 ? 0u : (uint32_t)(2 * (c + u - c0) - 1);
-          p[u] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                               ws, c + u <= c1 ? (slot * kPart + (uint32_t)at) * 4 : 0x80000000u, 0, kSc1));
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+            for (int h = 0; h < kSums; ++h) {
+              const int q = q0 + b * kThreads;
+              const uint32_t slot = c + u == c0 ? 0u : (uint32_t)(2 * (c + u - c0) - 1);
+              const uint32_t at = KIND == kGated ? (uint32_t)((q >> 4) * RC + 64 * h + (q & 15) * 4) : 4u * (uint32_t)q;
+              part[u][b][h] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                            ws, c + u <= c1 ? (slot * kPart + at) * 4 : 0x80000000u, 0, kSc1));
+            }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+            for (int h = 0; h < kSums; ++h) v[b][h] += part[u][b][h];
+      }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int q = q0 + b * kThreads;
+        if (kQuads % (kBatch * kThreads) != 0 && q >= kQuads) continue;
+        if constexpr (KIND == kGated) {
+          finish(tm0, tgroup, q >> 4, (q & 15) * 4, v[b][0], v[b][1]);
+        } else {
+          const int round = q / (BM * (RC / 4)), row = q / (RC / 4) % BM, c = (q % (RC / 4)) * 4;
+          finish(tm0, tgroup, row, round * RC + c, v[b][0], f32x4{});
         }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) v += p[u];
-      }
-      return v;
-    };
-    if constexpr (KIND == kGated) {
-      for (int q = tid; q < BM * 16; q += kThreads) {
-        const int row = q >> 4, c = (q & 15) * 4;
-        finish(tm0, tgroup, row, c, sum(row * RC + c), sum(row * RC + 64 + c));
-      }
-    } else {
-      for (int q = tid; q < kRounds * BM * (RC / 4); q += kThreads) {
-        const int round = q / (BM * (RC / 4)), row = q / (RC / 4) % BM, c = (q % (RC / 4)) * 4;
-        finish(tm0, tgroup, row, round * RC + c, sum((round * BM + row) * RC + c), f32x4{});
       }
     }
   }
@@ -1230,7 +1273,7 @@ constexpr int kMts = 5;
 // Tiles per wave and waves per SIMD for each number of row tiles. Forward up
 // to two row tiles: one tile per wave, whose finer units split more evenly.
 constexpr int wave_tiles(int kind, int mt) { return kind == kTransposed ? 4 : kind == kGated || mt > 2 ? 2 : 1; }
-constexpr int waves_per_simd(int kind, int mt) { return kind != kTransposed && mt <= (kind == kGated ? 4 : 2) ? 4 : 2; }
+constexpr int waves_per_simd(int kind, int mt) { return kind != kTransposed && mt <= 2 ? 4 : 2; }
 template <int BITS, int KIND, int MT>
 constexpr ProductFn product_one() {
   return &product_kernel<BITS, KIND, MT, wave_tiles(KIND, MT), waves_per_simd(KIND, MT)>;
