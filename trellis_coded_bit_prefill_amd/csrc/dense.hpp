@@ -189,7 +189,9 @@ __global__ __launch_bounds__(256) void gated_grad_pack_kernel(const uint16_t *__
 struct Dense {
   const uint16_t *p, *w;   // operands of the rows, and of the columns of this launch
   uint16_t *out, *gate, *up;
-  int32_t m, steps;
+  float *partials;         // [splits][m][16 wtiles], where the contraction is split
+  int32_t m, steps;        // steps: an even number
+  int32_t splits;          // of the contraction
   int32_t width;           // row length of the outputs
   int32_t first;           // first output column of this launch (gated: of one matrix)
   int32_t ptiles, wtiles;  // operand tiles
@@ -239,10 +241,13 @@ __global__ __launch_bounds__(kDenseThreads) void dense_kernel(Dense D) {
   const int j = lane & 15, g = lane >> 4;
   // Consecutive workgroups go to the eight XCDs in turn: each XCD gets a run
   // of consecutive tiles, row tiles first, whose operands its L2 shares.
-  const int total = D.mtiles * D.ntiles, each = total >> 3, rest = total & 7;
+  const int tiles = D.mtiles * D.ntiles, total = tiles * D.splits, each = total >> 3, rest = total & 7;
   const int xcd = blockIdx.x & 7, seq = blockIdx.x >> 3;
   const int id = xcd * each + (xcd < rest ? xcd : rest) + seq;
-  const int tn = id / D.mtiles, tm = id - tn * D.mtiles;
+  const int split = id / tiles, tn = (id - split * tiles) / D.mtiles, tm = id - split * tiles - tn * D.mtiles;
+  // this workgroup's steps: an even number from an even one on
+  const int begin = 2 * (int)((int64_t)(D.steps >> 1) * split / D.splits);
+  const int steps = 2 * (int)((int64_t)(D.steps >> 1) * (split + 1) / D.splits) - begin;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char *)lds;
 
   // Copy c of a step (1 KB): the first kA / 1024 are P's. Tiles past the last
@@ -251,6 +256,7 @@ __global__ __launch_bounds__(kDenseThreads) void dense_kernel(Dense D) {
   const unsigned char *const pa = reinterpret_cast<const unsigned char *>(D.p) + (int64_t)tm * (kDenseRows / 16) * 1024;
   const unsigned char *const pb = reinterpret_cast<const unsigned char *>(D.w) + (int64_t)tn * 2 * NT * 1024;
   const int64_t astride = (int64_t)D.ptiles * 1024, bstride = (int64_t)D.wtiles * 1024;
+  // (s counts from `begin`)
   auto stage = [&](int s, uint32_t buffer) {
 #pragma unroll
     for (int i = 0; i < kMost; ++i) {
@@ -258,7 +264,7 @@ __global__ __launch_bounds__(kDenseThreads) void dense_kernel(Dense D) {
       if (kFull == 8 || i < kMost - 1 || wave < kFull) {
         const bool is_a = i < kA / 8192;
         const int t = is_a ? c : c - kA / 1024, have = is_a ? atiles : btiles;
-        const unsigned char *src = is_a ? pa + s * astride : pb + s * bstride;
+        const unsigned char *src = is_a ? pa + (begin + s) * astride : pb + (begin + s) * bstride;
         copy_to_lds(lds0 + buffer + (uint32_t)(c * 1024), (uint32_t)lane * 16, src + (t < have ? t : have - 1) * 1024);
       }
     }
@@ -280,12 +286,12 @@ __global__ __launch_bounds__(kDenseThreads) void dense_kernel(Dense D) {
   const int row0 = tm * kDenseRows + 64 * wm, tile0 = tn * 2 * NT + wn * NT;
 #pragma unroll
   for (int b = 0; b < S; ++b)
-    if (b < D.steps) stage(b, b * kBuffer);
+    if (b < steps) stage(b, b * kBuffer);
   if constexpr (!GATED) {
     // The adapters' term first, while the first steps are on their way: lane l
     // looks up row row0 + l; for every adapter that the wave's rows name, the
     // products are kept only in the rows that name it (see low_rank_tile).
-    if (D.low.rank > 0) {
+    if (D.low.rank > 0 && split == 0) {
       int idx = row0 + lane < D.m ? D.low.index[row0 + lane] : -1;
       if (idx >= D.low.count) idx = -1;
       uint64_t left = __ballot(idx >= 0);
@@ -381,14 +387,14 @@ __global__ __launch_bounds__(kDenseThreads) void dense_kernel(Dense D) {
   step_barrier<0>();
   read(X, 0);
   auto step = [&](int s, const Operands &A, Operands &B) {
-    if (s + S - 1 < D.steps) landed(std::integral_constant<int, S - 2>{});
+    if (s + S - 1 < steps) landed(std::integral_constant<int, S - 2>{});
     else step_barrier<0>();
-    if (s + S < D.steps) stage(s + S, now);
+    if (s + S < steps) stage(s + S, now);
     now = now == (S - 1) * kBuffer ? 0 : now + kBuffer;
     read(B, now);  // (past the last step: a buffer's old operands, not used)
     multiply(A);
   };
-  for (int s = 0; s < D.steps; s += 2) {  // an even number of steps
+  for (int s = 0; s < steps; s += 2) {
     step(s, X, Y);
     step(s + 1, Y, X);
   }
@@ -397,6 +403,13 @@ __global__ __launch_bounds__(kDenseThreads) void dense_kernel(Dense D) {
   for (int r = 0; r < 4; ++r) {
     const int row = row0 + 16 * r + j;
     if (row >= D.m) continue;
+    if (D.splits > 1) {
+      float *const q = D.partials + ((int64_t)split * D.m + row) * (16 * (int64_t)D.wtiles) + tile0 * 16 + 4 * g;
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+        if (tile0 + i < D.wtiles) *reinterpret_cast<f32x4 *>(q + 16 * i) = acc[r][i];
+      continue;
+    }
     if constexpr (GATED) {
 #pragma unroll
       for (int i = 0; i < NT; i += 2) {
@@ -417,6 +430,36 @@ __global__ __launch_bounds__(kDenseThreads) void dense_kernel(Dense D) {
         if (col < D.width) store4(D.out + (int64_t)row * D.width + col, acc[r][i]);
       }
     }
+  }
+}
+
+// Sums of the splits, in order, rounded (gated: gate and up first, then the
+// product): four output columns a thread.
+template <bool GATED>
+__global__ __launch_bounds__(256) void join_splits_kernel(Dense D) {
+  const int quads = 4 * D.wtiles / (GATED ? 2 : 1);  // per row
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (id >= (int64_t)D.m * quads) return;
+  const int64_t row = id / quads;
+  const int c = (int)(id - row * quads) * 4;
+  if (D.first + c >= D.width) return;
+  const float *q = D.partials + row * (16 * (int64_t)D.wtiles) + (GATED ? (c >> 4) * 32 + (c & 15) : c);
+  const int64_t plane = (int64_t)D.m * 16 * D.wtiles;
+  f32x4 v = {0.f, 0.f, 0.f, 0.f}, u = {0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < D.splits; ++s) {
+    v += *reinterpret_cast<const f32x4 *>(q + s * plane);
+    if constexpr (GATED) u += *reinterpret_cast<const f32x4 *>(q + s * plane + 16);
+  }
+  const int64_t o = row * D.width + D.first + c;
+  if constexpr (GATED) {
+    f32x4 h;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e] = silu_mul(v[e], u[e]);
+    store4(D.out + o, h);
+    if (D.gate) store4(D.gate + o, v);
+    if (D.up) store4(D.up + o, u);
+  } else {
+    store4(D.out + o, v);
   }
 }
 

@@ -1353,18 +1353,30 @@ trellis_status launch(const Shape &s, Product p, hipStream_t stream) {
 
 // ---- many rows (dense.hpp) ---------------------------------------------------
 
-// Rows from which W is decoded once into the workspace.
-constexpr int kDenseFrom = 256;
+// Whether W is decoded once into the workspace: from a number of rows on that
+// grows for small matrices, where the extra launches (unpacking, packing the
+// rows, joining splits: 12 to 20 us) weigh more. Measured, decoding in the
+// product against this (us), K = 5120, N = 17408, k = 4: adapters 124 / 153 at
+// 384 rows, 164 / 156 at 512; gated 266 / 294 at 512, 430 / 346 at 768;
+// adapters_backward 195 / 203 at 257, 221 / 211 at 384; gated_backward 278 /
+// 309 at 257, 329 / 340 at 384, 428 / 349 at 512. K = 1024, N = 4096:
+// adapters 44 / 46 at 768, 33 / 47 at 1024; backward 65 / 70 at 384, 83 / 115
+// at 1024.
+bool decode_once(int kind, trellis_geom g, int32_t m, int matrices) {
+  const double weights = (double)g.n * g.k * (kind == kGated ? 2 : matrices);
+  return kind == kTransposed ? m > 280 + 4e9 / weights : m > 470 + 4e9 / weights;
+}
 // Operand workspace of one launch; larger matrices go in slabs of columns.
 constexpr int64_t kOperandBytes = (int64_t)1 << 30;
 
 struct DenseShape {
   int nt;              // accumulator tiles per wave
+  int splits;          // of the contraction
   int matrices;        // gated: 2 in the tiles, transposed: in the contraction
   int steps, steps1;
   int64_t tiles, slab;  // operand tiles in all and per launch
   int ptiles;
-  size_t operand_bytes, row_bytes;
+  size_t operand_bytes, row_bytes, partial_bytes;
 };
 DenseShape dense_shape(int kind, trellis_geom g, int32_t m, int matrices, int cus) {
   DenseShape s{};
@@ -1374,16 +1386,25 @@ DenseShape dense_shape(int kind, trellis_geom g, int32_t m, int matrices, int cu
   s.steps = t ? s.steps1 * matrices : s.steps1;
   const int64_t width = t ? g.k : g.n, one = (width + 15) / 16;
   s.tiles = kind == kGated ? 2 * one : one;
-  // The column tile whose rounds over the card cost least.
+  // The column tile and the split of the contraction whose rounds over the
+  // card cost least. A round costs its steps times the accumulator tiles and
+  // one more (staging), and about 100 tile steps to start and store; the
+  // partial sums of a split are written and read once more (32 MB cost about
+  // 12 us, a tile step 14 ns).
   const int64_t mt = (m + kDenseRows - 1) / kDenseRows;
   double best = 0;
   for (int nt = 8; nt >= 4; --nt) {
     if (kind == kGated && nt % 2) continue;
     const int64_t wg = mt * ((s.tiles + 2 * nt - 1) / (2 * nt));
-    const double cost = (double)((wg + cus - 1) / cus) * (nt + 1.0);
-    if (s.nt == 0 || cost < best) {
-      best = cost;
-      s.nt = nt;
+    for (int splits = 1; splits <= 8 && splits <= s.steps / 16; ++splits) {
+      const double rounds = (double)((wg * splits + cus - 1) / cus);
+      double cost = rounds * ((double)s.steps / splits * (nt + 1.0) + 100.0);
+      if (splits > 1) cost += 300.0 + (double)splits * m * s.tiles * 16 * 4 / 37000.0;
+      if (s.nt == 0 || cost < best) {
+        best = cost;
+        s.nt = nt;
+        s.splits = splits;
+      }
     }
   }
   const int64_t tile_bytes = (int64_t)s.steps * 1024;
@@ -1394,6 +1415,7 @@ DenseShape dense_shape(int kind, trellis_geom g, int32_t m, int matrices, int cu
   s.operand_bytes = (size_t)(slab * tile_bytes);
   s.ptiles = (int)(((int64_t)m + 15) / 16);
   s.row_bytes = (size_t)s.ptiles * s.steps * 1024;
+  s.partial_bytes = s.splits > 1 ? (size_t)s.splits * m * slab * 16 * 4 : 0;
   return s;
 }
 
@@ -1420,7 +1442,8 @@ struct GatedGrads {
 };
 
 trellis_status launch_dense(int kind, const DenseShape &s, trellis_geom g, const Product &p, const GatedGrads *grads,
-                            unsigned char *operands, unsigned char *rows, hipStream_t stream) {
+                            unsigned char *operands, hipStream_t stream) {
+  unsigned char *const rows = operands + up256(s.operand_bytes);
   const DenseFn fn = dense_fn(kind, s.nt);
   const size_t lds = (size_t)dense_buffers(s.nt) * dense_step_bytes(s.nt);
   static bool ready[kMaxDevices][3][9];
@@ -1440,6 +1463,8 @@ trellis_status launch_dense(int kind, const DenseShape &s, trellis_geom g, const
   d.up = p.up;
   d.m = p.m;
   d.steps = s.steps;
+  d.splits = s.splits;
+  d.partials = reinterpret_cast<float *>(rows + up256(s.row_bytes));
   d.ptiles = s.ptiles;
   d.width = kind == kTransposed ? g.k : g.n;
   d.mtiles = (p.m + kDenseRows - 1) / kDenseRows;
@@ -1480,8 +1505,15 @@ trellis_status launch_dense(int kind, const DenseShape &s, trellis_geom g, const
     d.first = (int)(first * 16 / (kind == kGated ? 2 : 1));
     d.wtiles = tiles;
     d.ntiles = (tiles + 2 * s.nt - 1) / (2 * s.nt);
-    hipLaunchKernelGGL(fn, dim3((unsigned)(d.mtiles * d.ntiles)), dim3(kDenseThreads), lds, stream, d);
+    hipLaunchKernelGGL(fn, dim3((unsigned)(d.mtiles * d.ntiles * s.splits)), dim3(kDenseThreads), lds, stream, d);
     if (hipGetLastError() != hipSuccess) return TRELLIS_E_HIP;
+    if (s.splits > 1) {
+      const int64_t quads = (int64_t)p.m * 4 * tiles / (kind == kGated ? 2 : 1);
+      const dim3 grid((unsigned)((quads + 255) / 256));
+      if (kind == kGated) hipLaunchKernelGGL(join_splits_kernel<true>, grid, dim3(256), 0, stream, d);
+      else hipLaunchKernelGGL(join_splits_kernel<false>, grid, dim3(256), 0, stream, d);
+      if (hipGetLastError() != hipSuccess) return TRELLIS_E_HIP;
+    }
   }
   return TRELLIS_OK;
 }
@@ -1496,10 +1528,10 @@ struct Plan {
 };
 Plan plan_of(int kind, trellis_geom g, int32_t m, int matrices, int cus) {
   Plan p{};
-  p.dense = m >= kDenseFrom;
+  p.dense = decode_once(kind, g, m, matrices);
   if (p.dense) {
     p.many = dense_shape(kind, g, m, matrices, cus);
-    p.bytes = up256(p.many.operand_bytes) + p.many.row_bytes;
+    p.bytes = up256(p.many.operand_bytes) + up256(p.many.row_bytes) + p.many.partial_bytes;
   } else {
     p.fused = shape_of(kind, g, m, matrices, cus);
     p.bytes = p.fused.partial_bytes;
@@ -1509,7 +1541,7 @@ Plan plan_of(int kind, trellis_geom g, int32_t m, int matrices, int cus) {
 }
 trellis_status run(const Plan &pl, int kind, trellis_geom g, Product p, const GatedGrads *grads, unsigned char *ws,
                    hipStream_t stream) {
-  if (pl.dense) return launch_dense(kind, pl.many, g, p, grads, ws, ws + up256(pl.many.operand_bytes), stream);
+  if (pl.dense) return launch_dense(kind, pl.many, g, p, grads, ws, stream);
   if (grads) {
     const int64_t quads = (int64_t)p.m * (g.n / 4);
     (void)hipGetLastError();
