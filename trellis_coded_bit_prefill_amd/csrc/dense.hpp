@@ -76,56 +76,74 @@ __global__ __launch_bounds__(256) void unpack_rows_kernel(Unpack U) {
   }
 }
 
-// Transposed: one wave per step (32 rows of W) and 64 columns; lane (j, g)
-// decodes columns 4 j .. +3 of rows 8 g .. +7 and so holds, for each of the
-// four columns, one lane's whole operand.
+// Transposed: one wave per step (32 rows of W) and 256-column block. The rows'
+// code words go through the wave's LDS (read from memory lane by lane they cost
+// a load per two weights); lane (j, g) then decodes, 64 columns at a time,
+// columns 4 j .. +3 of rows 8 g .. +7, which is one lane's whole operand for
+// each of the four columns.
 template <int BITS>
 __global__ __launch_bounds__(256) void unpack_columns_kernel(Unpack U) {
+  constexpr int wpb = 8 * BITS, kRow = wpb + 4;  // words of a row's block, and in LDS
+  __shared__ __attribute__((aligned(16))) uint32_t words[4][32 * kRow];
   __shared__ bf16x8 turn[4][4 * 64];
-  constexpr int wpb = 8 * BITS;
-  const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, j = lane & 15, g = lane >> 4;
   const int per = U.steps / U.matrices;  // steps of one matrix
-  const int groups = U.tiles >> 2;        // of 64 columns
-  const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (id >= (int64_t)groups * per) return;
+  const int blocks = U.tiles >> 4;       // of 256 columns
+  const int64_t id = (int64_t)blockIdx.x * 4 + wave;
+  if (id >= (int64_t)blocks * per) return;
   const int which = blockIdx.y;
-  const int ks = (int)(id / groups), grp = (int)(id - (int64_t)ks * groups);
-  const int col = (U.first + 4 * grp) * 16 + 4 * j;  // first of the lane's four columns
-  const int pos = (252 - (col & 255)) * BITS, w0 = pos >> 5, sh = pos & 31, w1 = w0 + 1 == wpb ? 0 : w0 + 1;
-  const int64_t row_words = (int64_t)(U.k >> 8) * wpb, blk = (int64_t)(col >> 8) * wpb;
-  bf16x8 v[4];
-  uint32_t f[8];
-  float s[8];
+  const int ks = (int)(id / blocks), blk = (int)(id - (int64_t)ks * blocks);
+  const int64_t row_words = (int64_t)(U.k >> 8) * wpb;
+  const uint32_t *const base = U.codes[which] + (int64_t)((U.first >> 4) + blk) * wpb;
+  u32x4 v[BITS];
+#pragma unroll
+  for (int i = 0; i < BITS; ++i) {
+    const int at = (64 * i + lane) * 4, n = ks * 32 + at / wpb;
+    v[i] = *reinterpret_cast<const u32x4 *>(base + (n < U.n ? n : U.n - 1) * row_words + at % wpb);
+  }
+  float q[8], kq[8], sc[8];
   bool in_range = true;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const int n = ks * 32 + 8 * g + e, row = n < U.n ? n : U.n - 1;
-    const uint32_t *bw = U.codes[which] + row * row_words + blk;
-    f[e] = __builtin_amdgcn_alignbit(bw[w1], bw[w0], sh);
-    s[e] = n < U.n ? bf16_bits_to_f32(U.scales[which][row]) : 0.f;
-    in_range = in_range && alu_scale_ok(s[e]);
+    const int n = ks * 32 + 8 * g + e;
+    sc[e] = n < U.n ? bf16_bits_to_f32(U.scales[which][n]) : 0.f;  // rows past N weigh nothing
+    alu_row_constants(sc[e], q[e], kq[e]);
+    in_range = in_range && alu_scale_ok(sc[e]);
   }
   const bool exact = !__all(in_range);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    float q, kq;
-    alu_row_constants(s[e], q, kq);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) v[c][e] = (__bf16)window_weight((f[e] >> ((3 - c) * BITS)) & 0xFFFu, s[e], q, kq, exact);
+  for (int i = 0; i < BITS; ++i) {
+    const int at = (64 * i + lane) * 4;
+    *reinterpret_cast<u32x4 *>(&words[wave][at / wpb * kRow + at % wpb]) = v[i];
   }
-  // Through the wave's own LDS, so that each store writes 1 KB in a row: lane
-  // (j, g) holds slots 16 g + 4 (j mod 4) .. +3 of tile j / 4.
-  bf16x8 *const mine = turn[threadIdx.x >> 6];
+  bf16x8 *const mine = turn[wave];
+  bf16x8 *out = reinterpret_cast<bf16x8 *>(U.w) + (((int64_t)which * per + ks) * U.tiles + 16 * blk) * 64 + lane;
 #pragma unroll
-  for (int c = 0; c < 4; ++c) mine[(j >> 2) * 64 + g * 16 + 4 * (j & 3) + c] = v[c];
-  bf16x8 *out = reinterpret_cast<bf16x8 *>(U.w) + (((int64_t)which * per + ks) * U.tiles + 4 * grp) * 64 + lane;
+  for (int part = 0; part < 4; ++part) {
+    const int pos = (252 - 64 * part - 4 * j) * BITS, w0 = pos >> 5, sh = pos & 31, w1 = w0 + 1 == wpb ? 0 : w0 + 1;
+    bf16x8 w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) out[i * 64] = mine[i * 64 + lane];
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t *row = &words[wave][(8 * g + e) * kRow];
+      const uint32_t f = __builtin_amdgcn_alignbit(row[w1], row[w0], sh);
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        w[c][e] = (__bf16)window_weight(__builtin_amdgcn_ubfe(f, (3 - c) * BITS, 12), sc[e], q[e], kq[e], exact);
+    }
+    // Through the wave's LDS again, so that each store writes 1 KB in a row:
+    // lane (j, g) holds slots 16 g + 4 (j mod 4) .. +3 of tile j / 4.
+#pragma unroll
+    for (int c = 0; c < 4; ++c) mine[(j >> 2) * 64 + g * 16 + 4 * (j & 3) + c] = w[c];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) out[(4 * part + i) * 64] = mine[i * 64 + lane];
+  }
 }
 
-// Rows of P as operands: one wave per two steps and 16-row tile. Rows past m and
-// columns past `cols` are zero (rows start at multiples of 8 bytes).
+// Eight columns of a row of P; rows past m and columns past `cols` are zero.
+// Rows start at multiples of 8 bytes, of 16 where WIDE (cols a multiple of 8).
+template <bool WIDE>
 __device__ __forceinline__ u32x4 row_vector(const uint16_t *src, int64_t row, int64_t m, int cols, int c) {
+  if constexpr (WIDE) return row < m && c < cols ? *reinterpret_cast<const u32x4 *>(src + row * cols + c) : u32x4{0u, 0u, 0u, 0u};
   u32x2 v[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -134,6 +152,8 @@ __device__ __forceinline__ u32x4 row_vector(const uint16_t *src, int64_t row, in
   }
   return u32x4{v[0][0], v[0][1], v[1][0], v[1][1]};
 }
+// Rows of P as operands: one wave per two steps and 16-row tile.
+template <bool WIDE>
 __global__ __launch_bounds__(256) void pack_rows_kernel(const uint16_t *__restrict__ src, int m, int cols, int tiles,
                                                         int steps, uint16_t *__restrict__ dst) {
   const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
@@ -144,11 +164,12 @@ __global__ __launch_bounds__(256) void pack_rows_kernel(const uint16_t *__restri
   u32x4 *out = reinterpret_cast<u32x4 *>(dst) + ((int64_t)step * tiles + tile) * 64 + lane;
 #pragma unroll
   for (int h = 0; h < 2; ++h)
-    out[(int64_t)h * tiles * 64] = row_vector(src, (int64_t)tile * 16 + j, m, cols, (step + h) * 32 + 8 * g);
+    out[(int64_t)h * tiles * 64] = row_vector<WIDE>(src, (int64_t)tile * 16 + j, m, cols, (step + h) * 32 + 8 * g);
 }
 
 // The gated block's elementwise gradients (see gated_grad_kernel) as rows and
 // as operands: steps 0 .. steps - 1 hold dgate, the next `steps` dup.
+template <bool WIDE>
 __global__ __launch_bounds__(256) void gated_grad_pack_kernel(const uint16_t *__restrict__ dh,
                                                               const uint16_t *__restrict__ gate,
                                                               const uint16_t *__restrict__ up, int m, int cols, int tiles,
@@ -164,7 +185,7 @@ __global__ __launch_bounds__(256) void gated_grad_pack_kernel(const uint16_t *__
   for (int h = 0; h < 2; ++h) {
     const int64_t row = (int64_t)tile * 16 + j;
     const int c = (step + h) * 32 + 8 * g;
-    const u32x4 d = row_vector(dh, row, m, cols, c), gv = row_vector(gate, row, m, cols, c), uv = row_vector(up, row, m, cols, c);
+    const u32x4 d = row_vector<WIDE>(dh, row, m, cols, c), gv = row_vector<WIDE>(gate, row, m, cols, c), uv = row_vector<WIDE>(up, row, m, cols, c);
     u32x4 pg, pu;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -177,6 +198,13 @@ __global__ __launch_bounds__(256) void gated_grad_pack_kernel(const uint16_t *__
     }
     out[(int64_t)h * tiles * 64] = pg;
     out[(int64_t)(steps + h) * tiles * 64] = pu;
+    if constexpr (WIDE) {
+      if (row < m && c < cols) {
+        *reinterpret_cast<u32x4 *>(dgate + row * cols + c) = pg;
+        *reinterpret_cast<u32x4 *>(dup + row * cols + c) = pu;
+      }
+      continue;
+    }
 #pragma unroll
     for (int k = 0; k < 2; ++k)
       if (row < m && c + 4 * k < cols) {

@@ -857,6 +857,9 @@ __global__ __launch_bounds__(64 * WAVES) void shrink_kernel(Shrink S) {
   const uint64_t named = __ballot(idx >= 0);
   int distinct = 0;
   for (uint64_t left = named; left; ++distinct) left &= ~__ballot(idx == __builtin_amdgcn_readlane(idx, __builtin_ctzll(left)));
+  const int rows_left = (int)(S.m - m0 < 16 * MS ? S.m - m0 : 16 * MS);
+  const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint16_t *>(S.p + m0 * S.cols), (short)0, (int)((uint32_t)rows_left * (uint32_t)S.cols * 2), kRawBuffer);
   const int c_end = S.cols - span * S.span < S.span ? S.cols : (span + 1) * S.span;
   f32x4 acc[MS][2];
 #pragma unroll
@@ -875,9 +878,15 @@ __global__ __launch_bounds__(64 * WAVES) void shrink_kernel(Shrink S) {
     f32x4 d[MS][2];
 #pragma unroll
     for (int i = 0; i < MS; ++i) d[i][0] = d[i][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-    // U steps of 32 columns are loaded before the first is multiplied.
+    // U steps of 32 columns are loaded before the first is multiplied. Loads
+    // of what does not exist (columns past the span, rows past m, rank columns
+    // past the rank) take an offset outside their buffer and give zero.
     constexpr int U = MS == 1 ? 4 : 2;
-    const bool vectors = T && (S.rank & 7) == 0;
+    constexpr uint32_t kNone = 0x80000000u;
+    const bool vectors = T && (S.rank & 7) == 0, wide = !T || (S.cols & 7) == 0;
+    const uint32_t block = (uint32_t)S.rank * (uint32_t)S.cols;
+    const __amdgpu_buffer_rsrc_t rf = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint16_t *>(S.factor + (int64_t)a * block), (short)0, (int)(block * 2), kRawBuffer);
     for (int c0 = span * S.span + 32 * part_i; c0 < c_end; c0 += 32 * parts * U) {
       bf16x8 w[U][2];
       u32x4 b[U][2], x[U][MS];
@@ -886,15 +895,22 @@ __global__ __launch_bounds__(64 * WAVES) void shrink_kernel(Shrink S) {
         const int cu = c0 + 32 * parts * u, c = cu + 8 * g;
         const bool in = cu < c_end;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          w[u][h] = bf16x8{};
-          b[u][h] = u32x4{0u, 0u, 0u, 0u};
+        for (int i = 0; i < MS; ++i) {
+          const uint32_t o = ((uint32_t)(16 * i + j) * (uint32_t)S.cols + (uint32_t)c) * 2;
+          if (wide) {
+            x[u][i] = __builtin_amdgcn_raw_buffer_load_b128(rx, in && c < S.cols ? o : kNone, 0, 0);
+          } else {  // rows start at multiples of 8 bytes
+            const u32x2 lo = __builtin_amdgcn_raw_buffer_load_b64(rx, in && c < S.cols ? o : kNone, 0, 0);
+            const u32x2 hi = __builtin_amdgcn_raw_buffer_load_b64(rx, in && c + 4 < S.cols ? o + 8 : kNone, 0, 0);
+            x[u][i] = u32x4{lo[0], lo[1], hi[0], hi[1]};
+          }
         }
         if constexpr (!T) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const int r = 32 * z + 16 * h + j;
-            if (in && r < S.rank) w[u][h] = *reinterpret_cast<const bf16x8 *>(S.factor + ((int64_t)a * S.rank + r) * S.cols + c);
+            const uint32_t r = (uint32_t)(32 * z + 16 * h + j);  // past the rank: outside the adapter's block
+            w[u][h] = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(
+                                                     rf, in ? (r * (uint32_t)S.cols + (uint32_t)c) * 2 : kNone, 0, 0));
           }
         } else if (vectors) {
           // 32 rows of B by 32 rank columns: lane l takes the 16 bytes at
@@ -902,35 +918,19 @@ __global__ __launch_bounds__(64 * WAVES) void shrink_kernel(Shrink S) {
           const int r = 32 * z + 8 * (lane & 3);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const int n = cu + 16 * h + (lane >> 2);
-            if (in && n < S.cols && r < S.rank)
-              b[u][h] = *reinterpret_cast<const u32x4 *>(S.factor + ((int64_t)a * S.cols + n) * S.rank + r);
+            const uint32_t n = (uint32_t)(cu + 16 * h + (lane >> 2));
+            b[u][h] = __builtin_amdgcn_raw_buffer_load_b128(
+                rf, in && r < S.rank ? (n * (uint32_t)S.rank + (uint32_t)r) * 2 : kNone, 0, 0);
           }
         } else {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int r = 32 * z + 16 * h + j;
-            const uint16_t *q = S.factor + ((int64_t)a * S.cols + c) * S.rank + r;
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              if (in && r < S.rank && c + e < S.cols) w[u][h][e] = __builtin_bit_cast(__bf16, q[(int64_t)e * S.rank]);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < MS; ++i) {
-          const int64_t row = m0 + 16 * i + j, rowc = row < S.m ? row : S.m - 1;
-          const uint16_t *xp = S.p + rowc * S.cols + c;
-          x[u][i] = u32x4{0u, 0u, 0u, 0u};
-          if constexpr (!T) {
-            if (in) x[u][i] = *reinterpret_cast<const u32x4 *>(xp);
-          } else {  // rows start at multiples of 8 bytes, columns past N are zero
-            u32x2 v[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              v[h] = u32x2{0u, 0u};
-              if (in && c + 4 * h < S.cols) v[h] = *reinterpret_cast<const u32x2 *>(xp + 4 * h);
-            }
-            x[u][i] = u32x4{v[0][0], v[0][1], v[1][0], v[1][1]};
+              w[u][h][e] = __builtin_bit_cast(
+                  __bf16, (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(
+                              rf, in && r < S.rank ? ((uint32_t)(c + e) * (uint32_t)S.rank + (uint32_t)r) * 2 : kNone, 0, 0));
           }
         }
       }
@@ -1079,6 +1079,7 @@ __global__ __launch_bounds__(256) void outer_kernel(Outer O) {
     uint32_t rows;  // which of the 32 rows are the adapter's
   };
   const int pc = c0 + 8 * (lane & 7);
+  const bool wide = (cols & 7) == 0;
   auto load = [&](int ch, Chunk &C) {
     const int m0 = ch * 32;
     const int mi = m0 + (lane & 31);
@@ -1087,11 +1088,18 @@ __global__ __launch_bounds__(256) void outer_kernel(Outer O) {
     for (int i = 0; i < 4; ++i) {
       const int m = m0 + 8 * i + (lane >> 3);
       const uint16_t *q = P + (int64_t)(m < O.m ? m : O.m - 1) * cols + pc;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        C.p[2 * i + h] = u32x2{0u, 0u};
-        if (pc + 4 * h < cols) C.p[2 * i + h] = *reinterpret_cast<const u32x2 *>(q + 4 * h);
+      C.p[2 * i] = C.p[2 * i + 1] = u32x2{0u, 0u};
+      if (wide) {
+        if (pc < cols) {
+          const u32x4 v = *reinterpret_cast<const u32x4 *>(q);
+          C.p[2 * i] = u32x2{v[0], v[1]};
+          C.p[2 * i + 1] = u32x2{v[2], v[3]};
+        }
+        continue;
       }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (pc + 4 * h < cols) C.p[2 * i + h] = *reinterpret_cast<const u32x2 *>(q + 4 * h);
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -1471,12 +1479,14 @@ trellis_status launch_dense(int kind, const DenseShape &s, trellis_geom g, const
   d.low = p.low;
   (void)hipGetLastError();
   const dim3 pack((unsigned)(((int64_t)s.ptiles * (s.steps1 / 2) + 3) / 4));
+  uint16_t *const to = reinterpret_cast<uint16_t *>(rows);
+  const int width = kind == kTransposed ? g.n : g.k;
   if (grads)
-    hipLaunchKernelGGL(gated_grad_pack_kernel, pack, dim3(256), 0, stream, grads->dh, grads->gate, grads->up, p.m, g.n,
-                       s.ptiles, s.steps1, grads->dgate, grads->dup, reinterpret_cast<uint16_t *>(rows));
+    hipLaunchKernelGGL(width % 8 ? gated_grad_pack_kernel<false> : gated_grad_pack_kernel<true>, pack, dim3(256), 0, stream,
+                       grads->dh, grads->gate, grads->up, p.m, width, s.ptiles, s.steps1, grads->dgate, grads->dup, to);
   else
-    hipLaunchKernelGGL(pack_rows_kernel, pack, dim3(256), 0, stream, p.p, p.m, kind == kTransposed ? g.n : g.k, s.ptiles,
-                       s.steps1, reinterpret_cast<uint16_t *>(rows));
+    hipLaunchKernelGGL(width % 8 ? pack_rows_kernel<false> : pack_rows_kernel<true>, pack, dim3(256), 0, stream, p.p, p.m,
+                       width, s.ptiles, s.steps1, to);
   if (hipGetLastError() != hipSuccess) return TRELLIS_E_HIP;
   for (int64_t first = 0; first < s.tiles; first += s.slab) {
     const int tiles = (int)(s.tiles - first < s.slab ? s.tiles - first : s.slab);
@@ -1485,7 +1495,7 @@ trellis_status launch_dense(int kind, const DenseShape &s, trellis_geom g, const
       u.first = (int)first;
       u.tiles = tiles;
       u.matrices = s.matrices;
-      const int64_t waves = (int64_t)(tiles / 4) * s.steps1;
+      const int64_t waves = (int64_t)(tiles / 16) * s.steps1;
       const dim3 grid((unsigned)((waves + 3) / 4), (unsigned)s.matrices);
       if (g.bits == 2) hipLaunchKernelGGL(unpack_columns_kernel<2>, grid, dim3(256), 0, stream, u);
       else if (g.bits == 3) hipLaunchKernelGGL(unpack_columns_kernel<3>, grid, dim3(256), 0, stream, u);
