@@ -401,16 +401,35 @@ def gate_up(x, codes_gate, scales_gate, codes_up, scales_up, bits: int, out=None
     return out
 
 
-def _packed_k(codes, bits: int) -> int:
-    """Input columns of a packed matrix, from its words per row."""
-    if bits not in (2, 3, 4) or (codes.shape[1] * 32) % bits:
-        raise ValueError(f"codes has {codes.shape[1]} words per row, which is no row of {bits}-bit codes")
-    return codes.shape[1] * 32 // bits
+_types = None
 
 
-def _check_shape(name, t, shape):
-    if tuple(t.shape) != tuple(shape):
+def _kinds():
+    """(Tensor, bf16 dtypes, code dtypes, float32, int32), looked up once."""
+    global _types
+    if _types is None:
+        import torch
+
+        _types = (torch.Tensor, *_dtypes(), (torch.float32,), (torch.int32,))
+    return _types
+
+
+def _address(name, t, dtypes, shape, device) -> int:
+    """The data address of a tensor of exactly this kind, shape and device
+    (contiguous), else the error that names what is wrong with it. One test of
+    everything first: a call checks up to ten tensors, and its launches take
+    only a few microseconds."""
+    if not (isinstance(t, _kinds()[0]) and t.dtype in dtypes and t.shape == shape and t.device == device
+            and t.is_contiguous()):
+        _check_tensor(name, t, dtypes, len(shape), device)
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t.data_ptr()
+
+
+def _rows_of(name, t):
+    """Shape and device of the tensor that the others are checked against: bf16 [rows, columns]."""
+    _check_tensor(name, t, _kinds()[1], 2)
+    return (*t.shape, t.device)
 
 
 def _output(name, t, shape, device):
@@ -419,38 +438,34 @@ def _output(name, t, shape, device):
 
     if t is None:
         return torch.empty(shape, dtype=torch.bfloat16, device=device)
-    _check_tensor(name, t, _dtypes()[0], len(shape), device)
-    _check_shape(name, t, shape)
+    _address(name, t, _kinds()[1], shape, device)
     return t
 
 
-def _check_packed(codes, scales, k: int, bits: int, device, suffix: str = "") -> int:
-    """Checks one packed matrix of k columns; returns its rows."""
-    bf, cw = _dtypes()
-    _check_tensor("codes" + suffix, codes, cw, 2, device)
-    _check_tensor("scales" + suffix, scales, bf, 1, device)
-    n = codes.shape[0]
-    if codes.shape[1] * 32 != k * bits:
-        raise ValueError(f"codes{suffix} has {codes.shape[1]} words per row, expected K*bits/32 = {k * bits // 32}")
-    _check_shape("scales" + suffix, scales, (n,))
-    return n
+def _packed_address(codes, scales, n, k: int, bits: int, device, suffix: str = ""):
+    """Addresses of one packed matrix [n, k] and its scales."""
+    _, bf, cw, _, _ = _kinds()
+    if bits not in (2, 3, 4):
+        raise ValueError(f"bits must be 2, 3 or 4, got {bits}")
+    return (_address("codes" + suffix, codes, cw, (n, k * bits // 32), device),
+            _address("scales" + suffix, scales, bf, (n,), device))
 
 
-def _check_adapters(a, b, gain, index, m: int, n: int, k: int, device):
-    """Checks an adapter set for m rows of a layer [n, k]; returns (count, rank)."""
-    import torch
+def _packed_rows(codes, suffix: str = "") -> int:
+    """Rows of a packed matrix, its kind not yet checked."""
+    if not isinstance(codes, _kinds()[0]) or codes.ndim != 2:
+        raise TypeError(f"codes{suffix} must be a torch.Tensor of two dims")
+    return codes.shape[0]
 
-    bf, _ = _dtypes()
-    _check_tensor("a", a, bf, 3, device)
-    _check_tensor("b", b, bf, 3, device)
-    _check_tensor("gain", gain, (torch.float32,), 1, device)
-    _check_tensor("index", index, (torch.int32,), 1, device)
-    count, rank = a.shape[0], a.shape[1]
-    _check_shape("a", a, (count, rank, k))
-    _check_shape("b", b, (count, n, rank))
-    _check_shape("gain", gain, (count,))
-    _check_shape("index", index, (m,))
-    return count, rank
+
+def _adapter_addresses(a, b, gain, index, m: int, n: int, k: int, device):
+    """(addresses of a, b, gain and index, count, rank) of an adapter set for m rows of a layer [n, k]."""
+    tensor, bf, _, f32, i32 = _kinds()
+    if not isinstance(a, tensor) or a.ndim != 3:
+        raise TypeError("a must be a torch.Tensor of three dims")
+    count, rank, _ = a.shape
+    return (_address("a", a, bf, (count, rank, k), device), _address("b", b, bf, (count, n, rank), device),
+            _address("gain", gain, f32, (count,), device), _address("index", index, i32, (m,), device), count, rank)
 
 
 def adapters(x, codes, scales, bits: int, a, b, gain, index, out=None):
@@ -463,14 +478,12 @@ def adapters(x, codes, scales, bits: int, a, b, gain, index, out=None):
     gain [count] in float32, index [M] in int32; any M from 1 to MAX_ROWS,
     any rank from 1 to MAX_RANK. A row whose index is not in [0, count) has
     no adapter."""
-    bf, _ = _dtypes()
-    _check_tensor("x", x, bf, 2)
-    m, k = x.shape
-    n = _check_packed(codes, scales, k, bits, x.device)
-    count, rank = _check_adapters(a, b, gain, index, m, n, k, x.device)
-    out = _output("out", out, (m, n), x.device)
-    adapters_raw(x.data_ptr(), m, codes.data_ptr(), scales.data_ptr(), geom(n, k, bits), a.data_ptr(), b.data_ptr(),
-                 gain.data_ptr(), index.data_ptr(), count, rank, out.data_ptr(), _stream_handle(x.device))
+    m, k, device = _rows_of("x", x)
+    n = _packed_rows(codes)
+    packed = _packed_address(codes, scales, n, k, bits, device)
+    set_ = _adapter_addresses(a, b, gain, index, m, n, k, device)
+    out = _output("out", out, (m, n), device)
+    adapters_raw(x.data_ptr(), m, *packed, geom(n, k, bits), *set_, out.data_ptr(), _stream_handle(device))
     return out
 
 
@@ -478,19 +491,17 @@ def adapters_backward(dout, x, codes, scales, bits: int, a, b, gain, index, dx=N
     """Gradients of adapters() for the gradient dout [M, N] of its output:
     (dx [M, K], da [count, rank, K], db [count, N, rank]), bf16, each written
     whole (an adapter without rows gets zeros)."""
-    bf, _ = _dtypes()
-    _check_tensor("x", x, bf, 2)
-    m, k = x.shape
-    n = _check_packed(codes, scales, k, bits, x.device)
-    _check_tensor("dout", dout, bf, 2, x.device)
-    _check_shape("dout", dout, (m, n))
-    count, rank = _check_adapters(a, b, gain, index, m, n, k, x.device)
-    dx = _output("dx", dx, (m, k), x.device)
-    da = _output("da", da, (count, rank, k), x.device)
-    db = _output("db", db, (count, n, rank), x.device)
-    adapters_backward_raw(dout.data_ptr(), x.data_ptr(), m, codes.data_ptr(), scales.data_ptr(), geom(n, k, bits),
-                          a.data_ptr(), b.data_ptr(), gain.data_ptr(), index.data_ptr(), count, rank, dx.data_ptr(),
-                          da.data_ptr(), db.data_ptr(), _stream_handle(x.device))
+    m, k, device = _rows_of("x", x)
+    n = _packed_rows(codes)
+    packed = _packed_address(codes, scales, n, k, bits, device)
+    dout_ptr = _address("dout", dout, _kinds()[1], (m, n), device)
+    set_ = _adapter_addresses(a, b, gain, index, m, n, k, device)
+    count, rank = set_[-2:]
+    dx = _output("dx", dx, (m, k), device)
+    da = _output("da", da, (count, rank, k), device)
+    db = _output("db", db, (count, n, rank), device)
+    adapters_backward_raw(dout_ptr, x.data_ptr(), m, *packed, geom(n, k, bits), *set_, dx.data_ptr(), da.data_ptr(),
+                          db.data_ptr(), _stream_handle(device))
     return dx, da, db
 
 
@@ -499,18 +510,15 @@ def gated(x, codes_gate, scales_gate, codes_up, scales_up, bits: int, out=None, 
     matrices, any M from 1 to MAX_ROWS, evaluated in float32 and rounded once.
     With keep, returns (h, gate, up): the projections that gated_backward()
     takes."""
-    bf, _ = _dtypes()
-    _check_tensor("x", x, bf, 2)
-    m, k = x.shape
-    n = _check_packed(codes_gate, scales_gate, k, bits, x.device, "_gate")
-    _check_packed(codes_up, scales_up, k, bits, x.device, "_up")
-    _check_shape("codes_up", codes_up, codes_gate.shape)
-    h = _output("out", out, (m, n), x.device)
-    gate = _output("gate", None, (m, n), x.device) if keep else None
-    up = _output("up", None, (m, n), x.device) if keep else None
-    gated_raw(x.data_ptr(), m, codes_gate.data_ptr(), scales_gate.data_ptr(), codes_up.data_ptr(),
-              scales_up.data_ptr(), geom(n, k, bits), h.data_ptr(), gate.data_ptr() if keep else 0,
-              up.data_ptr() if keep else 0, _stream_handle(x.device))
+    m, k, device = _rows_of("x", x)
+    n = _packed_rows(codes_gate, "_gate")
+    packed = (*_packed_address(codes_gate, scales_gate, n, k, bits, device, "_gate"),
+              *_packed_address(codes_up, scales_up, n, k, bits, device, "_up"))
+    h = _output("out", out, (m, n), device)
+    gate = _output("gate", None, (m, n), device) if keep else None
+    up = _output("up", None, (m, n), device) if keep else None
+    gated_raw(x.data_ptr(), m, *packed, geom(n, k, bits), h.data_ptr(), gate.data_ptr() if keep else 0,
+              up.data_ptr() if keep else 0, _stream_handle(device))
     return (h, gate, up) if keep else h
 
 
@@ -518,22 +526,16 @@ def gated_backward(dh, gate, up, codes_gate, scales_gate, codes_up, scales_up, b
                    dup=None):
     """Gradients of gated() for the gradient dh [M, N] of h and the kept
     projections: (dx [M, K], dgate [M, N], dup [M, N]), bf16."""
-    bf, cw = _dtypes()
-    _check_tensor("dh", dh, bf, 2)
-    m, n = dh.shape
-    for name, t in (("gate", gate), ("up", up)):
-        _check_tensor(name, t, bf, 2, dh.device)
-        _check_shape(name, t, (m, n))
-    _check_tensor("codes_gate", codes_gate, cw, 2, dh.device)
-    k = _packed_k(codes_gate, bits)
-    for suffix, c, s in (("_gate", codes_gate, scales_gate), ("_up", codes_up, scales_up)):
-        rows = _check_packed(c, s, k, bits, dh.device, suffix)
-        if rows != n:
-            raise ValueError(f"codes{suffix} must have {n} rows, got {rows}")
-    dx = _output("dx", dx, (m, k), dh.device)
-    dgate = _output("dgate", dgate, (m, n), dh.device)
-    dup = _output("dup", dup, (m, n), dh.device)
-    gated_backward_raw(dh.data_ptr(), gate.data_ptr(), up.data_ptr(), m, codes_gate.data_ptr(),
-                       scales_gate.data_ptr(), codes_up.data_ptr(), scales_up.data_ptr(), geom(n, k, bits),
-                       dx.data_ptr(), dgate.data_ptr(), dup.data_ptr(), _stream_handle(dh.device))
+    m, n, device = _rows_of("dh", dh)
+    bf = _kinds()[1]
+    kept = _address("gate", gate, bf, (m, n), device), _address("up", up, bf, (m, n), device)
+    _packed_rows(codes_gate, "_gate")
+    k = codes_gate.shape[1] * 32 // bits if bits in (2, 3, 4) else 0
+    packed = (*_packed_address(codes_gate, scales_gate, n, k, bits, device, "_gate"),
+              *_packed_address(codes_up, scales_up, n, k, bits, device, "_up"))
+    dx = _output("dx", dx, (m, k), device)
+    dgate = _output("dgate", dgate, (m, n), device)
+    dup = _output("dup", dup, (m, n), device)
+    gated_backward_raw(dh.data_ptr(), *kept, m, *packed, geom(n, k, bits), dx.data_ptr(), dgate.data_ptr(),
+                       dup.data_ptr(), _stream_handle(device))
     return dx, dgate, dup

@@ -838,7 +838,7 @@ struct Shrink {
   int32_t m, cols, count, rank, rank_p;
   int32_t span, spans;
 };
-constexpr int kMaxSpans = 16;      // one batch of loads
+constexpr int kSpanBatch = 16;     // spans that a thread adds: one batch of loads
 constexpr int kFactorStride = 40;  // elements per staged row of B: 32 and padding
 
 template <bool T, int MS, int WAVES>
@@ -847,6 +847,7 @@ __global__ __launch_bounds__(64 * WAVES) void shrink_kernel(Shrink S) {
   __shared__ f32x4 part[WAVES][kPart];
   __shared__ __attribute__((aligned(16))) uint16_t staged[T ? WAVES : 1][T ? 32 * kFactorStride : 1];
   __shared__ uint32_t arrived;
+  __shared__ float gains[16 * MS];  // of the rows; zero without an adapter
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int j = lane & 15, g = lane >> 4;
   const int span = blockIdx.y, z = blockIdx.z;
@@ -854,6 +855,8 @@ __global__ __launch_bounds__(64 * WAVES) void shrink_kernel(Shrink S) {
   // lane l: the adapter of row m0 + l
   int idx = lane < 16 * MS && m0 + lane < S.m ? S.index[m0 + lane] : -1;
   if (idx >= S.count) idx = -1;
+  float gain = 0.f;  // (used at the end only: loaded now, it is not waited for there)
+  if (wave == 0 && idx >= 0) gain = S.gain[idx];
   const uint64_t named = __ballot(idx >= 0);
   int distinct = 0;
   for (uint64_t left = named; left; ++distinct) left &= ~__ballot(idx == __builtin_amdgcn_readlane(idx, __builtin_ctzll(left)));
@@ -967,6 +970,7 @@ __global__ __launch_bounds__(64 * WAVES) void shrink_kernel(Shrink S) {
     part[wave][(2 * i) * 64 + lane] = acc[i][0];
     part[wave][(2 * i + 1) * 64 + lane] = acc[i][1];
   }
+  if (wave == 0 && lane < 16 * MS) gains[lane] = gain;
   __syncthreads();
   const int64_t cell = (int64_t)blockIdx.x * gridDim.z + z;
   float *const base = S.partials + cell * S.spans * (kPart * 4);
@@ -988,26 +992,35 @@ __global__ __launch_bounds__(64 * WAVES) void shrink_kernel(Shrink S) {
     if (arrived != (uint32_t)S.spans - 1) return;
     if (tid == 0) __hip_atomic_store(&S.counters[cell], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
+  // SHARES threads add a vector's spans, 16 each (past the last span: outside
+  // the buffer, zero), and their sums meet in LDS.
+  constexpr int SHARES = 64 * WAVES / kPart > 0 ? 64 * WAVES / kPart : 1;
+  if (S.spans > 1) {
+    for (int v = tid; v < kPart * SHARES; v += 64 * WAVES) {
+      f32x4 p[kSpanBatch], sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < kSpanBatch; ++s)
+        p[s] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                             ws, (uint32_t)(((v / kPart * kSpanBatch + s) * kPart + v % kPart) * 16), 0, kSc1));
+#pragma unroll
+      for (int s = 0; s < kSpanBatch; ++s) sum += p[s];
+      part[v / kPart][v % kPart] = sum;
+    }
+    __syncthreads();
+  }
   for (int v = tid; v < kPart; v += 64 * WAVES) {
     f32x4 sum = {0.f, 0.f, 0.f, 0.f};
     if (S.spans > 1) {
-      f32x4 p[kMaxSpans];
 #pragma unroll
-      for (int s = 0; s < kMaxSpans; ++s)  // past the last span: outside the buffer, zero
-        p[s] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(ws, (uint32_t)((s * kPart + v) * 16), 0, kSc1));
-#pragma unroll
-      for (int s = 0; s < kMaxSpans; ++s) sum += p[s];
+      for (int s = 0; s < SHARES; ++s) sum += part[s][v];
     } else {
       sum = sum_waves(v);
     }
     const int l = v & 63, r = 32 * z + 16 * ((v >> 6) & 1) + (l & 15);
-    const int64_t row0 = m0 + 16 * (v >> 7) + 4 * (l >> 4);
+    const int row0 = 16 * (v >> 7) + 4 * (l >> 4);
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      if (row0 + e < S.m) {
-        const int i = S.index[row0 + e];
-        S.t[(row0 + e) * S.rank_p + r] = i >= 0 && i < S.count ? sum[e] * S.gain[i] : 0.f;
-      }
+      if (m0 + row0 + e < S.m) S.t[(m0 + row0 + e) * S.rank_p + r] = sum[e] * gains[row0 + e];
   }
 }
 
@@ -1570,15 +1583,21 @@ struct ShrinkShape {
   int ms, spans, span;
   size_t partial_bytes;
 };
-ShrinkShape shrink_shape(int m, int cols, int rank, int cus) {
+ShrinkShape shrink_shape(int m, int cols, int count, int rank, int cus) {
   ShrinkShape s{};
   s.ms = m >= 512 ? 4 : 1;
   s.groups = ((int64_t)m + 16 * s.ms - 1) / (16 * s.ms);
   s.cells = s.groups * ((rank + 31) / 32);
   int64_t spans = (2 * (int64_t)cus + s.cells - 1) / s.cells;
-  const int most = (cols + 255) / 256;
+  // A wave takes 128 columns at a time, and the waves that share an adapter as
+  // many side by side: a narrower span leaves waves without work, and up to two
+  // such spans cost less than what joining spans does (about 3 us).
+  const int named = s.ms == 1 && count < 8 ? (count < m ? count : m) : 8;
+  const int least = 128 * (8 / named);
+  const int64_t most = cols <= 2 * least ? 1 : (cols + least - 1) / least;
   if (spans > most) spans = most;
-  if (spans > kMaxSpans) spans = kMaxSpans;
+  const int batches = s.ms == 1 ? 4 : 1;  // SHARES of the kernel
+  if (spans > kSpanBatch * batches) spans = kSpanBatch * batches;
   s.span = (int)((cols + spans - 1) / spans + 31) / 32 * 32;
   s.spans = (cols + s.span - 1) / s.span;
   s.partial_bytes = s.spans > 1 ? (size_t)s.cells * s.spans * s.ms * 2 * 1024 : 0;
@@ -1624,7 +1643,7 @@ trellis_status trellis_adapters(const uint16_t *x, int32_t m, const uint32_t *co
   TRELLIS_TRY(device(dev, cus));
   const int rank_p = (rank + 31) / 32 * 32;
   const Plan s = plan_of(kForward, g, m, 1, cus);
-  const ShrinkShape h = shrink_shape(m, g.k, rank, cus);
+  const ShrinkShape h = shrink_shape(m, g.k, count, rank, cus);
   const size_t t_bytes = up256((size_t)m * rank_p * 4), hp = up256(h.partial_bytes);
   Space *w = nullptr;
   TRELLIS_TRY(space(dev, stream, t_bytes + hp + s.bytes, (size_t)(s.counters > h.cells ? s.counters : h.cells), w));
@@ -1661,7 +1680,7 @@ trellis_status trellis_adapters_backward(const uint16_t *dout, const uint16_t *x
   TRELLIS_TRY(device(dev, cus));
   const int rank_p = (rank + 31) / 32 * 32;
   const Plan s = plan_of(kTransposed, g, m, 1, cus);
-  const ShrinkShape hx = shrink_shape(m, g.k, rank, cus), hd = shrink_shape(m, g.n, rank, cus);
+  const ShrinkShape hx = shrink_shape(m, g.k, count, rank, cus), hd = shrink_shape(m, g.n, count, rank, cus);
   const size_t t_bytes = up256((size_t)m * rank_p * 4), r_bytes = up256((size_t)count * sizeof(i32x2));
   size_t part = hx.partial_bytes > hd.partial_bytes ? hx.partial_bytes : hd.partial_bytes;
   if (s.bytes > part) part = s.bytes;
