@@ -66,6 +66,7 @@ struct Product {
   float *partials;
   uint32_t *counters;
   int32_t units_q, units_r;  // units (tiles * steps) of a workgroup: units_q, the first units_r one more
+  int32_t parts;             // > 0: instead, each tile's steps are split over this many workgroups
   int32_t m, n, k;
   int32_t groups;    // groups of output columns
   int32_t steps;     // contraction steps of a tile (all matrices)
@@ -252,8 +253,8 @@ namespace {
 //   transposed  group = one 256-column block; wave (wn, wk): columns 64 wn .. +63
 //               as four 16-column tiles (tile e: columns 4 j + e), rows
 //               128 wk .. +127 of each 256-row step
-// The units (tile, step) are split evenly over the workgroups; a tile that
-// several share goes through `partials`, summed in a fixed order by the
+// The units (tile, step) are split evenly over the workgroups, or each tile over
+// the same number of them (see shape_of); a tile that several share goes through `partials`, summed in a fixed order by the
 // workgroup that arrives last. Code words and P's rows are loaded two steps
 // ahead (transposed: code words one 32-row part, P's rows one step ahead).
 // OCC: waves per SIMD (4: two workgroups share a CU, so that one decodes while
@@ -284,7 +285,10 @@ __global__ __launch_bounds__(kThreads, OCC) void product_kernel(Product P) {
 
   const uint32_t row_bytes = (uint32_t)(P.k >> 8) * wpb * 4;
   const int cols = kT ? P.n : P.k;  // columns of P
-  auto start_of = [&](int c) { return c * P.units_q + (c < P.units_r ? c : P.units_r); };
+  auto start_of = [&](int c) {
+    return P.parts ? c / P.parts * P.steps + c % P.parts * P.steps / P.parts
+                   : c * P.units_q + (c < P.units_r ? c : P.units_r);
+  };
   int unit = start_of(blockIdx.x);
   const int end = start_of(blockIdx.x + 1);
   // The current segment: steps s0 .. s1 - 1 of a tile.
@@ -762,7 +766,7 @@ __global__ __launch_bounds__(kThreads, OCC) void product_kernel(Product P) {
   for (int i = 0; i < 2; ++i) {
     const int t = i ? shared1 : shared0;
     if (t < 0) continue;
-    const int c0 = owner(t * P.steps), c1 = owner(t * P.steps + P.steps - 1);
+    const int c0 = P.parts ? t * P.parts : owner(t * P.steps), c1 = P.parts ? c0 + P.parts - 1 : owner(t * P.steps + P.steps - 1);
     if (arrived[i] != (uint32_t)(c1 - c0)) continue;
     if (tid == 0) __hip_atomic_store(&P.counters[t], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     const int tm0 = t / P.groups * BM, tgroup = t % P.groups;
@@ -1322,7 +1326,7 @@ ProductFn product_fn(int kind, int bits, int i) {
 struct Shape {
   int kind, bits, mt;  // mt: index into kRowTiles
   int64_t tiles, units;
-  int groups, steps, steps1, grid;
+  int groups, steps, steps1, grid, parts;
   size_t partial_bytes, lds;
 };
 Shape shape_of(int kind, trellis_geom g, int32_t m, int matrices, int cus) {
@@ -1345,6 +1349,15 @@ Shape shape_of(int kind, trellis_geom g, int32_t m, int matrices, int cus) {
   s.units = s.tiles * s.steps;
   const int64_t room = (int64_t)cus * waves_per_simd(kind, mt) / 2;  // workgroups the card holds at once
   s.grid = (int)(s.units < room ? s.units : room);
+  // Tiles split over the same number of workgroups each, where that leaves at
+  // most a tenth of the card idle: no workgroup then reduces two tiles' parts
+  // (K = 17408, N = 5120, 117 rows: 40 tiles of 68 steps, 6 workgroups each).
+  // Tiles of up to three steps are not split: joining costs more than a step.
+  const int64_t each = room / s.tiles;
+  if (each >= 1 && (s.steps <= 3 || (each <= s.steps && s.tiles * each * 10 >= room * 9))) {
+    s.parts = s.steps <= 3 ? 1 : (int)each;
+    s.grid = (int)s.tiles * s.parts;
+  }
   s.partial_bytes = (size_t)2 * s.grid * bm * (kind == kGated ? 128 : bn) * 4;
   s.lds = (size_t)2 * bm * kStride + (kind == kTransposed ? 512 * 12 + 8 * 4 : 0);
   return s;
@@ -1364,6 +1377,7 @@ trellis_status launch(const Shape &s, Product p, hipStream_t stream) {
   }
   p.units_q = (int)(s.units / s.grid);
   p.units_r = (int)(s.units % s.grid);
+  p.parts = s.parts;
   p.groups = s.groups;
   p.steps = s.steps;
   p.steps1 = s.steps1;
