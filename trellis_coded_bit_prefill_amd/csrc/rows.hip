@@ -846,15 +846,24 @@ constexpr int kSpanBatch = 16;     // spans that a thread adds: one batch of loa
 constexpr int kFactorStride = 40;  // elements per staged row of B: 32 and padding
 
 template <bool T, int MS, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void shrink_kernel(Shrink S) {
+struct ShrinkSpace {
+  f32x4 part[WAVES][MS * 2 * 64];
+  uint16_t staged[T ? WAVES : 1][T ? 32 * kFactorStride : 8];
+  uint32_t arrived;
+  float gains[16 * MS];  // of the rows; zero without an adapter
+};
+
+// z of zs: the rank columns' tile.
+template <bool T, int MS, int WAVES>
+__device__ __forceinline__ void shrink(const Shrink &S, int z, int zs, ShrinkSpace<T, MS, WAVES> &space) {
   constexpr int kPart = MS * 2 * 64;  // vectors of four sums: [row tile][rank tile][lane]
-  __shared__ f32x4 part[WAVES][kPart];
-  __shared__ __attribute__((aligned(16))) uint16_t staged[T ? WAVES : 1][T ? 32 * kFactorStride : 1];
-  __shared__ uint32_t arrived;
-  __shared__ float gains[16 * MS];  // of the rows; zero without an adapter
+  auto &part = space.part;
+  auto &staged = space.staged;
+  auto &arrived = space.arrived;
+  auto &gains = space.gains;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int j = lane & 15, g = lane >> 4;
-  const int span = blockIdx.y, z = blockIdx.z;
+  const int span = blockIdx.y;
   const int64_t m0 = (int64_t)blockIdx.x * (16 * MS);
   // lane l: the adapter of row m0 + l
   int idx = lane < 16 * MS && m0 + lane < S.m ? S.index[m0 + lane] : -1;
@@ -976,7 +985,7 @@ __global__ __launch_bounds__(64 * WAVES) void shrink_kernel(Shrink S) {
   }
   if (wave == 0 && lane < 16 * MS) gains[lane] = gain;
   __syncthreads();
-  const int64_t cell = (int64_t)blockIdx.x * gridDim.z + z;
+  const int64_t cell = (int64_t)blockIdx.x * zs + z;
   float *const base = S.partials + cell * S.spans * (kPart * 4);
   const __amdgpu_buffer_rsrc_t ws = __builtin_amdgcn_make_buffer_rsrc(base, (short)0, S.spans * kPart * 16, kRawBuffer);
   auto sum_waves = [&](int v) {
@@ -1028,29 +1037,55 @@ __global__ __launch_bounds__(64 * WAVES) void shrink_kernel(Shrink S) {
   }
 }
 
+template <int MS, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void shrink_kernel(Shrink S) {
+  __shared__ __attribute__((aligned(16))) ShrinkSpace<false, MS, WAVES> space;
+  shrink<false, MS, WAVES>(S, blockIdx.z, gridDim.z, space);
+}
+
 // The 32-row chunks that an adapter's rows lie in: range[a] = [first, last + 1).
-__global__ __launch_bounds__(256) void range_kernel(const int32_t *__restrict__ index, int m, i32x2 *__restrict__ range) {
-  __shared__ int lo[4], hi[4];
-  const int a = blockIdx.x, tid = threadIdx.x;
+__device__ __forceinline__ void chunk_range(const int32_t *__restrict__ index, int m, int a, i32x2 *range, int (&ends)[2]) {
+  if (threadIdx.x == 0) {
+    ends[0] = 0x7fffffff;
+    ends[1] = -1;
+  }
+  __syncthreads();
   int first = 0x7fffffff, last = -1;
-  for (int i = tid; i < m; i += 256)
+  for (int i = threadIdx.x; i < m; i += blockDim.x)
     if (index[i] == a) {
       if (first == 0x7fffffff) first = i;
       last = i;
     }
-  for (int o = 32; o > 0; o >>= 1) {
-    first = min(first, __shfl_xor(first, o));
-    last = max(last, __shfl_xor(last, o));
-  }
-  if ((tid & 63) == 0) {
-    lo[tid >> 6] = first;
-    hi[tid >> 6] = last;
+  if (last >= 0) {
+    atomicMin(&ends[0], first);
+    atomicMax(&ends[1], last);
   }
   __syncthreads();
-  if (tid == 0) {
-    first = min(min(lo[0], lo[1]), min(lo[2], lo[3]));
-    last = max(max(hi[0], hi[1]), max(hi[2], hi[3]));
-    range[a] = last < 0 ? i32x2{0, 0} : i32x2{first >> 5, (last >> 5) + 1};
+  if (threadIdx.x == 0) range[a] = ends[1] < 0 ? i32x2{0, 0} : i32x2{ends[0] >> 5, (ends[1] >> 5) + 1};
+}
+
+// What the backward pass needs before its products, in one launch: t, u (z
+// below zs: t, below 2 zs: u) and the adapters' chunk ranges (z = 2 zs). Three
+// launches of their own took about 10 us more.
+struct BackwardSums {
+  Shrink t, u;
+  i32x2 *range;
+};
+template <int MS, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void backward_sums_kernel(BackwardSums B) {
+  __shared__ __attribute__((aligned(16))) union {
+    ShrinkSpace<false, MS, WAVES> t;
+    ShrinkSpace<true, MS, WAVES> u;
+    int ends[2];
+  } space;
+  const int zs = gridDim.z >> 1, z = blockIdx.z;
+  if (z < zs) {
+    if ((int64_t)blockIdx.x * (16 * MS) < B.t.m && (int)blockIdx.y < B.t.spans) shrink<false, MS, WAVES>(B.t, z, zs, space.t);
+  } else if (z < 2 * zs) {
+    if ((int64_t)blockIdx.x * (16 * MS) < B.u.m && (int)blockIdx.y < B.u.spans) shrink<true, MS, WAVES>(B.u, z - zs, zs, space.u);
+  } else {
+    for (int a = blockIdx.y * gridDim.x + blockIdx.x; a < B.t.count; a += gridDim.x * gridDim.y)
+      chunk_range(B.t.index, B.t.m, a, B.range, space.ends);
   }
 }
 
@@ -1617,14 +1652,18 @@ ShrinkShape shrink_shape(int m, int cols, int count, int rank, int cus) {
   s.partial_bytes = s.spans > 1 ? (size_t)s.cells * s.spans * s.ms * 2 * 1024 : 0;
   return s;
 }
-template <bool T>
-trellis_status launch_shrink(const ShrinkShape &h, Shrink s, hipStream_t stream) {
-  s.span = h.span;
-  s.spans = h.spans;
+trellis_status launch_shrink(const ShrinkShape &h, const Shrink &s, hipStream_t stream) {
   (void)hipGetLastError();
   const dim3 grid((unsigned)h.groups, (unsigned)h.spans, (unsigned)(s.rank_p / 32));
-  if (h.ms == 4) hipLaunchKernelGGL((shrink_kernel<T, 4, 4>), grid, dim3(256), 0, stream, s);
-  else hipLaunchKernelGGL((shrink_kernel<T, 1, 8>), grid, dim3(512), 0, stream, s);
+  if (h.ms == 4) hipLaunchKernelGGL((shrink_kernel<4, 4>), grid, dim3(256), 0, stream, s);
+  else hipLaunchKernelGGL((shrink_kernel<1, 8>), grid, dim3(512), 0, stream, s);
+  return hipGetLastError() == hipSuccess ? TRELLIS_OK : TRELLIS_E_HIP;
+}
+trellis_status launch_backward_sums(const ShrinkShape &ht, const ShrinkShape &hu, const BackwardSums &b, hipStream_t stream) {
+  (void)hipGetLastError();
+  const dim3 grid((unsigned)ht.groups, (unsigned)(ht.spans > hu.spans ? ht.spans : hu.spans), (unsigned)(2 * (b.t.rank_p / 32) + 1));
+  if (ht.ms == 4) hipLaunchKernelGGL((backward_sums_kernel<4, 4>), grid, dim3(256), 0, stream, b);
+  else hipLaunchKernelGGL((backward_sums_kernel<1, 8>), grid, dim3(512), 0, stream, b);
   return hipGetLastError() == hipSuccess ? TRELLIS_OK : TRELLIS_E_HIP;
 }
 
@@ -1662,8 +1701,8 @@ trellis_status trellis_adapters(const uint16_t *x, int32_t m, const uint32_t *co
   Space *w = nullptr;
   TRELLIS_TRY(space(dev, stream, t_bytes + hp + s.bytes, (size_t)(s.counters > h.cells ? s.counters : h.cells), w));
   float *const t = reinterpret_cast<float *>(w->bytes);
-  Shrink sh{x, a, gain, index, t, reinterpret_cast<float *>(w->bytes + t_bytes), w->counters, m, g.k, count, rank, rank_p, 0, 0};
-  TRELLIS_TRY(launch_shrink<false>(h, sh, stream));
+  Shrink sh{x, a, gain, index, t, reinterpret_cast<float *>(w->bytes + t_bytes), w->counters, m, g.k, count, rank, rank_p, h.span, h.spans};
+  TRELLIS_TRY(launch_shrink(h, sh, stream));
   Product p{};
   p.p = x;
   p.codes = codes;
@@ -1696,20 +1735,21 @@ trellis_status trellis_adapters_backward(const uint16_t *dout, const uint16_t *x
   const Plan s = plan_of(kTransposed, g, m, 1, cus);
   const ShrinkShape hx = shrink_shape(m, g.k, count, rank, cus), hd = shrink_shape(m, g.n, count, rank, cus);
   const size_t t_bytes = up256((size_t)m * rank_p * 4), r_bytes = up256((size_t)count * sizeof(i32x2));
-  size_t part = hx.partial_bytes > hd.partial_bytes ? hx.partial_bytes : hd.partial_bytes;
-  if (s.bytes > part) part = s.bytes;
-  const int64_t counters = s.counters > hx.cells ? s.counters : hx.cells;  // (hd has as many cells as hx)
+  // t's and u's spans are joined at the same time: partials and counters of their own.
+  const size_t part_t = up256(hx.partial_bytes), sums = part_t + hd.partial_bytes;
+  const int64_t cells = hx.cells + hd.cells;
   Space *w = nullptr;
-  TRELLIS_TRY(space(dev, stream, 2 * t_bytes + r_bytes + part, (size_t)counters, w));
+  TRELLIS_TRY(space(dev, stream, 2 * t_bytes + r_bytes + (sums > s.bytes ? sums : s.bytes),
+                    (size_t)(s.counters > cells ? s.counters : cells), w));
   float *const t = reinterpret_cast<float *>(w->bytes), *const u = reinterpret_cast<float *>(w->bytes + t_bytes);
   i32x2 *const range = reinterpret_cast<i32x2 *>(w->bytes + 2 * t_bytes);
-  float *const partials = reinterpret_cast<float *>(w->bytes + 2 * t_bytes + r_bytes);
-  TRELLIS_TRY(launch_shrink<false>(
-      hx, Shrink{x, a, gain, index, t, partials, w->counters, m, g.k, count, rank, rank_p, 0, 0}, stream));
-  TRELLIS_TRY(launch_shrink<true>(
-      hd, Shrink{dout, b, gain, index, u, partials, w->counters, m, g.n, count, rank, rank_p, 0, 0}, stream));
-  hipLaunchKernelGGL(range_kernel, dim3((unsigned)count), dim3(256), 0, stream, index, m, range);
-  if (hipGetLastError() != hipSuccess) return TRELLIS_E_HIP;
+  unsigned char *const rest = w->bytes + 2 * t_bytes + r_bytes;
+  const BackwardSums b_sums{Shrink{x, a, gain, index, t, reinterpret_cast<float *>(rest), w->counters, m, g.k, count, rank,
+                                   rank_p, hx.span, hx.spans},
+                            Shrink{dout, b, gain, index, u, reinterpret_cast<float *>(rest + part_t), w->counters + hx.cells, m,
+                                   g.n, count, rank, rank_p, hd.span, hd.spans},
+                            range};
+  TRELLIS_TRY(launch_backward_sums(hx, hd, b_sums, stream));
   Product p{};
   p.p = dout;
   p.codes = codes;
@@ -1720,7 +1760,7 @@ trellis_status trellis_adapters_backward(const uint16_t *dout, const uint16_t *x
   p.n = g.n;
   p.k = g.k;
   p.low = LowRank{index, a, u, count, rank, rank_p};
-  TRELLIS_TRY(run(s, kTransposed, g, p, nullptr, reinterpret_cast<unsigned char *>(partials), stream));
+  TRELLIS_TRY(run(s, kTransposed, g, p, nullptr, rest, stream));
   Outer o{x, dout, u, t, index, range, da, db, m, g.n, g.k, rank, rank_p, g.k / 64};
   hipLaunchKernelGGL(outer_kernel, dim3((unsigned)(o.tiles_a + (g.n + 63) / 64), (unsigned)count, (unsigned)(rank_p / 32)),
                      dim3(256), 0, stream, o);
