@@ -897,18 +897,18 @@ __device__ __forceinline__ void shrink(const Shrink &S, int z, int zs, ShrinkSpa
     // U steps of 32 columns are loaded before the first is multiplied. Loads
     // of what does not exist (columns past the span, rows past m, rank columns
     // past the rank) take an offset outside their buffer and give zero.
-    constexpr int U = MS == 1 ? 4 : 2;
+    constexpr int U = MS == 1 && !T ? 4 : 2;
     constexpr uint32_t kNone = 0x80000000u;
     const bool vectors = T && (S.rank & 7) == 0, wide = !T || (S.cols & 7) == 0;
     const uint32_t block = (uint32_t)S.rank * (uint32_t)S.cols;
     const __amdgpu_buffer_rsrc_t rf = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<uint16_t *>(S.factor + (int64_t)a * block), (short)0, (int)(block * 2), kRawBuffer);
-    for (int c0 = span * S.span + 32 * part_i; c0 < c_end; c0 += 32 * parts * U) {
+    for (int c0 = span * S.span + 32 * U * part_i; c0 < c_end; c0 += 32 * U * parts) {
       bf16x8 w[U][2];
       u32x4 b[U][2], x[U][MS];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int cu = c0 + 32 * parts * u, c = cu + 8 * g;
+        const int cu = c0 + 32 * u, c = cu + 8 * g;
         const bool in = cu < c_end;
 #pragma unroll
         for (int i = 0; i < MS; ++i) {
@@ -1637,7 +1637,7 @@ ShrinkShape shrink_shape(int m, int cols, int count, int rank, int cus) {
   s.ms = m >= 512 ? 4 : 1;
   s.groups = ((int64_t)m + 16 * s.ms - 1) / (16 * s.ms);
   s.cells = s.groups * ((rank + 31) / 32);
-  int64_t spans = (2 * (int64_t)cus + s.cells - 1) / s.cells;
+  int64_t spans = ((int64_t)cus + s.cells - 1) / s.cells;
   // A wave takes 128 columns at a time, and the waves that share an adapter as
   // many side by side: a narrower span leaves waves without work, and up to two
   // such spans cost less than what joining spans does (about 3 us).
