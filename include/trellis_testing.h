@@ -21,6 +21,18 @@ extern "C" {
  * affected. */
 int trellis_test_force_table(int kind);
 
+/* How later calls of the fine-tuned layers' entry points (trellis_adapters and
+ * the ones declared after it) compute their product, process-wide:
+ *   path   -1 the library's own choice (the default), 0 weights decoded in the
+ *          product, 1 weights decoded once into the workspace;
+ *   tiles  16-column tiles of weights decoded per launch with path 1, rounded
+ *          up to whole workgroup tiles: 0 the library's own limit.
+ * Both paths compute the same sums in different orders; the hook lets tests run
+ * each on any number of rows, and several launches on a small matrix. Returns
+ * 0, or -2 (and changes nothing) for a path outside [-1, 1] or tiles < 0.
+ * Thread-safe; a call already enqueued is not affected. */
+int trellis_test_force_path(int path, int tiles);
+
 #ifdef __cplusplus
 }
 #endif

@@ -103,6 +103,63 @@ def test_rows_without_an_adapter_equal_the_layer_alone():
     assert base.any() and np.array_equal(mixed[base], alone[base])
 
 
+@pytest.fixture
+def force_path():
+    """Setter for the library's product path; its own choice is restored when the test ends."""
+    yield tp.force_path
+    tp.force_path(None)
+
+
+# rows at which a tile, a workgroup's tile or the number of tiles changes
+@pytest.mark.parametrize("bits", [2, 3, 4])
+@pytest.mark.parametrize("m,n,k,rank", [(1, 4, 256, 3), (16, 68, 512, 8), (63, 260, 768, 32), (255, 132, 256, 40),
+                                        (256, 516, 512, 16), (257, 1028, 256, 7), (600, 36, 1280, 64)])
+def test_weights_decoded_once(force_path, m, n, k, rank, bits):
+    print(f"adapters once m={m} n={n} k={k} rank={rank} bits={bits}", flush=True)
+    d = ref.draw(np.random.default_rng(m + n + rank), m, n, k, bits, rank=rank, count=3)
+    force_path(True)
+    check_both(d, bits, f"once m={m} n={n} k={k} rank={rank}")
+
+
+@pytest.mark.parametrize("m", [300, 641])
+def test_weights_decoded_in_the_product_of_many_rows(force_path, m):
+    print(f"adapters in the product m={m}", flush=True)
+    d = ref.draw(np.random.default_rng(m), m, 388, 1024, 4, rank=16, count=4)
+    force_path(False)
+    check_both(d, 4, f"in the product m={m}")
+
+
+def test_weights_decoded_in_several_launches(force_path):
+    # 64 and 96 tiles of weights per launch: forward 1540 / 16 = 97 tiles, transposed 2048 / 16 = 128
+    print("adapters slabs", flush=True)
+    d = ref.draw(np.random.default_rng(31), 70, 1540, 2048, 4, rank=24, count=3)
+    force_path(True, 16)
+    check_both(d, 4, "slabs")
+    force_path(True, 0)
+    whole = forward(d, 4)
+    force_path(True, 16)
+    assert np.array_equal(forward(d, 4), whole)
+
+
+@pytest.mark.parametrize("path", [False, True])
+def test_infinite_weights_of_another_adapter(force_path, path):
+    # Rows 0 .. 19 and 20 .. 39 share tiles of 16 rows: the second adapter's
+    # infinities must not turn the first's rows into NaN by a zero.
+    print(f"adapters infinite path={path}", flush=True)
+    d = ref.draw(np.random.default_rng(32), 40, 132, 512, 4, rank=8, count=2)
+    d["index"] = np.repeat([0, 1], 20).astype(np.int32)
+    force_path(path)
+    clean, grads = forward(d, 4), backward(d, 4)
+    a_bits, b_bits = d["a_bits"].copy(), d["b_bits"].copy()
+    a_bits[1], b_bits[1] = 0x7F80, 0xFF80
+    bad = dict(d, a_bits=a_bits, b_bits=b_bits)
+    out, bad_grads = forward(bad, 4), backward(bad, 4)
+    assert np.array_equal(out[:20], clean[:20])
+    assert np.array_equal(bad_grads["dx"][:20], grads["dx"][:20])
+    for name in ("da", "db"):
+        assert np.array_equal(bad_grads[name][0], grads[name][0])
+
+
 def test_an_adapters_nan_and_infinity_stay_in_its_rows():
     print("adapters nan", flush=True)
     m, n, k = 40, 68, 512
@@ -125,10 +182,13 @@ def test_an_adapters_nan_and_infinity_stay_in_its_rows():
     assert np.isnan(ref.bf16_bits_to_f32(out[d["index"] == 1])).all()
 
 
-def test_extreme_scales():
+@pytest.mark.parametrize("path", [False, True])
+@pytest.mark.parametrize("bits", [2, 3, 4])
+def test_extreme_scales(force_path, bits, path):
     # Rows whose scale is zero, subnormal, tiny or huge decode by the page's chain.
-    print("adapters scales", flush=True)
-    bits, n, k = 4, 132, 512
+    print(f"adapters scales bits={bits} path={path}", flush=True)
+    n, k = 132, 512
+    force_path(path)
     d = ref.draw(np.random.default_rng(9), 20, n, k, bits, rank=4, count=2)
     for i, s in enumerate([0.0, 2.0 ** -130, 2.0 ** -115, 2.0 ** 112, -0.01]):
         d["scales"][5 + 9 * i] = ref.bf16(np.float32(s))[0][0]

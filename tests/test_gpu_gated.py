@@ -79,6 +79,40 @@ def test_rows(m):
     check_backward(d, f"m={m}")
 
 
+@pytest.fixture
+def force_path():
+    """Setter for the library's product path; its own choice is restored when the test ends."""
+    yield tp.force_path
+    tp.force_path(None)
+
+
+@pytest.mark.parametrize("bits", [2, 3, 4])
+@pytest.mark.parametrize("m,n,k", [(1, 4, 256), (16, 68, 512), (255, 132, 256), (257, 1028, 256), (600, 36, 1280)])
+def test_weights_decoded_once(force_path, m, n, k, bits):
+    print(f"gated once m={m} n={n} k={k} bits={bits}", flush=True)
+    d = draw(m + n + k, m, n, k, bits)
+    force_path(True)
+    check_forward(d, f"once m={m} n={n} k={k}")
+    check_backward(d, f"once m={m} n={n} k={k}")
+
+
+@pytest.mark.parametrize("m", [300, 641])
+def test_weights_decoded_in_the_product_of_many_rows(force_path, m):
+    print(f"gated in the product m={m}", flush=True)
+    d = draw(m, m, 388, 1024, 4)
+    force_path(False)
+    check_forward(d, f"in the product m={m}")
+    check_backward(d, f"in the product m={m}")
+
+
+def test_weights_decoded_in_several_launches(force_path):
+    print("gated slabs", flush=True)
+    d = draw(9, 70, 1540, 2048, 4)
+    force_path(True, 16)
+    check_forward(d, "slabs")
+    check_backward(d, "slabs")
+
+
 def test_far_gates_keep_their_limits():
     # Gates at which exp overflows: silu and its derivative reach their limits.
     print("gated far gates", flush=True)

@@ -66,6 +66,16 @@ def test_adapter_refusals(lib, entry):
         tp.adapters_raw(FAKE, 1, FAKE, FAKE, tp.geom(**GOOD), FAKE, FAKE, FAKE, FAKE, 1, 129, FAKE, 0)
 
 
+def test_path_hook_checks_its_arguments(lib):
+    tp.force_path(True, 16)
+    tp.force_path(False)
+    tp.force_path(None)
+    assert lib.trellis_test_force_path(2, 0) == -2
+    assert lib.trellis_test_force_path(0, -1) == -2
+    with pytest.raises(ValueError):
+        tp.force_path(5)
+
+
 def test_python_checks_refuse_host_tensors():
     import torch
 

@@ -45,7 +45,7 @@ EXPORTED = ("trellis_supported", "trellis_decode", "trellis_prefill", "trellis_m
             "trellis_gate_up", "trellis_prefill_noalloc", "trellis_adapters", "trellis_adapters_backward",
             "trellis_gated", "trellis_gated_backward", "trellis_status_string")
 # Test and tuning hooks (include/trellis_testing.h).
-EXPORTED_TESTING = ("trellis_test_force_table",)
+EXPORTED_TESTING = ("trellis_test_force_table", "trellis_test_force_path")
 TABLES = {"value": 0, "code": 1, "pair": 2}
 
 
@@ -120,6 +120,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     L.trellis_gated_backward.restype = ctypes.c_int
     L.trellis_test_force_table.argtypes = [ctypes.c_int]
     L.trellis_test_force_table.restype = ctypes.c_int
+    L.trellis_test_force_path.argtypes = [ctypes.c_int, ctypes.c_int]
+    L.trellis_test_force_path.restype = ctypes.c_int
     _lib = L
     return L
 
@@ -133,6 +135,15 @@ def force_table(name):
     if prev < -1:
         raise ValueError(f"bad table {name!r}")
     return None if prev == -1 else {v: k for k, v in TABLES.items()}[prev]
+
+
+def force_path(path, tiles: int = 0) -> None:
+    """Test hook: how later calls of adapters(), gated() and their backward
+    passes compute their product: False decodes the weights in the product,
+    True decodes them once (at most `tiles` 16-column tiles a launch), None
+    leaves it to the library."""
+    if load_library().trellis_test_force_path(-1 if path is None else int(path), tiles) != 0:
+        raise ValueError(f"bad path {path!r} or tiles {tiles!r}")
 
 
 def status_string(status: int) -> str:

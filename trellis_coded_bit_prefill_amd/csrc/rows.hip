@@ -20,6 +20,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <map>
 #include <mutex>
 #include <thread>
@@ -28,6 +29,7 @@
 
 #include "decode.hpp"
 #include "trellis.h"
+#include "trellis_testing.h"
 
 namespace trellis {
 namespace {
@@ -401,10 +403,12 @@ __global__ __launch_bounds__(kThreads, OCC) void product_kernel(Product P) {
         // last step, half of the row tiles in each wk.
         if (KIND != kGated && a1 == P.steps && P.low.rank > 0) {
           // (one row tile: the first wk alone)
-          if (MT > 1 || wk == 0) {
-            constexpr int TILES = (MT + 1) / 2;
+          // Transposed: one row tile at a time, as the sums of the second
+          // round are still in registers.
+          constexpr int TILES = kT ? 1 : (MT + 1) / 2;
+          for (int first = wk; first < MT; first += 2 * TILES) {
             f32x4 term[TILES][NT];
-            low_rank_tiles<TILES, NT>(P.low, P.m, am0 + 16 * wk, et & 63, term, [&](int a, int r0, bf16x8 (&w)[NT]) {
+            low_rank_tiles<TILES, NT>(P.low, P.m, am0 + 16 * first, et & 63, term, [&](int a, int r0, bf16x8 (&w)[NT]) {
               if constexpr (kT) {
                 const int k0 = agroup * BN + 64 * wn + 4 * ej;
                 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
@@ -436,7 +440,7 @@ __global__ __launch_bounds__(kThreads, OCC) void product_kernel(Product P) {
             for (int t = 0; t < TILES; ++t)
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                float *r = red + (wk * BM + (2 * t + wk) * 16 + 4 * eg + e) * kRedStride;
+                float *r = red + (wk * BM + (2 * t + first) * 16 + 4 * eg + e) * kRedStride;
                 if constexpr (kT) {
                   f32x4 *v = reinterpret_cast<f32x4 *>(r + 64 * (wn & 1) + 4 * ej);
                   *v += f32x4{term[t][0][e], term[t][1][e], term[t][2][e], term[t][3][e]};
@@ -1309,8 +1313,15 @@ trellis_status space(int dev, hipStream_t stream, size_t size, size_t ncounters,
   const std::thread::id tid = stream == hipStreamPerThread ? std::this_thread::get_id() : std::thread::id();
   Space &w = g_space[Key{dev, stream, tid}];
   if (w.size < size) {
+    // By half as much again at least, so that the outgrown buffers of ever
+    // longer calls stay within twice the last one's size.
+    const size_t more = w.size + w.size / 2;
     void *p = nullptr;
-    if (hipMalloc(&p, size) != hipSuccess) return TRELLIS_E_HIP;
+    if (size < more && hipMalloc(&p, more) == hipSuccess) {
+      size = more;
+    } else if (hipMalloc(&p, size) != hipSuccess) {
+      return TRELLIS_E_HIP;
+    }
     w.bytes = static_cast<unsigned char *>(p);
     w.size = size;
   }
@@ -1344,8 +1355,8 @@ ProductFn product_of(int i) {
     case 0: return product_one<BITS, KIND, 1>();
     case 1: return product_one<BITS, KIND, 2>();
     case 2: return product_one<BITS, KIND, 4>();
-    case 3: return product_one<BITS, KIND, KIND == kTransposed ? 4 : 6>();
-    default: return product_one<BITS, KIND, KIND == kTransposed ? 4 : 8>();
+    case 3: return product_one<BITS, KIND, 6>();
+    default: return product_one<BITS, KIND, KIND == kTransposed ? 6 : 8>();
   }
 }
 template <int KIND>
@@ -1369,7 +1380,7 @@ Shape shape_of(int kind, trellis_geom g, int32_t m, int matrices, int cus) {
   s.kind = kind;
   s.bits = g.bits;
   // at most 128 rows a tile, transposed 64 (its waves hold four column tiles)
-  const int most_rows = kind == kTransposed ? 64 : 128;
+  const int most_rows = kind == kTransposed ? 96 : 128;
   const int64_t chunks = ((int64_t)m + most_rows - 1) / most_rows;
   const int need = (int)((((int64_t)m + chunks - 1) / chunks + 15) / 16);
   while (kRowTiles[s.mt] < need) ++s.mt;
@@ -1423,6 +1434,9 @@ trellis_status launch(const Shape &s, Product p, hipStream_t stream) {
 
 // ---- many rows (dense.hpp) ---------------------------------------------------
 
+// Test hook (trellis_test_force_path).
+std::atomic<int> g_path{-1}, g_tiles{0};
+
 // Whether W is decoded once into the workspace: from a number of rows on that
 // grows for small matrices, where the extra launches (unpacking, packing the
 // rows, joining splits: 12 to 20 us) weigh more. Measured, decoding in the
@@ -1433,6 +1447,8 @@ trellis_status launch(const Shape &s, Product p, hipStream_t stream) {
 // adapters 44 / 46 at 768, 33 / 47 at 1024; backward 65 / 70 at 384, 83 / 115
 // at 1024.
 bool decode_once(int kind, trellis_geom g, int32_t m, int matrices) {
+  const int forced = g_path.load(std::memory_order_relaxed);
+  if (forced >= 0) return forced == 1;
   const double weights = (double)g.n * g.k * (kind == kGated ? 2 : matrices);
   return kind == kTransposed ? m > 280 + 4e9 / weights : m > 470 + 4e9 / weights;
 }
@@ -1479,7 +1495,10 @@ DenseShape dense_shape(int kind, trellis_geom g, int32_t m, int matrices, int cu
   }
   const int64_t tile_bytes = (int64_t)s.steps * 1024;
   int64_t slab = kOperandBytes / tile_bytes / (16 * s.nt) * (16 * s.nt);  // whole workgroup tiles, fours and pairs
-  if (slab < 16 * s.nt) slab = 16 * s.nt;
+  const int forced = g_tiles.load(std::memory_order_relaxed);
+  if (forced > 0) slab = ((int64_t)forced + 16 * s.nt - 1) / (16 * s.nt) * (16 * s.nt);
+  if (slab == 0) slab = kOperandBytes / tile_bytes / 16 * 16;  // long contractions: whole 256-column blocks
+  if (slab == 0) slab = 16;
   if (slab > s.tiles) slab = s.tiles;
   s.slab = slab;
   s.operand_bytes = (size_t)(slab * tile_bytes);
@@ -1601,11 +1620,14 @@ struct Plan {
 Plan plan_of(int kind, trellis_geom g, int32_t m, int matrices, int cus) {
   Plan p{};
   p.dense = decode_once(kind, g, m, matrices);
+  if (!p.dense) {
+    p.fused = shape_of(kind, g, m, matrices, cus);
+    p.dense = p.fused.units >= ((int64_t)1 << 30);  // the product kernel counts them in 32 bits
+  }
   if (p.dense) {
     p.many = dense_shape(kind, g, m, matrices, cus);
     p.bytes = up256(p.many.operand_bytes) + up256(p.many.row_bytes) + p.many.partial_bytes;
   } else {
-    p.fused = shape_of(kind, g, m, matrices, cus);
     p.bytes = p.fused.partial_bytes;
     p.counters = p.fused.tiles;
   }
@@ -1679,6 +1701,13 @@ using namespace trellis;
   } while (0)
 
 extern "C" {
+
+int trellis_test_force_path(int path, int tiles) {
+  if (path < -1 || path > 1 || tiles < 0) return -2;
+  g_path.store(path);
+  g_tiles.store(tiles);
+  return 0;
+}
 
 trellis_status trellis_adapters(const uint16_t *x, int32_t m, const uint32_t *codes, const uint16_t *scales,
                                 trellis_geom g, const uint16_t *a, const uint16_t *b, const float *gain,
