@@ -1440,17 +1440,18 @@ std::atomic<int> g_path{-1}, g_tiles{0};
 // Whether W is decoded once into the workspace: from a number of rows on that
 // grows for small matrices, where the extra launches (unpacking, packing the
 // rows, joining splits: 12 to 20 us) weigh more. Measured, decoding in the
-// product against this (us), K = 5120, N = 17408, k = 4: adapters 124 / 153 at
-// 384 rows, 164 / 156 at 512; gated 266 / 294 at 512, 430 / 346 at 768;
-// adapters_backward 195 / 203 at 257, 221 / 211 at 384; gated_backward 278 /
-// 309 at 257, 329 / 340 at 384, 428 / 349 at 512. K = 1024, N = 4096:
-// adapters 44 / 46 at 768, 33 / 47 at 1024; backward 65 / 70 at 384, 83 / 115
-// at 1024.
+// product against this (us), k = 4, on one card: K = 5120, N = 17408: adapters
+// 128 / 154 at 384 rows, 168 / 156 at 512, 234 / 189 at 768; gated 259 / 291
+// at 512, 345 / 336 at 640; adapters_backward 150 / 175 at 257, 184 / 185 at
+// 384, 225 / 193 at 480; gated_backward 215 / 274 at 257, 280 / 305 at 384,
+// 345 / 307 at 480. K = 17408, N = 5120: adapters 194 / 210 at 640, gated 327 /
+// 351; backward 193 / 171 and 275 / 274 at 384. K = 1024, N = 4096: adapters
+// 42 / 44 at 768, 33 / 45 at 1024; backward 70 / 101 and 51 / 51 at 480.
 bool decode_once(int kind, trellis_geom g, int32_t m, int matrices) {
   const int forced = g_path.load(std::memory_order_relaxed);
   if (forced >= 0) return forced == 1;
   const double weights = (double)g.n * g.k * (kind == kGated ? 2 : matrices);
-  return kind == kTransposed ? m > 280 + 4e9 / weights : m > 470 + 4e9 / weights;
+  return kind == kTransposed ? m > 352 + 4e8 / weights : m > 540 + 2e9 / weights;
 }
 // Operand workspace of one launch; larger matrices go in slabs of columns.
 constexpr int64_t kOperandBytes = (int64_t)1 << 30;
