@@ -261,6 +261,17 @@ namespace {
 // ahead (transposed: code words one 32-row part, P's rows one step ahead).
 // OCC: waves per SIMD (4: two workgroups share a CU, so that one decodes while
 // the other waits at its barrier).
+//
+// What bounds it: VALU issue and LDS reads of the decode, about 4.9 VALU
+// operations a weight (314 of them, 32 gathers, 8 operand reads and 16 MFMAs
+// per step of two tiles, k = 4), once per tile of rows. Measured, K = 5120,
+// N = 17408, k = 4 unless said: 27 us at 1 row, 34 us at 24, 50 us for both
+// matrices at 19 rows (VALU 44%, LDS 41%, MFMA 8% busy); K = 17408, N = 5120,
+// k = 3 at 117 rows 57 us; transposed, k = 3, two matrices, 257 rows in three
+// tiles 229 us (VALU 42%, LDS 36%, MFMA 18%). Tried and slower: one column tile
+// per wave from four row tiles on (53 against 49 us at 64 rows), two up to two
+// (40 against 38.7 at 24), four waves per SIMD from four row tiles on (97
+// against 47 at 64: registers spill).
 template <int BITS, int KIND, int MT, int NT, int OCC>
 __global__ __launch_bounds__(kThreads, OCC) void product_kernel(Product P) {
   constexpr bool kT = KIND == kTransposed;
@@ -834,6 +845,10 @@ __global__ __launch_bounds__(kThreads, OCC) void product_kernel(Product P) {
 // waves, the columns; an adapter's product is kept in its own rows only. The
 // waves' sums meet in LDS, the spans' in `partials`, added in order by the
 // workgroup that arrives last.
+// Bound by latency on few rows (6 us for 1 row and 8 us for 24 rows with 16
+// adapters at K = 5120: a load, a product, and a second round trip to join
+// spans) and by reading P on many (2048 rows, K = 5120, rank 32: 15 us, 1.4
+// TB/s; with N = 17408 beside it 45 us).
 // ---------------------------------------------------------------------------
 struct Shrink {
   const uint16_t *p;
@@ -1070,7 +1085,8 @@ __device__ __forceinline__ void chunk_range(const int32_t *__restrict__ index, i
 
 // What the backward pass needs before its products, in one launch: t, u (z
 // below zs: t, below 2 zs: u) and the adapters' chunk ranges (z = 2 zs). Three
-// launches of their own took about 10 us more.
+// launches of their own took about 10 us more. 23 us at 509 rows (K = 17408,
+// N = 5120, rank 8), 45 us at 2048 (K = 5120, N = 17408, rank 32).
 struct BackwardSums {
   Shrink t, u;
   i32x2 *range;
@@ -1101,7 +1117,9 @@ __global__ __launch_bounds__(64 * WAVES) void backward_sums_kernel(BackwardSums 
 // waves' sums meet in LDS in order. A chunk of P goes through the wave's own
 // LDS, which turns it (contraction is over rows); rows of other adapters enter
 // as zeros on both sides (a NaN in them must not count). V as the sum of two
-// bf16 numbers (2^-16 relative). The next chunk is loaded ahead.
+// bf16 numbers (2^-16 relative). The next chunk is loaded ahead. 2048 rows,
+// K = 5120, N = 17408, rank 32, two adapters: 46 us, 97 MB read (2.1 TB/s; what
+// it waits for is each wave's own chain of chunks).
 struct Outer {
   const uint16_t *x, *dout;
   const float *u, *t;
