@@ -309,3 +309,24 @@ def test_two_streams_at_once():
         torch.cuda.synchronize()
         for i in range(2):
             assert all(torch.equal(p, q) for p, q in zip(got[i], alone[i]))
+
+
+@pytest.mark.parametrize("path", [False, True])
+def test_infinities_stay_infinities(force_path, path):
+    # An infinite t, u, x, dout or factor gives the infinity (or the NaN) that
+    # the formula gives: a float32 number enters these products in two halves.
+    print(f"adapters infinities path={path}", flush=True)
+    d = ref.draw(np.random.default_rng(41), 40, 68, 512, 4, rank=8, count=4)
+    d["index"] = np.arange(40, dtype=np.int32) % 5
+    for name, at, value in (("a", (1, 3, 5), np.inf), ("b", (2, 7, 1), -np.inf), ("x", (3, 9), np.inf),
+                            ("dout", (5, 11), -np.inf)):
+        d[name][at] = value
+        d[name + "_bits"][at] = 0x7F80 if value > 0 else 0xFF80
+    force_path(path)
+    with np.errstate(invalid="ignore"):
+        check_both(d, 4, f"infinities path={path}")
+        value = {"out": ref.adapters(d)[0], **{k: v[0] for k, v in ref.adapters_backward(d).items()}}
+    got = {"out": forward(d, 4), **backward(d, 4)}
+    for name, v in value.items():
+        at = np.isinf(v)
+        assert at.any() and np.array_equal(ref.bf16_bits_to_f32(got[name])[at], v[at]), name

@@ -335,7 +335,7 @@ __global__ __launch_bounds__(kDenseThreads) void dense_kernel(Dense D) {
   if constexpr (!GATED) {
     // The adapters' term first, while the first steps are on their way: lane l
     // looks up row row0 + l; for every adapter that the wave's rows name, the
-    // products are kept only in the rows that name it (see low_rank_tile).
+    // products are kept only in the rows that name it (see low_rank_tiles).
     if (D.low.rank > 0 && split == 0) {
       int idx = row0 + lane < D.m ? D.low.index[row0 + lane] : -1;
       if (idx >= D.low.count) idx = -1;
@@ -383,12 +383,7 @@ __global__ __launch_bounds__(kDenseThreads) void dense_kernel(Dense D) {
               const int row = row0 + 16 * (rp + r) + j;
               const f32x4 *tp = reinterpret_cast<const f32x4 *>(D.low.t + (int64_t)(row < D.m ? row : D.m - 1) * D.low.rank_p + r0);
               const f32x4 t0 = tp[0], t1 = tp[1];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float v = e < 4 ? t0[e] : t1[e - 4];
-                hi[r][e] = (__bf16)v;
-                lo[r][e] = (__bf16)(v - (float)hi[r][e]);
-              }
+              halves({t0[0], t0[1], t0[2], t0[3], t1[0], t1[1], t1[2], t1[3]}, hi[r], lo[r]);
             }
             bf16x8 next = fetch(0);
 #pragma unroll

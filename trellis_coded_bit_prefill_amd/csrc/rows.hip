@@ -76,9 +76,29 @@ struct Product {
   LowRank low;
 };
 
+// Eight float32 factors of a matrix product, each as the sum of two bf16
+// numbers of one sign: the upper half of its bits, and the rest rounded (off by
+// at most 2^-16 of v: a half step of the rest, which is below 2^-7). Cut
+// instead of rounded, and without a zero or a NaN as the rest of what is not
+// zero, so that an infinity on either side of the product gives the infinity
+// that v times it gives: of opposite signs the halves' infinities would cancel
+// to a NaN.
+__device__ __forceinline__ void halves(const float (&v)[8], bf16x8 &hi, bf16x8 &lo) {
+  u32x4 top;
+#pragma unroll
+  for (int e = 0; e < 8; e += 2)
+    top[e / 2] = __builtin_amdgcn_perm(__float_as_uint(v[e + 1]), __float_as_uint(v[e]), 0x07060302u);
+  hi = __builtin_bit_cast(bf16x8, top);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float t = __uint_as_float(__float_as_uint(v[e]) & 0xFFFF0000u), rest = v[e] - t;
+    lo[e] = (__bf16)(fabsf(rest) > 0.f ? rest : t * 0x1p-30f);
+  }
+}
+
 // The adapters' term of TILES 16-row tiles (every second one from m0 on) and a
 // wave's NT column tiles: for every adapter that the rows name, the product of
-// t's rows (as the sum of two bf16 numbers, 2^-16 relative) with the factor,
+// t's rows (split in two bf16 numbers) with the factor,
 // kept only in the rows that name it, so an adapter's infinities and NaNs stay
 // in its own rows. Several adapters' operands are loaded before the first is
 // multiplied: one at a time cost about a microsecond each.
@@ -122,12 +142,7 @@ __device__ __forceinline__ void low_rank_tiles(const LowRank &L, int m, int m0, 
 #pragma unroll
       for (int t = 0; t < TILES; ++t) {
         bf16x8 hi, lo;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float v = tv[t][e >> 2][e & 3];
-          hi[e] = (__bf16)v;
-          lo[e] = (__bf16)(v - (float)hi[e]);
-        }
+        halves({tv[t][0][0], tv[t][0][1], tv[t][0][2], tv[t][0][3], tv[t][1][0], tv[t][1][1], tv[t][1][2], tv[t][1][3]}, hi, lo);
 #pragma unroll
         for (int b = 0; b < B; ++b) {
           const uint32_t of = (uint32_t)(rows[b] >> (16 * t)) & 0xFFFFu;
@@ -1052,7 +1067,8 @@ __device__ __forceinline__ void shrink(const Shrink &S, int z, int zs, ShrinkSpa
     const int row0 = 16 * (v >> 7) + 4 * (l >> 4);
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      if (m0 + row0 + e < S.m) S.t[(m0 + row0 + e) * S.rank_p + r] = sum[e] * gains[row0 + e];
+      // (past the rank an infinity of P gave a NaN)
+      if (m0 + row0 + e < S.m) S.t[(m0 + row0 + e) * S.rank_p + r] = r < S.rank ? sum[e] * gains[row0 + e] : 0.f;
   }
 }
 
@@ -1194,13 +1210,12 @@ __global__ __launch_bounds__(256) void outer_kernel(Outer O) {
     }
     bf16x8 hi[2], lo[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < 2; ++h) {
+      float v[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float v = (C.rows >> (8 * g + e)) & 1 ? C.v[h][e] : 0.f;
-        hi[h][e] = (__bf16)v;
-        lo[h][e] = (__bf16)(v - (float)hi[h][e]);
-      }
+      for (int e = 0; e < 8; ++e) v[e] = (C.rows >> (8 * g + e)) & 1 ? C.v[h][e] : 0.f;
+      halves(v, hi[h], lo[h]);
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       bf16x8 p;
@@ -1397,7 +1412,7 @@ Shape shape_of(int kind, trellis_geom g, int32_t m, int matrices, int cus) {
   Shape s{};
   s.kind = kind;
   s.bits = g.bits;
-  // at most 128 rows a tile, transposed 64 (its waves hold four column tiles)
+  // at most 128 rows a tile, transposed 96 (its waves hold four column tiles)
   const int most_rows = kind == kTransposed ? 96 : 128;
   const int64_t chunks = ((int64_t)m + most_rows - 1) / most_rows;
   const int need = (int)((((int64_t)m + chunks - 1) / chunks + 15) / 16);
