@@ -226,10 +226,13 @@ trellis_status trellis_prefill_noalloc(const uint16_t *x_bf16, int32_t m,
  * above; a stream's workspace of these entry points is a second one, under the
  * same rules (allocated by the first call that needs it, kept, one per device
  * and stream: call once before capturing, and order a captured graph's replays
- * with every other use of the capture stream). From some hundred rows on it
+ * with every other use of the capture stream; a call that would have to
+ * allocate while its stream is captured, in any capture mode, returns
+ * TRELLIS_E_HIP before any GPU work). From some hundred rows on it
  * holds the decoded weights (2 bytes each, at most 1 GiB at a time) and a copy
  * of x or of the output's gradient, below that partial sums of at most some
- * 64 MB; it grows by half at least. All sums are float32; outputs
+ * 64 MB, and 8 bytes a row and rank column for adapters; it grows by half at
+ * least. All sums are float32; outputs
  * are rounded to bf16 once. Results do not depend on timing: every sum has a
  * fixed order. Inputs and outputs must not overlap. */
 

@@ -330,3 +330,47 @@ def test_infinities_stay_infinities(force_path, path):
     for name, v in value.items():
         at = np.isinf(v)
         assert at.any() and np.array_equal(ref.bf16_bits_to_f32(got[name])[at], v[at]), name
+
+
+@pytest.mark.parametrize("mode", ["global", "relaxed"])
+def test_a_capture_without_a_call_before_it_is_refused(mode):
+    import torch
+
+    print(f"adapters first call in a capture, {mode}", flush=True)
+    d = ref.draw(np.random.default_rng(42), 50, 260, 1024, 4, rank=16, count=3)
+    s, _ = on_gpu(d)
+    want = forward(d, 4)
+    out = torch.zeros((50, 260), dtype=torch.bfloat16, device="cuda")
+    stream = torch.cuda.Stream()
+    # Streams come from a pool, so one that an earlier test used has a
+    # workspace: many rows need more than any of them.
+    rows = 1 << 16
+    big = dict(s, x=s["x"].repeat(rows // 50, 1), index=s["index"].repeat(rows // 50))
+    big_out = torch.zeros((rows // 50 * 50, 260), dtype=torch.bfloat16, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with pytest.raises(tp.TrellisError):
+        with torch.cuda.graph(graph, stream=stream, capture_error_mode=mode):
+            out.add_(0)
+            tp.adapters(bits=4, out=big_out, **big)
+    torch.cuda.synchronize()
+    for _ in range(2):
+        out.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(stream):
+            tp.adapters(bits=4, out=out, **s)
+        torch.cuda.synchronize()
+        assert np.array_equal(from_dev_bf16(out), want)
+    with torch.cuda.stream(stream):
+        tp.adapters(bits=4, out=big_out, **big)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream, capture_error_mode=mode):
+        tp.adapters(bits=4, out=out, **s)
+    for _ in range(2):
+        out.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(stream):
+            graph.replay()
+        torch.cuda.synchronize()
+        assert np.array_equal(from_dev_bf16(out), want)

@@ -23,6 +23,7 @@
 #include <atomic>
 #include <map>
 #include <mutex>
+#include <new>
 #include <thread>
 #include <type_traits>
 #include <utility>
@@ -1342,9 +1343,22 @@ trellis_status device(int &dev, int &cus) {
 
 // The stream's workspace: grown on demand and kept (launches still queued and
 // captured graphs may hold an outgrown buffer's address, so none is freed).
+// Not while the stream is captured: the clearing of new counters would become
+// part of the graph, and eager calls before its first replay would find them
+// as the allocator left them.
 trellis_status space(int dev, hipStream_t stream, size_t size, size_t ncounters, Space *&out) {
   const std::thread::id tid = stream == hipStreamPerThread ? std::this_thread::get_id() : std::thread::id();
-  Space &w = g_space[Key{dev, stream, tid}];
+  Space *slot = nullptr;
+  try {
+    slot = &g_space[Key{dev, stream, tid}];
+  } catch (const std::bad_alloc &) {
+    return TRELLIS_E_HIP;
+  }
+  Space &w = *slot;
+  if (w.size < size || w.ncounters < ncounters) {
+    hipStreamCaptureStatus capture = hipStreamCaptureStatusNone;
+    if (hipStreamIsCapturing(stream, &capture) != hipSuccess || capture != hipStreamCaptureStatusNone) return TRELLIS_E_HIP;
+  }
   if (w.size < size) {
     // By half as much again at least, so that the outgrown buffers of ever
     // longer calls stay within twice the last one's size.
