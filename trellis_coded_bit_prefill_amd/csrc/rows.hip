@@ -1731,7 +1731,11 @@ trellis_status launch_shrink(const ShrinkShape &h, const Shrink &s, hipStream_t 
 }
 trellis_status launch_backward_sums(const ShrinkShape &ht, const ShrinkShape &hu, const BackwardSums &b, hipStream_t stream) {
   (void)hipGetLastError();
-  const dim3 grid((unsigned)ht.groups, (unsigned)(ht.spans > hu.spans ? ht.spans : hu.spans), (unsigned)(2 * (b.t.rank_p / 32) + 1));
+  // Many adapters for few rows: workgroups beside the sums' for their ranges.
+  const int64_t ranges = ((b.t.count < 256 ? b.t.count : 256) + ht.groups - 1) / ht.groups;
+  int64_t y = ht.spans > hu.spans ? ht.spans : hu.spans;
+  if (y < ranges) y = ranges;
+  const dim3 grid((unsigned)ht.groups, (unsigned)y, (unsigned)(2 * (b.t.rank_p / 32) + 1));
   if (ht.ms == 4) hipLaunchKernelGGL((backward_sums_kernel<4, 4>), grid, dim3(256), 0, stream, b);
   else hipLaunchKernelGGL((backward_sums_kernel<1, 8>), grid, dim3(512), 0, stream, b);
   return hipGetLastError() == hipSuccess ? TRELLIS_OK : TRELLIS_E_HIP;
