@@ -25,3 +25,14 @@ def test_rows_host_side_under_asan_ubsan(tmp_path):
          os.path.join(ROOT, "trellis_coded_bit_prefill_amd", "csrc", "rows.hip")], env=env)
     r = run([exe], env=dict(SAN_ENV, HIP_VISIBLE_DEVICES=""))
     assert "rows driver ok" in r.stdout
+
+
+@pytest.mark.skipif(not os.path.exists("/opt/rocm/bin/hipcc"), reason="hipcc not installed")
+def test_layouts_of_all_sizes_under_ubsan(tmp_path):
+    exe = str(tmp_path / "rows_plan")
+    run(["/opt/rocm/bin/hipcc", "--offload-arch=gfx950", "-O1", "-g", "-std=c++17", "-ffp-contract=off",
+         "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops", "-Wno-unused-command-line-argument",
+         "-Xarch_host", "-fsanitize=undefined", "-Xarch_host", "-fno-sanitize-recover=undefined",
+         "-I", os.path.join(ROOT, "include"), "-I", os.path.join(ROOT, "trellis_coded_bit_prefill_amd", "csrc"),
+         "-o", exe, os.path.join(HERE, "rows_plan.hip")], env=dict(os.environ))
+    assert "rows plan ok" in run([exe], env=SAN_ENV).stdout

@@ -1530,7 +1530,7 @@ DenseShape dense_shape(int kind, trellis_geom g, int32_t m, int matrices, int cu
   for (int nt = 8; nt >= 4; --nt) {
     if (kind == kGated && nt % 2) continue;
     const int64_t wg = mt * ((s.tiles + 2 * nt - 1) / (2 * nt));
-    for (int splits = 1; splits <= 8 && splits <= s.steps / 16; ++splits) {
+    for (int splits = 1; splits == 1 || (splits <= 8 && splits <= s.steps / 16); ++splits) {
       const double rounds = (double)((wg * splits + cus - 1) / cus);
       double cost = rounds * ((double)s.steps / splits * (nt + 1.0) + 100.0);
       if (splits > 1) cost += 300.0 + (double)splits * m * s.tiles * 16 * 4 / 37000.0;
