@@ -1332,9 +1332,18 @@ bool geom_ok(const trellis_geom &g) {
 bool on(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
 
+// Whether a runtime call worked. The runtime keeps a call's error until it is
+// read, whatever succeeds after it: left there, it would be taken for the next
+// launch's, here or in the caller's program.
+bool worked(hipError_t e) {
+  if (e == hipSuccess) return true;
+  (void)hipGetLastError();
+  return false;
+}
+
 trellis_status device(int &dev, int &cus) {
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices) return TRELLIS_E_HIP;
-  if (g_cus[dev] == 0 && (hipDeviceGetAttribute(&g_cus[dev], hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess ||
+  if (!worked(hipGetDevice(&dev)) || dev < 0 || dev >= kMaxDevices) return TRELLIS_E_HIP;
+  if (g_cus[dev] == 0 && (!worked(hipDeviceGetAttribute(&g_cus[dev], hipDeviceAttributeMultiprocessorCount, dev)) ||
                           g_cus[dev] <= 0))
     return TRELLIS_E_HIP;
   cus = g_cus[dev];
@@ -1357,16 +1366,16 @@ trellis_status space(int dev, hipStream_t stream, size_t size, size_t ncounters,
   Space &w = *slot;
   if (w.size < size || w.ncounters < ncounters) {
     hipStreamCaptureStatus capture = hipStreamCaptureStatusNone;
-    if (hipStreamIsCapturing(stream, &capture) != hipSuccess || capture != hipStreamCaptureStatusNone) return TRELLIS_E_HIP;
+    if (!worked(hipStreamIsCapturing(stream, &capture)) || capture != hipStreamCaptureStatusNone) return TRELLIS_E_HIP;
   }
   if (w.size < size) {
     // By half as much again at least, so that the outgrown buffers of ever
     // longer calls stay within twice the last one's size.
     const size_t more = w.size + w.size / 2;
     void *p = nullptr;
-    if (size < more && hipMalloc(&p, more) == hipSuccess) {
+    if (size < more && worked(hipMalloc(&p, more))) {
       size = more;
-    } else if (hipMalloc(&p, size) != hipSuccess) {
+    } else if (!worked(hipMalloc(&p, size))) {
       return TRELLIS_E_HIP;
     }
     w.bytes = static_cast<unsigned char *>(p);
@@ -1374,10 +1383,14 @@ trellis_status space(int dev, hipStream_t stream, size_t size, size_t ncounters,
   }
   if (w.ncounters < ncounters) {
     void *p = nullptr;
-    if (hipMalloc(&p, ncounters * 4) != hipSuccess) return TRELLIS_E_HIP;
+    if (!worked(hipMalloc(&p, ncounters * 4))) return TRELLIS_E_HIP;
+    (void)hipGetLastError();
     hipLaunchKernelGGL(clear_kernel, dim3((unsigned)((ncounters + 255) / 256)), dim3(256), 0, stream,
                        static_cast<uint32_t *>(p), (int64_t)ncounters);
-    if (hipGetLastError() != hipSuccess) return TRELLIS_E_HIP;
+    if (hipGetLastError() != hipSuccess) {
+      (void)worked(hipFree(p));
+      return TRELLIS_E_HIP;
+    }
     w.counters = static_cast<uint32_t *>(p);
     w.ncounters = ncounters;
   }
@@ -1463,8 +1476,7 @@ trellis_status launch(const Shape &s, Product p, hipStream_t stream) {
   if (device(dev, cus) != TRELLIS_OK) return TRELLIS_E_HIP;
   bool &done = ready[dev][s.kind][s.bits - 2][s.mt];
   if (!done) {
-    if (hipFuncSetAttribute(reinterpret_cast<const void *>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, (int)s.lds) !=
-        hipSuccess)
+    if (!worked(hipFuncSetAttribute(reinterpret_cast<const void *>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, (int)s.lds)))
       return TRELLIS_E_HIP;
     done = true;
   }
@@ -1587,8 +1599,7 @@ trellis_status launch_dense(int kind, const DenseShape &s, trellis_geom g, const
   int dev = 0, cus = 0;
   if (device(dev, cus) != TRELLIS_OK) return TRELLIS_E_HIP;
   if (!ready[dev][kind][s.nt]) {
-    if (hipFuncSetAttribute(reinterpret_cast<const void *>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) !=
-        hipSuccess)
+    if (!worked(hipFuncSetAttribute(reinterpret_cast<const void *>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds)))
       return TRELLIS_E_HIP;
     ready[dev][kind][s.nt] = true;
   }
