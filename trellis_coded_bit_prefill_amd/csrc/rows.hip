@@ -1512,7 +1512,8 @@ bool decode_once(int kind, trellis_geom g, int32_t m, int matrices) {
   const double weights = (double)g.n * g.k * (kind == kGated ? 2 : matrices);
   return kind == kTransposed ? m > 352 + 4e8 / weights : m > 540 + 2e9 / weights;
 }
-// Operand workspace of one launch; larger matrices go in slabs of columns.
+// Operand workspace of one launch; larger matrices go in slabs of columns, one
+// 256-column block at least (more than this from 2^21 rows of W on, transposed).
 constexpr int64_t kOperandBytes = (int64_t)1 << 30;
 
 struct DenseShape {
@@ -1538,9 +1539,16 @@ DenseShape dense_shape(int kind, trellis_geom g, int32_t m, int matrices, int cu
   // partial sums of a split are written and read once more (32 MB cost about
   // 12 us, a tile step 14 ns).
   const int64_t mt = (m + kDenseRows - 1) / kDenseRows;
+  const int64_t tile_bytes = (int64_t)s.steps * 1024;
+  const bool several = s.tiles > 16 && tile_bytes * s.tiles > kOperandBytes;  // launches
   double best = 0;
   for (int nt = 8; nt >= 4; --nt) {
     if (kind == kGated && nt % 2) continue;
+    // Contractions so long that 16 nt operand tiles exceed a launch's operands
+    // go in slabs of 16 tiles and multiples of it: of whole workgroup tiles for
+    // nt = 4 and 8 alone (the rest of a cut one would be stored over the next
+    // slab's columns).
+    if (several && nt % 4 && tile_bytes * 16 * nt > kOperandBytes) continue;
     const int64_t wg = mt * ((s.tiles + 2 * nt - 1) / (2 * nt));
     for (int splits = 1; splits == 1 || (splits <= 8 && splits <= s.steps / 16); ++splits) {
       const double rounds = (double)((wg * splits + cus - 1) / cus);
@@ -1553,12 +1561,11 @@ DenseShape dense_shape(int kind, trellis_geom g, int32_t m, int matrices, int cu
       }
     }
   }
-  const int64_t tile_bytes = (int64_t)s.steps * 1024;
   int64_t slab = kOperandBytes / tile_bytes / (16 * s.nt) * (16 * s.nt);  // whole workgroup tiles, fours and pairs
   const int forced = g_tiles.load(std::memory_order_relaxed);
   if (forced > 0) slab = ((int64_t)forced + 16 * s.nt - 1) / (16 * s.nt) * (16 * s.nt);
-  if (slab == 0) slab = kOperandBytes / tile_bytes / 16 * 16;  // long contractions: whole 256-column blocks
-  if (slab == 0) slab = 16;
+  if (slab == 0) slab = kOperandBytes / tile_bytes / 16 * 16;  // long contractions: whole 256-column blocks,
+  if (slab == 0) slab = 16;                                    // one at least (512 bytes per row of W)
   if (slab > s.tiles) slab = s.tiles;
   s.slab = slab;
   s.operand_bytes = (size_t)(slab * tile_bytes);
