@@ -21,3 +21,7 @@ def rules(tmp_path_factory):
 
 def test_slabs_are_whole_workgroup_tiles(rules):
     assert "slabs ok" in rules
+
+
+def test_splits_are_near_the_fastest_measured(rules):
+    assert "splits ok" in rules

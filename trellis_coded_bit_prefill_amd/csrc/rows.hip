@@ -1534,10 +1534,14 @@ DenseShape dense_shape(int kind, trellis_geom g, int32_t m, int matrices, int cu
   const int64_t width = t ? g.k : g.n, one = (width + 15) / 16;
   s.tiles = kind == kGated ? 2 * one : one;
   // The column tile and the split of the contraction whose rounds over the
-  // card cost least. A round costs its steps times the accumulator tiles and
-  // one more (staging), and about 100 tile steps to start and store; the
-  // partial sums of a split are written and read once more (32 MB cost about
-  // 12 us, a tile step 14 ns).
+  // card cost least, in us. A round costs 0.073 a step and accumulator tile,
+  // 0.125 a step (staging) and 3.7 to start and store; the partial sums of a
+  // split are written and read once more, 0.32 a MB. Fitted to the times of
+  // every column tile and split at 448 sizes (all four operators, 200 to 4096
+  // rows, K and N from 256 to 17408): the choice is 0.3% slower than the best on
+  // average and 9% at most, as fewer than all 256 workgroups cost what they
+  // leave idle (gated, K = 4096, N = 1024, 384 rows: 75.6 us in one split, 35.7
+  // in seven).
   const int64_t mt = (m + kDenseRows - 1) / kDenseRows;
   const int64_t tile_bytes = (int64_t)s.steps * 1024;
   const bool several = s.tiles > 16 && tile_bytes * s.tiles > kOperandBytes;  // launches
@@ -1552,8 +1556,8 @@ DenseShape dense_shape(int kind, trellis_geom g, int32_t m, int matrices, int cu
     const int64_t wg = mt * ((s.tiles + 2 * nt - 1) / (2 * nt));
     for (int splits = 1; splits == 1 || (splits <= 8 && splits <= s.steps / 16); ++splits) {
       const double rounds = (double)((wg * splits + cus - 1) / cus);
-      double cost = rounds * ((double)s.steps / splits * (nt + 1.0) + 100.0);
-      if (splits > 1) cost += 300.0 + (double)splits * m * s.tiles * 16 * 4 / 37000.0;
+      double cost = rounds * ((double)s.steps / splits * (0.073 * nt + 0.125) + 3.7);
+      if (splits > 1) cost += 0.8 + 0.32e-6 * ((double)splits * m * s.tiles * 16 * 4);
       if (s.nt == 0 || cost < best) {
         best = cost;
         s.nt = nt;
