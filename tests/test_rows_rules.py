@@ -25,3 +25,7 @@ def test_slabs_are_whole_workgroup_tiles(rules):
 
 def test_splits_are_near_the_fastest_measured(rules):
     assert "splits ok" in rules
+
+
+def test_the_faster_measured_side_is_taken(rules):
+    assert "sides ok" in rules

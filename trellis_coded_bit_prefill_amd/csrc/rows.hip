@@ -1496,22 +1496,6 @@ trellis_status launch(const Shape &s, Product p, hipStream_t stream) {
 // Test hook (trellis_test_force_path).
 std::atomic<int> g_path{-1}, g_tiles{0};
 
-// Whether W is decoded once into the workspace: from a number of rows on that
-// grows for small matrices, where the extra launches (unpacking, packing the
-// rows, joining splits: 12 to 20 us) weigh more. Measured, decoding in the
-// product against this (us), k = 4, on one card: K = 5120, N = 17408: adapters
-// 128 / 154 at 384 rows, 168 / 156 at 512, 234 / 189 at 768; gated 259 / 291
-// at 512, 345 / 336 at 640; adapters_backward 150 / 175 at 257, 184 / 185 at
-// 384, 225 / 193 at 480; gated_backward 215 / 274 at 257, 280 / 305 at 384,
-// 345 / 307 at 480. K = 17408, N = 5120: adapters 194 / 210 at 640, gated 327 /
-// 351; backward 193 / 171 and 275 / 274 at 384. K = 1024, N = 4096: adapters
-// 42 / 44 at 768, 33 / 45 at 1024; backward 70 / 101 and 51 / 51 at 480.
-bool decode_once(int kind, trellis_geom g, int32_t m, int matrices) {
-  const int forced = g_path.load(std::memory_order_relaxed);
-  if (forced >= 0) return forced == 1;
-  const double weights = (double)g.n * g.k * (kind == kGated ? 2 : matrices);
-  return kind == kTransposed ? m > 352 + 4e8 / weights : m > 540 + 2e9 / weights;
-}
 // Operand workspace of one launch; larger matrices go in slabs of columns, one
 // 256-column block at least (more than this from 2^21 rows of W on, transposed).
 constexpr int64_t kOperandBytes = (int64_t)1 << 30;
@@ -1523,6 +1507,7 @@ struct DenseShape {
   int steps, steps1;
   int64_t tiles, slab;  // operand tiles in all and per launch
   int ptiles;
+  double us;           // what the product's rounds are reckoned to take
   size_t operand_bytes, row_bytes, partial_bytes;
 };
 DenseShape dense_shape(int kind, trellis_geom g, int32_t m, int matrices, int cus) {
@@ -1574,6 +1559,7 @@ DenseShape dense_shape(int kind, trellis_geom g, int32_t m, int matrices, int cu
   s.slab = slab;
   s.operand_bytes = (size_t)(slab * tile_bytes);
   s.ptiles = (int)(((int64_t)m + 15) / 16);
+  s.us = best;
   s.row_bytes = (size_t)s.ptiles * s.steps * 1024;
   s.partial_bytes = s.splits > 1 ? (size_t)s.splits * m * slab * 16 * 4 : 0;
   return s;
@@ -1687,15 +1673,58 @@ struct Plan {
   size_t bytes;
   int64_t counters;
 };
+// What decoding in the product is reckoned to take (us): the longest workgroup's
+// steps, by kind and row tiles (three-bit codes straddle words: 0.42 more), the
+// reduction of each tile that it has a part of, and the joining of shared tiles
+// (their partials through memory, and one tile's through one workgroup).
+double fused_us(const Shape &s) {
+  static const double step[3][kMts] = {{1.5, 1.5, 1.5, 2.2, 2.8}, {2.1, 2.1, 2.1, 2.5, 2.6}, {2.0, 2.0, 4.1, 5.5, 5.5}};
+  const int64_t steps = s.parts ? (s.steps + s.parts - 1) / s.parts : (s.units + s.grid - 1) / s.grid;
+  const double part = (double)s.partial_bytes / 2 / s.grid;
+  int64_t tiles = 1;
+  if (!s.parts) tiles = s.units % s.grid == 0 && steps % s.steps == 0 ? steps / s.steps : (steps - 1) / s.steps + (s.steps > 1 ? 2 : 1);
+  double us = steps * (step[s.kind][s.mt] + (s.bits == 3 ? 0.42 : 0)) + tiles * (0.8 + 20e-6 * part);
+  if (s.parts != 1) {
+    double share = s.parts ? s.parts : (double)s.grid / s.tiles + 1;
+    if (share > s.steps) share = s.steps;
+    us += part * (0.366e-6 * s.grid + 8.5e-6 * share);
+  }
+  return us;
+}
+// Whether W is decoded once into the workspace: where unpacking it, packing the
+// rows and the dense product of both are reckoned to take less than decoding it
+// in the product for every tile of rows. The figures of both sides are fitted
+// to their times at 3776 points (all four operators, 1 to 4096 rows, sixteen
+// matrices with K and N from 256 to 17408): the side taken is 0.4% slower than
+// the better one on average, at 48 points more than 10% and at most 21%.
+// Measured, decoding in the product against this (us), k = 4. K = 5120, N =
+// 17408: adapters 130 / 146 at 353 rows, 167 / 149 at 385, 200 / 195 at 576;
+// gated 260 / 295 at 449, 337 / 335 at 576, 420 / 339 at 768; adapters_backward
+// 148 / 141 at 193, 155 / 172 at 257, 188 / 178 at 353; gated_backward 215 /
+// 266 at 257, 279 / 276 at 353, 339 / 292 at 385. K = 17408, N = 5120: adapters
+// 196 / 216 at 640, 270 / 242 at 1024; gated 185 / 249 at 353, 334 / 322 at 640
+// (at 512 it takes the 263 of 247 / 263); adapters_backward 156 / 172 at 257,
+// 194 / 176 at 353; gated_backward 210 / 270 at 257, 336 / 277 at 385. K =
+// 1024, N = 4096: adapters 32 / 45 at 1024, 53 / 47 at 2048; gated 20 / 35 at
+// 449, 69 / 52 at 2048; adapters_backward 47 / 48 at 97, 66 / 60 at 449;
+// gated_backward 44 / 41 at 97, 50 / 45 at 449.
 Plan plan_of(int kind, trellis_geom g, int32_t m, int matrices, int cus) {
   Plan p{};
-  p.dense = decode_once(kind, g, m, matrices);
-  if (!p.dense) {
-    p.fused = shape_of(kind, g, m, matrices, cus);
-    p.dense = p.fused.units >= ((int64_t)1 << 30);  // the product kernel counts them in 32 bits
-  }
+  p.fused = shape_of(kind, g, m, matrices, cus);
+  const int forced = g_path.load(std::memory_order_relaxed);
+  p.dense = forced == 1 || p.fused.units >= ((int64_t)1 << 30);  // (the product kernel counts them in 32 bits)
   if (p.dense) {
     p.many = dense_shape(kind, g, m, matrices, cus);
+  } else if (forced < 0) {
+    const double mb = 2e-6 * (kind == kGated ? 2 : matrices) * g.n * g.k;
+    const double rows_mb = 4e-6 * m * (kind == kTransposed ? (double)g.n * matrices : g.k);
+    const double rest = fused_us(p.fused) - (6.5 + 0.187 * mb + 0.14 * rows_mb);
+    if (rest > 0) {  // (the layout of few rows' dense product is not worked out)
+      p.many = dense_shape(kind, g, m, matrices, cus);
+      p.dense = p.many.us < rest;
+    }
+  }
+  if (p.dense) {
     p.bytes = up256(p.many.operand_bytes) + up256(p.many.row_bytes) + p.many.partial_bytes;
   } else {
     p.bytes = p.fused.partial_bytes;
