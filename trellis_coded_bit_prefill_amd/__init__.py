@@ -420,12 +420,14 @@ _types = None
 
 
 def _kinds():
-    """(Tensor, bf16 dtypes, code dtypes, float32, int32), looked up once."""
+    """(Tensor, bf16 dtypes, code dtypes, float32, int32, torch.is_grad_enabled,
+    torch.autograd.forward_ad), looked up once."""
     global _types
     if _types is None:
         import torch
 
-        _types = (torch.Tensor, *_dtypes(), (torch.float32,), (torch.int32,))
+        _types = (torch.Tensor, *_dtypes(), (torch.float32,), (torch.int32,), torch.is_grad_enabled,
+                  torch.autograd.forward_ad)
     return _types
 
 
@@ -459,7 +461,7 @@ def _output(name, t, shape, device):
 
 def _packed_address(codes, scales, n, k: int, bits: int, device, suffix: str = ""):
     """Addresses of one packed matrix [n, k] and its scales."""
-    _, bf, cw, _, _ = _kinds()
+    _, bf, cw = _kinds()[:3]
     if bits not in (2, 3, 4):
         raise ValueError(f"bits must be 2, 3 or 4, got {bits}")
     return (_address("codes" + suffix, codes, cw, (n, k * bits // 32), device),
@@ -475,12 +477,51 @@ def _packed_rows(codes, suffix: str = "") -> int:
 
 def _adapter_addresses(a, b, gain, index, m: int, n: int, k: int, device):
     """(addresses of a, b, gain and index, count, rank) of an adapter set for m rows of a layer [n, k]."""
-    tensor, bf, _, f32, i32 = _kinds()
+    tensor, bf, _, f32, i32 = _kinds()[:5]
     if not isinstance(a, tensor) or a.ndim != 3:
         raise TypeError("a must be a torch.Tensor of three dims")
     count, rank, _ = a.shape
     return (_address("a", a, bf, (count, rank, k), device), _address("b", b, bf, (count, n, rank), device),
             _address("gain", gain, f32, (count,), device), _address("index", index, i32, (m,), device), count, rank)
+
+
+def _may_be_recorded(*tensors) -> bool:
+    """Whether autograd has anything to do with a call: what follows is looked at only then."""
+    grad_enabled, forward_ad = _kinds()[-2:]
+    if forward_ad._current_level >= 0:
+        return True
+    if grad_enabled():
+        for t in tensors:
+            if t.requires_grad:
+                return True
+    return False
+
+
+def _recorded(what: str, trained, frozen, out) -> bool:
+    """Whether autograd has to record this call: gradients are enabled and one
+    of `trained` requires one. What would lose a gradient without a word is
+    refused: a tensor of `frozen` (by name) that requires one, `out` given to a
+    recorded call, a tangent of forward mode, and a recorded call while its
+    stream is captured (see _autograd.py)."""
+    grad_enabled, forward_ad = _kinds()[-2:]
+    if forward_ad._current_level >= 0:
+        for t in (*trained, *frozen.values()):
+            if t.is_floating_point() and forward_ad.unpack_dual(t).tangent is not None:
+                raise NotImplementedError(f"{what}() has no forward-mode derivative")
+    if not grad_enabled():
+        return False
+    for name, t in frozen.items():
+        if t.requires_grad:
+            raise ValueError(f"{name} gets no gradient from {what}(): pass {name}.detach()")
+    if not any(t.requires_grad for t in trained):
+        return False
+    if out is not None:
+        raise ValueError(f"{what}() with out= is not recorded by autograd, and an input requires a gradient: "
+                         f"leave out= away, or call it under torch.no_grad()")
+    from ._autograd import refuse_capture
+
+    refuse_capture(what)
+    return True
 
 
 def adapters(x, codes, scales, bits: int, a, b, gain, index, out=None):
@@ -492,11 +533,18 @@ def adapters(x, codes, scales, bits: int, a, b, gain, index, out=None):
     x [M, K], a [count, rank, K], b [count, N, rank] and out [M, N] in bf16,
     gain [count] in float32, index [M] in int32; any M from 1 to MAX_ROWS,
     any rank from 1 to MAX_RANK. A row whose index is not in [0, count) has
-    no adapter."""
+    no adapter.
+
+    Where x, a or b requires a gradient, autograd records the call and takes
+    the gradients from adapters_backward(). scales and gain get none."""
     m, k, device = _rows_of("x", x)
     n = _packed_rows(codes)
     packed = _packed_address(codes, scales, n, k, bits, device)
     set_ = _adapter_addresses(a, b, gain, index, m, n, k, device)
+    if _may_be_recorded(x, a, b, scales, gain) and _recorded("adapters", (x, a, b), {"scales": scales, "gain": gain}, out):
+        from ._autograd import Adapters
+
+        return Adapters.apply(x, codes, scales, bits, a, b, gain, index)
     out = _output("out", out, (m, n), device)
     adapters_raw(x.data_ptr(), m, *packed, geom(n, k, bits), *set_, out.data_ptr(), _stream_handle(device))
     return out
@@ -505,7 +553,8 @@ def adapters(x, codes, scales, bits: int, a, b, gain, index, out=None):
 def adapters_backward(dout, x, codes, scales, bits: int, a, b, gain, index, dx=None, da=None, db=None):
     """Gradients of adapters() for the gradient dout [M, N] of its output:
     (dx [M, K], da [count, rank, K], db [count, N, rank]), bf16, each written
-    whole (an adapter without rows gets zeros)."""
+    whole (an adapter without rows gets zeros). They are not differentiated
+    further: autograd records nothing of this call."""
     m, k, device = _rows_of("x", x)
     n = _packed_rows(codes)
     packed = _packed_address(codes, scales, n, k, bits, device)
@@ -524,11 +573,20 @@ def gated(x, codes_gate, scales_gate, codes_up, scales_up, bits: int, out=None, 
     """h[M, N] = silu(x . Wg^T) * (x . Wu^T) in one pass over both packed
     matrices, any M from 1 to MAX_ROWS, evaluated in float32 and rounded once.
     With keep, returns (h, gate, up): the projections that gated_backward()
-    takes."""
+    takes.
+
+    Where x requires a gradient, autograd records the call, keeps both
+    projections for it and takes the gradient from gated_backward(). The
+    scales get none, and a gradient of a returned gate or up is refused."""
     m, k, device = _rows_of("x", x)
     n = _packed_rows(codes_gate, "_gate")
     packed = (*_packed_address(codes_gate, scales_gate, n, k, bits, device, "_gate"),
               *_packed_address(codes_up, scales_up, n, k, bits, device, "_up"))
+    if _may_be_recorded(x, scales_gate, scales_up) and _recorded(
+            "gated", (x,), {"scales_gate": scales_gate, "scales_up": scales_up}, out):
+        from ._autograd import Gated
+
+        return Gated.apply(x, codes_gate, scales_gate, codes_up, scales_up, bits, keep)
     h = _output("out", out, (m, n), device)
     gate = _output("gate", None, (m, n), device) if keep else None
     up = _output("up", None, (m, n), device) if keep else None
@@ -540,7 +598,9 @@ def gated(x, codes_gate, scales_gate, codes_up, scales_up, bits: int, out=None, 
 def gated_backward(dh, gate, up, codes_gate, scales_gate, codes_up, scales_up, bits: int, dx=None, dgate=None,
                    dup=None):
     """Gradients of gated() for the gradient dh [M, N] of h and the kept
-    projections: (dx [M, K], dgate [M, N], dup [M, N]), bf16."""
+    projections: (dx [M, K], dgate [M, N], dup [M, N]), bf16; dx is that of the
+    rounded dgate and dup. They are not differentiated further: autograd
+    records nothing of this call."""
     m, n, device = _rows_of("dh", dh)
     bf = _kinds()[1]
     kept = _address("gate", gate, bf, (m, n), device), _address("up", up, bf, (m, n), device)
