@@ -25,10 +25,10 @@ constexpr int kDenseRows = 256;   // rows of a workgroup's tile
 constexpr int kDenseStep = 32;    // contraction columns per step
 constexpr int kDenseThreads = 512;
 
-// bf16 weight of a window: code * q where the row's scale allows it, else the
-// page's chain (see decode.hpp).
-__device__ __forceinline__ float window_weight(uint32_t win, float s, float q, float k, bool exact) {
-  return exact ? trellis_value(code_of(win)) * s : __builtin_fmaf(code_plus_magic(win), q, k);
+// bf16 weight of a window: code * q, or the page's chain where a row's scale
+// lies outside the range in which the two agree (see decode.hpp).
+__device__ __forceinline__ float window_weight(uint32_t win, float s, float q, float k, bool chain) {
+  return chain ? trellis_value(code_of(win)) * s : __builtin_fmaf(code_plus_magic(win), q, k);
 }
 
 struct Unpack {
@@ -58,7 +58,7 @@ __global__ __launch_bounds__(256) void unpack_rows_kernel(Unpack U) {
   const float s = bf16_bits_to_f32(U.scales[which][row]);
   float q, kq;
   alu_row_constants(s, q, kq);
-  const bool exact = !__all(alu_scale_ok(s));
+  const bool chain = !__all(alu_scale_ok(s));
   const int base = (248 - 8 * g) * BITS, w0 = base >> 5, off = base & 31;
   uint64_t f[8];
 #pragma unroll
@@ -73,7 +73,7 @@ __global__ __launch_bounds__(256) void unpack_rows_kernel(Unpack U) {
     bf16x8 v;
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      v[e] = (__bf16)window_weight((uint32_t)(f[st] >> ((7 - e) * BITS)) & 0xFFFu, s, q, kq, exact);
+      v[e] = (__bf16)window_weight((uint32_t)(f[st] >> ((7 - e) * BITS)) & 0xFFFu, s, q, kq, chain);
     out[st * stride] = v;
   }
 }
@@ -114,7 +114,7 @@ __global__ __launch_bounds__(256) void unpack_columns_kernel(Unpack U) {
     alu_row_constants(sc[e], q[e], kq[e]);
     in_range = in_range && alu_scale_ok(sc[e]);
   }
-  const bool exact = !__all(in_range);
+  const bool chain = !__all(in_range);
 #pragma unroll
   for (int i = 0; i < BITS; ++i) {
     const int at = (64 * i + lane) * 4;
@@ -132,7 +132,7 @@ __global__ __launch_bounds__(256) void unpack_columns_kernel(Unpack U) {
       const uint32_t f = __builtin_amdgcn_alignbit(row[w1], row[w0], sh);
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        w[c][e] = (__bf16)window_weight(__builtin_amdgcn_ubfe(f, (3 - c) * BITS, 12), sc[e], q[e], kq[e], exact);
+        w[c][e] = (__bf16)window_weight(__builtin_amdgcn_ubfe(f, (3 - c) * BITS, 12), sc[e], q[e], kq[e], chain);
     }
     // Through the wave's LDS again, so that each store writes 1 KB in a row:
     // lane (j, g) holds slots 16 g + 4 (j mod 4) .. +3 of tile j / 4.
@@ -173,8 +173,12 @@ __global__ __launch_bounds__(256) void pack_rows_kernel(const uint16_t *__restri
 }
 
 // The gated block's elementwise gradients (see gated_grad_kernel) as rows and
-// as operands: steps 0 .. steps - 1 hold dgate, the next `steps` dup. 2048 rows
-// of 17408 in 112 us: 214 MB read and 285 MB written, 4.5 TB/s.
+// as operands: steps 0 .. steps - 1 hold dgate, the next `steps` dup. The
+// operands are the rounded gradients: bf16 is what the matrix cores multiply at
+// this rate, the rounded ones are outputs anyway, and two halves of each would
+// double the product. dx is then off by 1.4 times what one rounding costs (each
+// of its 2 N terms by up to 2^-8, of either sign). 2048 rows of 17408 in 112 us:
+// 214 MB read and 285 MB written, 4.5 TB/s.
 template <bool WIDE>
 __global__ __launch_bounds__(256) void gated_grad_pack_kernel(const uint16_t *__restrict__ dh,
                                                               const uint16_t *__restrict__ gate,
@@ -274,6 +278,10 @@ constexpr int dense_buffers(int nt) { return 160 * 1024 / dense_step_bytes(nt) <
 // ms. Tried and not kept: four waves of 128 x 128 (2.0 ms), a raised wave
 // priority around the MFMAs, the reads before the copies, the other order of
 // the accumulators (all within 1%).
+// Registers: forward with six to eight column tiles a wave, the adapters' term
+// does not fit beside the accumulators, and its operands go through 16, 176 and
+// 312 bytes of scratch memory a lane, in and around the term's loop (once per
+// named adapter and 32 rank columns); the steps use none.
 template <int NT, bool GATED, bool T>
 __global__ __launch_bounds__(kDenseThreads) void dense_kernel(Dense D) {
   constexpr int kA = kDenseRows / 16 * 1024, kBuffer = dense_step_bytes(NT), S = dense_buffers(NT);

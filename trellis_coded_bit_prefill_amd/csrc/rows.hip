@@ -8,8 +8,9 @@
 //   transposed  out[M, K] = P[M, N] . W     (contraction over N)
 // and product_kernel computes both: a workgroup owns a tile of rows of P and a
 // group of output columns, stages P in LDS one step of the contraction at a
-// time, and its waves decode the weights straight into MFMA operand registers.
-// W is decoded once per tile of rows and never stored.
+// time, and its waves decode the weights straight into MFMA operand registers,
+// once per tile of rows. Where decoding W once for all rows takes less, it goes
+// through memory instead (dense.hpp; plan_of chooses).
 //
 // The low-rank parts are sums of their own: t = x A^T and u = dout B
 // (shrink_kernel), added to the product before it is rounded, and the
@@ -287,7 +288,8 @@ namespace {
 // tiles 229 us (VALU 42%, LDS 36%, MFMA 18%). Tried and slower: one column tile
 // per wave from four row tiles on (53 against 49 us at 64 rows), two up to two
 // (40 against 38.7 at 24), four waves per SIMD from four row tiles on (97
-// against 47 at 64: registers spill).
+// against 47 at 64: registers spill). Transposed with six row tiles 48 bytes a
+// lane go through scratch memory outside the steps.
 template <int BITS, int KIND, int MT, int NT, int OCC>
 __global__ __launch_bounds__(kThreads, OCC) void product_kernel(Product P) {
   constexpr bool kT = KIND == kTransposed;
