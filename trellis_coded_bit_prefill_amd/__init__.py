@@ -416,18 +416,18 @@ def gate_up(x, codes_gate, scales_gate, codes_up, scales_up, bits: int, out=None
     return out
 
 
-_types = None
+_types = _grad_enabled = _forward_ad = None
 
 
 def _kinds():
-    """(Tensor, bf16 dtypes, code dtypes, float32, int32, torch.is_grad_enabled,
-    torch.autograd.forward_ad), looked up once."""
-    global _types
+    """(Tensor, bf16 dtypes, code dtypes, float32, int32), looked up once, and
+    with them torch.is_grad_enabled and torch.autograd.forward_ad."""
+    global _types, _grad_enabled, _forward_ad
     if _types is None:
         import torch
 
-        _types = (torch.Tensor, *_dtypes(), (torch.float32,), (torch.int32,), torch.is_grad_enabled,
-                  torch.autograd.forward_ad)
+        _grad_enabled, _forward_ad = torch.is_grad_enabled, torch.autograd.forward_ad
+        _types = (torch.Tensor, *_dtypes(), (torch.float32,), (torch.int32,))
     return _types
 
 
@@ -461,7 +461,7 @@ def _output(name, t, shape, device):
 
 def _packed_address(codes, scales, n, k: int, bits: int, device, suffix: str = ""):
     """Addresses of one packed matrix [n, k] and its scales."""
-    _, bf, cw = _kinds()[:3]
+    _, bf, cw, _, _ = _kinds()
     if bits not in (2, 3, 4):
         raise ValueError(f"bits must be 2, 3 or 4, got {bits}")
     return (_address("codes" + suffix, codes, cw, (n, k * bits // 32), device),
@@ -477,7 +477,7 @@ def _packed_rows(codes, suffix: str = "") -> int:
 
 def _adapter_addresses(a, b, gain, index, m: int, n: int, k: int, device):
     """(addresses of a, b, gain and index, count, rank) of an adapter set for m rows of a layer [n, k]."""
-    tensor, bf, _, f32, i32 = _kinds()[:5]
+    tensor, bf, _, f32, i32 = _kinds()
     if not isinstance(a, tensor) or a.ndim != 3:
         raise TypeError("a must be a torch.Tensor of three dims")
     count, rank, _ = a.shape
@@ -485,30 +485,19 @@ def _adapter_addresses(a, b, gain, index, m: int, n: int, k: int, device):
             _address("gain", gain, f32, (count,), device), _address("index", index, i32, (m,), device), count, rank)
 
 
-def _may_be_recorded(*tensors) -> bool:
-    """Whether autograd has anything to do with a call: what follows is looked at only then."""
-    grad_enabled, forward_ad = _kinds()[-2:]
-    if forward_ad._current_level >= 0:
-        return True
-    if grad_enabled():
-        for t in tensors:
-            if t.requires_grad:
-                return True
-    return False
-
-
 def _recorded(what: str, trained, frozen, out) -> bool:
     """Whether autograd has to record this call: gradients are enabled and one
     of `trained` requires one. What would lose a gradient without a word is
     refused: a tensor of `frozen` (by name) that requires one, `out` given to a
     recorded call, a tangent of forward mode, and a recorded call while its
-    stream is captured (see _autograd.py)."""
-    grad_enabled, forward_ad = _kinds()[-2:]
-    if forward_ad._current_level >= 0:
+    stream is captured (see _autograd.py). The calls come here only if one of
+    their tensors requires a gradient or forward mode is on: the tests of that
+    stand in their own lines, as launches take only a few microseconds."""
+    if _forward_ad._current_level >= 0:
         for t in (*trained, *frozen.values()):
-            if t.is_floating_point() and forward_ad.unpack_dual(t).tangent is not None:
+            if t.is_floating_point() and _forward_ad.unpack_dual(t).tangent is not None:
                 raise NotImplementedError(f"{what}() has no forward-mode derivative")
-    if not grad_enabled():
+    if not _grad_enabled():
         return False
     for name, t in frozen.items():
         if t.requires_grad:
@@ -541,7 +530,9 @@ def adapters(x, codes, scales, bits: int, a, b, gain, index, out=None):
     n = _packed_rows(codes)
     packed = _packed_address(codes, scales, n, k, bits, device)
     set_ = _adapter_addresses(a, b, gain, index, m, n, k, device)
-    if _may_be_recorded(x, a, b, scales, gain) and _recorded("adapters", (x, a, b), {"scales": scales, "gain": gain}, out):
+    if ((x.requires_grad or a.requires_grad or b.requires_grad or scales.requires_grad or gain.requires_grad
+         or _forward_ad._current_level >= 0)
+            and _recorded("adapters", (x, a, b), {"scales": scales, "gain": gain}, out)):
         from ._autograd import Adapters
 
         return Adapters.apply(x, codes, scales, bits, a, b, gain, index)
@@ -582,8 +573,8 @@ def gated(x, codes_gate, scales_gate, codes_up, scales_up, bits: int, out=None, 
     n = _packed_rows(codes_gate, "_gate")
     packed = (*_packed_address(codes_gate, scales_gate, n, k, bits, device, "_gate"),
               *_packed_address(codes_up, scales_up, n, k, bits, device, "_up"))
-    if _may_be_recorded(x, scales_gate, scales_up) and _recorded(
-            "gated", (x,), {"scales_gate": scales_gate, "scales_up": scales_up}, out):
+    if ((x.requires_grad or scales_gate.requires_grad or scales_up.requires_grad or _forward_ad._current_level >= 0)
+            and _recorded("gated", (x,), {"scales_gate": scales_gate, "scales_up": scales_up}, out)):
         from ._autograd import Gated
 
         return Gated.apply(x, codes_gate, scales_gate, codes_up, scales_up, bits, keep)
