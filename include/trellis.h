@@ -228,18 +228,30 @@ trellis_status trellis_prefill_noalloc(const uint16_t *x_bf16, int32_t m,
  * and stream: call once before capturing, and order a captured graph's replays
  * with every other use of the capture stream; a call that would have to
  * allocate while its stream is captured, in any capture mode, returns
- * TRELLIS_E_HIP before any GPU work). From some hundred rows on it
- * holds the decoded weights (2 bytes each, at most 1 GiB at a time) and a copy
- * of x or of the output's gradient, below that partial sums of at most some
- * 64 MB, and 8 bytes a row and rank column for adapters; it grows by half at
- * least. All sums are float32; outputs
+ * TRELLIS_E_HIP before any GPU work). It holds
+ *   - where the weights are decoded once for all rows (from some hundred rows
+ *     on): the decoded weights of a launch, 2 bytes each, at most 1 GiB, but
+ *     one 256-column block at least: in the backward passes 512 bytes per row
+ *     of W, of both matrices (beyond 1 GiB from 2^21 such rows on);
+ *     a copy of x, or of the gradient that the product takes (of both dgate
+ *     and dup), 2 bytes a value however many rows there are; and the float32
+ *     partial sums of a split contraction, 4 bytes per output and split (at
+ *     most eight; hundreds of MB where long contractions meet thousands of rows);
+ *   - else partial sums of at most some 64 MB;
+ *   - for adapters 4 bytes a row and rank column (rounded up to 32; the backward
+ *     pass: 8).
+ * It grows by half at least, and outgrown buffers stay allocated: in all at most
+ * four and a half times what the largest call needs. All sums are float32; outputs
  * are rounded to bf16 once. Results do not depend on timing: every sum has a
  * fixed order. Inputs and outputs must not overlap. */
 
 /* Low-rank adapters of many requests beside one shared projection:
  *   out[r] = W x[r] + gain[i] * B[i] (A[i] x[r]),   i = index[r],
  * for the m rows r of x; a row whose index lies outside [0, count) has no
- * adapter (out[r] = W x[r]). Rows of one adapter need not stand together.
+ * adapter (out[r] = W x[r]). Rows of one adapter need not stand together, but
+ * cost less if they do: the low-rank sums take every adapter that 16 or 64
+ * neighbouring rows name in turn, and the backward pass reads x and dout between
+ * an adapter's first and last row.
  *   x      bf16 [m, K]            out   bf16 [m, N]
  *   a      bf16 [count, rank, K]  b     bf16 [count, N, rank]
  *   gain   float32 [count]        index int32 [m]

@@ -1,6 +1,6 @@
 // Many rows: W is decoded once into a workspace of MFMA operands, P's rows are
 // copied into the same form, and a dense product reads both from there
-// (rows.hip decides from how many rows on).
+// (plan_of in rows.hip decides where).
 //
 // Workspace layout of either side. A "tile" is 16 rows of P or 16 output
 // columns, a "step" 32 columns of the contraction; [step][tile][lane][8] bf16

@@ -1138,7 +1138,11 @@ __global__ __launch_bounds__(64 * WAVES) void backward_sums_kernel(BackwardSums 
 // as zeros on both sides (a NaN in them must not count). V as the sum of two
 // bf16 numbers (2^-16 relative). The next chunk is loaded ahead. 2048 rows,
 // K = 5120, N = 17408, rank 32, two adapters: 46 us, 97 MB read (2.1 TB/s; what
-// it waits for is each wave's own chain of chunks).
+// it waits for is each wave's own chain of chunks). A chunk between an adapter's
+// first and last row is read whether or not it holds one of its rows: adapters
+// whose rows alternate read all of x and dout each (the whole backward call of
+// these sizes: 442 us with eight adapters in runs, 689 alternating; 492 and 1538
+// with 32).
 struct Outer {
   const uint16_t *x, *dout;
   const float *u, *t;
