@@ -84,7 +84,8 @@ struct Product {
 // instead of rounded, and without a zero or a NaN as the rest of what is not
 // zero, so that an infinity on either side of the product gives the infinity
 // that v times it gives: of opposite signs the halves' infinities would cancel
-// to a NaN.
+// to a NaN. (Below 2^-96 the rest of a v that is one bf16 number already
+// vanishes, and an infinity times it gives a NaN.)
 __device__ __forceinline__ void halves(const float (&v)[8], bf16x8 &hi, bf16x8 &lo) {
   u32x4 top;
 #pragma unroll
