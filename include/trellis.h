@@ -100,6 +100,11 @@ extern "C" {
 #define TRELLIS_MAX_ROWS (1 << 20)
 #define TRELLIS_MAX_ADAPTERS 4096
 #define TRELLIS_MAX_RANK 128
+/* Limits of the entry points for a model's two ends (trellis_cross_entropy and below). */
+#define TRELLIS_MAX_TOP 256
+#define TRELLIS_MIN_TEMPERATURE 0.01f
+#define TRELLIS_MAX_TEMPERATURE 100.0f
+#define TRELLIS_MAX_TRAINED (1 << 22)
 /* Device memory of trellis_prefill_noalloc, per GPU: 1 MiB of tile counters
  * plus 31 MiB of float32 partial tiles. */
 #define TRELLIS_NOALLOC_SCRATCH_BYTES (32u << 20)
@@ -123,7 +128,8 @@ typedef enum trellis_status {
     TRELLIS_E_ALIGN = -4,    /* a pointer is not aligned as documented */
     TRELLIS_E_HIP = -5,      /* the HIP runtime reported a launch error */
     TRELLIS_E_SCRATCH = -6,  /* trellis_prefill_noalloc: the call's workspace exceeds the fixed scratch */
-    TRELLIS_E_ADAPTERS = -7  /* the number of adapters or their rank outside the accepted range */
+    TRELLIS_E_ADAPTERS = -7, /* the number of adapters or their rank outside the accepted range */
+  TRELLIS_E_RANGE = -8     /* listed entries, temperature, trained rows or scale outside the accepted range */
 } trellis_status;
 
 /* 1 if (g, m) is inside the accepted domain of trellis_prefill, else 0.
@@ -300,6 +306,83 @@ trellis_status trellis_gated_backward(const uint16_t *dh_bf16, const uint16_t *g
                                       int32_t m, const uint32_t *codes_gate, const uint16_t *scales_gate,
                                       const uint32_t *codes_up, const uint16_t *scales_up, trellis_geom g,
                                       uint16_t *dx_bf16, uint16_t *dgate_bf16, uint16_t *dup_bf16, void *hip_stream);
+
+/* ---- A model's two ends on packed vocabulary matrices -----------------------
+ *
+ * W[N, K] has a row per vocabulary entry: the output layer that the loss is
+ * taken of, the embedding that tokens are looked up in, or both at once. Formats,
+ * accepted geometries, execution, errors and workspaces are those of the
+ * fine-tuned layers above (1 <= m <= TRELLIS_MAX_ROWS).
+ *
+ * The losses never keep the logits: they live in the stream's workspace, in
+ * pieces of at most 1 GiB. Sums and softmax statistics are float32. */
+
+/* Softmax cross entropy of the logits l = W x[r] against one entry a row:
+ *   lse[r] = log sum_v exp(l_v),  loss[r] = lse[r] - l[target[r]],
+ *   dx[r]  = sum_v p_v W_v - W[target[r]],  p = exp(l - lse[r]).
+ * A row whose target lies outside [0, N) has no part in the loss: loss[r] and
+ * dx[r] are 0 (lse[r] is written). dx[r] is the gradient of loss[r] alone (see
+ * trellis_loss_backward); NULL where it is not wanted, which saves half of the
+ * work and more.
+ *   x      bf16 [m, K]       target int32 [m]
+ *   loss   float32 [m]       lse    float32 [m]
+ *   dx     bf16 [m, K] or NULL
+ * x and dx 16-byte aligned, target, loss and lse 4-byte aligned. The loss of a
+ * likely target and its part 1 - p of dx are computed from the sum over the
+ * other entries, so they keep their relative accuracy. */
+trellis_status trellis_cross_entropy(const uint16_t *x_bf16, int32_t m, const uint32_t *codes,
+                                     const uint16_t *scales_bf16, trellis_geom g, const int32_t *target, float *loss,
+                                     float *lse, uint16_t *dx_bf16, void *hip_stream);
+
+/* The same against a teacher's best entries: row r's list holds the vocabulary
+ * entries index[r, 0 .. top) with the teacher's logits z[r, 0 .. top), and with
+ * the temperature T
+ *   q = softmax(z / T) over the list,  p = softmax(l / T) over the vocabulary,
+ *   loss[r] = T^2 sum_j q_j (log q_j - log p_{index_j}),
+ *   lse[r]  = log sum_v exp(l_v / T),
+ *   dx[r]   = T (sum_v p_v W_v - sum_j q_j W_{index_j}).
+ * An entry whose index lies outside [0, N) is none, whatever its logit (lists of
+ * different lengths), as is one with the logit -infinity; a row without entries
+ * has no part in the loss (loss[r] and dx[r] 0). An index may stand in a list
+ * several times: each place is an entry j of its own.
+ *   index int32 [m, top]     logits float32 [m, top]   4-byte aligned
+ * 1 <= top <= TRELLIS_MAX_TOP, TRELLIS_MIN_TEMPERATURE <= temperature <=
+ * TRELLIS_MAX_TEMPERATURE; the rest as in trellis_cross_entropy. The index and
+ * the teacher's logits get no gradient. */
+trellis_status trellis_distill(const uint16_t *x_bf16, int32_t m, const uint32_t *codes, const uint16_t *scales_bf16,
+                               trellis_geom g, const int32_t *index, const float *logits, int32_t top,
+                               float temperature, float *loss, float *lse, uint16_t *dx_bf16, void *hip_stream);
+
+/* The gradient of x from that of the rows' losses and the dx that
+ * trellis_cross_entropy or trellis_distill gave: out[r] = dloss[r] * dx[r],
+ * rounded once more. dloss float32 [m], dx and out bf16 [m, k] (k a multiple of
+ * 256 up to TRELLIS_MAX_K), 16-byte aligned; out may be dx. */
+trellis_status trellis_loss_backward(const float *dloss, const uint16_t *dx_bf16, int32_t m, int32_t k,
+                                     uint16_t *out_bf16, void *hip_stream);
+
+/* Embedding: out[r] = scale * W[token[r]], one product of the bf16 weight with
+ * the float32 scale, rounded once. Tokens N .. N + count - 1 are those of the
+ * trained rows extra [count, K] (added tokens, learned prompts); any other token
+ * gives a row of zeros.
+ *   tokens int32 [m], 4-byte aligned   extra bf16 [count, K] or NULL (count 0)
+ *   out    bf16 [m, K]                 extra and out 16-byte aligned
+ * 0 <= count <= TRELLIS_MAX_TRAINED; scale finite. */
+trellis_status trellis_embed(const int32_t *tokens, int32_t m, const uint32_t *codes, const uint16_t *scales_bf16,
+                             trellis_geom g, float scale, const uint16_t *extra_bf16, int32_t count,
+                             uint16_t *out_bf16, void *hip_stream);
+
+/* Gradient of the trained rows for the gradient dout [m, k] of trellis_embed's
+ * output: dextra[e] = scale * (sum of dout[r] over the rows r with token first +
+ * e), first being the packed matrix's N. The rows are sorted by token, stable,
+ * and summed in float32 in an order that depends on their number and positions
+ * alone; all of dextra bf16 [count, k] is written (a token that no row has
+ * gets zeros). k a multiple of 256 up to TRELLIS_MAX_K, 1 <= count <=
+ * TRELLIS_MAX_TRAINED, 0 <= first <= TRELLIS_MAX_N; dout and dextra 16-byte
+ * aligned. The workspace takes 16 bytes a row, and 4 bytes for each of 256
+ * digits and 2048 rows, and at most 1024 * 2 float32 rows of partial sums. */
+trellis_status trellis_embed_backward(const uint16_t *dout_bf16, const int32_t *tokens, int32_t m, int32_t k,
+                                      int32_t first, int32_t count, float scale, uint16_t *dextra_bf16,
+                                      void *hip_stream);
 
 /* Static, NUL-terminated description of a status code. */
 const char *trellis_status_string(trellis_status s);

@@ -29,6 +29,11 @@ MAX_GROUP_ROWS = 1 << 20
 MAX_ROWS = 1 << 20
 MAX_ADAPTERS = 4096
 MAX_RANK = 128
+MAX_N = 1 << 22
+MAX_TOP = 256
+MIN_TEMPERATURE = 0.01
+MAX_TEMPERATURE = 100.0
+MAX_TRAINED = 1 << 22
 
 OK = 0
 E_GEOMETRY = -1
@@ -38,12 +43,14 @@ E_ALIGN = -4
 E_HIP = -5
 E_SCRATCH = -6
 E_ADAPTERS = -7
+E_RANGE = -8
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
 # Every symbol declared in include/trellis.h.
 EXPORTED = ("trellis_supported", "trellis_decode", "trellis_prefill", "trellis_matvec", "trellis_prefill_packed",
             "trellis_gate_up", "trellis_prefill_noalloc", "trellis_adapters", "trellis_adapters_backward",
-            "trellis_gated", "trellis_gated_backward", "trellis_status_string")
+            "trellis_gated", "trellis_gated_backward", "trellis_cross_entropy", "trellis_distill",
+            "trellis_loss_backward", "trellis_embed", "trellis_embed_backward", "trellis_status_string")
 # Test and tuning hooks (include/trellis_testing.h).
 EXPORTED_TESTING = ("trellis_test_force_table", "trellis_test_force_path")
 TABLES = {"value": 0, "code": 1, "pair": 2}
@@ -118,6 +125,17 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     L.trellis_gated.restype = ctypes.c_int
     L.trellis_gated_backward.argtypes = [vp, vp, vp, i32, vp, vp, vp, vp, Geom, vp, vp, vp, vp]
     L.trellis_gated_backward.restype = ctypes.c_int
+    f32 = ctypes.c_float
+    L.trellis_cross_entropy.argtypes = [vp, i32, vp, vp, Geom, vp, vp, vp, vp, vp]
+    L.trellis_cross_entropy.restype = ctypes.c_int
+    L.trellis_distill.argtypes = [vp, i32, vp, vp, Geom, vp, vp, i32, f32, vp, vp, vp, vp]
+    L.trellis_distill.restype = ctypes.c_int
+    L.trellis_loss_backward.argtypes = [vp, vp, i32, i32, vp, vp]
+    L.trellis_loss_backward.restype = ctypes.c_int
+    L.trellis_embed.argtypes = [vp, i32, vp, vp, Geom, f32, vp, i32, vp, vp]
+    L.trellis_embed.restype = ctypes.c_int
+    L.trellis_embed_backward.argtypes = [vp, vp, i32, i32, i32, i32, f32, vp, vp]
+    L.trellis_embed_backward.restype = ctypes.c_int
     L.trellis_test_force_table.argtypes = [ctypes.c_int]
     L.trellis_test_force_table.restype = ctypes.c_int
     L.trellis_test_force_path.argtypes = [ctypes.c_int, ctypes.c_int]
@@ -271,6 +289,38 @@ def gated_backward_raw(dh_ptr: int, gate_ptr: int, up_ptr: int, m: int, codes_ga
     """Direct C-ABI call with raw device addresses."""
     _raise(load_library().trellis_gated_backward(dh_ptr, gate_ptr, up_ptr, m, codes_gate_ptr, scales_gate_ptr,
                                                  codes_up_ptr, scales_up_ptr, g, dx_ptr, dgate_ptr, dup_ptr, stream))
+
+
+def cross_entropy_raw(x_ptr: int, m: int, codes_ptr: int, scales_ptr: int, g: Geom, target_ptr: int, loss_ptr: int,
+                      lse_ptr: int, dx_ptr: int, stream: int) -> None:
+    """Direct C-ABI call with raw device addresses (dx_ptr may be 0)."""
+    _raise(load_library().trellis_cross_entropy(x_ptr, m, codes_ptr, scales_ptr, g, target_ptr, loss_ptr, lse_ptr,
+                                                dx_ptr, stream))
+
+
+def distill_raw(x_ptr: int, m: int, codes_ptr: int, scales_ptr: int, g: Geom, index_ptr: int, logits_ptr: int, top: int,
+                temperature: float, loss_ptr: int, lse_ptr: int, dx_ptr: int, stream: int) -> None:
+    """Direct C-ABI call with raw device addresses (dx_ptr may be 0)."""
+    _raise(load_library().trellis_distill(x_ptr, m, codes_ptr, scales_ptr, g, index_ptr, logits_ptr, top, temperature,
+                                          loss_ptr, lse_ptr, dx_ptr, stream))
+
+
+def loss_backward_raw(dloss_ptr: int, dx_ptr: int, m: int, k: int, out_ptr: int, stream: int) -> None:
+    """Direct C-ABI call with raw device addresses."""
+    _raise(load_library().trellis_loss_backward(dloss_ptr, dx_ptr, m, k, out_ptr, stream))
+
+
+def embed_raw(tokens_ptr: int, m: int, codes_ptr: int, scales_ptr: int, g: Geom, scale: float, extra_ptr: int,
+              count: int, out_ptr: int, stream: int) -> None:
+    """Direct C-ABI call with raw device addresses (extra_ptr may be 0 where count is 0)."""
+    _raise(load_library().trellis_embed(tokens_ptr, m, codes_ptr, scales_ptr, g, scale, extra_ptr, count, out_ptr,
+                                        stream))
+
+
+def embed_backward_raw(dout_ptr: int, tokens_ptr: int, m: int, k: int, first: int, count: int, scale: float,
+                       dextra_ptr: int, stream: int) -> None:
+    """Direct C-ABI call with raw device addresses."""
+    _raise(load_library().trellis_embed_backward(dout_ptr, tokens_ptr, m, k, first, count, scale, dextra_ptr, stream))
 
 
 @dataclass
@@ -605,3 +655,132 @@ def gated_backward(dh, gate, up, codes_gate, scales_gate, codes_up, scales_up, b
     gated_backward_raw(dh.data_ptr(), *kept, m, *packed, geom(n, k, bits), dx.data_ptr(), dgate.data_ptr(),
                        dup.data_ptr(), _stream_handle(device))
     return dx, dgate, dup
+
+
+def _loss(what, raw, x, codes, scales, bits, lists, keep):
+    """The common part of the losses: lists are the addresses and numbers that stand between g and the outputs."""
+    import torch
+
+    m, k, device = _rows_of("x", x)
+    n = codes.shape[0]
+    packed = _packed_address(codes, scales, n, k, bits, device)
+    loss = torch.empty(m, dtype=torch.float32, device=device)
+    lse = torch.empty(m, dtype=torch.float32, device=device)
+    dx = torch.empty((m, k), dtype=torch.bfloat16, device=device) if keep else None
+    raw(x.data_ptr(), m, *packed, geom(n, k, bits), *lists, loss.data_ptr(), lse.data_ptr(),
+        dx.data_ptr() if keep else 0, _stream_handle(device))
+    return (loss, lse, dx) if keep else (loss, lse)
+
+
+def cross_entropy(x, codes, scales, bits: int, target, keep: bool = False):
+    """Softmax cross entropy of the logits x . W^T over a packed vocabulary
+    matrix, which are never kept: (loss [M], lse [M]) in float32 on the current
+    stream, with keep (loss, lse, dx [M, K] bf16):
+
+        lse[r] = log sum_v exp(W_v x[r]),  loss[r] = lse[r] - W_target x[r],
+        dx[r]  = the gradient of loss[r] with respect to x[r]
+
+    target [M] in int32; a row whose target is not in [0, N) has loss and dx 0.
+    loss_backward() multiplies dx by the rows' gradients.
+
+    Where x requires a gradient, autograd records the call, which then computes
+    dx as well (half as much work again and more) and keeps it for the backward
+    pass. lse and a returned dx carry no gradient."""
+    m, _, device = _rows_of("x", x)
+    _packed_rows(codes)
+    target_ptr = _address("target", target, _kinds()[4], (m,), device)
+    if ((x.requires_grad or scales.requires_grad or _forward_ad._current_level >= 0)
+            and _recorded("cross_entropy", (x,), {"scales": scales}, None)):
+        from ._autograd import CrossEntropy
+
+        return CrossEntropy.apply(x, codes, scales, bits, target, keep)
+    return _loss("cross_entropy", cross_entropy_raw, x, codes, scales, bits, (target_ptr,), keep)
+
+
+def distill(x, codes, scales, bits: int, index, logits, temperature: float = 1.0, keep: bool = False):
+    """Distillation from a teacher's best logits: with T the temperature,
+    q = softmax(logits / T) over each row's list and p the softmax of
+    x . W^T / T over the whole packed vocabulary,
+
+        loss[r] = T^2 sum_j q_j (log q_j - log p_index_j),
+        lse[r]  = log sum_v exp(W_v x[r] / T),
+        dx[r]   = the gradient of loss[r] with respect to x[r]
+
+    (loss, lse), with keep (loss, lse, dx). index [M, top] in int32 and logits
+    [M, top] in float32, top from 1 to MAX_TOP. An entry whose index is not in
+    [0, N) or whose logit is -inf is none; a row without entries has loss and dx
+    0. Recorded by autograd as cross_entropy() is; index and logits get no
+    gradient."""
+    m, _, device = _rows_of("x", x)
+    _packed_rows(codes)
+    tensor, _, _, f32, i32 = _kinds()
+    if not isinstance(index, tensor) or index.ndim != 2:
+        raise TypeError("index must be a torch.Tensor of two dims")
+    top = index.shape[1]
+    lists = (_address("index", index, i32, (m, top), device), _address("logits", logits, f32, (m, top), device), top,
+             temperature)
+    if ((x.requires_grad or scales.requires_grad or logits.requires_grad or _forward_ad._current_level >= 0)
+            and _recorded("distill", (x,), {"scales": scales, "logits": logits}, None)):
+        from ._autograd import Distill
+
+        return Distill.apply(x, codes, scales, bits, index, logits, temperature, keep)
+    return _loss("distill", distill_raw, x, codes, scales, bits, lists, keep)
+
+
+def loss_backward(dloss, dx, out=None):
+    """The gradient of x from the gradients dloss [M] (float32) of the rows'
+    losses and the dx [M, K] that cross_entropy() or distill() kept: dloss[r]
+    dx[r], rounded once more. out may be dx. Not differentiated further:
+    autograd records nothing of this call."""
+    m, k, device = _rows_of("dx", dx)
+    dloss_ptr = _address("dloss", dloss, _kinds()[3], (m,), device)
+    out = _output("out", out, (m, k), device)
+    loss_backward_raw(dloss_ptr, dx.data_ptr(), m, k, out.data_ptr(), _stream_handle(device))
+    return out
+
+
+def embed(tokens, codes, scales, k: int, bits: int, scale: float = 1.0, extra=None, out=None):
+    """Rows of a packed vocabulary matrix: out[r] = scale * W[tokens[r]] in bf16,
+    rounded once, on the current stream. tokens [M] in int32. With extra
+    [count, K] in bf16, the tokens N .. N + count - 1 are those trained rows; any
+    other token gives a row of zeros.
+
+    Where extra requires a gradient, autograd records the call and takes the
+    gradient from embed_backward(); scales get none."""
+    if not isinstance(tokens, _kinds()[0]) or tokens.ndim != 1:
+        raise TypeError("tokens must be a torch.Tensor of one dim")
+    m, device = tokens.shape[0], tokens.device
+    n = _packed_rows(codes)
+    if k < T_BLOCK or k % T_BLOCK:
+        raise ValueError(f"k must be a multiple of {T_BLOCK}, got {k}")
+    tokens_ptr = _address("tokens", tokens, _kinds()[4], (m,), device)
+    packed = _packed_address(codes, scales, n, k, bits, device)
+    count = 0
+    if extra is not None:
+        count = extra.shape[0] if isinstance(extra, _kinds()[0]) and extra.ndim == 2 else -1
+        extra_ptr = _address("extra", extra, _kinds()[1], (count, k), device)
+    recorded = extra if extra is not None else scales
+    if ((recorded.requires_grad or scales.requires_grad or _forward_ad._current_level >= 0)
+            and _recorded("embed", () if extra is None else (extra,), {"scales": scales}, out)):
+        from ._autograd import Embed
+
+        return Embed.apply(tokens, codes, scales, k, bits, scale, extra)
+    out = _output("out", out, (m, k), device)
+    embed_raw(tokens_ptr, m, *packed, geom(n, k, bits), scale, extra_ptr if count else 0, count, out.data_ptr(),
+              _stream_handle(device))
+    return out
+
+
+def embed_backward(dout, tokens, first: int, count: int, scale: float = 1.0, dextra=None):
+    """Gradient of embed()'s trained rows for the gradient dout [M, K] of its
+    output: dextra[e] = scale * the sum of dout[r] over the rows with token
+    first + e (first: the packed matrix's rows N), [count, K] in bf16, all of it
+    written. Summed in float32 in a fixed order and rounded once; not
+    differentiated further."""
+    m, k, device = _rows_of("dout", dout)
+    tokens_ptr = _address("tokens", tokens, _kinds()[4], (m,), device)
+    if not 1 <= count <= MAX_TRAINED:
+        raise ValueError(f"count must be in [1, {MAX_TRAINED}], got {count}")
+    dextra = _output("dextra", dextra, (count, k), device)
+    embed_backward_raw(dout.data_ptr(), tokens_ptr, m, k, first, count, scale, dextra.data_ptr(), _stream_handle(device))
+    return dextra

@@ -1,7 +1,7 @@
-"""What torch's autograd records for adapters() and gated(): the calls
-themselves, and their backward passes adapters_backward() and
-gated_backward() as the gradients. Loaded by the first call that a graph is
-recorded for.
+"""What torch's autograd records for adapters(), gated(), cross_entropy(),
+distill() and embed(): the calls themselves, and their backward passes
+adapters_backward(), gated_backward(), loss_backward() and embed_backward() as
+the gradients. Loaded by the first call that a graph is recorded for.
 """
 from __future__ import annotations
 
@@ -65,3 +65,62 @@ class Gated(torch.autograd.Function):
             return (None,) * 7
         dx = tp.gated_backward(_rows(dh), *ctx.saved_tensors, ctx.bits)[0]
         return (dx,) + (None,) * 6
+
+
+def _loss_outputs(ctx, out, keep):
+    """loss, lse[, dx]: dx is kept for the backward pass, and loss alone is differentiated."""
+    loss, lse, dx = out
+    ctx.save_for_backward(dx)
+    ctx.set_materialize_grads(False)
+    if keep:
+        dx = dx.view_as(dx)
+        ctx.mark_non_differentiable(dx)
+        return loss, lse, dx
+    return loss, lse
+
+
+def _loss_gradient(ctx, what, dloss, dlse):
+    refuse_capture(what)
+    if dlse is not None:
+        raise RuntimeError(f"{what}(): a gradient of lse is not carried back to x")
+    if dloss is None:
+        return None
+    dx, = ctx.saved_tensors
+    return tp.loss_backward(dloss.contiguous(), dx)
+
+
+class CrossEntropy(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, codes, scales, bits, target, keep):
+        return _loss_outputs(ctx, tp.cross_entropy(x, codes, scales, bits, target, keep=True), keep)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dloss, dlse, *_):
+        return (_loss_gradient(ctx, "cross_entropy", dloss, dlse),) + (None,) * 5
+
+
+class Distill(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, codes, scales, bits, index, logits, temperature, keep):
+        return _loss_outputs(ctx, tp.distill(x, codes, scales, bits, index, logits, temperature, keep=True), keep)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dloss, dlse, *_):
+        return (_loss_gradient(ctx, "distill", dloss, dlse),) + (None,) * 7
+
+
+class Embed(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, tokens, codes, scales, k, bits, scale, extra):
+        ctx.save_for_backward(tokens)
+        ctx.at = codes.shape[0], extra.shape[0], scale
+        return tp.embed(tokens, codes, scales, k, bits, scale, extra)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dout):
+        refuse_capture("embed")
+        tokens, = ctx.saved_tensors
+        return (None,) * 6 + (tp.embed_backward(_rows(dout), tokens, *ctx.at),)

@@ -67,6 +67,7 @@ struct Product {
   const uint32_t *codes, *codes2;  // codes2: gated (up), or transposed with two matrices
   const uint16_t *scales, *scales2;
   uint16_t *out, *gate, *up;       // gate, up: gated only, null where they are not kept
+  float *logits;                   // forward: float32 [m, n] in place of out, or null
   float *partials;
   uint32_t *counters;
   int32_t units_q, units_r;  // units (tiles * steps) of a workgroup: units_q, the first units_r one more
@@ -398,6 +399,12 @@ __global__ __launch_bounds__(kThreads, OCC) void product_kernel(Product P) {
     } else {
       const int width = kT ? P.k : P.n, n = agroup * BN + c;
       if (n >= width) return;
+      if constexpr (KIND == kForward) {
+        if (P.logits) {
+          *reinterpret_cast<f32x4 *>(P.logits + (int64_t)mrow * width + n) = v;
+          return;
+        }
+      }
       store4(P.out + (int64_t)mrow * width + n, v);
     }
   };
@@ -1973,3 +1980,6 @@ trellis_status trellis_gated_backward(const uint16_t *dh, const uint16_t *gate, 
 }
 
 }  // extern "C"
+
+#include "loss.hpp"
+#include "embed.hpp"

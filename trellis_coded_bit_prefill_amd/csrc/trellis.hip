@@ -1612,6 +1612,7 @@ const char *trellis_status_string(trellis_status s) {
     case TRELLIS_E_HIP: return "HIP runtime error";
     case TRELLIS_E_SCRATCH: return "the call needs more workspace than the no-allocation entry point's fixed scratch holds";
     case TRELLIS_E_ADAPTERS: return "unsupported adapters: count must be in [1, 4096] and rank in [1, 128]";
+    case TRELLIS_E_RANGE: return "unsupported range: listed entries must be in [1, 256], the temperature in [0.01, 100], trained rows at most 2^22, the scale finite";
   }
   return "unknown status";
 }
