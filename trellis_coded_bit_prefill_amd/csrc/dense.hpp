@@ -227,7 +227,7 @@ __global__ __launch_bounds__(256) void gated_grad_pack_kernel(const uint16_t *__
 struct Dense {
   const uint16_t *p, *w;   // operands of the rows, and of the columns of this launch
   uint16_t *out, *gate, *up;
-  float *partials;         // [splits][m][16 wtiles], where the contraction is split
+  float *partials;         // [splits][m][16 wtiles], where the contraction is split or float32 sums are wanted, else null
   int32_t m, steps;        // steps: an even number
   int32_t splits;          // of the contraction
   int32_t width;           // row length of the outputs
@@ -282,8 +282,14 @@ constexpr int dense_buffers(int nt) { return 160 * 1024 / dense_step_bytes(nt) <
 // does not fit beside the accumulators, and its operands go through 16, 176 and
 // 312 bytes of scratch memory a lane, in and around the term's loop (once per
 // named adapter and 32 rank columns); the steps use none.
-template <int NT, bool GATED, bool T>
-__global__ __launch_bounds__(kDenseThreads) void dense_kernel(Dense D) {
+// Where a lane's sums lie: lane (j, g), accumulator (r, i): row row0 + 16 r + j,
+// operand tile tile0 + i, its columns 4 g .. +3.
+struct DenseAt {
+  int row0, tile0, split;
+};
+// between(at): work of the wave's own while the first steps are on their way.
+template <int NT, typename Between>
+__device__ __forceinline__ DenseAt dense_sums(const Dense &D, f32x4 (&acc)[4][NT], Between between) {
   constexpr int kA = kDenseRows / 16 * 1024, kBuffer = dense_step_bytes(NT), S = dense_buffers(NT);
   constexpr int kCopies = kBuffer / 1024;  // of 1 KB
   constexpr int kMost = (kCopies + 7) / 8, kFull = kCopies % 8 == 0 ? 8 : kCopies % 8;  // waves 0 .. kFull - 1 copy kMost, the others one less
@@ -291,7 +297,6 @@ __global__ __launch_bounds__(kDenseThreads) void dense_kernel(Dense D) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave & 3, wn = wave >> 2;
-  const int j = lane & 15, g = lane >> 4;
   // Consecutive workgroups go to the eight XCDs in turn: each XCD gets a run
   // of consecutive tiles, row tiles first, whose operands its L2 shares.
   const int tiles = D.mtiles * D.ntiles, total = tiles * D.splits, each = total >> 3, rest = total & 7;
@@ -329,91 +334,15 @@ __global__ __launch_bounds__(kDenseThreads) void dense_kernel(Dense D) {
     else step_barrier<N *(kMost - 1)>();
   };
 
-  f32x4 acc[4][NT];
 #pragma unroll
   for (int a = 0; a < 4; ++a)
 #pragma unroll
     for (int b = 0; b < NT; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-  // Lane (j, g), accumulator (r, i): row row0 + 16 r + j, operand tile
-  // tile0 + i, its columns 4 g .. +3.
-  const int row0 = tm * kDenseRows + 64 * wm, tile0 = tn * 2 * NT + wn * NT;
+  const DenseAt at{tm * kDenseRows + 64 * wm, tn * 2 * NT + wn * NT, split};
 #pragma unroll
   for (int b = 0; b < S; ++b)
     if (b < steps) stage(b, b * kBuffer);
-  if constexpr (!GATED) {
-    // The adapters' term first, while the first steps are on their way: lane l
-    // looks up row row0 + l; for every adapter that the wave's rows name, the
-    // products are kept only in the rows that name it (see low_rank_tiles).
-    if (D.low.rank > 0 && split == 0) {
-      int idx = row0 + lane < D.m ? D.low.index[row0 + lane] : -1;
-      if (idx >= D.low.count) idx = -1;
-      uint64_t left = __ballot(idx >= 0);
-      while (left) {
-        const int a = __builtin_amdgcn_readlane(idx, __builtin_ctzll(left));
-        const uint64_t rows = __ballot(idx == a);
-        left &= ~rows;
-        for (int r0 = 8 * g; r0 < D.low.rank_p + 8 * g; r0 += 32) {
-          // The factor's operands, each loaded while the one before it is
-          // multiplied (the barriers keep the loads in flight to two tiles').
-          // Offsets past the adapter's block, and those of rank columns past
-          // the rank, read as zero.
-          const uint32_t block = (uint32_t)D.low.rank * (uint32_t)D.width * 2;
-          const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-              const_cast<uint16_t *>(D.low.factor + (int64_t)a * D.low.rank * D.width), (short)0, (int)block, kRawBuffer);
-          const uint32_t col0 = (uint32_t)(D.first + tile0 * 16 + j);
-          auto fetch = [&](int i) {
-            if constexpr (T) {
-              bf16x8 f;
-              const uint32_t o = ((uint32_t)r0 * (uint32_t)D.width + col0) * 2 + 32u * (uint32_t)i;
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                f[e] = __builtin_bit_cast(__bf16, (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(
-                                                      rs, o + (uint32_t)e * (uint32_t)D.width * 2, 0, 0));
-              return f;
-            } else {
-              const uint32_t o = ((col0 + 16u * (uint32_t)i) * (uint32_t)D.low.rank + (uint32_t)r0) * 2;
-              if ((D.low.rank & 7) == 0)
-                return __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(rs, r0 < D.low.rank ? o : 0x80000000u, 0, 0));
-              bf16x8 f;
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                f[e] = __builtin_bit_cast(__bf16, (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(
-                                                      rs, r0 + e < D.low.rank ? o + 2u * (uint32_t)e : 0x80000000u, 0, 0));
-              return f;
-            }
-          };
-          // (two row tiles at a time: t's operands for four take too many registers)
-#pragma unroll
-          for (int rp = 0; rp < 4; rp += 2) {
-            bf16x8 hi[2], lo[2];
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              const int row = row0 + 16 * (rp + r) + j;
-              const f32x4 *tp = reinterpret_cast<const f32x4 *>(D.low.t + (int64_t)(row < D.m ? row : D.m - 1) * D.low.rank_p + r0);
-              const f32x4 t0 = tp[0], t1 = tp[1];
-              halves({t0[0], t0[1], t0[2], t0[3], t1[0], t1[1], t1[2], t1[3]}, hi[r], lo[r]);
-            }
-            bf16x8 next = fetch(0);
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-              const bf16x8 f = next;
-              __builtin_amdgcn_sched_barrier(0);
-              if (i + 1 < NT) next = fetch(i + 1);
-#pragma unroll
-              for (int r = 0; r < 2; ++r) {
-                f32x4 d = {0.f, 0.f, 0.f, 0.f};
-                d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, hi[r], d, 0, 0, 0);
-                d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, lo[r], d, 0, 0, 0);
-                const bool mine = (rows >> (16 * (rp + r) + j)) & 1;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[rp + r][i][e] += mine ? d[e] : 0.f;
-              }
-            }
-          }
-        }
-      }
-    }
-  }
+  between(at);
   struct Operands {
     bf16x8 a[4], b[NT];
   };
@@ -446,12 +375,96 @@ __global__ __launch_bounds__(kDenseThreads) void dense_kernel(Dense D) {
     step(s, X, Y);
     step(s + 1, Y, X);
   }
+  return at;
+}
 
+template <int NT, bool GATED, bool T>
+__global__ __launch_bounds__(kDenseThreads) void dense_kernel(Dense D) {
+  const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
+  f32x4 acc[4][NT];
+  const DenseAt at = dense_sums<NT>(D, acc, [&](const DenseAt &at) {
+    const int row0 = at.row0, tile0 = at.tile0, split = at.split;
+    if constexpr (!GATED) {
+      // The adapters' term first, while the first steps are on their way: lane l
+      // looks up row row0 + l; for every adapter that the wave's rows name, the
+      // products are kept only in the rows that name it (see low_rank_tiles).
+      if (D.low.rank > 0 && split == 0) {
+        int idx = row0 + lane < D.m ? D.low.index[row0 + lane] : -1;
+        if (idx >= D.low.count) idx = -1;
+        uint64_t left = __ballot(idx >= 0);
+        while (left) {
+          const int a = __builtin_amdgcn_readlane(idx, __builtin_ctzll(left));
+          const uint64_t rows = __ballot(idx == a);
+          left &= ~rows;
+          for (int r0 = 8 * g; r0 < D.low.rank_p + 8 * g; r0 += 32) {
+            // The factor's operands, each loaded while the one before it is
+            // multiplied (the barriers keep the loads in flight to two tiles').
+            // Offsets past the adapter's block, and those of rank columns past
+            // the rank, read as zero.
+            const uint32_t block = (uint32_t)D.low.rank * (uint32_t)D.width * 2;
+            const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+                const_cast<uint16_t *>(D.low.factor + (int64_t)a * D.low.rank * D.width), (short)0, (int)block, kRawBuffer);
+            const uint32_t col0 = (uint32_t)(D.first + tile0 * 16 + j);
+            auto fetch = [&](int i) {
+              if constexpr (T) {
+                bf16x8 f;
+                const uint32_t o = ((uint32_t)r0 * (uint32_t)D.width + col0) * 2 + 32u * (uint32_t)i;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  f[e] = __builtin_bit_cast(__bf16, (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(
+                                                        rs, o + (uint32_t)e * (uint32_t)D.width * 2, 0, 0));
+                return f;
+              } else {
+                const uint32_t o = ((col0 + 16u * (uint32_t)i) * (uint32_t)D.low.rank + (uint32_t)r0) * 2;
+                if ((D.low.rank & 7) == 0)
+                  return __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(rs, r0 < D.low.rank ? o : 0x80000000u, 0, 0));
+                bf16x8 f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  f[e] = __builtin_bit_cast(__bf16, (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(
+                                                        rs, r0 + e < D.low.rank ? o + 2u * (uint32_t)e : 0x80000000u, 0, 0));
+                return f;
+              }
+            };
+            // (two row tiles at a time: t's operands for four take too many registers)
+#pragma unroll
+            for (int rp = 0; rp < 4; rp += 2) {
+              bf16x8 hi[2], lo[2];
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                const int row = row0 + 16 * (rp + r) + j;
+                const f32x4 *tp = reinterpret_cast<const f32x4 *>(D.low.t + (int64_t)(row < D.m ? row : D.m - 1) * D.low.rank_p + r0);
+                const f32x4 t0 = tp[0], t1 = tp[1];
+                halves({t0[0], t0[1], t0[2], t0[3], t1[0], t1[1], t1[2], t1[3]}, hi[r], lo[r]);
+              }
+              bf16x8 next = fetch(0);
+#pragma unroll
+              for (int i = 0; i < NT; ++i) {
+                const bf16x8 f = next;
+                __builtin_amdgcn_sched_barrier(0);
+                if (i + 1 < NT) next = fetch(i + 1);
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                  f32x4 d = {0.f, 0.f, 0.f, 0.f};
+                  d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, hi[r], d, 0, 0, 0);
+                  d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, lo[r], d, 0, 0, 0);
+                  const bool mine = (rows >> (16 * (rp + r) + j)) & 1;
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) acc[rp + r][i][e] += mine ? d[e] : 0.f;
+                }
+              }
+            }
+          }
+        }
+      }
+    }
+  });
+  const int row0 = at.row0, tile0 = at.tile0, split = at.split;
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     const int row = row0 + 16 * r + j;
     if (row >= D.m) continue;
-    if (D.splits > 1) {
+    if (D.partials) {
       float *const q = D.partials + ((int64_t)split * D.m + row) * (16 * (int64_t)D.wtiles) + tile0 * 16 + 4 * g;
 #pragma unroll
       for (int i = 0; i < NT; ++i)

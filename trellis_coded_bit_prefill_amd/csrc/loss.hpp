@@ -9,7 +9,10 @@
 // that a row with one entry has 1 - p = S' / S from the sum S' over the others:
 // as the difference of two numbers near 1 it would lose its digits.
 //
-// The logits of a chunk of rows lie in the workspace in float32 (loss_rows).
+// Few rows: the logits of a chunk of rows lie in the workspace in float32
+// (loss_rows). Many rows: the product's tiles are turned into 2^(l2 - ref) in
+// bf16 before they leave the registers, as the second product's operands, with
+// each tile's sums beside them (vocabulary_kernel, loss_dense).
 
 namespace trellis {
 namespace {
@@ -73,8 +76,8 @@ constexpr int kStatSpan = 4096;  // logits of a workgroup
 __global__ __launch_bounds__(256) void row_stats_kernel(const float *__restrict__ logits, int n, float scale2,
                                                         f32x2 *__restrict__ stats) {
   __shared__ f32x2 part[4];
-  const int64_t row = blockIdx.y;
-  const int c0 = blockIdx.x * kStatSpan + 4 * (int)threadIdx.x;
+  const int64_t row = blockIdx.x;  // (y and z of a grid are limited to 2^16)
+  const int c0 = blockIdx.y * kStatSpan + 4 * (int)threadIdx.x;
   const float *const l = logits + row * n;
   f32x4 v[kStatSpan / 1024];
   float r = kLowest;
@@ -95,7 +98,7 @@ __global__ __launch_bounds__(256) void row_stats_kernel(const float *__restrict_
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = a;
   __syncthreads();
   if (threadIdx.x == 0)
-    stats[row * gridDim.x + blockIdx.x] = join_stats(join_stats(part[0], part[1]), join_stats(part[2], part[3]));
+    stats[row * gridDim.y + blockIdx.y] = join_stats(join_stats(part[0], part[1]), join_stats(part[2], part[3]));
 }
 
 // What a workgroup of 256 threads works out of a row's list and of its other
@@ -124,10 +127,11 @@ __device__ __forceinline__ float max_256(float v, float *red) {
   __syncthreads();
   return fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
 }
-// rest: R' and S' of the entries that are not listed. Returns whether the row
-// has entries; loss and lse where `write`.
+// rest: R' and S' of the entries that are not listed, or of all (`whole`; then
+// the list has not exactly one entry, else some digits of 1 - p are lost).
+// Returns whether the row has entries; loss and lse where `write`.
 static_assert(kMaxTop == 256, "one thread an entry");
-__device__ bool row_list(const Lists &L, int64_t row, f32x2 rest, RowList &S, bool write) {
+__device__ bool row_list(const Lists &L, int64_t row, f32x2 rest, bool whole, RowList &S, bool write) {
   const int j = threadIdx.x;
   int at = j < L.top ? L.index[row * L.top + j] : -1;
   if (at >= L.n) at = -1;
@@ -155,13 +159,13 @@ __device__ bool row_list(const Lists &L, int64_t row, f32x2 rest, RowList &S, bo
       qs += S.q[k];
       if (k < j) first = false;
     }
-  const float rmax = fmaxf(max_256(first ? l2 : -inf, S.red[0]), rest[0]);
+  const float rmax = whole ? rest[0] : fmaxf(max_256(first ? l2 : -inf, S.red[0]), rest[0]);
   const float here = first ? __builtin_amdgcn_exp2f(l2 - rmax) : 0.f;
   const float others = rest[1] * __builtin_amdgcn_exp2f(rest[0] - rmax);
-  const float sum = others + sum_256(here, S.red[1]);
+  const float sum = others + (whole ? 0.f : sum_256(here, S.red[1]));
   const float lse2 = rmax + __builtin_amdgcn_logf(sum);
   // one entry alone: 1 - p and the loss from the others' sum
-  const bool alone = sum_256(first ? 1.f : 0.f, S.red[0]) == 1.f;
+  const bool alone = sum_256(first ? 1.f : 0.f, S.red[0]) == 1.f && !whole;
   if (j == 0) S.total = f32x2{rmax, sum};
   S.first[j] = first;
   S.add[j] = !first ? 0.f : alone ? -others / sum : here / sum - qs;
@@ -189,15 +193,15 @@ __global__ __launch_bounds__(256) void row_loss_kernel(Lists L, const float *__r
                                                        const f32x2 *__restrict__ stats, int spans,
                                                        uint16_t *__restrict__ d) {
   __shared__ RowList S;
-  const int64_t row = blockIdx.y;
+  const int64_t row = blockIdx.x;
   // every wave joins the spans, in the same order
   f32x2 rest = {kLowest, 0.f};
   for (int i = threadIdx.x & 63; i < spans; i += 64) rest = join_stats(rest, stats[row * spans + i]);
   rest = join_stats_wave(rest);
-  const bool alive = row_list(L, row, rest, S, blockIdx.x == 0);
+  const bool alive = row_list(L, row, rest, false, S, blockIdx.y == 0);
   if (!d) return;
   const float r = S.total[0], f = alive ? L.temperature / S.total[1] : 0.f;
-  const int c0 = blockIdx.x * kStatSpan;
+  const int c0 = blockIdx.y * kStatSpan;
   const float *const l = logits + row * L.n;
   uint16_t *const o = d + row * L.n;
 #pragma unroll
@@ -230,12 +234,364 @@ __global__ __launch_bounds__(256) void scale_rows_kernel(const float *__restrict
   reinterpret_cast<u32x4 *>(dst)[i] = o;
 }
 
+// ---- many rows ------------------------------------------------------------------
+
+// Logits that are used as they are: a row's tile whose largest l2 lies within
+// +-kPlain has 0 in place of its R. The logits of trained models do, and then
+// all tiles of a row agree; another tile's reference is its largest l2 rounded
+// down, a whole number, so that bringing it to the row's reference later is an
+// exact product with a power of two. (2^60 times 2^22 entries stays far below
+// float32's and bf16's largest, 2^-60 above their smallest.)
+constexpr float kPlain = 60.f;
+
+struct Vocabulary {
+  const int32_t *sole;  // a row's only entry, taken out of its sum, or outside [0, n)
+  float *sole_l2;       // its l2
+  f32x2 *stats;         // [m][blocks]: reference and sum of a row in a block of columns
+  uint16_t *e;          // 2^(l2 - reference) as operands [step][ptiles][lane][8], or null
+  float scale2;
+  int32_t n, blocks, first_tile, first_block, steps;  // steps: of the operands e
+};
+
+// The product's tile in, 2^(l2 - reference) and its sums out. Beside the
+// product's steps (see dense_sums) a tile's end costs 4 operations and one
+// exponential (a quarter of the rate) for each of its sums.
+template <int NT>
+__global__ __launch_bounds__(kDenseThreads) void vocabulary_kernel(Dense D, Vocabulary V) {
+  const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
+  f32x4 acc[4][NT];
+  const DenseAt at = dense_sums<NT>(D, acc, [](const DenseAt &) {});
+  const int col0 = (V.first_tile + at.tile0) * 16 + 4 * g;  // this lane's first column
+  const int block = V.first_block + at.tile0 / NT;
+  const float inf = __builtin_inff();
+  if (col0 + 16 * NT > V.n) {  // (columns past n: their sums are of whatever the last tile's operands were)
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+      if (col0 + 16 * i >= V.n)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[r][i] = f32x4{-inf, -inf, -inf, -inf};
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int row = at.row0 + 16 * r + j;
+    const bool in = row < D.m;
+    const uint32_t sole = (uint32_t)(in ? V.sole[row] : -1) - (uint32_t)col0;
+    if (__any(sole < 16u * NT)) {
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (sole == 16u * i + e && col0 + 16 * i < V.n) {
+            V.sole_l2[row] = acc[r][i][e] * V.scale2;
+            acc[r][i][e] = -inf;
+          }
+    }
+    float top = -inf;
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top = fmaxf(top, acc[r][i][e]);
+    top = fmaxf(top, __shfl_xor(top, 16));
+    top = fmaxf(top, __shfl_xor(top, 32)) * V.scale2;
+    float ref = 0.f;
+    if (!(fabsf(top) <= kPlain)) ref = top == -inf ? kLowest : __builtin_floorf(top);
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      f32x4 x;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[r][i][e], V.scale2, -ref));
+        sum += x[e];
+      }
+      const int tile = V.first_tile + at.tile0 + i;
+      if (V.e && in && (tile >> 1) < V.steps)
+        store4(V.e + ((((int64_t)(tile >> 1) * D.ptiles + (row >> 4)) * 64 + j + 16 * (2 * (tile & 1) + (g >> 1))) * 8 + 4 * (g & 1)), x);
+    }
+    sum += __shfl_xor(sum, 16);
+    sum += __shfl_xor(sum, 32);
+    if (g == 0 && in && block < V.blocks) V.stats[(int64_t)row * V.blocks + block] = f32x2{ref, sum};
+  }
+}
+
+// The only entry of each list, or -1: one wave a row.
+__global__ __launch_bounds__(64) void sole_kernel(Lists L, int32_t *__restrict__ sole) {
+  const int64_t row = blockIdx.x;
+  int one = -1;
+  bool several = false;
+  for (int j0 = 0; j0 < L.top; j0 += 64) {
+    const int j = j0 + (int)threadIdx.x;
+    const int at = j < L.top ? L.index[row * L.top + j] : -1;
+    const uint64_t named = __ballot(at >= 0 && at < L.n);
+    if (!named) continue;
+    if (one < 0) one = __builtin_amdgcn_readlane(at, __builtin_ctzll(named));
+    several = several || __any(at >= 0 && at < L.n && at != one);
+  }
+  if (threadIdx.x == 0) sole[row] = several ? -1 : one;
+}
+
+// l2 of the listed entries of lists with several: W's rows decoded where they
+// are named, one wave an entry. Bound by the decode's VALU work.
+template <int BITS>
+__global__ __launch_bounds__(256) void listed_kernel(Lists L, const int32_t *__restrict__ sole,
+                                                     const uint16_t *__restrict__ x, const uint32_t *__restrict__ codes,
+                                                     const uint16_t *__restrict__ scales, int blocks) {
+  constexpr int wpb = 8 * BITS;
+  const int64_t row = blockIdx.x;
+  const int j = blockIdx.y * 4 + (int)(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  if (j >= L.top || sole[row] >= 0) return;
+  const int at = L.index[row * L.top + j];
+  if (at < 0 || at >= L.n) return;
+  const float s = bf16_bits_to_f32(scales[at]);
+  float q, kq;
+  alu_row_constants(s, q, kq);
+  const bool chain = !alu_scale_ok(s);
+  const int pos = (252 - 4 * lane) * BITS, w0 = pos >> 5, w1 = w0 + 1 == wpb ? 0 : w0 + 1, sh = pos & 31;
+  const uint32_t *bw = codes + (int64_t)at * blocks * wpb;
+  const uint16_t *xr = x + row * blocks * 256 + 4 * lane;
+  float sum = 0.f;
+  for (int b = 0; b < blocks; ++b, bw += wpb, xr += 256) {
+    const uint32_t f = __builtin_amdgcn_alignbit(bw[w1], bw[w0], sh);
+    const u32x2 v = *reinterpret_cast<const u32x2 *>(xr);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const float w = (float)(__bf16)window_weight(__builtin_amdgcn_ubfe(f, (3 - c) * BITS, 12), s, q, kq, chain);
+      sum = __builtin_fmaf(w, bf16_half(v[c >> 1], c & 1), sum);
+    }
+  }
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) sum += __shfl_xor(sum, o);
+  if (lane == 0) L.listed[row * L.top + j] = sum * L.scale2;
+}
+
+// A row's blocks joined: its loss, lse and the factor of its dx (T / S in the
+// operands' unit; 0 for a row without entries). Tiles whose reference is not the
+// row's are brought to it, and the listed entries' operands become (p - q) S.
+__global__ __launch_bounds__(256) void row_join_kernel(Lists L, Vocabulary V, int ptiles, int block_columns,
+                                                       float *__restrict__ factor) {
+  __shared__ RowList S;
+  const int64_t row = blockIdx.x;
+  const f32x2 *const stats = V.stats + row * V.blocks;
+  const int sole = V.sole[row];
+  const bool whole = !(sole >= 0 && sole < L.n);
+  float ref = kLowest;
+  for (int b = threadIdx.x; b < V.blocks; b += 256) ref = fmaxf(ref, stats[b][0]);
+  ref = max_256(ref, S.red[0]);
+  float sum = 0.f, moved = 0.f;
+  for (int b = threadIdx.x; b < V.blocks; b += 256) {
+    const f32x2 a = stats[b];
+    if (a[0] != ref && a[1] != 0.f) moved = 1.f;
+    sum += a[1] * __builtin_amdgcn_exp2f(a[0] - ref);
+  }
+  sum = sum_256(sum, S.red[1]);
+  moved = max_256(moved, S.red[0]);
+  if (!whole && threadIdx.x == 0) {
+    for (int j = 0; j < L.top; ++j) L.listed[row * L.top + j] = V.sole_l2[row];
+  }
+  __syncthreads();
+  const bool alive = row_list(L, row, f32x2{ref, sum}, whole, S, true);
+  if (!V.e) return;
+  const float rmax = S.total[0], total = S.total[1];
+  if (threadIdx.x == 0) factor[row] = alive ? L.temperature * __builtin_amdgcn_exp2f(ref - rmax) / total : 0.f;
+  // operand of a column of this row
+  auto place = [&](int col) {
+    return V.e + (((int64_t)(col >> 5) * ptiles + (row >> 4)) * 64 + (row & 15) + 16 * ((col >> 3) & 3)) * 8 + (col & 7);
+  };
+  if (moved != 0.f) {
+    for (int c = 8 * (int)threadIdx.x; c < V.n; c += 8 * 256) {
+      const f32x2 a = stats[c / block_columns];
+      if (a[0] == ref) continue;
+      const float f = __builtin_amdgcn_exp2f(a[0] - ref);
+      u32x4 *const p = reinterpret_cast<u32x4 *>(place(c));
+      u32x4 v = *p;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        v[e] = (uint32_t)bf16_of(f * bf16_half(v[e], 0)) | ((uint32_t)bf16_of(f * bf16_half(v[e], 1)) << 16);
+      *p = v;
+    }
+    __syncthreads();
+  }
+  if (S.first[threadIdx.x] && alive)
+    *place(S.at[threadIdx.x]) = bf16_of(whole ? S.add[threadIdx.x] * total : -sum);
+}
+
+// dx: the splits' sums in order, times the row's factor, rounded. Four columns a thread.
+__global__ __launch_bounds__(256) void loss_gradient_kernel(const float *__restrict__ partials, int splits, int64_t plane,
+                                                            int columns, int width, const float *__restrict__ factor,
+                                                            int m, uint16_t *__restrict__ dx) {
+  const int quads = columns >> 2;
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t row = id / quads;
+  if (row >= m) return;
+  const int c = (int)(id - row * quads) * 4;
+  const float f = factor[row];
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  if (f != 0.f) {
+    for (int s = 0; s < splits; ++s) v += *reinterpret_cast<const f32x4 *>(partials + s * plane + row * columns + c);
+    v *= f;
+  }
+  store4(dx + row * width + c, v);
+}
+
+typedef void (*VocabularyFn)(Dense, Vocabulary);
+VocabularyFn vocabulary_fn(int nt) {
+  return nt == 4 ? &vocabulary_kernel<4> : nt == 6 ? &vocabulary_kernel<6> : &vocabulary_kernel<8>;
+}
+
+// How the dense products of a loss are laid out: the first one's column tile by
+// the costs of dense_shape (one split: a tile's exponentials need its whole sum).
+constexpr int64_t kVocabularyBytes = (int64_t)1 << 31;  // decoded weights of a launch
+struct LossShape {
+  int32_t rows;       // of a chunk: its operands of the second product take at most 1 GiB, or 256 rows
+  int nt, steps, ptiles, blocks;
+  int64_t tiles, slab;
+  DenseShape back;
+  size_t operand_bytes, row_bytes, e_bytes, stat_bytes, partial_bytes;
+};
+LossShape loss_shape(trellis_geom g, int32_t m, bool keep, int cus) {
+  LossShape s{};
+  s.tiles = ((int64_t)g.n + 15) / 16;
+  s.steps = (g.k + 63) / 64 * 2;
+  const int64_t n_pad = ((int64_t)g.n + 63) / 64 * 64;
+  // (statistics: 8 bytes a row and 64 columns at the most, kept below 512 MiB)
+  int64_t rows = (keep ? kLogitBytes / (2 * n_pad) : ((int64_t)1 << 29) / (n_pad / 8)) / 256 * 256;
+  if (rows < 256) rows = 256;
+  if (rows > m) rows = m;
+  s.rows = (int32_t)rows;
+  double best = 0;
+  for (int nt = 8; nt >= 4; nt -= 2) {
+    const int64_t wg = (rows + kDenseRows - 1) / kDenseRows * ((s.tiles + 2 * nt - 1) / (2 * nt));
+    const double cost = (double)((wg + cus - 1) / cus) * (s.steps * (0.073 * nt + 0.125) + 3.7);
+    if (s.nt == 0 || cost < best) {
+      best = cost;
+      s.nt = nt;
+    }
+  }
+  s.blocks = (int)((s.tiles + s.nt - 1) / s.nt);
+  const int64_t tile_bytes = (int64_t)s.steps * 1024;
+  s.slab = kVocabularyBytes / tile_bytes / (2 * s.nt) * (2 * s.nt);  // whole workgroup tiles (a tile takes 8 MB at most)
+  const int forced = g_tiles.load(std::memory_order_relaxed);
+  if (forced > 0) s.slab = ((int64_t)forced + 2 * s.nt - 1) / (2 * s.nt) * (2 * s.nt);
+  if (s.slab > s.tiles) s.slab = s.tiles;
+  s.operand_bytes = (size_t)(s.slab * tile_bytes);
+  s.ptiles = (int)((rows + 15) / 16);
+  s.row_bytes = up256((size_t)s.ptiles * tile_bytes);
+  s.stat_bytes = up256((size_t)rows * s.blocks * 8);
+  if (keep) {
+    s.back = dense_shape(kTransposed, g, (int32_t)rows, 1, cus, kVocabularyBytes);
+    if (s.operand_bytes < s.back.operand_bytes) s.operand_bytes = s.back.operand_bytes;
+    s.e_bytes = up256(s.back.row_bytes);
+    s.partial_bytes = up256((size_t)s.back.splits * rows * s.back.slab * 16 * 4);
+  }
+  s.operand_bytes = up256(s.operand_bytes);
+  return s;
+}
+
+trellis_status loss_dense(const uint16_t *x, int32_t m, const uint32_t *codes, const uint16_t *scales, trellis_geom g,
+                          Lists L, uint16_t *dx, hipStream_t stream) {
+  int dev = 0, cus = 0;
+  TRELLIS_TRY(device(dev, cus));
+  const LossShape s = loss_shape(g, m, dx != nullptr, cus);
+  const size_t list_bytes = up256((size_t)s.rows * L.top * 4), word_bytes = up256((size_t)s.rows * 4);
+  Space *w = nullptr;
+  TRELLIS_TRY(space(dev, stream,
+                    s.operand_bytes + s.row_bytes + s.e_bytes + s.stat_bytes + s.partial_bytes + list_bytes + 3 * word_bytes, 0, w));
+  unsigned char *at = w->bytes;
+  auto take = [&](size_t bytes) {
+    unsigned char *const p = at;
+    at += bytes;
+    return p;
+  };
+  uint16_t *const operands = reinterpret_cast<uint16_t *>(take(s.operand_bytes)),
+                 *const packed = reinterpret_cast<uint16_t *>(take(s.row_bytes)),
+                 *const e = reinterpret_cast<uint16_t *>(take(s.e_bytes));
+  f32x2 *const stats = reinterpret_cast<f32x2 *>(take(s.stat_bytes));
+  float *const partials = reinterpret_cast<float *>(take(s.partial_bytes));
+  L.listed = reinterpret_cast<float *>(take(list_bytes));
+  int32_t *const sole = reinterpret_cast<int32_t *>(take(word_bytes));
+  float *const sole_l2 = reinterpret_cast<float *>(take(word_bytes)), *const factor = reinterpret_cast<float *>(take(word_bytes));
+  static bool ready[kMaxDevices][2][9];
+  const VocabularyFn fn = vocabulary_fn(s.nt);
+  const DenseFn back = dx ? dense_fn(kTransposed, s.back.nt) : nullptr;
+  const size_t lds = (size_t)dense_buffers(s.nt) * dense_step_bytes(s.nt),
+               lds_back = dx ? (size_t)dense_buffers(s.back.nt) * dense_step_bytes(s.back.nt) : 0;
+  auto allow = [&](bool &done, const void *f, size_t bytes) {
+    done = done || worked(hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes));
+    return done;
+  };
+  if (!allow(ready[dev][0][s.nt], reinterpret_cast<const void *>(fn), lds) ||
+      (dx && !allow(ready[dev][1][s.back.nt], reinterpret_cast<const void *>(back), lds_back)))
+    return TRELLIS_E_HIP;
+  const Lists all = L;
+  (void)hipGetLastError();
+  for (int32_t m0 = 0; m0 < m; m0 += s.rows) {
+    const int32_t mc = m - m0 < s.rows ? m - m0 : s.rows;
+    const int ptiles = (mc + 15) / 16;
+    L.m = mc;
+    L.index = all.index + (int64_t)m0 * L.top;
+    L.logits = all.logits ? all.logits + (int64_t)m0 * L.top : nullptr;
+    L.loss = all.loss + m0;
+    L.lse = all.lse + m0;
+    const uint16_t *const xc = x + (int64_t)m0 * g.k;
+    if (L.top > 1) {
+      hipLaunchKernelGGL(sole_kernel, dim3((unsigned)mc), dim3(64), 0, stream, L, sole);
+      const dim3 grid((unsigned)mc, (unsigned)((L.top + 3) / 4));
+      const auto listed = g.bits == 2 ? &listed_kernel<2> : g.bits == 3 ? &listed_kernel<3> : &listed_kernel<4>;
+      hipLaunchKernelGGL(listed, grid, dim3(256), 0, stream, L, sole, xc, codes, scales, g.k >> 8);
+    }
+    hipLaunchKernelGGL(pack_rows_kernel<true>, dim3((unsigned)(((int64_t)ptiles * (s.steps / 2) + 3) / 4)), dim3(256), 0,
+                       stream, xc, mc, g.k, ptiles, s.steps, packed);
+    Dense d{};
+    d.p = packed;
+    d.w = operands;
+    d.m = mc;
+    d.steps = s.steps;
+    d.splits = 1;
+    d.ptiles = ptiles;
+    d.mtiles = (mc + kDenseRows - 1) / kDenseRows;
+    Vocabulary v{L.top > 1 ? sole : L.index, sole_l2, stats, dx ? e : nullptr, L.scale2, g.n, s.blocks, 0, 0,
+                 dx ? s.back.steps : 0};
+    for (int64_t first = 0; first < s.tiles; first += s.slab) {
+      d.wtiles = (int)(s.tiles - first < s.slab ? s.tiles - first : s.slab);
+      d.ntiles = (d.wtiles + 2 * s.nt - 1) / (2 * s.nt);
+      v.first_tile = (int)first;
+      v.first_block = (int)(first / s.nt);
+      const Unpack u{{codes, nullptr}, {scales, nullptr}, operands, g.n, g.k, s.steps, (int)first, d.wtiles, 1};
+      TRELLIS_TRY(launch_unpack_rows(g.bits, u, stream));
+      hipLaunchKernelGGL(fn, dim3((unsigned)(d.mtiles * d.ntiles)), dim3(kDenseThreads), lds, stream, d, v);
+    }
+    hipLaunchKernelGGL(row_join_kernel, dim3((unsigned)mc), dim3(256), 0, stream, L, v, ptiles, 16 * s.nt, factor);
+    if (hipGetLastError() != hipSuccess) return TRELLIS_E_HIP;
+    if (!dx) continue;
+    d.p = e;
+    d.steps = s.back.steps;
+    d.splits = s.back.splits;
+    d.partials = partials;
+    d.width = g.k;
+    for (int64_t first = 0; first < s.back.tiles; first += s.back.slab) {
+      d.wtiles = (int)(s.back.tiles - first < s.back.slab ? s.back.tiles - first : s.back.slab);
+      d.ntiles = (d.wtiles + 2 * s.back.nt - 1) / (2 * s.back.nt);
+      d.first = (int)first * 16;
+      const Unpack u{{codes, nullptr}, {scales, nullptr}, operands, g.n, g.k, s.back.steps, (int)first, d.wtiles, 1};
+      TRELLIS_TRY(launch_unpack_columns(g.bits, u, stream));
+      hipLaunchKernelGGL(back, dim3((unsigned)(d.mtiles * d.ntiles * d.splits)), dim3(kDenseThreads), lds_back, stream, d);
+      const int columns = 16 * d.wtiles;
+      const int64_t threads = (int64_t)mc * (columns / 4);
+      hipLaunchKernelGGL(loss_gradient_kernel, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, stream, partials,
+                         d.splits, (int64_t)mc * columns, columns, g.k, factor, mc, dx + (int64_t)m0 * g.k + d.first);
+      if (hipGetLastError() != hipSuccess) return TRELLIS_E_HIP;
+    }
+  }
+  return TRELLIS_OK;
+}
+
 // The logits of a chunk of rows in float32, decoded in the product; then the
 // rows' losses; then the transposed product of the logits' gradients.
 trellis_status loss_rows(const uint16_t *x, int32_t m, const uint32_t *codes, const uint16_t *scales, trellis_geom g,
                          Lists L, uint16_t *dx, hipStream_t stream) {
   int dev = 0, cus = 0;
   TRELLIS_TRY(device(dev, cus));
+  if (plan_of(kForward, g, m, 1, cus).dense) return loss_dense(x, m, codes, scales, g, L, dx, stream);
   const int64_t most = kLogitBytes / (4 * (int64_t)g.n) / 16 * 16;  // 64 rows at least: n is at most 2^22
   const int32_t rows = m < most ? m : (int32_t)most;
   // Plans of the full chunks and of the last one; the workspace holds either.
@@ -283,9 +639,9 @@ trellis_status loss_rows(const uint16_t *x, int32_t m, const uint32_t *codes, co
     p.k = g.k;
     TRELLIS_TRY(launch(fwd[which], p, stream));
     hipLaunchKernelGGL(pluck_kernel, dim3((unsigned)mc), dim3(64), 0, stream, L, logits);
-    hipLaunchKernelGGL(row_stats_kernel, dim3((unsigned)spans, (unsigned)mc), dim3(256), 0, stream, logits, g.n, L.scale2,
+    hipLaunchKernelGGL(row_stats_kernel, dim3((unsigned)mc, (unsigned)spans), dim3(256), 0, stream, logits, g.n, L.scale2,
                        stats);
-    hipLaunchKernelGGL(row_loss_kernel, dim3(dx ? (unsigned)spans : 1u, (unsigned)mc), dim3(256), 0, stream, L, logits, stats,
+    hipLaunchKernelGGL(row_loss_kernel, dim3((unsigned)mc, dx ? (unsigned)spans : 1u), dim3(256), 0, stream, L, logits, stats,
                        spans, dx ? d : nullptr);
     if (hipGetLastError() != hipSuccess) return TRELLIS_E_HIP;
     if (!dx) continue;

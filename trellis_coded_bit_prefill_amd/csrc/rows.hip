@@ -1319,6 +1319,13 @@ __global__ __launch_bounds__(256) void clear_kernel(uint32_t *__restrict__ p, in
 // ---------------------------------------------------------------------------
 constexpr int kMaxDevices = 64;
 
+#define TRELLIS_TRY(e)                      \
+  do {                                      \
+    const trellis_status rc_ = (e);         \
+    if (rc_ != TRELLIS_OK) return rc_;      \
+  } while (0)
+
+
 struct Space {
   unsigned char *bytes = nullptr;
   size_t size = 0;
@@ -1524,7 +1531,7 @@ struct DenseShape {
   double us;           // what the product's rounds are reckoned to take
   size_t operand_bytes, row_bytes, partial_bytes;
 };
-DenseShape dense_shape(int kind, trellis_geom g, int32_t m, int matrices, int cus) {
+DenseShape dense_shape(int kind, trellis_geom g, int32_t m, int matrices, int cus, int64_t limit = kOperandBytes) {
   DenseShape s{};
   s.matrices = matrices;
   const bool t = kind == kTransposed;
@@ -1543,7 +1550,7 @@ DenseShape dense_shape(int kind, trellis_geom g, int32_t m, int matrices, int cu
   // in seven).
   const int64_t mt = (m + kDenseRows - 1) / kDenseRows;
   const int64_t tile_bytes = (int64_t)s.steps * 1024;
-  const bool several = s.tiles > 16 && tile_bytes * s.tiles > kOperandBytes;  // launches
+  const bool several = s.tiles > 16 && tile_bytes * s.tiles > limit;  // launches
   double best = 0;
   for (int nt = 8; nt >= 4; --nt) {
     if (kind == kGated && nt % 2) continue;
@@ -1551,7 +1558,7 @@ DenseShape dense_shape(int kind, trellis_geom g, int32_t m, int matrices, int cu
     // go in slabs of 16 tiles and multiples of it: of whole workgroup tiles for
     // nt = 4 and 8 alone (the rest of a cut one would be stored over the next
     // slab's columns).
-    if (several && nt % 4 && tile_bytes * 16 * nt > kOperandBytes) continue;
+    if (several && nt % 4 && tile_bytes * 16 * nt > limit) continue;
     const int64_t wg = mt * ((s.tiles + 2 * nt - 1) / (2 * nt));
     for (int splits = 1; splits == 1 || (splits <= 8 && splits <= s.steps / 16); ++splits) {
       const double rounds = (double)((wg * splits + cus - 1) / cus);
@@ -1564,10 +1571,10 @@ DenseShape dense_shape(int kind, trellis_geom g, int32_t m, int matrices, int cu
       }
     }
   }
-  int64_t slab = kOperandBytes / tile_bytes / (16 * s.nt) * (16 * s.nt);  // whole workgroup tiles, fours and pairs
+  int64_t slab = limit / tile_bytes / (16 * s.nt) * (16 * s.nt);  // whole workgroup tiles, fours and pairs
   const int forced = g_tiles.load(std::memory_order_relaxed);
   if (forced > 0) slab = ((int64_t)forced + 16 * s.nt - 1) / (16 * s.nt) * (16 * s.nt);
-  if (slab == 0) slab = kOperandBytes / tile_bytes / 16 * 16;  // long contractions: whole 256-column blocks,
+  if (slab == 0) slab = limit / tile_bytes / 16 * 16;  // long contractions: whole 256-column blocks,
   if (slab == 0) slab = 16;                                    // one at least (512 bytes per row of W)
   if (slab > s.tiles) slab = s.tiles;
   s.slab = slab;
@@ -1601,6 +1608,23 @@ struct GatedGrads {
   uint16_t *dgate, *dup;
 };
 
+trellis_status launch_unpack_rows(int bits, const Unpack &u, hipStream_t stream) {
+  const int64_t waves = (int64_t)u.tiles * (u.k >> 8);
+  const dim3 grid((unsigned)((waves + 3) / 4), (unsigned)u.matrices);
+  if (bits == 2) hipLaunchKernelGGL(unpack_rows_kernel<2>, grid, dim3(256), 0, stream, u);
+  else if (bits == 3) hipLaunchKernelGGL(unpack_rows_kernel<3>, grid, dim3(256), 0, stream, u);
+  else hipLaunchKernelGGL(unpack_rows_kernel<4>, grid, dim3(256), 0, stream, u);
+  return hipGetLastError() == hipSuccess ? TRELLIS_OK : TRELLIS_E_HIP;
+}
+trellis_status launch_unpack_columns(int bits, const Unpack &u, hipStream_t stream) {
+  const int64_t waves = (int64_t)(u.tiles / 16) * (u.steps / u.matrices);
+  const dim3 grid((unsigned)((waves + 3) / 4), (unsigned)u.matrices);
+  if (bits == 2) hipLaunchKernelGGL(unpack_columns_kernel<2>, grid, dim3(256), 0, stream, u);
+  else if (bits == 3) hipLaunchKernelGGL(unpack_columns_kernel<3>, grid, dim3(256), 0, stream, u);
+  else hipLaunchKernelGGL(unpack_columns_kernel<4>, grid, dim3(256), 0, stream, u);
+  return hipGetLastError() == hipSuccess ? TRELLIS_OK : TRELLIS_E_HIP;
+}
+
 trellis_status launch_dense(int kind, const DenseShape &s, trellis_geom g, const Product &p, const GatedGrads *grads,
                             unsigned char *operands, hipStream_t stream) {
   unsigned char *const rows = operands + up256(s.operand_bytes);
@@ -1623,7 +1647,7 @@ trellis_status launch_dense(int kind, const DenseShape &s, trellis_geom g, const
   d.m = p.m;
   d.steps = s.steps;
   d.splits = s.splits;
-  d.partials = reinterpret_cast<float *>(rows + up256(s.row_bytes));
+  d.partials = s.splits > 1 ? reinterpret_cast<float *>(rows + up256(s.row_bytes)) : nullptr;
   d.ptiles = s.ptiles;
   d.width = kind == kTransposed ? g.k : g.n;
   d.mtiles = (p.m + kDenseRows - 1) / kDenseRows;
@@ -1646,23 +1670,13 @@ trellis_status launch_dense(int kind, const DenseShape &s, trellis_geom g, const
       u.first = (int)first;
       u.tiles = tiles;
       u.matrices = s.matrices;
-      const int64_t waves = (int64_t)(tiles / 16) * s.steps1;
-      const dim3 grid((unsigned)((waves + 3) / 4), (unsigned)s.matrices);
-      if (g.bits == 2) hipLaunchKernelGGL(unpack_columns_kernel<2>, grid, dim3(256), 0, stream, u);
-      else if (g.bits == 3) hipLaunchKernelGGL(unpack_columns_kernel<3>, grid, dim3(256), 0, stream, u);
-      else hipLaunchKernelGGL(unpack_columns_kernel<4>, grid, dim3(256), 0, stream, u);
+      TRELLIS_TRY(launch_unpack_columns(g.bits, u, stream));
     } else {
-      const int mats = kind == kGated ? 2 : 1;
-      u.first = (int)(first / mats);
-      u.tiles = tiles / mats;
-      u.matrices = mats;
-      const int64_t waves = (int64_t)u.tiles * (g.k >> 8);
-      const dim3 grid((unsigned)((waves + 3) / 4), (unsigned)mats);
-      if (g.bits == 2) hipLaunchKernelGGL(unpack_rows_kernel<2>, grid, dim3(256), 0, stream, u);
-      else if (g.bits == 3) hipLaunchKernelGGL(unpack_rows_kernel<3>, grid, dim3(256), 0, stream, u);
-      else hipLaunchKernelGGL(unpack_rows_kernel<4>, grid, dim3(256), 0, stream, u);
+      u.matrices = kind == kGated ? 2 : 1;
+      u.first = (int)(first / u.matrices);
+      u.tiles = tiles / u.matrices;
+      TRELLIS_TRY(launch_unpack_rows(g.bits, u, stream));
     }
-    if (hipGetLastError() != hipSuccess) return TRELLIS_E_HIP;
     d.first = (int)(first * 16 / (kind == kGated ? 2 : 1));
     d.wtiles = tiles;
     d.ntiles = (tiles + 2 * s.nt - 1) / (2 * s.nt);
@@ -1810,12 +1824,6 @@ trellis_status launch_backward_sums(const ShrinkShape &ht, const ShrinkShape &hu
 }  // namespace trellis
 
 using namespace trellis;
-
-#define TRELLIS_TRY(e)                      \
-  do {                                      \
-    const trellis_status rc_ = (e);         \
-    if (rc_ != TRELLIS_OK) return rc_;      \
-  } while (0)
 
 extern "C" {
 
