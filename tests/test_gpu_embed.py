@@ -51,7 +51,8 @@ def test_embed(m, n, k, count, scale, bits):
 # pairs of one, two and three bytes; one workgroup of the sort and several; runs
 # within a chunk, over chunk borders and over all of them
 GRADIENTS = [(1, 256, 1, "any"), (7, 256, 3, "any"), (300, 512, 40, "any"), (300, 256, 1000, "none"), (2500, 256, 1, "same"),
-             (5000, 768, 300, "skewed"), (5000, 256, 70000, "any"), (20000, 256, 5, "any"), (33000, 256, 2000, "skewed"),
+             (5000, 768, 300, "skewed"), (5000, 256, 70000, "any"), (20000, 256, 5, "any"), (33000, 256, 2000, "skewed"), (16384, 256, 70000, "skewed"),
+             (16385, 512, 300, "same"),
              (4096, 1280, 256, "sorted")]
 
 

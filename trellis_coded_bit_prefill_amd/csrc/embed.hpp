@@ -4,38 +4,58 @@
 namespace trellis {
 namespace {
 
-// One wave a row and 256-column block: lane l decodes columns 4 l .. +3, whose
-// windows lie in 24 bits of two words.
+// A wave takes `pairs` pairs of 256-column blocks of one row, half of it a
+// block: lane l of a half decodes columns 8 l .. +7, whose windows lie in 40
+// bits of two words, and stores 16 bytes.
 template <int BITS>
-__global__ __launch_bounds__(256) void embed_kernel(const int32_t *__restrict__ tokens, int64_t waves, int blocks,
-                                                    const uint32_t *__restrict__ codes,
+__global__ __launch_bounds__(256) void embed_kernel(const int32_t *__restrict__ tokens, int64_t waves, int per_row,
+                                                    int pairs, int blocks, const uint32_t *__restrict__ codes,
                                                     const uint16_t *__restrict__ scales, int n, float scale,
                                                     const uint16_t *__restrict__ extra, int count,
                                                     uint16_t *__restrict__ out) {
   constexpr int wpb = 8 * BITS;
-  const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t id = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (id >= waves) return;
-  const int64_t row = id / blocks;
-  const int b = (int)(id - row * blocks), lane = threadIdx.x & 63;
+  const int64_t row = id / per_row;
+  const int lane = threadIdx.x & 31, b0 = (int)(id - row * per_row) * 2 * pairs + ((threadIdx.x >> 5) & 1);
+  const int b1 = b0 + 2 * pairs < blocks ? b0 + 2 * pairs : blocks;
   const int token = tokens[row];
-  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  uint16_t *const o = out + row * blocks * 256 + 8 * lane;
   if (token >= 0 && token < n) {
-    const uint32_t *const bw = codes + ((int64_t)token * blocks + b) * wpb;
+    const uint32_t *const w = codes + (int64_t)token * blocks * wpb;
     const float s = bf16_bits_to_f32(scales[token]);
     float q, kq;
     alu_row_constants(s, q, kq);
     const bool chain = !alu_scale_ok(s);
-    const int pos = (252 - 4 * lane) * BITS, w0 = pos >> 5, w1 = w0 + 1 == wpb ? 0 : w0 + 1;
-    const uint32_t f = __builtin_amdgcn_alignbit(bw[w1], bw[w0], pos & 31);
+    const int pos = (248 - 8 * lane) * BITS, w0 = pos >> 5, w1 = w0 + 1 == wpb ? 0 : w0 + 1;
+    for (int b = b0; b < b1; b += 2) {
+      const uint32_t *const bw = w + b * wpb;
+      const uint64_t f = (((uint64_t)bw[w1] << 32) | bw[w0]) >> (pos & 31);
+      u32x4 v;
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      v[c] = (float)(__bf16)window_weight(__builtin_amdgcn_ubfe(f, (3 - c) * BITS, 12), s, q, kq, chain) * scale;
-  } else if (token >= n && token - n < count) {
-    const u32x2 e = *reinterpret_cast<const u32x2 *>(extra + ((int64_t)(token - n) * blocks + b) * 256 + 4 * lane);
+      for (int c = 0; c < 4; ++c) {
+        float e[2];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) v[c] = bf16_half(e[c >> 1], c & 1) * scale;
+        for (int h = 0; h < 2; ++h)
+          e[h] = (float)(__bf16)window_weight((uint32_t)(f >> ((7 - 2 * c - h) * BITS)) & 0xFFFu, s, q, kq, chain) * scale;
+        v[c] = (uint32_t)bf16_of(e[0]) | ((uint32_t)bf16_of(e[1]) << 16);
+      }
+      *reinterpret_cast<u32x4 *>(o + b * 256) = v;
+    }
+    return;
   }
-  store4(out + id * 256 + 4 * lane, v);
+  const bool trained = token >= n && token - n < count;
+  const uint16_t *const x = extra + (trained ? (int64_t)(token - n) * blocks * 256 + 8 * lane : 0);
+  for (int b = b0; b < b1; b += 2) {
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (trained) {
+      v = *reinterpret_cast<const u32x4 *>(x + b * 256);
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        v[c] = (uint32_t)bf16_of(bf16_half(v[c], 0) * scale) | ((uint32_t)bf16_of(bf16_half(v[c], 1) * scale) << 16);
+    }
+    *reinterpret_cast<u32x4 *>(o + b * 256) = v;
+  }
 }
 
 // ---- gradient: rows sorted by token -------------------------------------------
@@ -155,17 +175,126 @@ __global__ __launch_bounds__(256) void sort_place_kernel(Sort S, const uint32_t 
   }
 }
 
+// Up to 16384 rows in one workgroup and one launch: every lane keeps up to 16
+// pairs in registers, each wave's in a row of positions, and LDS takes them to
+// their next places, the last ones too (stored to memory as they come, four
+// bytes a line, they took 13 us of 32).
+constexpr int kSmallRows = 16384;
+struct SmallSort {
+  int32_t key[kSmallRows];
+  uint16_t row[kSmallRows];
+  uint16_t counts[16][256];
+  uint32_t waves[4];
+  uint32_t total;
+};
+__global__ __launch_bounds__(1024) void sort_small_kernel(Sort S, uint32_t *__restrict__ arrived, int counters) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char small_space[];
+  SmallSort &M = *reinterpret_cast<SmallSort *>(small_space);
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  for (int i = tid; i < counters; i += 1024) arrived[i] = 0u;
+  constexpr int kEach = kSmallRows / 1024;
+  int key[kEach], row[kEach], rank[kEach];
+  uint32_t in = 0;  // bit i: pair i exists
+  const int each = (S.m + 1023) >> 10, i0 = wave * (64 * each) + lane;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int at = i0 + 64 * i, token = S.tokens[at < S.m ? at : S.m - 1];
+    const bool have = i < each && at < S.m && token >= S.first && token - S.first < S.count;
+    key[i] = have ? token - S.first : 0;
+    row[i] = at;
+    in |= (uint32_t)have << i;
+  }
+  for (int shift = 0;; shift += 8) {
+    for (int i = tid; i < 16 * 256; i += 1024) (&M.counts[0][0])[i] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const bool have = (in >> i) & 1;
+      uint64_t same = __ballot(have);
+      int place = 0;
+      if (same) {
+        const uint32_t digit = (uint32_t)(key[i] >> shift) & 255u;
+#pragma unroll
+        for (int b = 0; b < 8; ++b) {
+          const uint64_t set = __ballot((digit >> b) & 1u);
+          same &= (digit >> b) & 1u ? set : ~set;
+        }
+        const int before = M.counts[wave][digit];
+        place = before + (int)__popcll(same & ((1ull << lane) - 1ull));
+        __builtin_amdgcn_wave_barrier();
+        if (have && (same >> lane) == 1ull) M.counts[wave][digit] = (uint16_t)(before + (int)__popcll(same));
+        __builtin_amdgcn_wave_barrier();
+      }
+      rank[i] = place;
+    }
+    __syncthreads();
+    // places of each digit's first pair of each wave: thread d < 256, digit d
+    uint32_t own = 0, sum = 0;
+    if (tid < 256) {
+#pragma unroll
+      for (int w = 0; w < 16; ++w) own += M.counts[w][tid];
+      sum = own;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const uint32_t up = __shfl_up(sum, o);
+        if (lane >= o) sum += up;
+      }
+      if (lane == 63) M.waves[wave] = sum;
+    }
+    __syncthreads();
+    if (tid < 256) {
+      uint32_t at = sum - own;
+      for (int w = 0; w < wave; ++w) at += M.waves[w];
+      if (tid == 255) M.total = at + own;
+#pragma unroll
+      for (int w = 0; w < 16; ++w) {
+        const uint32_t c = M.counts[w][tid];
+        M.counts[w][tid] = (uint16_t)at;
+        at += c;
+      }
+    }
+    __syncthreads();
+    const bool last = (S.count - 1) >> shift >> 8 == 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      if ((in >> i) & 1) {
+        const int at = M.counts[wave][(key[i] >> shift) & 255] + rank[i];
+        M.key[at] = key[i];
+        M.row[at] = (uint16_t)row[i];
+      }
+    __syncthreads();
+    if (last) break;
+    in = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int at = i0 + 64 * i;
+      in |= (uint32_t)(i < each && at < (int)M.total) << i;
+      key[i] = M.key[at < kSmallRows ? at : 0];  // (past the last pair: not used)
+      row[i] = M.row[at < kSmallRows ? at : 0];
+    }
+    __syncthreads();
+  }
+  for (int i = tid; i < (int)M.total; i += 1024) {
+    S.key_out[i] = M.key[i];
+    S.row_out[i] = M.row[i];
+  }
+  if (tid == 0) *S.total = M.total;
+}
+
 // Sums of the sorted rows: a wave takes one chunk of pairs and 512 columns (8 a
 // lane), and adds up the runs of equal tokens. A run that lies within the chunk
 // is finished; what the chunk holds of one that goes on before or behind it goes
-// to `parts`, and join_runs_kernel adds those up, chunk by chunk.
+// to `parts`, and the wave that arrives last at the run adds its parts in order.
+// The workgroups behind those write zeros in the trained rows that no pair
+// names: a wave a row, which looks its token up in the sorted pairs.
 struct Sums {
   const uint16_t *dout;
   const int32_t *key, *row;
   const uint32_t *total;
   uint16_t *dextra;
-  float *parts;  // [chunks][2][k]: of the chunk's first run, of its last
-  int32_t k, chunk, count;
+  float *parts;       // [chunks][2][k]: of the chunk's first run, of its last
+  uint32_t *arrived;  // [chunks][column blocks]: at the run that begins in the chunk and goes on behind it; zero
+  int32_t k, chunk, chunks, count, columns;  // columns: blocks of 512
   float scale;
 };
 __device__ __forceinline__ void store8(uint16_t *p, const float (&v)[8], float scale) {
@@ -174,87 +303,132 @@ __device__ __forceinline__ void store8(uint16_t *p, const float (&v)[8], float s
   for (int e = 0; e < 4; ++e) o[e] = (uint32_t)bf16_of(v[2 * e] * scale) | ((uint32_t)bf16_of(v[2 * e + 1] * scale) << 16);
   *reinterpret_cast<u32x4 *>(p) = o;
 }
+// Whether a pair has this key: the wave looks at 64 places at a time.
+__device__ __forceinline__ bool find_pair(const int32_t *keys, int total, int key, int lane) {
+  int low = 0, high = total;  // the first pair whose key is not below `key` lies in low .. high
+  while (low < high) {
+    const int step = (high - low + 63) >> 6, at = low + lane * step;
+    const int k = at < high ? keys[at] : 0x7fffffff;
+    if (__any(k == key)) return true;
+    const int below = (int)__popcll(__ballot(k < key));
+    if (step == 1) return false;
+    const int next = low + below * step;
+    high = next < high ? next : high;
+    low += below > 0 ? (below - 1) * step + 1 : 0;
+    if (below == 0) return false;
+  }
+  return false;
+}
 __global__ __launch_bounds__(64) void sum_runs_kernel(Sums S) {
-  const int total = (int)*S.total, c = blockIdx.y * 512 + 8 * (int)threadIdx.x;
-  const int begin = blockIdx.x * S.chunk, end = total - begin < S.chunk ? total : begin + S.chunk;
-  if (begin >= end || c >= S.k) return;
+  const int total = (int)*S.total, lane = threadIdx.x;
+  if ((int)blockIdx.x >= S.chunks * S.columns) {
+    const int e = (int)blockIdx.x - S.chunks * S.columns;
+    if (find_pair(S.key, total, e, lane)) return;
+    for (int c = 8 * lane; c < S.k; c += 512)
+      *reinterpret_cast<u32x4 *>(S.dextra + (int64_t)e * S.k + c) = u32x4{0u, 0u, 0u, 0u};
+    return;
+  }
+  const int chunk = (int)blockIdx.x / S.columns, column = (int)blockIdx.x - chunk * S.columns;
+  const int c = column * 512 + 8 * lane;
+  const bool mine = c < S.k;  // (the last block may be half a wave's)
+  const int begin = chunk * S.chunk, end = total - begin < S.chunk ? total : begin + S.chunk;
+  if (begin >= end) return;
+  const int before_key = begin > 0 ? S.key[begin - 1] : -1, behind_key = end < total ? S.key[end] : -1;
+  const __amdgpu_buffer_rsrc_t ws =
+      __builtin_amdgcn_make_buffer_rsrc(S.parts, (short)0, (int)((uint32_t)S.chunks * 2u * (uint32_t)S.k * 4u), kRawBuffer);
+  auto part_at = [&](int chunk, int which) { return ((uint32_t)(chunk * 2 + which) * (uint32_t)S.k + (uint32_t)c) * 4u; };
   float acc[8] = {};
-  int run = begin, key = S.key[begin];  // the run's first pair here, and its token
-  const bool goes_on_before = begin > 0 && S.key[begin - 1] == key;
-  const bool goes_on_behind = end < total && S.key[end] == S.key[end - 1];
-  auto flush = [&](int next, bool last) {
-    // (a run that fills the chunk and goes on to both sides is its first)
-    const bool before = run == begin && goes_on_before, behind = last && goes_on_behind;
+  int key = -1, run = begin, shared[2] = {-1, -1};
+  auto flush = [&](int next) {
+    const bool before = run == begin && before_key == key, behind = next == end && behind_key == key;
     if (before || behind) {
-      float *const p = S.parts + ((int64_t)blockIdx.x * 2 + (before ? 0 : 1)) * S.k + c;
+      shared[before ? 0 : 1] = key;  // (a run that fills the chunk and goes on to both sides is its first)
+      if (mine) {
 #pragma unroll
-      for (int e = 0; e < 8; e += 4) *reinterpret_cast<f32x4 *>(p + e) = f32x4{acc[e], acc[e + 1], acc[e + 2], acc[e + 3]};
-    } else {
+        for (int e = 0; e < 8; e += 4)
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, f32x4{acc[e], acc[e + 1], acc[e + 2], acc[e + 3]}),
+                                                 ws, part_at(chunk, before ? 0 : 1) + 4u * e, 0, kSc1);
+      }
+    } else if (mine) {
       store8(S.dextra + (int64_t)key * S.k + c, acc, S.scale);
     }
     run = next;
   };
-  constexpr int U = 8;  // rows loaded at a time
-  for (int i = begin; i < end; i += U) {
-    u32x4 v[U];
-    int keys[U];
+  for (int i0 = begin; i0 < end; i0 += 64) {
+    // 64 pairs, one a lane, and their rows eight at a time
+    const int n = end - i0 < 64 ? end - i0 : 64;
+    const int at = i0 + (lane < n ? lane : n - 1);
+    const int keys = S.key[at], rows = S.row[at];
+    constexpr int U = 8;
+    for (int i = 0; i < n; i += U) {
+      u32x4 v[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int at = i + u < end ? i + u : end - 1;
-      keys[u] = S.key[at];
-      v[u] = *reinterpret_cast<const u32x4 *>(S.dout + (int64_t)S.row[at] * S.k + c);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (i + u >= end) break;
-      if (keys[u] != key) {
-        flush(i + u, false);
-        key = keys[u];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+      for (int u = 0; u < U; ++u) {
+        const int r = __builtin_amdgcn_readlane(rows, i + u < n ? i + u : n - 1);
+        v[u] = u32x4{0u, 0u, 0u, 0u};
+        if (mine) v[u] = *reinterpret_cast<const u32x4 *>(S.dout + (int64_t)r * S.k + c);
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] += bf16_half(v[u][e >> 1], e & 1);
+      for (int u = 0; u < U; ++u) {
+        if (i + u >= n) break;
+        const int next = __builtin_amdgcn_readlane(keys, i + u);
+        if (next != key) {
+          if (key >= 0) flush(i0 + i + u);
+          key = next;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] += bf16_half(v[u][e >> 1], e & 1);
+      }
     }
   }
-  flush(end, true);
-}
-
-// Runs over several chunks: the workgroup of the chunk that a run begins in (and
-// does not end in) adds the parts in order.
-__global__ __launch_bounds__(64) void join_runs_kernel(Sums S) {
-  const int total = (int)*S.total, c = blockIdx.y * 512 + 8 * (int)threadIdx.x;
-  const int begin = blockIdx.x * S.chunk, end = begin + S.chunk;
-  if (end >= total || c >= S.k) return;  // (the last chunk: nothing goes on behind it)
-  const int key = S.key[end - 1];
-  if (S.key[end] != key) return;
-  if (begin > 0 && S.key[begin - 1] == key && S.key[begin] == key) return;  // begun before this chunk
-  float acc[8] = {};
-  // its part here is the last run's
-  for (int chunk = blockIdx.x, which = 1;; ++chunk, which = 0) {
-    const float *const p = S.parts + ((int64_t)chunk * 2 + which) * S.k + c;
+  flush(end);
+  // Runs over several chunks: the parts are complete at the coherent level
+  // before the count moves.
+  if (shared[0] < 0 && shared[1] < 0) return;
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] += p[e];
-    const int stop = (chunk + 1) * S.chunk;
-    if (stop >= total || S.key[stop] != key) break;
+  for (int i = 0; i < 2; ++i) {
+    if (shared[i] < 0) continue;
+    // The run's chunks: the borders on both sides that it goes over, 64 at a time.
+    int c0 = chunk, c1 = chunk;
+    for (;;) {
+      const int border = c0 - lane;
+      const uint64_t over = __ballot(border > 0 && S.key[border > 0 ? (int64_t)border * S.chunk - 1 : 0] == shared[i]);
+      c0 -= over == ~0ull ? 64 : __builtin_ctzll(~over);
+      if (over != ~0ull) break;
+    }
+    for (;;) {
+      const int64_t border = (int64_t)(c1 + 1 + lane) * S.chunk;
+      const uint64_t over = __ballot(border < total && S.key[border < total ? border : 0] == shared[i]);
+      c1 += over == ~0ull ? 64 : __builtin_ctzll(~over);
+      if (over != ~0ull) break;
+    }
+    uint32_t *const count = S.arrived + (int64_t)c0 * S.columns + column;
+    uint32_t was = 0;
+    if (lane == 0) was = __hip_atomic_fetch_add(count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (__builtin_amdgcn_readfirstlane(was) != (uint32_t)(c1 - c0)) continue;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+    // (a run's first chunk keeps its part as the last run's, the others as the
+    // first's; past the last chunk: outside the buffer, zero)
+    constexpr int U = 8;
+    for (int p = c0; p <= c1; p += U) {
+      f32x4 v[U][2];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          v[u][h] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                  ws, mine && p + u <= c1 ? part_at(p + u, p + u == c0) + 16u * h : 0xFFFFFFF0u, 0, kSc1));
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] += v[u][e >> 2][e & 3];
+    }
+    if (mine) store8(S.dextra + (int64_t)shared[i] * S.k + c, acc, S.scale);
   }
-  store8(S.dextra + (int64_t)key * S.k + c, acc, S.scale);
-}
-
-// Zeros in the trained rows that no pair names: a wave a row, which looks its
-// token up in the sorted pairs.
-__global__ __launch_bounds__(256) void clear_rows_kernel(Sums S) {
-  const int e = blockIdx.x * 4 + (int)(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  if (e >= S.count) return;
-  int low = 0, high = (int)*S.total;
-  while (low < high) {
-    const int mid = (low + high) >> 1;
-    if (S.key[mid] < e) low = mid + 1;
-    else high = mid;
-  }
-  if (low < (int)*S.total && S.key[low] == e) return;
-  for (int c = 8 * lane; c < S.k; c += 512)
-    *reinterpret_cast<u32x4 *>(S.dextra + (int64_t)e * S.k + c) = u32x4{0u, 0u, 0u, 0u};
 }
 
 }  // namespace
@@ -272,11 +446,17 @@ trellis_status trellis_embed(const int32_t *tokens, int32_t m, const uint32_t *c
   if (!on(tokens, 4) || !on(codes, 16) || !on(scales, 2) || !on(extra, 16) || !on(out, 16)) return TRELLIS_E_ALIGN;
   hipStream_t stream = reinterpret_cast<hipStream_t>(hip_stream);
   const int blocks = g.k >> 8;
-  const int64_t waves = (int64_t)m * blocks;
+  // One pair of blocks a wave until the card is full (8192 waves), then up to
+  // four, which share the token's and the scale's loads.
+  const int both = (blocks + 1) / 2;
+  int pairs = (int)((int64_t)m * both / 8192);
+  pairs = pairs < 1 ? 1 : pairs > 4 ? 4 : pairs;
+  const int per_row = (both + pairs - 1) / pairs;
+  const int64_t waves = (int64_t)m * per_row;
   const dim3 grid((unsigned)((waves + 3) / 4));
   (void)hipGetLastError();
   const auto fn = g.bits == 2 ? &embed_kernel<2> : g.bits == 3 ? &embed_kernel<3> : &embed_kernel<4>;
-  hipLaunchKernelGGL(fn, grid, dim3(256), 0, stream, tokens, waves, blocks, codes, scales, g.n, scale, extra, count, out);
+  hipLaunchKernelGGL(fn, grid, dim3(256), 0, stream, tokens, waves, per_row, pairs, blocks, codes, scales, g.n, scale, extra, count, out);
   return hipGetLastError() == hipSuccess ? TRELLIS_OK : TRELLIS_E_HIP;
 }
 
@@ -293,34 +473,51 @@ trellis_status trellis_embed_backward(const uint16_t *dout, const int32_t *token
   int dev = 0, cus = 0;
   TRELLIS_TRY(device(dev, cus));
   const int blocks = (m + kSortRows - 1) / kSortRows;
-  int chunk = (m + 1023) / 1024;
+  // Chunks of 16 pairs at least; at most 1024 chunks and 2 GiB of parts.
+  int64_t most = ((int64_t)1 << 31) / ((int64_t)k * 8);
+  if (most > 1024) most = 1024;
+  int chunk = (int)((m + most - 1) / most);
   if (chunk < 16) chunk = 16;
-  const int chunks = (m + chunk - 1) / chunk;
+  const int chunks = (m + chunk - 1) / chunk, columns = (k + 511) / 512;
   const size_t pair_bytes = up256((size_t)m * 4), count_bytes = up256((size_t)blocks * 1024),
-               part_bytes = (size_t)chunks * 2 * k * 4;
+               part_bytes = (size_t)chunks * 2 * k * 4, arrived_bytes = up256((size_t)chunks * columns * 4);
   Space *w = nullptr;
-  TRELLIS_TRY(space(dev, stream, 4 * pair_bytes + count_bytes + 256 + part_bytes, 0, w));
-  int32_t *const pairs[4] = {reinterpret_cast<int32_t *>(w->bytes), reinterpret_cast<int32_t *>(w->bytes + pair_bytes),
-                             reinterpret_cast<int32_t *>(w->bytes + 2 * pair_bytes),
-                             reinterpret_cast<int32_t *>(w->bytes + 3 * pair_bytes)};
-  uint32_t *const counts = reinterpret_cast<uint32_t *>(w->bytes + 4 * pair_bytes);
-  uint32_t *const total = reinterpret_cast<uint32_t *>(w->bytes + 4 * pair_bytes + count_bytes);
-  float *const parts = reinterpret_cast<float *>(w->bytes + 4 * pair_bytes + count_bytes + 256);
+  TRELLIS_TRY(space(dev, stream, 4 * pair_bytes + count_bytes + 256 + arrived_bytes + part_bytes, 0, w));
+  unsigned char *at = w->bytes;
+  auto take = [&](size_t bytes) {
+    unsigned char *const p = at;
+    at += bytes;
+    return p;
+  };
+  int32_t *pairs[4];
+  for (auto &p : pairs) p = reinterpret_cast<int32_t *>(take(pair_bytes));
+  uint32_t *const counts = reinterpret_cast<uint32_t *>(take(count_bytes)), *const total = reinterpret_cast<uint32_t *>(take(256)),
+           *const arrived = reinterpret_cast<uint32_t *>(take(arrived_bytes));
+  float *const parts = reinterpret_cast<float *>(take(part_bytes));
   (void)hipGetLastError();
   int to = 0;
-  for (int shift = 0; shift == 0 || (count - 1) >> shift; shift += 8, to ^= 2) {
-    Sort s{shift ? nullptr : tokens, pairs[to ^ 2], pairs[(to ^ 2) + 1], pairs[to], pairs[to + 1], counts, total, m, first,
-           count, shift, blocks};
-    hipLaunchKernelGGL(sort_count_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, s);
-    hipLaunchKernelGGL(sort_sum_kernel, dim3(1), dim3(1024), 0, stream, counts, 256 * blocks, total);
-    hipLaunchKernelGGL(sort_place_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, s, total);
+  if (m <= kSmallRows) {
+    static bool ready[kMaxDevices];
+    if (!ready[dev] && !worked(hipFuncSetAttribute(reinterpret_cast<const void *>(&sort_small_kernel),
+                                                   hipFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(SmallSort))))
+      return TRELLIS_E_HIP;
+    ready[dev] = true;
+    const Sort s{tokens, nullptr, nullptr, pairs[0], pairs[1], nullptr, total, m, first, count, 0, 0};
+    hipLaunchKernelGGL(sort_small_kernel, dim3(1), dim3(1024), sizeof(SmallSort), stream, s, arrived, chunks * columns);
+  } else {
+    hipLaunchKernelGGL(clear_kernel, dim3((unsigned)((chunks * columns + 255) / 256)), dim3(256), 0, stream, arrived,
+                       (int64_t)chunks * columns);
+    for (int shift = 0; shift == 0 || (count - 1) >> shift; shift += 8, to ^= 2) {
+      const Sort s{shift ? nullptr : tokens, pairs[to ^ 2], pairs[(to ^ 2) + 1], pairs[to], pairs[to + 1], counts, total, m,
+                   first, count, shift, blocks};
+      hipLaunchKernelGGL(sort_count_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, s);
+      hipLaunchKernelGGL(sort_sum_kernel, dim3(1), dim3(1024), 0, stream, counts, 256 * blocks, total);
+      hipLaunchKernelGGL(sort_place_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, s, total);
+    }
+    to ^= 2;  // the last pass's output
   }
-  to ^= 2;  // the last pass's output
-  const Sums s{dout, pairs[to], pairs[to + 1], total, dextra, parts, k, chunk, count, scale};
-  const dim3 grid((unsigned)chunks, (unsigned)((k + 511) / 512));
-  hipLaunchKernelGGL(clear_rows_kernel, dim3((unsigned)((count + 3) / 4)), dim3(256), 0, stream, s);
-  hipLaunchKernelGGL(sum_runs_kernel, grid, dim3(64), 0, stream, s);
-  hipLaunchKernelGGL(join_runs_kernel, grid, dim3(64), 0, stream, s);
+  const Sums s{dout, pairs[to], pairs[to + 1], total, dextra, parts, arrived, k, chunk, chunks, count, columns, scale};
+  hipLaunchKernelGGL(sum_runs_kernel, dim3((unsigned)(chunks * columns + count)), dim3(64), 0, stream, s);
   return hipGetLastError() == hipSuccess ? TRELLIS_OK : TRELLIS_E_HIP;
 }
 

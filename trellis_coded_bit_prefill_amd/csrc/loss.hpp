@@ -105,7 +105,7 @@ __global__ __launch_bounds__(256) void row_stats_kernel(const float *__restrict_
 // entries' sum; the list in LDS.
 struct RowList {
   int at[kMaxTop];       // -1: none
-  float q[kMaxTop], l2[kMaxTop];
+  float q[kMaxTop], qs[kMaxTop];  // of each place; of the entry, all its places together
   float add[kMaxTop];    // d of the entry (its first place in the list), without T
   uint8_t first[kMaxTop];
   float red[2][4];
@@ -127,15 +127,48 @@ __device__ __forceinline__ float max_256(float v, float *red) {
   __syncthreads();
   return fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
 }
+// -log p of a row's only entry: log(1 + S' / e).
+__device__ __forceinline__ float sole_loss(f32x2 rest, float l2) {
+  if (l2 == __builtin_inff()) return l2 - l2;
+  const float ratio = (rest[0] - l2) * kLn2 + logf(rest[1]);
+  return ratio > 0.f ? ratio + log1pf(expf(-ratio)) : log1pf(expf(ratio));
+}
+// row_list for lists of one: nothing to sum, every thread works it out.
+__device__ __forceinline__ bool row_single(const Lists &L, int64_t row, f32x2 rest, bool whole, RowList &S, bool write) {
+  int at = L.index[row];
+  if (at >= L.n) at = -1;
+  const bool valid = at >= 0;
+  const float z = valid && L.logits ? L.logits[row] * L.scale2 : 0.f;
+  const bool alive = valid && z != -__builtin_inff();
+  const float q = (z - z) + 1.f;  // softmax of one logit; NaN where it is not a number
+  const float l2 = valid ? L.listed[row] : 0.f;
+  const float rmax = valid && !whole ? fmaxf(l2, rest[0]) : rest[0];
+  const float others = rest[1] * __builtin_amdgcn_exp2f(rest[0] - rmax);
+  const float sum = others + (valid && !whole ? __builtin_amdgcn_exp2f(l2 - rmax) : 0.f);
+  S.at[threadIdx.x] = threadIdx.x == 0 ? at : -1;
+  S.first[threadIdx.x] = threadIdx.x == 0 && valid;
+  S.add[threadIdx.x] = q * (-others / sum);
+  S.qs[threadIdx.x] = q;
+  if (threadIdx.x == 0) {
+    S.total = f32x2{rmax, sum};
+    if (write) {
+      L.loss[row] = alive ? L.temperature * L.temperature * q * sole_loss(rest, l2) : 0.f;
+      L.lse[row] = (rmax + __builtin_amdgcn_logf(sum)) * kLn2;
+    }
+  }
+  __syncthreads();
+  return alive;
+}
 // rest: R' and S' of the entries that are not listed, or of all (`whole`; then
 // the list has not exactly one entry, else some digits of 1 - p are lost).
 // Returns whether the row has entries; loss and lse where `write`.
 static_assert(kMaxTop == 256, "one thread an entry");
 __device__ bool row_list(const Lists &L, int64_t row, f32x2 rest, bool whole, RowList &S, bool write) {
   const int j = threadIdx.x;
+  const float inf = __builtin_inff();
+  if (L.top == 1) return row_single(L, row, rest, whole, S, write);
   int at = j < L.top ? L.index[row * L.top + j] : -1;
   if (at >= L.n) at = -1;
-  const float inf = __builtin_inff();
   float z = -inf, l2 = -inf;
   if (at >= 0) {
     z = L.logits ? L.logits[row * L.top + j] * L.scale2 : 0.f;
@@ -149,7 +182,6 @@ __device__ bool row_list(const Lists &L, int64_t row, f32x2 rest, bool whole, Ro
   const bool alive = total != 0.f;
   const float q = alive ? e / total : 0.f;
   S.q[j] = q;
-  S.l2[j] = l2;
   __syncthreads();
   // every entry once: its first place adds to the sum
   bool first = at >= 0;
@@ -168,14 +200,13 @@ __device__ bool row_list(const Lists &L, int64_t row, f32x2 rest, bool whole, Ro
   const bool alone = sum_256(first ? 1.f : 0.f, S.red[0]) == 1.f && !whole;
   if (j == 0) S.total = f32x2{rmax, sum};
   S.first[j] = first;
-  S.add[j] = !first ? 0.f : alone ? -others / sum : here / sum - qs;
+  S.qs[j] = qs;
+  S.add[j] = !first ? 0.f : alone ? qs * (-others / sum) : here / sum - qs;
   float term = q != 0.f ? q * (z - zmax - __builtin_amdgcn_logf(total)) * kLn2 : 0.f;  // q log q
   if (!alone) {
     if (q != 0.f) term += q * (lse2 - l2) * kLn2;
   } else if (first) {
-    const float ratio = (rest[0] - l2) * kLn2 + logf(rest[1]);  // log(S' / e)
-    term += ratio > 0.f ? ratio + log1pf(expf(-ratio)) : log1pf(expf(ratio));
-    if (l2 == inf) term = l2 - l2;
+    term += sole_loss(rest, l2);
   }
   const float loss = sum_256(term, S.red[1]);
   if (write && j == 0) {
@@ -218,6 +249,73 @@ __global__ __launch_bounds__(256) void row_loss_kernel(Lists L, const float *__r
   const int at = S.at[threadIdx.x];
   if (S.first[threadIdx.x] && at >= c0 && at < c0 + kStatSpan && alive)
     o[at] = bf16_of(L.temperature * S.add[threadIdx.x]);
+}
+
+// Rows of up to 16384 logits in one launch instead of three: the row stays in
+// registers, 64 logits a thread at most, and a bit map in LDS says which are listed.
+constexpr int kWholeRow = 16384;
+__global__ __launch_bounds__(256) void whole_row_kernel(Lists L, const float *__restrict__ logits,
+                                                        uint16_t *__restrict__ d) {
+  __shared__ RowList S;
+  __shared__ uint32_t listed[kWholeRow / 32];
+  __shared__ f32x2 part[4];
+  const int64_t row = blockIdx.x;
+  const int tid = threadIdx.x;
+  const float *const l = logits + row * L.n;
+  constexpr int kQuads = kWholeRow / 1024;
+  const float inf = __builtin_inff();
+  f32x4 v[kQuads];
+#pragma unroll
+  for (int i = 0; i < kQuads; ++i) {
+    const int c = 1024 * i + 4 * tid;
+    v[i] = f32x4{-inf, -inf, -inf, -inf};
+    if (c < L.n) v[i] = *reinterpret_cast<const f32x4 *>(l + c);
+  }
+  int at = tid < L.top ? L.index[row * L.top + tid] : -1;
+  if (at >= L.n) at = -1;
+  if (tid < L.top) L.listed[row * L.top + tid] = at >= 0 ? l[at] * L.scale2 : 0.f;
+  for (int i = tid; i < (L.n + 31) / 32; i += 256) listed[i] = 0u;
+  __syncthreads();
+  if (at >= 0) atomicOr(&listed[at >> 5], 1u << (at & 31));
+  __syncthreads();
+  float r = kLowest;
+#pragma unroll
+  for (int i = 0; i < kQuads; ++i) {
+    if (1024 * i < L.n) {
+      const int c = 1024 * i + 4 * tid;
+      const uint32_t out = c < L.n ? listed[c >> 5] >> (c & 31) : 0u;
+      const f32x4 x = v[i] * L.scale2;
+      v[i] = f32x4{out & 1 ? -inf : x[0], out & 2 ? -inf : x[1], out & 4 ? -inf : x[2], out & 8 ? -inf : x[3]};
+      r = fmaxf(r, fmaxf(fmaxf(v[i][0], v[i][1]), fmaxf(v[i][2], v[i][3])));
+    }
+  }
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < kQuads; ++i) {
+    if (1024 * i < L.n)
+      s += (__builtin_amdgcn_exp2f(v[i][0] - r) + __builtin_amdgcn_exp2f(v[i][1] - r)) +
+           (__builtin_amdgcn_exp2f(v[i][2] - r) + __builtin_amdgcn_exp2f(v[i][3] - r));
+  }
+  const f32x2 a = join_stats_wave(f32x2{r, s});
+  if ((tid & 63) == 0) part[tid >> 6] = a;
+  __syncthreads();
+  const f32x2 rest = join_stats(join_stats(part[0], part[1]), join_stats(part[2], part[3]));
+  const bool alive = row_list(L, row, rest, false, S, true);
+  if (!d) return;
+  const float rmax = S.total[0], f = L.temperature / S.total[1];
+  uint16_t *const o = d + row * L.n;
+#pragma unroll
+  for (int i = 0; i < kQuads; ++i) {
+    const int c = 1024 * i + 4 * tid;
+    if (c < L.n) {
+      f32x4 g;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) g[e] = alive ? f * __builtin_amdgcn_exp2f(v[i][e] - rmax) : 0.f;
+      store4(o + c, g);
+    }
+  }
+  __syncthreads();
+  if (S.first[tid] && alive) o[S.at[tid]] = bf16_of(L.temperature * S.add[tid]);
 }
 
 // dx = dloss[row] * dx: a factor a row.
@@ -412,7 +510,7 @@ __global__ __launch_bounds__(256) void row_join_kernel(Lists L, Vocabulary V, in
     __syncthreads();
   }
   if (S.first[threadIdx.x] && alive)
-    *place(S.at[threadIdx.x]) = bf16_of(whole ? S.add[threadIdx.x] * total : -sum);
+    *place(S.at[threadIdx.x]) = bf16_of(whole ? S.add[threadIdx.x] * total : S.qs[threadIdx.x] * -sum);
 }
 
 // dx: the splits' sums in order, times the row's factor, rounded. Four columns a thread.
@@ -638,11 +736,15 @@ trellis_status loss_rows(const uint16_t *x, int32_t m, const uint32_t *codes, co
     p.n = g.n;
     p.k = g.k;
     TRELLIS_TRY(launch(fwd[which], p, stream));
-    hipLaunchKernelGGL(pluck_kernel, dim3((unsigned)mc), dim3(64), 0, stream, L, logits);
-    hipLaunchKernelGGL(row_stats_kernel, dim3((unsigned)mc, (unsigned)spans), dim3(256), 0, stream, logits, g.n, L.scale2,
-                       stats);
-    hipLaunchKernelGGL(row_loss_kernel, dim3((unsigned)mc, dx ? (unsigned)spans : 1u), dim3(256), 0, stream, L, logits, stats,
-                       spans, dx ? d : nullptr);
+    if (g.n <= kWholeRow) {
+      hipLaunchKernelGGL(whole_row_kernel, dim3((unsigned)mc), dim3(256), 0, stream, L, logits, dx ? d : nullptr);
+    } else {
+      hipLaunchKernelGGL(pluck_kernel, dim3((unsigned)mc), dim3(64), 0, stream, L, logits);
+      hipLaunchKernelGGL(row_stats_kernel, dim3((unsigned)mc, (unsigned)spans), dim3(256), 0, stream, logits, g.n, L.scale2,
+                         stats);
+      hipLaunchKernelGGL(row_loss_kernel, dim3((unsigned)mc, dx ? (unsigned)spans : 1u), dim3(256), 0, stream, L, logits,
+                         stats, spans, dx ? d : nullptr);
+    }
     if (hipGetLastError() != hipSuccess) return TRELLIS_E_HIP;
     if (!dx) continue;
     Product t{};
