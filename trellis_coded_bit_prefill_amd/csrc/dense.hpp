@@ -40,19 +40,30 @@ struct Unpack {
   int32_t first, tiles;  // tiles of this launch: first, number (per matrix)
   int32_t matrices;
 };
+// Operands of a launch beyond what the Infinity Cache holds (256 MB) are stored
+// past the caches, which pass them on faster than they take them in: 671 MB in
+// 146 us instead of 190 (columns 142 instead of 183). Smaller ones are kept: the
+// product reads them from there.
+constexpr int64_t kFarBytes = (int64_t)256 << 20;
+template <bool FAR>
+__device__ __forceinline__ void store_operand(bf16x8 *p, bf16x8 v) {
+  if constexpr (FAR) __builtin_nontemporal_store(v, p);
+  else *p = v;
+}
 
 // Forward: one wave per 16 rows of W and 256-weight block, 8 operands. Bound by
 // its writes: K = 5120, N = 17408, k = 4 in 48 us, 223 MB at 4.6 TB/s (a plain
 // copy reaches 5.2).
-template <int BITS>
+template <int BITS, bool FAR>
 __global__ __launch_bounds__(256) void unpack_rows_kernel(Unpack U) {
   constexpr int wpb = 8 * BITS;
   const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
   const int blocks = U.k >> 8;
-  const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  // (at most 2^18 tiles of 2^10 blocks)
+  const uint32_t id = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
   const int which = blockIdx.y;
-  if (id >= (int64_t)U.tiles * blocks) return;
-  const int tile = (int)(id / blocks), b = (int)(id - (int64_t)tile * blocks);
+  if (id >= (uint32_t)U.tiles * (uint32_t)blocks) return;
+  const int tile = (int)(id / (uint32_t)blocks), b = (int)(id - (uint32_t)tile * (uint32_t)blocks);
   const int n = (U.first + tile) * 16 + j, row = n < U.n ? n : U.n - 1;  // columns past N are not stored
   const uint32_t *bw = U.codes[which] + ((int64_t)row * blocks + b) * wpb;
   const float s = bf16_bits_to_f32(U.scales[which][row]);
@@ -68,14 +79,19 @@ __global__ __launch_bounds__(256) void unpack_rows_kernel(Unpack U) {
   }
   const int64_t stride = (int64_t)U.tiles * U.matrices * 64;  // of a step
   bf16x8 *out = reinterpret_cast<bf16x8 *>(U.w) + 8 * b * stride + ((int64_t)tile * U.matrices + which) * 64 + lane;
+  // (two loops: a choice at every weight costs more than the weight)
+  auto decode = [&](auto chained) {
 #pragma unroll
-  for (int st = 0; st < 8; ++st) {
-    bf16x8 v;
+    for (int st = 0; st < 8; ++st) {
+      bf16x8 v;
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      v[e] = (__bf16)window_weight((uint32_t)(f[st] >> ((7 - e) * BITS)) & 0xFFFu, s, q, kq, chain);
-    out[st * stride] = v;
-  }
+      for (int e = 0; e < 8; ++e)
+        v[e] = (__bf16)window_weight((uint32_t)(f[st] >> ((7 - e) * BITS)) & 0xFFFu, s, q, kq, decltype(chained)::value);
+      store_operand<FAR>(out + st * stride, v);
+    }
+  };
+  if (chain) decode(std::true_type{});
+  else decode(std::false_type{});
 }
 
 // Transposed: one wave per step (32 rows of W) and 256-column block. The rows'
@@ -85,7 +101,7 @@ __global__ __launch_bounds__(256) void unpack_rows_kernel(Unpack U) {
 // each of the four columns. K = 5120, N = 17408, k = 4 in 51 us, 224 MB at 4.4
 // TB/s (64 us with the words read by each lane, 87 us before the operands were
 // stored a kilobyte at a time).
-template <int BITS>
+template <int BITS, bool FAR>
 __global__ __launch_bounds__(256) void unpack_columns_kernel(Unpack U) {
   constexpr int wpb = 8 * BITS, kRow = wpb + 4;  // words of a row's block, and in LDS
   __shared__ __attribute__((aligned(16))) uint32_t words[4][32 * kRow];
@@ -93,10 +109,11 @@ __global__ __launch_bounds__(256) void unpack_columns_kernel(Unpack U) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, j = lane & 15, g = lane >> 4;
   const int per = U.steps / U.matrices;  // steps of one matrix
   const int blocks = U.tiles >> 4;       // of 256 columns
-  const int64_t id = (int64_t)blockIdx.x * 4 + wave;
-  if (id >= (int64_t)blocks * per) return;
+  // (at most 2^10 blocks of 2^17 steps)
+  const uint32_t id = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + wave);
+  if (id >= (uint32_t)blocks * (uint32_t)per) return;
   const int which = blockIdx.y;
-  const int ks = (int)(id / blocks), blk = (int)(id - (int64_t)ks * blocks);
+  const int ks = (int)(id / (uint32_t)blocks), blk = (int)(id - (uint32_t)ks * (uint32_t)blocks);
   const int64_t row_words = (int64_t)(U.k >> 8) * wpb;
   const uint32_t *const base = U.codes[which] + (int64_t)((U.first >> 4) + blk) * wpb;
   u32x4 v[BITS];
@@ -122,25 +139,29 @@ __global__ __launch_bounds__(256) void unpack_columns_kernel(Unpack U) {
   }
   bf16x8 *const mine = turn[wave];
   bf16x8 *out = reinterpret_cast<bf16x8 *>(U.w) + (((int64_t)which * per + ks) * U.tiles + 16 * blk) * 64 + lane;
+  auto decode = [&](auto chained) {
 #pragma unroll
-  for (int part = 0; part < 4; ++part) {
-    const int pos = (252 - 64 * part - 4 * j) * BITS, w0 = pos >> 5, sh = pos & 31, w1 = w0 + 1 == wpb ? 0 : w0 + 1;
-    bf16x8 w[4];
+    for (int part = 0; part < 4; ++part) {
+      const int pos = (252 - 64 * part - 4 * j) * BITS, w0 = pos >> 5, sh = pos & 31, w1 = w0 + 1 == wpb ? 0 : w0 + 1;
+      bf16x8 w[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint32_t *row = &words[wave][(8 * g + e) * kRow];
-      const uint32_t f = __builtin_amdgcn_alignbit(row[w1], row[w0], sh);
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t *row = &words[wave][(8 * g + e) * kRow];
+        const uint32_t f = __builtin_amdgcn_alignbit(row[w1], row[w0], sh);
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        w[c][e] = (__bf16)window_weight(__builtin_amdgcn_ubfe(f, (3 - c) * BITS, 12), sc[e], q[e], kq[e], chain);
+        for (int c = 0; c < 4; ++c)
+          w[c][e] = (__bf16)window_weight(__builtin_amdgcn_ubfe(f, (3 - c) * BITS, 12), sc[e], q[e], kq[e], decltype(chained)::value);
+      }
+      // Through the wave's LDS again, so that each store writes 1 KB in a row:
+      // lane (j, g) holds slots 16 g + 4 (j mod 4) .. +3 of tile j / 4.
+#pragma unroll
+      for (int c = 0; c < 4; ++c) mine[(j >> 2) * 64 + g * 16 + 4 * (j & 3) + c] = w[c];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) store_operand<FAR>(out + (4 * part + i) * 64, mine[i * 64 + lane]);
     }
-    // Through the wave's LDS again, so that each store writes 1 KB in a row:
-    // lane (j, g) holds slots 16 g + 4 (j mod 4) .. +3 of tile j / 4.
-#pragma unroll
-    for (int c = 0; c < 4; ++c) mine[(j >> 2) * 64 + g * 16 + 4 * (j & 3) + c] = w[c];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) out[(4 * part + i) * 64] = mine[i * 64 + lane];
-  }
+  };
+  if (chain) decode(std::true_type{});
+  else decode(std::false_type{});
 }
 
 // Eight columns of a row of P; rows past m and columns past `cols` are zero.
@@ -227,7 +248,7 @@ __global__ __launch_bounds__(256) void gated_grad_pack_kernel(const uint16_t *__
 struct Dense {
   const uint16_t *p, *w;   // operands of the rows, and of the columns of this launch
   uint16_t *out, *gate, *up;
-  float *partials;         // [splits][m][16 wtiles], where the contraction is split or float32 sums are wanted, else null
+  float *partials;         // [splits][m][16 wtiles], where the contraction is split
   int32_t m, steps;        // steps: an even number
   int32_t splits;          // of the contraction
   int32_t width;           // row length of the outputs
@@ -256,8 +277,10 @@ __device__ __forceinline__ void step_barrier() {
 }
 
 // LDS buffers of a step: as many as fit in 160 KB, at most 6.
-constexpr int dense_step_bytes(int nt) { return (kDenseRows / 16 + 2 * nt) * 1024; }
-constexpr int dense_buffers(int nt) { return 160 * 1024 / dense_step_bytes(nt) < 6 ? 160 * 1024 / dense_step_bytes(nt) : 6; }
+constexpr int dense_step_bytes(int nt, int rt = 4) { return (4 * rt + 2 * nt) * 1024; }
+constexpr int dense_buffers(int nt, int rt = 4) {
+  return 160 * 1024 / dense_step_bytes(nt, rt) < 6 ? 160 * 1024 / dense_step_bytes(nt, rt) : 6;
+}
 
 // One workgroup (8 waves, 4 by rows x 2 by columns): 256 rows by 32 NT
 // columns. Wave: 64 rows by 16 NT columns, 4 x NT accumulators. A step's
@@ -288,9 +311,10 @@ struct DenseAt {
   int row0, tile0, split;
 };
 // between(at): work of the wave's own while the first steps are on their way.
-template <int NT, typename Between>
-__device__ __forceinline__ DenseAt dense_sums(const Dense &D, f32x4 (&acc)[4][NT], Between between) {
-  constexpr int kA = kDenseRows / 16 * 1024, kBuffer = dense_step_bytes(NT), S = dense_buffers(NT);
+// RT: row tiles of a wave, 4, or 3 for 192 rows a workgroup.
+template <int NT, int RT = 4, typename Between>
+__device__ __forceinline__ DenseAt dense_sums(const Dense &D, f32x4 (&acc)[RT][NT], Between between) {
+  constexpr int kRows = 64 * RT, kA = kRows / 16 * 1024, kBuffer = dense_step_bytes(NT, RT), S = dense_buffers(NT, RT);
   constexpr int kCopies = kBuffer / 1024;  // of 1 KB
   constexpr int kMost = (kCopies + 7) / 8, kFull = kCopies % 8 == 0 ? 8 : kCopies % 8;  // waves 0 .. kFull - 1 copy kMost, the others one less
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
@@ -310,8 +334,8 @@ __device__ __forceinline__ DenseAt dense_sums(const Dense &D, f32x4 (&acc)[4][NT
 
   // Copy c of a step (1 KB): the first kA / 1024 are P's. Tiles past the last
   // repeat it (what they feed is not stored).
-  const int atiles = D.ptiles - tm * (kDenseRows / 16), btiles = D.wtiles - tn * 2 * NT;
-  const unsigned char *const pa = reinterpret_cast<const unsigned char *>(D.p) + (int64_t)tm * (kDenseRows / 16) * 1024;
+  const int atiles = D.ptiles - tm * (kRows / 16), btiles = D.wtiles - tn * 2 * NT;
+  const unsigned char *const pa = reinterpret_cast<const unsigned char *>(D.p) + (int64_t)tm * (kRows / 16) * 1024;
   const unsigned char *const pb = reinterpret_cast<const unsigned char *>(D.w) + (int64_t)tn * 2 * NT * 1024;
   const int64_t astride = (int64_t)D.ptiles * 1024, bstride = (int64_t)D.wtiles * 1024;
   // (s counts from `begin`)
@@ -320,7 +344,7 @@ __device__ __forceinline__ DenseAt dense_sums(const Dense &D, f32x4 (&acc)[4][NT
     for (int i = 0; i < kMost; ++i) {
       const int c = wave + 8 * i;
       if (kFull == 8 || i < kMost - 1 || wave < kFull) {
-        const bool is_a = i < kA / 8192;
+        const bool is_a = kA % 8192 == 0 ? i < kA / 8192 : c < kA / 1024;
         const int t = is_a ? c : c - kA / 1024, have = is_a ? atiles : btiles;
         const unsigned char *src = is_a ? pa + (begin + s) * astride : pb + (begin + s) * bstride;
         copy_to_lds(lds0 + buffer + (uint32_t)(c * 1024), (uint32_t)lane * 16, src + (t < have ? t : have - 1) * 1024);
@@ -335,29 +359,29 @@ __device__ __forceinline__ DenseAt dense_sums(const Dense &D, f32x4 (&acc)[4][NT
   };
 
 #pragma unroll
-  for (int a = 0; a < 4; ++a)
+  for (int a = 0; a < RT; ++a)
 #pragma unroll
     for (int b = 0; b < NT; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const DenseAt at{tm * kDenseRows + 64 * wm, tn * 2 * NT + wn * NT, split};
+  const DenseAt at{tm * kRows + 16 * RT * wm, tn * 2 * NT + wn * NT, split};
 #pragma unroll
   for (int b = 0; b < S; ++b)
     if (b < steps) stage(b, b * kBuffer);
   between(at);
   struct Operands {
-    bf16x8 a[4], b[NT];
+    bf16x8 a[RT], b[NT];
   };
   auto read = [&](Operands &O, uint32_t buffer) {
     const unsigned char *const buf = lds + buffer + lane * 16;
 #pragma unroll
     for (int i = 0; i < NT; ++i) O.b[i] = *reinterpret_cast<const bf16x8 *>(buf + kA + (wn * NT + i) * 1024);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) O.a[i] = *reinterpret_cast<const bf16x8 *>(buf + (4 * wm + i) * 1024);
+    for (int i = 0; i < RT; ++i) O.a[i] = *reinterpret_cast<const bf16x8 *>(buf + (RT * wm + i) * 1024);
   };
   auto multiply = [&](const Operands &O) {
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) acc[r][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(O.b[i], O.a[r], acc[r][i], 0, 0, 0);
+      for (int r = 0; r < RT; ++r) acc[r][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(O.b[i], O.a[r], acc[r][i], 0, 0, 0);
   };
   Operands X, Y;
   uint32_t now = 0;  // buffer of step s
@@ -464,7 +488,7 @@ __global__ __launch_bounds__(kDenseThreads) void dense_kernel(Dense D) {
   for (int r = 0; r < 4; ++r) {
     const int row = row0 + 16 * r + j;
     if (row >= D.m) continue;
-    if (D.partials) {
+    if (D.splits > 1) {
       float *const q = D.partials + ((int64_t)split * D.m + row) * (16 * (int64_t)D.wtiles) + tile0 * 16 + 4 * g;
 #pragma unroll
       for (int i = 0; i < NT; ++i)

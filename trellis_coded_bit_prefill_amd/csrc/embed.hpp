@@ -19,29 +19,33 @@ __global__ __launch_bounds__(256) void embed_kernel(const int32_t *__restrict__ 
   const int64_t row = id / per_row;
   const int lane = threadIdx.x & 31, b0 = (int)(id - row * per_row) * 2 * pairs + ((threadIdx.x >> 5) & 1);
   const int b1 = b0 + 2 * pairs < blocks ? b0 + 2 * pairs : blocks;
-  const int token = tokens[row];
+  const int token = __builtin_amdgcn_readfirstlane(tokens[row]);
   uint16_t *const o = out + row * blocks * 256 + 8 * lane;
   if (token >= 0 && token < n) {
     const uint32_t *const w = codes + (int64_t)token * blocks * wpb;
     const float s = bf16_bits_to_f32(scales[token]);
     float q, kq;
     alu_row_constants(s, q, kq);
-    const bool chain = !alu_scale_ok(s);
+    const bool chain = __builtin_amdgcn_readfirstlane(!alu_scale_ok(s)) != 0;
     const int pos = (248 - 8 * lane) * BITS, w0 = pos >> 5, w1 = w0 + 1 == wpb ? 0 : w0 + 1;
-    for (int b = b0; b < b1; b += 2) {
-      const uint32_t *const bw = w + b * wpb;
-      const uint64_t f = (((uint64_t)bw[w1] << 32) | bw[w0]) >> (pos & 31);
-      u32x4 v;
+    auto decode = [&](auto chained) {
+      for (int b = b0; b < b1; b += 2) {
+        const uint32_t *const bw = w + b * wpb;
+        const uint64_t f = (((uint64_t)bw[w1] << 32) | bw[w0]) >> (pos & 31);
+        u32x4 v;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        float e[2];
+        for (int c = 0; c < 4; ++c) {
+          float e[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          e[h] = (float)(__bf16)window_weight((uint32_t)(f >> ((7 - 2 * c - h) * BITS)) & 0xFFFu, s, q, kq, chain) * scale;
-        v[c] = (uint32_t)bf16_of(e[0]) | ((uint32_t)bf16_of(e[1]) << 16);
+          for (int h = 0; h < 2; ++h)
+            e[h] = (float)(__bf16)window_weight((uint32_t)(f >> ((7 - 2 * c - h) * BITS)) & 0xFFFu, s, q, kq, decltype(chained)::value) * scale;
+          v[c] = (uint32_t)bf16_of(e[0]) | ((uint32_t)bf16_of(e[1]) << 16);
+        }
+        *reinterpret_cast<u32x4 *>(o + b * 256) = v;
       }
-      *reinterpret_cast<u32x4 *>(o + b * 256) = v;
-    }
+    };
+    if (chain) decode(std::true_type{});  // (two loops: a choice at every weight costs more than the weight)
+    else decode(std::false_type{});
     return;
   }
   const bool trained = token >= n && token - n < count;
@@ -204,7 +208,11 @@ __global__ __launch_bounds__(1024) void sort_small_kernel(Sort S, uint32_t *__re
     row[i] = at;
     in |= (uint32_t)have << i;
   }
-  for (int shift = 0;; shift += 8) {
+  // As few passes as 8 bits each allow, of as few bits as they need: every bit of
+  // a digit costs six operations a pair.
+  const int all = 32 - __builtin_clz((S.count - 1) | 1), passes = (all + 7) >> 3, bits = (all + passes - 1) / passes;
+  const uint32_t mask = (1u << bits) - 1u;
+  for (int shift = 0;; shift += bits) {
     for (int i = tid; i < 16 * 256; i += 1024) (&M.counts[0][0])[i] = 0;
     __syncthreads();
 #pragma unroll
@@ -213,12 +221,13 @@ __global__ __launch_bounds__(1024) void sort_small_kernel(Sort S, uint32_t *__re
       uint64_t same = __ballot(have);
       int place = 0;
       if (same) {
-        const uint32_t digit = (uint32_t)(key[i] >> shift) & 255u;
+        const uint32_t digit = (uint32_t)(key[i] >> shift) & mask;
 #pragma unroll
-        for (int b = 0; b < 8; ++b) {
-          const uint64_t set = __ballot((digit >> b) & 1u);
-          same &= (digit >> b) & 1u ? set : ~set;
-        }
+        for (int b = 0; b < 8; ++b)
+          if (b < bits) {
+            const uint64_t set = __ballot((digit >> b) & 1u);
+            same &= (digit >> b) & 1u ? set : ~set;
+          }
         const int before = M.counts[wave][digit];
         place = before + (int)__popcll(same & ((1ull << lane) - 1ull));
         __builtin_amdgcn_wave_barrier();
@@ -254,11 +263,11 @@ __global__ __launch_bounds__(1024) void sort_small_kernel(Sort S, uint32_t *__re
       }
     }
     __syncthreads();
-    const bool last = (S.count - 1) >> shift >> 8 == 0;
+    const bool last = shift + bits >= all;
 #pragma unroll
     for (int i = 0; i < kEach; ++i)
       if ((in >> i) & 1) {
-        const int at = M.counts[wave][(key[i] >> shift) & 255] + rank[i];
+        const int at = M.counts[wave][(uint32_t)(key[i] >> shift) & mask] + rank[i];
         M.key[at] = key[i];
         M.row[at] = (uint16_t)row[i];
       }
@@ -301,7 +310,7 @@ __device__ __forceinline__ void store8(uint16_t *p, const float (&v)[8], float s
   u32x4 o;
 #pragma unroll
   for (int e = 0; e < 4; ++e) o[e] = (uint32_t)bf16_of(v[2 * e] * scale) | ((uint32_t)bf16_of(v[2 * e + 1] * scale) << 16);
-  *reinterpret_cast<u32x4 *>(p) = o;
+  __builtin_nontemporal_store(o, reinterpret_cast<u32x4 *>(p));
 }
 // Whether a pair has this key: the wave looks at 64 places at a time.
 __device__ __forceinline__ bool find_pair(const int32_t *keys, int total, int key, int lane) {
@@ -325,7 +334,7 @@ __global__ __launch_bounds__(64) void sum_runs_kernel(Sums S) {
     const int e = (int)blockIdx.x - S.chunks * S.columns;
     if (find_pair(S.key, total, e, lane)) return;
     for (int c = 8 * lane; c < S.k; c += 512)
-      *reinterpret_cast<u32x4 *>(S.dextra + (int64_t)e * S.k + c) = u32x4{0u, 0u, 0u, 0u};
+      __builtin_nontemporal_store(u32x4{0u, 0u, 0u, 0u}, reinterpret_cast<u32x4 *>(S.dextra + (int64_t)e * S.k + c));
     return;
   }
   const int chunk = (int)blockIdx.x / S.columns, column = (int)blockIdx.x - chunk * S.columns;

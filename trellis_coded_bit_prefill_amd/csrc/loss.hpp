@@ -354,11 +354,11 @@ struct Vocabulary {
 // The product's tile in, 2^(l2 - reference) and its sums out. Beside the
 // product's steps (see dense_sums) a tile's end costs 4 operations and one
 // exponential (a quarter of the rate) for each of its sums.
-template <int NT>
+template <int NT, int RT>
 __global__ __launch_bounds__(kDenseThreads) void vocabulary_kernel(Dense D, Vocabulary V) {
   const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
-  f32x4 acc[4][NT];
-  const DenseAt at = dense_sums<NT>(D, acc, [](const DenseAt &) {});
+  f32x4 acc[RT][NT];
+  const DenseAt at = dense_sums<NT, RT>(D, acc, [](const DenseAt &) {});
   const int col0 = (V.first_tile + at.tile0) * 16 + 4 * g;  // this lane's first column
   const int block = V.first_block + at.tile0 / NT;
   const float inf = __builtin_inff();
@@ -367,10 +367,10 @@ __global__ __launch_bounds__(kDenseThreads) void vocabulary_kernel(Dense D, Voca
     for (int i = 0; i < NT; ++i)
       if (col0 + 16 * i >= V.n)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[r][i] = f32x4{-inf, -inf, -inf, -inf};
+        for (int r = 0; r < RT; ++r) acc[r][i] = f32x4{-inf, -inf, -inf, -inf};
   }
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
+  for (int r = 0; r < RT; ++r) {
     const int row = at.row0 + 16 * r + j;
     const bool in = row < D.m;
     const uint32_t sole = (uint32_t)(in ? V.sole[row] : -1) - (uint32_t)col0;
@@ -412,6 +412,23 @@ __global__ __launch_bounds__(kDenseThreads) void vocabulary_kernel(Dense D, Voca
   }
 }
 
+// The second product: float32 sums of every split.
+template <int NT, int RT>
+__global__ __launch_bounds__(kDenseThreads) void vocabulary_back_kernel(Dense D) {
+  const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
+  f32x4 acc[RT][NT];
+  const DenseAt at = dense_sums<NT, RT>(D, acc, [](const DenseAt &) {});
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    const int row = at.row0 + 16 * r + j;
+    if (row >= D.m) continue;
+    float *const q = D.partials + ((int64_t)at.split * D.m + row) * (16 * (int64_t)D.wtiles) + at.tile0 * 16 + 4 * g;
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+      if (at.tile0 + i < D.wtiles) *reinterpret_cast<f32x4 *>(q + 16 * i) = acc[r][i];
+  }
+}
+
 // The only entry of each list, or -1: one wave a row.
 __global__ __launch_bounds__(64) void sole_kernel(Lists L, int32_t *__restrict__ sole) {
   const int64_t row = blockIdx.x;
@@ -436,27 +453,32 @@ __global__ __launch_bounds__(256) void listed_kernel(Lists L, const int32_t *__r
                                                      const uint16_t *__restrict__ scales, int blocks) {
   constexpr int wpb = 8 * BITS;
   const int64_t row = blockIdx.x;
-  const int j = blockIdx.y * 4 + (int)(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int j = blockIdx.y * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   if (j >= L.top || sole[row] >= 0) return;
-  const int at = L.index[row * L.top + j];
+  const int at = __builtin_amdgcn_readfirstlane(L.index[row * L.top + j]);
   if (at < 0 || at >= L.n) return;
   const float s = bf16_bits_to_f32(scales[at]);
   float q, kq;
   alu_row_constants(s, q, kq);
-  const bool chain = !alu_scale_ok(s);
+  const bool chain = __builtin_amdgcn_readfirstlane(!alu_scale_ok(s)) != 0;
   const int pos = (252 - 4 * lane) * BITS, w0 = pos >> 5, w1 = w0 + 1 == wpb ? 0 : w0 + 1, sh = pos & 31;
-  const uint32_t *bw = codes + (int64_t)at * blocks * wpb;
-  const uint16_t *xr = x + row * blocks * 256 + 4 * lane;
+  const uint32_t *const bw = codes + (int64_t)at * blocks * wpb;
+  const uint16_t *const xr = x + row * blocks * 256 + 4 * lane;
   float sum = 0.f;
-  for (int b = 0; b < blocks; ++b, bw += wpb, xr += 256) {
-    const uint32_t f = __builtin_amdgcn_alignbit(bw[w1], bw[w0], sh);
-    const u32x2 v = *reinterpret_cast<const u32x2 *>(xr);
+  auto dot = [&](auto chained) {
+#pragma unroll 4
+    for (int b = 0; b < blocks; ++b) {
+      const uint32_t f = __builtin_amdgcn_alignbit(bw[b * wpb + w1], bw[b * wpb + w0], sh);
+      const u32x2 v = *reinterpret_cast<const u32x2 *>(xr + 256 * b);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const float w = (float)(__bf16)window_weight(__builtin_amdgcn_ubfe(f, (3 - c) * BITS, 12), s, q, kq, chain);
-      sum = __builtin_fmaf(w, bf16_half(v[c >> 1], c & 1), sum);
+      for (int c = 0; c < 4; ++c) {
+        const float w = (float)(__bf16)window_weight(__builtin_amdgcn_ubfe(f, (3 - c) * BITS, 12), s, q, kq, decltype(chained)::value);
+        sum = __builtin_fmaf(w, bf16_half(v[c >> 1], c & 1), sum);
+      }
     }
-  }
+  };
+  if (chain) dot(std::true_type{});
+  else dot(std::false_type{});
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) sum += __shfl_xor(sum, o);
   if (lane == 0) L.listed[row * L.top + j] = sum * L.scale2;
@@ -525,61 +547,105 @@ __global__ __launch_bounds__(256) void loss_gradient_kernel(const float *__restr
   const float f = factor[row];
   f32x4 v = {0.f, 0.f, 0.f, 0.f};
   if (f != 0.f) {
-    for (int s = 0; s < splits; ++s) v += *reinterpret_cast<const f32x4 *>(partials + s * plane + row * columns + c);
+    for (int s0 = 0; s0 < splits; s0 += 4) {
+      f32x4 part[4];
+#pragma unroll
+      for (int s = 0; s < 4; ++s)  // (past the last split: its sums again, not added)
+        part[s] = *reinterpret_cast<const f32x4 *>(partials + (s0 + s < splits ? s0 + s : splits - 1) * plane + row * columns + c);
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        if (s0 + s < splits) v += part[s];
+    }
     v *= f;
   }
   store4(dx + row * width + c, v);
 }
 
 typedef void (*VocabularyFn)(Dense, Vocabulary);
-VocabularyFn vocabulary_fn(int nt) {
-  return nt == 4 ? &vocabulary_kernel<4> : nt == 6 ? &vocabulary_kernel<6> : &vocabulary_kernel<8>;
+VocabularyFn vocabulary_fn(int nt, int rt) {
+  if (rt == 3) return nt == 4 ? &vocabulary_kernel<4, 3> : nt == 6 ? &vocabulary_kernel<6, 3> : &vocabulary_kernel<8, 3>;
+  return nt == 4 ? &vocabulary_kernel<4, 4> : nt == 6 ? &vocabulary_kernel<6, 4> : &vocabulary_kernel<8, 4>;
 }
+template <int RT>
+DenseFn vocabulary_back_of(int nt) {
+  switch (nt) {
+    case 4: return &vocabulary_back_kernel<4, RT>;
+    case 5: return &vocabulary_back_kernel<5, RT>;
+    case 6: return &vocabulary_back_kernel<6, RT>;
+    case 7: return &vocabulary_back_kernel<7, RT>;
+    default: return &vocabulary_back_kernel<8, RT>;
+  }
+}
+DenseFn vocabulary_back_fn(int nt, int rt) { return rt == 3 ? vocabulary_back_of<3>(nt) : vocabulary_back_of<4>(nt); }
 
-// How the dense products of a loss are laid out: the first one's column tile by
-// the costs of dense_shape (one split: a tile's exponentials need its whole sum).
+// How the dense products of a loss are laid out: column tile, row tile and (the
+// second one: a tile's exponentials need its whole sum) split of the contraction
+// whose rounds over the card cost least.
 constexpr int64_t kVocabularyBytes = (int64_t)1 << 31;  // decoded weights of a launch
+struct VocabularyTile {
+  int nt, rt, splits;
+  double us;
+};
+VocabularyTile vocabulary_tile(int64_t m, int64_t tiles, int64_t steps, bool back, int cus) {
+  VocabularyTile best{};
+  for (int rt = 4; rt >= 3; --rt)
+    for (int nt = 8; nt >= 4; nt -= back ? 1 : 2) {
+      const int64_t wg = (m + 64 * rt - 1) / (64 * rt) * ((tiles + 2 * nt - 1) / (2 * nt));
+      for (int splits = 1; splits == 1 || (back && splits <= 8 && splits <= steps / 16); ++splits) {
+        // A last round that leaves workgroups idle costs half of what it leaves:
+        // with all of them at work the card's power holds its clock down.
+        const double rounds = 0.5 * ((double)((wg * splits + cus - 1) / cus) + (double)(wg * splits) / cus);
+        double us = (rounds < 1 ? 1 : rounds) * ((double)steps / splits * (0.02625 * rt * nt + 0.09) + 6);
+        if (splits > 1) us += 0.32e-6 * ((double)splits * m * tiles * 16 * 4);
+        if (best.nt == 0 || us < best.us) best = VocabularyTile{nt, rt, splits, us};
+      }
+    }
+  return best;
+}
 struct LossShape {
   int32_t rows;       // of a chunk: its operands of the second product take at most 1 GiB, or 256 rows
-  int nt, steps, ptiles, blocks;
-  int64_t tiles, slab;
-  DenseShape back;
+  VocabularyTile fwd, back;
+  int steps, back_steps, ptiles, blocks;
+  int64_t tiles, slab, back_tiles, back_slab;  // operand tiles in all and per launch
   size_t operand_bytes, row_bytes, e_bytes, stat_bytes, partial_bytes;
+  double us;
 };
 LossShape loss_shape(trellis_geom g, int32_t m, bool keep, int cus) {
   LossShape s{};
   s.tiles = ((int64_t)g.n + 15) / 16;
   s.steps = (g.k + 63) / 64 * 2;
-  const int64_t n_pad = ((int64_t)g.n + 63) / 64 * 64;
+  s.back_tiles = g.k / 16;
+  s.back_steps = (g.n + 63) / 64 * 2;
+  const int64_t n_pad = (int64_t)s.back_steps * kDenseStep;
   // (statistics: 8 bytes a row and 64 columns at the most, kept below 512 MiB)
   int64_t rows = (keep ? kLogitBytes / (2 * n_pad) : ((int64_t)1 << 29) / (n_pad / 8)) / 256 * 256;
   if (rows < 256) rows = 256;
   if (rows > m) rows = m;
   s.rows = (int32_t)rows;
-  double best = 0;
-  for (int nt = 8; nt >= 4; nt -= 2) {
-    const int64_t wg = (rows + kDenseRows - 1) / kDenseRows * ((s.tiles + 2 * nt - 1) / (2 * nt));
-    const double cost = (double)((wg + cus - 1) / cus) * (s.steps * (0.073 * nt + 0.125) + 3.7);
-    if (s.nt == 0 || cost < best) {
-      best = cost;
-      s.nt = nt;
-    }
-  }
-  s.blocks = (int)((s.tiles + s.nt - 1) / s.nt);
-  const int64_t tile_bytes = (int64_t)s.steps * 1024;
-  s.slab = kVocabularyBytes / tile_bytes / (2 * s.nt) * (2 * s.nt);  // whole workgroup tiles (a tile takes 8 MB at most)
+  s.fwd = vocabulary_tile(rows, s.tiles, s.steps, false, cus);
+  s.blocks = (int)((s.tiles + s.fwd.nt - 1) / s.fwd.nt);
+  const int64_t tile_bytes = (int64_t)s.steps * 1024, back_bytes = (int64_t)s.back_steps * 1024;
   const int forced = g_tiles.load(std::memory_order_relaxed);
-  if (forced > 0) s.slab = ((int64_t)forced + 2 * s.nt - 1) / (2 * s.nt) * (2 * s.nt);
+  // Whole workgroup tiles a launch (a tile takes 8 MB at most).
+  const int unit = 2 * s.fwd.nt;
+  s.slab = forced > 0 ? ((int64_t)forced + unit - 1) / unit * unit : kVocabularyBytes / tile_bytes / unit * unit;
   if (s.slab > s.tiles) s.slab = s.tiles;
   s.operand_bytes = (size_t)(s.slab * tile_bytes);
   s.ptiles = (int)((rows + 15) / 16);
   s.row_bytes = up256((size_t)s.ptiles * tile_bytes);
   s.stat_bytes = up256((size_t)rows * s.blocks * 8);
+  s.us = s.fwd.us;
   if (keep) {
-    s.back = dense_shape(kTransposed, g, (int32_t)rows, 1, cus, kVocabularyBytes);
-    if (s.operand_bytes < s.back.operand_bytes) s.operand_bytes = s.back.operand_bytes;
-    s.e_bytes = up256(s.back.row_bytes);
-    s.partial_bytes = up256((size_t)s.back.splits * rows * s.back.slab * 16 * 4);
+    s.back = vocabulary_tile(rows, s.back_tiles, s.back_steps, true, cus);
+    // Here whole 256-column blocks as well (a tile takes up to 128 MB: one block
+    // at least, whose last workgroup tile may be cut, as may every launch's last).
+    s.back_slab = (forced > 0 ? (int64_t)forced : kVocabularyBytes / back_bytes) / 16 * 16;
+    if (s.back_slab == 0) s.back_slab = 16;
+    if (s.back_slab > s.back_tiles) s.back_slab = s.back_tiles;
+    if (s.operand_bytes < (size_t)(s.back_slab * back_bytes)) s.operand_bytes = (size_t)(s.back_slab * back_bytes);
+    s.e_bytes = up256((size_t)s.ptiles * back_bytes);
+    s.partial_bytes = up256((size_t)s.back.splits * rows * s.back_slab * 16 * 4);
+    s.us += s.back.us;
   }
   s.operand_bytes = up256(s.operand_bytes);
   return s;
@@ -608,17 +674,17 @@ trellis_status loss_dense(const uint16_t *x, int32_t m, const uint32_t *codes, c
   L.listed = reinterpret_cast<float *>(take(list_bytes));
   int32_t *const sole = reinterpret_cast<int32_t *>(take(word_bytes));
   float *const sole_l2 = reinterpret_cast<float *>(take(word_bytes)), *const factor = reinterpret_cast<float *>(take(word_bytes));
-  static bool ready[kMaxDevices][2][9];
-  const VocabularyFn fn = vocabulary_fn(s.nt);
-  const DenseFn back = dx ? dense_fn(kTransposed, s.back.nt) : nullptr;
-  const size_t lds = (size_t)dense_buffers(s.nt) * dense_step_bytes(s.nt),
-               lds_back = dx ? (size_t)dense_buffers(s.back.nt) * dense_step_bytes(s.back.nt) : 0;
+  static bool ready[kMaxDevices][2][2][9];
+  const VocabularyFn fn = vocabulary_fn(s.fwd.nt, s.fwd.rt);
+  const DenseFn back = dx ? vocabulary_back_fn(s.back.nt, s.back.rt) : nullptr;
+  auto lds_of = [](const VocabularyTile &t) { return (size_t)dense_buffers(t.nt, t.rt) * dense_step_bytes(t.nt, t.rt); };
+  const size_t lds = lds_of(s.fwd), lds_back = dx ? lds_of(s.back) : 0;
   auto allow = [&](bool &done, const void *f, size_t bytes) {
     done = done || worked(hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes));
     return done;
   };
-  if (!allow(ready[dev][0][s.nt], reinterpret_cast<const void *>(fn), lds) ||
-      (dx && !allow(ready[dev][1][s.back.nt], reinterpret_cast<const void *>(back), lds_back)))
+  if (!allow(ready[dev][0][s.fwd.rt - 3][s.fwd.nt], reinterpret_cast<const void *>(fn), lds) ||
+      (dx && !allow(ready[dev][1][s.back.rt - 3][s.back.nt], reinterpret_cast<const void *>(back), lds_back)))
     return TRELLIS_E_HIP;
   const Lists all = L;
   (void)hipGetLastError();
@@ -646,32 +712,33 @@ trellis_status loss_dense(const uint16_t *x, int32_t m, const uint32_t *codes, c
     d.steps = s.steps;
     d.splits = 1;
     d.ptiles = ptiles;
-    d.mtiles = (mc + kDenseRows - 1) / kDenseRows;
+    d.mtiles = (mc + 64 * s.fwd.rt - 1) / (64 * s.fwd.rt);
     Vocabulary v{L.top > 1 ? sole : L.index, sole_l2, stats, dx ? e : nullptr, L.scale2, g.n, s.blocks, 0, 0,
-                 dx ? s.back.steps : 0};
+                 dx ? s.back_steps : 0};
     for (int64_t first = 0; first < s.tiles; first += s.slab) {
       d.wtiles = (int)(s.tiles - first < s.slab ? s.tiles - first : s.slab);
-      d.ntiles = (d.wtiles + 2 * s.nt - 1) / (2 * s.nt);
+      d.ntiles = (d.wtiles + 2 * s.fwd.nt - 1) / (2 * s.fwd.nt);
       v.first_tile = (int)first;
-      v.first_block = (int)(first / s.nt);
+      v.first_block = (int)(first / s.fwd.nt);
       const Unpack u{{codes, nullptr}, {scales, nullptr}, operands, g.n, g.k, s.steps, (int)first, d.wtiles, 1};
-      TRELLIS_TRY(launch_unpack_rows(g.bits, u, stream));
+      TRELLIS_TRY(launch_unpack(false, g.bits, u, stream));
       hipLaunchKernelGGL(fn, dim3((unsigned)(d.mtiles * d.ntiles)), dim3(kDenseThreads), lds, stream, d, v);
     }
-    hipLaunchKernelGGL(row_join_kernel, dim3((unsigned)mc), dim3(256), 0, stream, L, v, ptiles, 16 * s.nt, factor);
+    hipLaunchKernelGGL(row_join_kernel, dim3((unsigned)mc), dim3(256), 0, stream, L, v, ptiles, 16 * s.fwd.nt, factor);
     if (hipGetLastError() != hipSuccess) return TRELLIS_E_HIP;
     if (!dx) continue;
     d.p = e;
-    d.steps = s.back.steps;
+    d.steps = s.back_steps;
+    d.mtiles = (mc + 64 * s.back.rt - 1) / (64 * s.back.rt);
     d.splits = s.back.splits;
     d.partials = partials;
     d.width = g.k;
-    for (int64_t first = 0; first < s.back.tiles; first += s.back.slab) {
-      d.wtiles = (int)(s.back.tiles - first < s.back.slab ? s.back.tiles - first : s.back.slab);
+    for (int64_t first = 0; first < s.back_tiles; first += s.back_slab) {
+      d.wtiles = (int)(s.back_tiles - first < s.back_slab ? s.back_tiles - first : s.back_slab);
       d.ntiles = (d.wtiles + 2 * s.back.nt - 1) / (2 * s.back.nt);
       d.first = (int)first * 16;
-      const Unpack u{{codes, nullptr}, {scales, nullptr}, operands, g.n, g.k, s.back.steps, (int)first, d.wtiles, 1};
-      TRELLIS_TRY(launch_unpack_columns(g.bits, u, stream));
+      const Unpack u{{codes, nullptr}, {scales, nullptr}, operands, g.n, g.k, s.back_steps, (int)first, d.wtiles, 1};
+      TRELLIS_TRY(launch_unpack(true, g.bits, u, stream));
       hipLaunchKernelGGL(back, dim3((unsigned)(d.mtiles * d.ntiles * d.splits)), dim3(kDenseThreads), lds_back, stream, d);
       const int columns = 16 * d.wtiles;
       const int64_t threads = (int64_t)mc * (columns / 4);
@@ -683,13 +750,46 @@ trellis_status loss_dense(const uint16_t *x, int32_t m, const uint32_t *codes, c
   return TRELLIS_OK;
 }
 
+// The transposed product of few rows' gradients. Its operands in several
+// launches lose to decoding in the product (256 rows, K = 5120, N = 131072: the
+// whole call 1.51 ms against 1.28).
+Plan loss_back_plan(trellis_geom g, int32_t m, int cus) {
+  Plan p = plan_of(kTransposed, g, m, 1, cus);
+  if (p.dense && p.many.slab < p.many.tiles && p.fused.units < ((int64_t)1 << 30)) {
+    p.dense = false;
+    p.bytes = p.fused.partial_bytes;
+    p.counters = p.fused.tiles;
+  }
+  return p;
+}
+// Whether W is decoded once into operands for a loss (loss_dense), by what both
+// sides are reckoned to take in us: fitted to 34 sizes, 96 to 768 rows of five
+// matrices (N, K: 8192 2048 to 131072 5120), where the side taken is at most 6%
+// slower than the other. Measured, few rows' way against this: K = 5120, N =
+// 131072, losses 445 / 588 at 192 rows, 780 / 785 at 333, 1029 / 875 at 509; with
+// gradient 965 / 1184, 1783 / 1648, 2528 / 1887; K = 2048, N = 8192, losses 34 /
+// 54 at 256 rows, 62 / 54 at 640.
+bool loss_by_operands(trellis_geom g, int32_t m, bool keep, int cus) {
+  const int forced = g_path.load(std::memory_order_relaxed);
+  if (forced >= 0) return forced == 1;
+  const Shape f = shape_of(kForward, g, m, 1, cus);
+  if (f.units >= ((int64_t)1 << 30)) return true;  // (the product kernel counts them in 32 bits)
+  const double mn = 1e-6 * m * (double)g.n, mb = 2e-6 * g.n * (double)g.k;
+  double rows = fused_us(f) + (keep ? 20 + 2.8 * mn : 13 + 1.4 * mn);
+  if (keep) {
+    const Plan b = loss_back_plan(g, m, cus);
+    rows += b.dense ? b.many.us + 6.5 + 0.187 * mb + 0.56 * mn : fused_us(b.fused);
+  }
+  return loss_shape(g, m, keep, cus).us + 14 + (keep ? 0.46 : 0.23) * mb < rows;
+}
+
 // The logits of a chunk of rows in float32, decoded in the product; then the
 // rows' losses; then the transposed product of the logits' gradients.
 trellis_status loss_rows(const uint16_t *x, int32_t m, const uint32_t *codes, const uint16_t *scales, trellis_geom g,
                          Lists L, uint16_t *dx, hipStream_t stream) {
   int dev = 0, cus = 0;
   TRELLIS_TRY(device(dev, cus));
-  if (plan_of(kForward, g, m, 1, cus).dense) return loss_dense(x, m, codes, scales, g, L, dx, stream);
+  if (loss_by_operands(g, m, dx != nullptr, cus)) return loss_dense(x, m, codes, scales, g, L, dx, stream);
   const int64_t most = kLogitBytes / (4 * (int64_t)g.n) / 16 * 16;  // 64 rows at least: n is at most 2^22
   const int32_t rows = m < most ? m : (int32_t)most;
   // Plans of the full chunks and of the last one; the workspace holds either.
@@ -700,7 +800,7 @@ trellis_status loss_rows(const uint16_t *x, int32_t m, const uint32_t *codes, co
   int64_t counters = 0;
   for (int i = 0; i < 2; ++i) {
     fwd[i] = shape_of(kForward, g, counts[i], 1, cus);
-    if (dx) bwd[i] = plan_of(kTransposed, g, counts[i], 1, cus);
+    if (dx) bwd[i] = loss_back_plan(g, counts[i], cus);
     if (parts < fwd[i].partial_bytes) parts = fwd[i].partial_bytes;
     if (parts < bwd[i].bytes) parts = bwd[i].bytes;
     if (counters < fwd[i].tiles) counters = fwd[i].tiles;

@@ -67,7 +67,7 @@ struct Product {
   const uint32_t *codes, *codes2;  // codes2: gated (up), or transposed with two matrices
   const uint16_t *scales, *scales2;
   uint16_t *out, *gate, *up;       // gate, up: gated only, null where they are not kept
-  float *logits;                   // forward: float32 [m, n] in place of out, or null
+  float *logits;                   // logits_kernel: float32 [m, n] in place of out
   float *partials;
   uint32_t *counters;
   int32_t units_q, units_r;  // units (tiles * steps) of a workgroup: units_q, the first units_r one more
@@ -292,8 +292,9 @@ namespace {
 // (40 against 38.7 at 24), four waves per SIMD from four row tiles on (97
 // against 47 at 64: registers spill). Transposed with six row tiles 48 bytes a
 // lane go through scratch memory outside the steps.
-template <int BITS, int KIND, int MT, int NT, int OCC>
-__global__ __launch_bounds__(kThreads, OCC) void product_kernel(Product P) {
+// LOGITS: forward, float32 sums to P.logits, and no adapters.
+template <int BITS, int KIND, int MT, int NT, bool LOGITS>
+__device__ __forceinline__ void product(const Product &P) {
   constexpr bool kT = KIND == kTransposed;
   static_assert(kT ? NT == 4 : KIND == kGated ? NT == 2 : NT <= 2, "tiles per wave");
   constexpr int BM = 16 * MT;
@@ -399,13 +400,8 @@ __global__ __launch_bounds__(kThreads, OCC) void product_kernel(Product P) {
     } else {
       const int width = kT ? P.k : P.n, n = agroup * BN + c;
       if (n >= width) return;
-      if constexpr (KIND == kForward) {
-        if (P.logits) {
-          *reinterpret_cast<f32x4 *>(P.logits + (int64_t)mrow * width + n) = v;
-          return;
-        }
-      }
-      store4(P.out + (int64_t)mrow * width + n, v);
+      if constexpr (LOGITS) *reinterpret_cast<f32x4 *>(P.logits + (int64_t)mrow * width + n) = v;
+      else store4(P.out + (int64_t)mrow * width + n, v);
     }
   };
   f32x4 acc[MT][NT];
@@ -438,7 +434,7 @@ __global__ __launch_bounds__(kThreads, OCC) void product_kernel(Product P) {
           }
         // The adapters' term joins the sums of the wave that holds the tile's
         // last step, half of the row tiles in each wk.
-        if (KIND != kGated && a1 == P.steps && P.low.rank > 0) {
+        if (KIND != kGated && !LOGITS && a1 == P.steps && P.low.rank > 0) {
           // (one row tile: the first wk alone)
           // Transposed: one row tile at a time, as the sums of the second
           // round are still in registers.
@@ -859,6 +855,15 @@ __global__ __launch_bounds__(kThreads, OCC) void product_kernel(Product P) {
       }
     }
   }
+}
+
+template <int BITS, int KIND, int MT, int NT, int OCC>
+__global__ __launch_bounds__(kThreads, OCC) void product_kernel(Product P) {
+  product<BITS, KIND, MT, NT, false>(P);
+}
+template <int BITS, int MT, int NT, int OCC>
+__global__ __launch_bounds__(kThreads, OCC) void logits_kernel(Product P) {
+  product<BITS, kForward, MT, NT, true>(P);
 }
 
 // ---------------------------------------------------------------------------
@@ -1444,7 +1449,18 @@ template <int KIND>
 ProductFn product_of(int bits, int i) {
   return bits == 2 ? product_of<2, KIND>(i) : bits == 3 ? product_of<3, KIND>(i) : product_of<4, KIND>(i);
 }
-ProductFn product_fn(int kind, int bits, int i) {
+template <int BITS>
+ProductFn logits_of(int i) {
+  switch (i) {
+    case 0: return &logits_kernel<BITS, 1, wave_tiles(kForward, 1), waves_per_simd(kForward, 1)>;
+    case 1: return &logits_kernel<BITS, 2, wave_tiles(kForward, 2), waves_per_simd(kForward, 2)>;
+    case 2: return &logits_kernel<BITS, 4, wave_tiles(kForward, 4), waves_per_simd(kForward, 4)>;
+    case 3: return &logits_kernel<BITS, 6, wave_tiles(kForward, 6), waves_per_simd(kForward, 6)>;
+    default: return &logits_kernel<BITS, 8, wave_tiles(kForward, 8), waves_per_simd(kForward, 8)>;
+  }
+}
+ProductFn product_fn(int kind, int bits, int i, bool logits) {
+  if (logits) return bits == 2 ? logits_of<2>(i) : bits == 3 ? logits_of<3>(i) : logits_of<4>(i);
   return kind == kForward ? product_of<kForward>(bits, i) : kind == kGated ? product_of<kGated>(bits, i)
                                                                            : product_of<kTransposed>(bits, i);
 }
@@ -1491,11 +1507,11 @@ Shape shape_of(int kind, trellis_geom g, int32_t m, int matrices, int cus) {
 }
 
 trellis_status launch(const Shape &s, Product p, hipStream_t stream) {
-  const ProductFn fn = product_fn(s.kind, s.bits, s.mt);
-  static bool ready[kMaxDevices][3][3][kMts];
+  const ProductFn fn = product_fn(s.kind, s.bits, s.mt, p.logits != nullptr);
+  static bool ready[kMaxDevices][2][3][3][kMts];
   int dev = 0, cus = 0;
   if (device(dev, cus) != TRELLIS_OK) return TRELLIS_E_HIP;
-  bool &done = ready[dev][s.kind][s.bits - 2][s.mt];
+  bool &done = ready[dev][p.logits != nullptr][s.kind][s.bits - 2][s.mt];
   if (!done) {
     if (!worked(hipFuncSetAttribute(reinterpret_cast<const void *>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, (int)s.lds)))
       return TRELLIS_E_HIP;
@@ -1608,20 +1624,18 @@ struct GatedGrads {
   uint16_t *dgate, *dup;
 };
 
-trellis_status launch_unpack_rows(int bits, const Unpack &u, hipStream_t stream) {
-  const int64_t waves = (int64_t)u.tiles * (u.k >> 8);
-  const dim3 grid((unsigned)((waves + 3) / 4), (unsigned)u.matrices);
-  if (bits == 2) hipLaunchKernelGGL(unpack_rows_kernel<2>, grid, dim3(256), 0, stream, u);
-  else if (bits == 3) hipLaunchKernelGGL(unpack_rows_kernel<3>, grid, dim3(256), 0, stream, u);
-  else hipLaunchKernelGGL(unpack_rows_kernel<4>, grid, dim3(256), 0, stream, u);
-  return hipGetLastError() == hipSuccess ? TRELLIS_OK : TRELLIS_E_HIP;
+typedef void (*UnpackFn)(Unpack);
+template <bool FAR>
+UnpackFn unpack_fn(bool columns, int bits) {
+  if (columns)
+    return bits == 2 ? &unpack_columns_kernel<2, FAR> : bits == 3 ? &unpack_columns_kernel<3, FAR> : &unpack_columns_kernel<4, FAR>;
+  return bits == 2 ? &unpack_rows_kernel<2, FAR> : bits == 3 ? &unpack_rows_kernel<3, FAR> : &unpack_rows_kernel<4, FAR>;
 }
-trellis_status launch_unpack_columns(int bits, const Unpack &u, hipStream_t stream) {
-  const int64_t waves = (int64_t)(u.tiles / 16) * (u.steps / u.matrices);
-  const dim3 grid((unsigned)((waves + 3) / 4), (unsigned)u.matrices);
-  if (bits == 2) hipLaunchKernelGGL(unpack_columns_kernel<2>, grid, dim3(256), 0, stream, u);
-  else if (bits == 3) hipLaunchKernelGGL(unpack_columns_kernel<3>, grid, dim3(256), 0, stream, u);
-  else hipLaunchKernelGGL(unpack_columns_kernel<4>, grid, dim3(256), 0, stream, u);
+trellis_status launch_unpack(bool columns, int bits, const Unpack &u, hipStream_t stream) {
+  const int64_t waves = columns ? (int64_t)(u.tiles / 16) * (u.steps / u.matrices) : (int64_t)u.tiles * (u.k >> 8);
+  const int64_t bytes = (int64_t)u.tiles * (columns ? 1 : u.matrices) * u.steps * 1024;
+  const UnpackFn fn = bytes > kFarBytes ? unpack_fn<true>(columns, bits) : unpack_fn<false>(columns, bits);
+  hipLaunchKernelGGL(fn, dim3((unsigned)((waves + 3) / 4), (unsigned)u.matrices), dim3(256), 0, stream, u);
   return hipGetLastError() == hipSuccess ? TRELLIS_OK : TRELLIS_E_HIP;
 }
 
@@ -1647,7 +1661,7 @@ trellis_status launch_dense(int kind, const DenseShape &s, trellis_geom g, const
   d.m = p.m;
   d.steps = s.steps;
   d.splits = s.splits;
-  d.partials = s.splits > 1 ? reinterpret_cast<float *>(rows + up256(s.row_bytes)) : nullptr;
+  d.partials = reinterpret_cast<float *>(rows + up256(s.row_bytes));
   d.ptiles = s.ptiles;
   d.width = kind == kTransposed ? g.k : g.n;
   d.mtiles = (p.m + kDenseRows - 1) / kDenseRows;
@@ -1670,12 +1684,12 @@ trellis_status launch_dense(int kind, const DenseShape &s, trellis_geom g, const
       u.first = (int)first;
       u.tiles = tiles;
       u.matrices = s.matrices;
-      TRELLIS_TRY(launch_unpack_columns(g.bits, u, stream));
+      TRELLIS_TRY(launch_unpack(true, g.bits, u, stream));
     } else {
       u.matrices = kind == kGated ? 2 : 1;
       u.first = (int)(first / u.matrices);
       u.tiles = tiles / u.matrices;
-      TRELLIS_TRY(launch_unpack_rows(g.bits, u, stream));
+      TRELLIS_TRY(launch_unpack(false, g.bits, u, stream));
     }
     d.first = (int)(first * 16 / (kind == kGated ? 2 : 1));
     d.wtiles = tiles;
