@@ -181,18 +181,26 @@ def _raise(status: int):
     raise TrellisValueError(status, msg)
 
 
+_current_device = _raw_stream = None
+
+
 def _stream_handle(device) -> int:
     """The current stream of `device`, which must be the current device (the
     library works on the current device)."""
-    import torch
+    global _current_device, _raw_stream
+    if _current_device is None:
+        import torch
 
-    if device.index is not None and device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {device} but the current device is cuda:{torch.cuda.current_device()}")
-    # The handle alone, where torch offers it: the Stream object around it costs 2 us.
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if raw is not None and device.index is not None:
-        return raw(device.index)
-    return torch.cuda.current_stream(device).cuda_stream
+        _current_device = torch.cuda.current_device
+        # The handle alone, where torch offers it: the Stream object around it costs 2 us.
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
+    current, index = _current_device(), device.index
+    if index is None:
+        index = current
+    if index != current:
+        raise ValueError(f"tensors are on {device} but the current device is cuda:{current}")
+    return _raw_stream(index)
 
 
 def _check_tensor(name, t, dtypes, ndim, device=None):
@@ -495,8 +503,11 @@ def _address(name, t, dtypes, shape, device) -> int:
 
 def _rows_of(name, t):
     """Shape and device of the tensor that the others are checked against: bf16 [rows, columns]."""
-    _check_tensor(name, t, _kinds()[1], 2)
-    return (*t.shape, t.device)
+    tensor, bf = _kinds()[:2]
+    if not (isinstance(t, tensor) and t.dtype in bf and t.ndim == 2 and t.is_cuda and t.is_contiguous()):
+        _check_tensor(name, t, bf, 2)
+    rows, columns = t.shape
+    return rows, columns, t.device
 
 
 def _output(name, t, shape, device):
@@ -657,17 +668,37 @@ def gated_backward(dh, gate, up, codes_gate, scales_gate, codes_up, scales_up, b
     return dx, dgate, dup
 
 
-def _loss(what, raw, x, codes, scales, bits, lists, keep):
-    """The common part of the losses: lists are the addresses and numbers that stand between g and the outputs."""
-    import torch
+_geoms = {}
 
-    m, k, device = _rows_of("x", x)
-    n = codes.shape[0]
-    packed = _packed_address(codes, scales, n, k, bits, device)
-    loss = torch.empty(m, dtype=torch.float32, device=device)
-    lse = torch.empty(m, dtype=torch.float32, device=device)
-    dx = torch.empty((m, k), dtype=torch.bfloat16, device=device) if keep else None
-    raw(x.data_ptr(), m, *packed, geom(n, k, bits), *lists, loss.data_ptr(), lse.data_ptr(),
+
+def _geom_of(n: int, k: int, bits: int) -> Geom:
+    """geom(n, k, bits), built once: the structure costs as much as its checks."""
+    g = _geoms.get((n, k, bits))
+    if g is None:
+        if len(_geoms) >= 256:
+            _geoms.clear()
+        g = _geoms[n, k, bits] = geom(n, k, bits)
+    return g
+
+
+def _new(shape, dtype, device):
+    """A new tensor; torch looked up once."""
+    global _empty, _f32, _bf16
+    if _empty is None:
+        import torch
+
+        _empty, _f32, _bf16 = torch.empty, torch.float32, torch.bfloat16
+    return _empty(shape, dtype=_f32 if dtype == "f32" else _bf16, device=device)
+
+
+_empty = _f32 = _bf16 = None
+
+
+def _loss(raw, x, m: int, k: int, device, packed, n: int, bits: int, lists, keep):
+    """The common part of the losses: lists are the addresses and numbers that stand between g and the outputs."""
+    loss, lse = _new((m,), "f32", device), _new((m,), "f32", device)
+    dx = _new((m, k), "bf16", device) if keep else None
+    raw(x.data_ptr(), m, *packed, _geom_of(n, k, bits), *lists, loss.data_ptr(), lse.data_ptr(),
         dx.data_ptr() if keep else 0, _stream_handle(device))
     return (loss, lse, dx) if keep else (loss, lse)
 
@@ -684,17 +715,18 @@ def cross_entropy(x, codes, scales, bits: int, target, keep: bool = False):
     loss_backward() multiplies dx by the rows' gradients.
 
     Where x requires a gradient, autograd records the call, which then computes
-    dx as well (half as much work again and more) and keeps it for the backward
-    pass. lse and a returned dx carry no gradient."""
-    m, _, device = _rows_of("x", x)
-    _packed_rows(codes)
+    dx as well (as much work again and more) and keeps it for the backward pass.
+    lse and a returned dx carry no gradient."""
+    m, k, device = _rows_of("x", x)
+    n = _packed_rows(codes)
+    packed = _packed_address(codes, scales, n, k, bits, device)
     target_ptr = _address("target", target, _kinds()[4], (m,), device)
     if ((x.requires_grad or scales.requires_grad or _forward_ad._current_level >= 0)
             and _recorded("cross_entropy", (x,), {"scales": scales}, None)):
         from ._autograd import CrossEntropy
 
         return CrossEntropy.apply(x, codes, scales, bits, target, keep)
-    return _loss("cross_entropy", cross_entropy_raw, x, codes, scales, bits, (target_ptr,), keep)
+    return _loss(cross_entropy_raw, x, m, k, device, packed, n, bits, (target_ptr,), keep)
 
 
 def distill(x, codes, scales, bits: int, index, logits, temperature: float = 1.0, keep: bool = False):
@@ -707,12 +739,13 @@ def distill(x, codes, scales, bits: int, index, logits, temperature: float = 1.0
         dx[r]   = the gradient of loss[r] with respect to x[r]
 
     (loss, lse), with keep (loss, lse, dx). index [M, top] in int32 and logits
-    [M, top] in float32, top from 1 to MAX_TOP. An entry whose index is not in
-    [0, N) or whose logit is -inf is none; a row without entries has loss and dx
-    0. Recorded by autograd as cross_entropy() is; index and logits get no
-    gradient."""
-    m, _, device = _rows_of("x", x)
-    _packed_rows(codes)
+    [M, top] in float32, top from 1 to MAX_TOP, T from MIN_TEMPERATURE to
+    MAX_TEMPERATURE. An entry whose index is not in [0, N) or whose logit is -inf
+    is none; a row without entries has loss and dx 0. Recorded by autograd as
+    cross_entropy() is; index and logits get no gradient."""
+    m, k, device = _rows_of("x", x)
+    n = _packed_rows(codes)
+    packed = _packed_address(codes, scales, n, k, bits, device)
     tensor, _, _, f32, i32 = _kinds()
     if not isinstance(index, tensor) or index.ndim != 2:
         raise TypeError("index must be a torch.Tensor of two dims")
@@ -724,7 +757,7 @@ def distill(x, codes, scales, bits: int, index, logits, temperature: float = 1.0
         from ._autograd import Distill
 
         return Distill.apply(x, codes, scales, bits, index, logits, temperature, keep)
-    return _loss("distill", distill_raw, x, codes, scales, bits, lists, keep)
+    return _loss(distill_raw, x, m, k, device, packed, n, bits, lists, keep)
 
 
 def loss_backward(dloss, dx, out=None):
@@ -765,8 +798,11 @@ def embed(tokens, codes, scales, k: int, bits: int, scale: float = 1.0, extra=No
         from ._autograd import Embed
 
         return Embed.apply(tokens, codes, scales, k, bits, scale, extra)
-    out = _output("out", out, (m, k), device)
-    embed_raw(tokens_ptr, m, *packed, geom(n, k, bits), scale, extra_ptr if count else 0, count, out.data_ptr(),
+    if out is None:
+        out = _new((m, k), "bf16", device)
+    else:
+        _address("out", out, _kinds()[1], (m, k), device)
+    embed_raw(tokens_ptr, m, *packed, _geom_of(n, k, bits), scale, extra_ptr if count else 0, count, out.data_ptr(),
               _stream_handle(device))
     return out
 
