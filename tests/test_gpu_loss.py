@@ -20,9 +20,11 @@ def need_gpu():
     tp.load_library()
 
 
-@pytest.fixture(params=[None, False, True], ids=["auto", "decode", "once"])
+@pytest.fixture(params=[(None, 0), (False, 0), (True, 0), (True, 4096)], ids=["auto", "few", "many", "operands"])
 def path(request):
-    tp.force_path(request.param)
+    """The library's choice, decoding in the few rows' products, the many rows' products (the first one decoding on
+    its way where that is reckoned to pay), and those with all weights decoded beforehand."""
+    tp.force_path(*request.param)
     yield request.param
     tp.force_path(None)
 

@@ -355,10 +355,8 @@ struct Vocabulary {
 // product's steps (see dense_sums) a tile's end costs 4 operations and one
 // exponential (a quarter of the rate) for each of its sums.
 template <int NT, int RT>
-__global__ __launch_bounds__(kDenseThreads) void vocabulary_kernel(Dense D, Vocabulary V) {
+__device__ __forceinline__ void vocabulary_out(const Dense &D, const Vocabulary &V, const DenseAt &at, f32x4 (&acc)[RT][NT]) {
   const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
-  f32x4 acc[RT][NT];
-  const DenseAt at = dense_sums<NT, RT>(D, acc, [](const DenseAt &) {});
   const int col0 = (V.first_tile + at.tile0) * 16 + 4 * g;  // this lane's first column
   const int block = V.first_block + at.tile0 / NT;
   const float inf = __builtin_inff();
@@ -410,6 +408,175 @@ __global__ __launch_bounds__(kDenseThreads) void vocabulary_kernel(Dense D, Voca
     sum += __shfl_xor(sum, 32);
     if (g == 0 && in && block < V.blocks) V.stats[(int64_t)row * V.blocks + block] = f32x2{ref, sum};
   }
+}
+template <int NT, int RT>
+__global__ __launch_bounds__(kDenseThreads) void vocabulary_kernel(Dense D, Vocabulary V) {
+  f32x4 acc[RT][NT];
+  const DenseAt at = dense_sums<NT, RT>(D, acc, [](const DenseAt &) {});
+  vocabulary_out<NT, RT>(D, V, at, acc);
+}
+
+// The same with W decoded on the way: few hundred rows, which one or two tiles
+// hold (64 RT rows by 128 columns a workgroup, 8 waves, 4 by rows x 2 by columns).
+// P's operands reach LDS as in dense_sums, S steps ahead; a 256-weight block's
+// code words too, a block ahead, and in every step each wave decodes 16 columns
+// of the step after next into one of two LDS tiles. Everything that comes from
+// memory is a copy to LDS, so that the waits are the kernel's own: a copy is
+// waited for by the number of P's copies issued after it, which the words'
+// copies between them only make stricter.
+// Bound by the LDS and the decode side by side: a step of 384 rows and 128
+// columns takes 768 clocks of MFMA, 640 of LDS reads and 256 of writes, and 450
+// of the decode's VALU work.
+struct Packed {
+  const uint32_t *codes;
+  const uint16_t *scales;
+  int32_t k;
+};
+constexpr int kDecodeColumns = 128;
+constexpr int decode_lds_fixed(int bits) { return 2 * 8192 + 2 * 4096 * bits; }  // decoded tiles, code words
+constexpr int decode_buffers(int bits, int rt) {
+  return (160 * 1024 - decode_lds_fixed(bits)) / (4096 * rt) < 6 ? (160 * 1024 - decode_lds_fixed(bits)) / (4096 * rt) : 6;
+}
+constexpr int decode_lds(int bits, int rt) { return decode_buffers(bits, rt) * 4096 * rt + decode_lds_fixed(bits); }
+// Where a row's 16-byte piece c of a block's words lies in LDS: rows lie 128, 96
+// or 64 bytes apart, which without this would put 16 or 4 of them in one bank.
+template <int BITS>
+__device__ __forceinline__ int code_piece(int row, int c) {
+  return BITS == 4 ? c ^ (row & 7) : BITS == 2 ? c ^ ((row >> 2) & 3) : c;
+}
+template <int BITS, int RT>
+__global__ __launch_bounds__(kDenseThreads) void vocabulary_decode_kernel(Dense D, Vocabulary V, Packed C) {
+  constexpr int NT = 4, kRows = 64 * RT, kA = kRows / 16 * 1024, S = decode_buffers(BITS, RT), kMost = RT / 2;
+  constexpr int wpb = 8 * BITS, kCode = 4096 * BITS, kPieces = 2 * BITS;  // words of a row's block; bytes of 128; pieces
+  static_assert(RT % 2 == 0 && S >= 3 && S <= 8, "every wave copies as many tiles; words are a block ahead");
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
+  constexpr uint32_t kB = S * kA, kC = kB + 2 * 8192;
+  const int tid = threadIdx.x, lane = tid & 63, j = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave & 3, wn = wave >> 2;
+  const int total = D.mtiles * D.ntiles, each = total >> 3, rest = total & 7;
+  const int xcd = blockIdx.x & 7, seq = blockIdx.x >> 3;
+  const int id = xcd * each + (xcd < rest ? xcd : rest) + seq;
+  const int tn = id / D.mtiles, tm = id - tn * D.mtiles;
+  const int steps = D.steps, blocks = steps >> 3;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char *)lds;
+  const int atiles = D.ptiles - tm * (kRows / 16);
+  const unsigned char *const pa = reinterpret_cast<const unsigned char *>(D.p) + (int64_t)tm * (kRows / 16) * 1024;
+  const int64_t astride = (int64_t)D.ptiles * 1024;
+  auto stage = [&](int s, uint32_t buffer) {
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+      const int t = wave + 8 * i;  // (tiles past the last repeat it)
+      copy_to_lds(lds0 + buffer + (uint32_t)(t * 1024), (uint32_t)lane * 16, pa + s * astride + (t < atiles ? t : atiles - 1) * 1024);
+    }
+  };
+  // code words: copy c takes pieces 64 c .. +63 of the 128 rows' block
+  const int n0 = tn * kDecodeColumns;
+  const uint32_t row_bytes = (uint32_t)(C.k >> 8) * wpb * 4;
+  const unsigned char *const pc = reinterpret_cast<const unsigned char *>(C.codes) + (int64_t)n0 * row_bytes;
+  uint32_t from[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int q = (wave + 8 * i) * 64 + lane, row = q / kPieces, c = code_piece<BITS>(row, q % kPieces);
+    from[i] = (uint32_t)(n0 + row < V.n ? row : V.n - 1 - n0) * row_bytes + 16u * (uint32_t)c;
+  }
+  auto words = [&](int b) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (wave + 8 * i < kCode / 1024)
+        copy_to_lds(lds0 + kC + (uint32_t)((b & 1) * kCode + (wave + 8 * i) * 1024), from[i], pc + (int64_t)b * (wpb * 4));
+  };
+  // this lane's row of W in the tile that its wave decodes
+  const int row = 16 * wave + j, n = n0 + row < V.n ? n0 + row : V.n - 1;
+  const float sc = bf16_bits_to_f32(C.scales[n]);
+  float q, kq;
+  alu_row_constants(sc, q, kq);
+  const bool chain = !__all(alu_scale_ok(sc));
+  const int base = (248 - 8 * g) * BITS, w0 = base >> 5, off = base & 31;
+  // The stream bits of a lane's eight weights of step s, and their weights into
+  // the step's tile. (Past the last step: bits and a tile that nobody uses.)
+  auto bits = [&](int s) {
+    const unsigned char *const mine = lds + kC + ((s >> 3) & 1) * kCode + row * (wpb * 4);
+    const int w = w0 - (s & 7) * BITS, next = w + 1 == wpb ? 0 : w + 1;
+    const uint32_t lo = *reinterpret_cast<const uint32_t *>(mine + code_piece<BITS>(row, w >> 2) * 16 + (w & 3) * 4);
+    const uint32_t hi = *reinterpret_cast<const uint32_t *>(mine + code_piece<BITS>(row, next >> 2) * 16 + (next & 3) * 4);
+    return (((uint64_t)hi << 32) | lo) >> off;
+  };
+  auto decode = [&](int s, uint64_t f, auto chained) {
+    bf16x8 v;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      v[e] = (__bf16)window_weight((uint32_t)(f >> ((7 - e) * BITS)) & 0xFFFu, sc, q, kq, decltype(chained)::value);
+    *reinterpret_cast<bf16x8 *>(lds + kB + (s & 1) * 8192 + wave * 1024 + lane * 16) = v;
+  };
+  f32x4 acc[RT][NT];
+#pragma unroll
+  for (int a = 0; a < RT; ++a)
+#pragma unroll
+    for (int b = 0; b < NT; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+  words(0);
+  if (blocks > 1) words(1);
+#pragma unroll
+  for (int b = 0; b < S; ++b)
+    if (b < steps) stage(b, b * kA);
+  step_barrier<0>();
+  if (chain) {
+    decode(0, bits(0), std::true_type{});
+    decode(1, bits(1), std::true_type{});
+  } else {
+    decode(0, bits(0), std::false_type{});
+    decode(1, bits(1), std::false_type{});
+  }
+  lds_barrier();
+  struct Operands {
+    bf16x8 a[RT], b[NT];
+  };
+  auto read = [&](Operands &O, uint32_t buffer, int s) {
+    const unsigned char *const bb = lds + kB + (s & 1) * 8192 + lane * 16, *const ba = lds + buffer + lane * 16;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) O.b[i] = *reinterpret_cast<const bf16x8 *>(bb + (wn * NT + i) * 1024);
+#pragma unroll
+    for (int i = 0; i < RT; ++i) O.a[i] = *reinterpret_cast<const bf16x8 *>(ba + (RT * wm + i) * 1024);
+  };
+  Operands X, Y;
+  uint32_t now = 0;
+  read(X, 0, 0);
+  uint64_t f = bits(2);
+  // Step s: the barrier says that step s + 1 of P has landed, that its decoded
+  // tile is written and that step s has been read.
+  auto step = [&](int s, const Operands &A, Operands &B, auto chained) {
+    if (s + S - 1 < steps) step_barrier<(S - 2) * kMost>();
+    else step_barrier<0>();
+    if ((s & 7) == 6 && (s >> 3) + 2 < blocks) words((s >> 3) + 2);  // (its place was last read in step s - 2)
+    if (s + S < steps) stage(s + S, now);
+    now = now == (S - 1) * kA ? 0 : now + kA;
+    read(B, now, s + 1);  // (past the last step: old operands, not used)
+    const uint64_t next = bits(s + 3);
+    decode(s + 2, f, chained);
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int r = 0; r < RT; ++r) acc[r][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A.b[i], A.a[r], acc[r][i], 0, 0, 0);
+    f = next;
+    // The reads and the decode go between the matrix instructions.
+#pragma unroll
+    for (int i = 0; i < NT * RT; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      if (i < RT + NT + 2) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
+  };
+  auto loop = [&](auto chained) {
+    for (int s = 0; s < steps; s += 2) {
+      step(s, X, Y, chained);
+      step(s + 1, Y, X, chained);
+    }
+  };
+  if (chain) loop(std::true_type{});
+  else loop(std::false_type{});
+  const DenseAt at{tm * kRows + 16 * RT * wm, tn * 2 * NT + wn * NT, 0};
+  vocabulary_out<NT, RT>(D, V, at, acc);
 }
 
 // The second product: float32 sums of every split.
@@ -566,6 +733,14 @@ VocabularyFn vocabulary_fn(int nt, int rt) {
   if (rt == 3) return nt == 4 ? &vocabulary_kernel<4, 3> : nt == 6 ? &vocabulary_kernel<6, 3> : &vocabulary_kernel<8, 3>;
   return nt == 4 ? &vocabulary_kernel<4, 4> : nt == 6 ? &vocabulary_kernel<6, 4> : &vocabulary_kernel<8, 4>;
 }
+typedef void (*VocabularyDecodeFn)(Dense, Vocabulary, Packed);
+template <int BITS>
+VocabularyDecodeFn vocabulary_decode_of(int rt) {
+  return rt == 4 ? &vocabulary_decode_kernel<BITS, 4> : &vocabulary_decode_kernel<BITS, 6>;
+}
+VocabularyDecodeFn vocabulary_decode_fn(int bits, int rt) {
+  return bits == 2 ? vocabulary_decode_of<2>(rt) : bits == 3 ? vocabulary_decode_of<3>(rt) : vocabulary_decode_of<4>(rt);
+}
 template <int RT>
 DenseFn vocabulary_back_of(int nt) {
   switch (nt) {
@@ -584,7 +759,8 @@ DenseFn vocabulary_back_fn(int nt, int rt) { return rt == 3 ? vocabulary_back_of
 constexpr int64_t kVocabularyBytes = (int64_t)1 << 31;  // decoded weights of a launch
 struct VocabularyTile {
   int nt, rt, splits;
-  double us;
+  bool decode;  // vocabulary_decode_kernel
+  double us;    // with unpacking
 };
 VocabularyTile vocabulary_tile(int64_t m, int64_t tiles, int64_t steps, bool back, int cus) {
   VocabularyTile best{};
@@ -595,11 +771,24 @@ VocabularyTile vocabulary_tile(int64_t m, int64_t tiles, int64_t steps, bool bac
         // A last round that leaves workgroups idle costs half of what it leaves:
         // with all of them at work the card's power holds its clock down.
         const double rounds = 0.5 * ((double)((wg * splits + cus - 1) / cus) + (double)(wg * splits) / cus);
-        double us = (rounds < 1 ? 1 : rounds) * ((double)steps / splits * (0.02625 * rt * nt + 0.09) + 6);
+        double us = (rounds < 1 ? 1 : rounds) * ((double)steps / splits * (0.0203 * rt * nt + 0.206) + 6);
         if (splits > 1) us += 0.32e-6 * ((double)splits * m * tiles * 16 * 4);
-        if (best.nt == 0 || us < best.us) best = VocabularyTile{nt, rt, splits, us};
+        if (best.nt == 0 || us < best.us) best = VocabularyTile{nt, rt, splits, false, us};
       }
     }
+  return best;
+}
+// The first product's tile, or that of the kernel which decodes on its way.
+VocabularyTile vocabulary_first(trellis_geom g, int64_t m, int64_t tiles, int64_t steps, int cus) {
+  VocabularyTile best = vocabulary_tile(m, tiles, steps, false, cus);
+  best.us += 4 + 0.43e-6 * g.n * (double)g.k;
+  if (g_tiles.load(std::memory_order_relaxed) > 0) return best;  // (launches of so many tiles: there are none here)
+  for (int rt = 4; rt <= 6; rt += 2) {
+    const int64_t wg = (m + 64 * rt - 1) / (64 * rt) * ((tiles + 7) / 8);
+    const double rounds = 0.5 * ((double)((wg + cus - 1) / cus) + (double)wg / cus);
+    const double us = (rounds < 1 ? 1 : rounds) * (steps * (0.09 * rt + 0.23) + 6);
+    if (us < best.us) best = VocabularyTile{4, rt, 1, true, us};
+  }
   return best;
 }
 struct LossShape {
@@ -622,15 +811,15 @@ LossShape loss_shape(trellis_geom g, int32_t m, bool keep, int cus) {
   if (rows < 256) rows = 256;
   if (rows > m) rows = m;
   s.rows = (int32_t)rows;
-  s.fwd = vocabulary_tile(rows, s.tiles, s.steps, false, cus);
+  s.fwd = vocabulary_first(g, rows, s.tiles, s.steps, cus);
   s.blocks = (int)((s.tiles + s.fwd.nt - 1) / s.fwd.nt);
   const int64_t tile_bytes = (int64_t)s.steps * 1024, back_bytes = (int64_t)s.back_steps * 1024;
   const int forced = g_tiles.load(std::memory_order_relaxed);
   // Whole workgroup tiles a launch (a tile takes 8 MB at most).
   const int unit = 2 * s.fwd.nt;
   s.slab = forced > 0 ? ((int64_t)forced + unit - 1) / unit * unit : kVocabularyBytes / tile_bytes / unit * unit;
-  if (s.slab > s.tiles) s.slab = s.tiles;
-  s.operand_bytes = (size_t)(s.slab * tile_bytes);
+  if (s.slab > s.tiles || s.fwd.decode) s.slab = s.tiles;
+  s.operand_bytes = s.fwd.decode ? 0 : (size_t)(s.slab * tile_bytes);
   s.ptiles = (int)((rows + 15) / 16);
   s.row_bytes = up256((size_t)s.ptiles * tile_bytes);
   s.stat_bytes = up256((size_t)rows * s.blocks * 8);
@@ -645,7 +834,7 @@ LossShape loss_shape(trellis_geom g, int32_t m, bool keep, int cus) {
     if (s.operand_bytes < (size_t)(s.back_slab * back_bytes)) s.operand_bytes = (size_t)(s.back_slab * back_bytes);
     s.e_bytes = up256((size_t)s.ptiles * back_bytes);
     s.partial_bytes = up256((size_t)s.back.splits * rows * s.back_slab * 16 * 4);
-    s.us += s.back.us;
+    s.us += s.back.us + 4 + 0.46e-6 * g.n * (double)g.k;
   }
   s.operand_bytes = up256(s.operand_bytes);
   return s;
@@ -674,16 +863,18 @@ trellis_status loss_dense(const uint16_t *x, int32_t m, const uint32_t *codes, c
   L.listed = reinterpret_cast<float *>(take(list_bytes));
   int32_t *const sole = reinterpret_cast<int32_t *>(take(word_bytes));
   float *const sole_l2 = reinterpret_cast<float *>(take(word_bytes)), *const factor = reinterpret_cast<float *>(take(word_bytes));
-  static bool ready[kMaxDevices][2][2][9];
-  const VocabularyFn fn = vocabulary_fn(s.fwd.nt, s.fwd.rt);
+  static bool ready[kMaxDevices][2][2][9], decode_ready[kMaxDevices][3][7];
+  const VocabularyFn fn = s.fwd.decode ? nullptr : vocabulary_fn(s.fwd.nt, s.fwd.rt);
+  const VocabularyDecodeFn decode_fn = s.fwd.decode ? vocabulary_decode_fn(g.bits, s.fwd.rt) : nullptr;
   const DenseFn back = dx ? vocabulary_back_fn(s.back.nt, s.back.rt) : nullptr;
   auto lds_of = [](const VocabularyTile &t) { return (size_t)dense_buffers(t.nt, t.rt) * dense_step_bytes(t.nt, t.rt); };
-  const size_t lds = lds_of(s.fwd), lds_back = dx ? lds_of(s.back) : 0;
+  const size_t lds = s.fwd.decode ? (size_t)decode_lds(g.bits, s.fwd.rt) : lds_of(s.fwd), lds_back = dx ? lds_of(s.back) : 0;
   auto allow = [&](bool &done, const void *f, size_t bytes) {
     done = done || worked(hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes));
     return done;
   };
-  if (!allow(ready[dev][0][s.fwd.rt - 3][s.fwd.nt], reinterpret_cast<const void *>(fn), lds) ||
+  if (!(s.fwd.decode ? allow(decode_ready[dev][g.bits - 2][s.fwd.rt], reinterpret_cast<const void *>(decode_fn), lds)
+                     : allow(ready[dev][0][s.fwd.rt - 3][s.fwd.nt], reinterpret_cast<const void *>(fn), lds)) ||
       (dx && !allow(ready[dev][1][s.back.rt - 3][s.back.nt], reinterpret_cast<const void *>(back), lds_back)))
     return TRELLIS_E_HIP;
   const Lists all = L;
@@ -720,6 +911,11 @@ trellis_status loss_dense(const uint16_t *x, int32_t m, const uint32_t *codes, c
       d.ntiles = (d.wtiles + 2 * s.fwd.nt - 1) / (2 * s.fwd.nt);
       v.first_tile = (int)first;
       v.first_block = (int)(first / s.fwd.nt);
+      if (s.fwd.decode) {  // (one launch)
+        hipLaunchKernelGGL(decode_fn, dim3((unsigned)(d.mtiles * d.ntiles)), dim3(kDenseThreads), lds, stream, d, v,
+                           Packed{codes, scales, g.k});
+        continue;
+      }
       const Unpack u{{codes, nullptr}, {scales, nullptr}, operands, g.n, g.k, s.steps, (int)first, d.wtiles, 1};
       TRELLIS_TRY(launch_unpack(false, g.bits, u, stream));
       hipLaunchKernelGGL(fn, dim3((unsigned)(d.mtiles * d.ntiles)), dim3(kDenseThreads), lds, stream, d, v);
@@ -780,7 +976,7 @@ bool loss_by_operands(trellis_geom g, int32_t m, bool keep, int cus) {
     const Plan b = loss_back_plan(g, m, cus);
     rows += b.dense ? b.many.us + 6.5 + 0.187 * mb + 0.56 * mn : fused_us(b.fused);
   }
-  return loss_shape(g, m, keep, cus).us + 14 + (keep ? 0.46 : 0.23) * mb < rows;
+  return loss_shape(g, m, keep, cus).us + 10 < rows;
 }
 
 // The logits of a chunk of rows in float32, decoded in the product; then the
