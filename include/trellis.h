@@ -314,8 +314,16 @@ trellis_status trellis_gated_backward(const uint16_t *dh_bf16, const uint16_t *g
  * accepted geometries, execution, errors and workspaces are those of the
  * fine-tuned layers above (1 <= m <= TRELLIS_MAX_ROWS).
  *
- * The losses never keep the logits: they live in the stream's workspace, in
- * pieces of at most 1 GiB. Sums and softmax statistics are float32. */
+ * The losses never keep the logits. Sums and softmax statistics are float32, and
+ * results do not depend on timing. Their workspace holds, for a chunk of rows at a
+ * time (256 rows at least),
+ *   - for few rows the float32 logits (at most 1 GiB), with dx their bf16 gradients
+ *     (half as much) and what the product of these with W takes (see above);
+ *   - else the decoded weights of a launch (at most 2 GiB, but 512 bytes a row of W
+ *     at least), a copy of x (at most 1 GiB), statistics (at most 512 MiB), and with
+ *     dx the exponentials in bf16 (at most 1 GiB) and its float32 sums, 4 bytes per
+ *     column, row and split (at most eight).
+ * 256 rows of 2^22 entries take twice these 1 GiB. */
 
 /* Softmax cross entropy of the logits l = W x[r] against one entry a row:
  *   lse[r] = log sum_v exp(l_v),  loss[r] = lse[r] - l[target[r]],
@@ -378,8 +386,9 @@ trellis_status trellis_embed(const int32_t *tokens, int32_t m, const uint32_t *c
  * alone; all of dextra bf16 [count, k] is written (a token that no row has
  * gets zeros). k a multiple of 256 up to TRELLIS_MAX_K, 1 <= count <=
  * TRELLIS_MAX_TRAINED, 0 <= first <= TRELLIS_MAX_N; dout and dextra 16-byte
- * aligned. The workspace takes 16 bytes a row, and 4 bytes for each of 256
- * digits and 2048 rows, and at most 1024 * 2 float32 rows of partial sums. */
+ * aligned. Where a token has many rows its sum is taken in parts of 16 rows at
+ * least. The workspace takes 16.5 bytes a row of dout and at most 2048 float32
+ * rows of partial sums. */
 trellis_status trellis_embed_backward(const uint16_t *dout_bf16, const int32_t *tokens, int32_t m, int32_t k,
                                       int32_t first, int32_t count, float scale, uint16_t *dextra_bf16,
                                       void *hip_stream);

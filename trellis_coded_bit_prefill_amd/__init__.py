@@ -780,13 +780,14 @@ def embed(tokens, codes, scales, k: int, bits: int, scale: float = 1.0, extra=No
 
     Where extra requires a gradient, autograd records the call and takes the
     gradient from embed_backward(); scales get none."""
-    if not isinstance(tokens, _kinds()[0]) or tokens.ndim != 1:
-        raise TypeError("tokens must be a torch.Tensor of one dim")
+    tensor, _, _, _, i32 = _kinds()
+    if not (isinstance(tokens, tensor) and tokens.dtype in i32 and tokens.ndim == 1 and tokens.is_cuda
+            and tokens.is_contiguous()):
+        _check_tensor("tokens", tokens, i32, 1)
     m, device = tokens.shape[0], tokens.device
     n = _packed_rows(codes)
     if k < T_BLOCK or k % T_BLOCK:
         raise ValueError(f"k must be a multiple of {T_BLOCK}, got {k}")
-    tokens_ptr = _address("tokens", tokens, _kinds()[4], (m,), device)
     packed = _packed_address(codes, scales, n, k, bits, device)
     count = 0
     if extra is not None:
@@ -802,7 +803,7 @@ def embed(tokens, codes, scales, k: int, bits: int, scale: float = 1.0, extra=No
         out = _new((m, k), "bf16", device)
     else:
         _address("out", out, _kinds()[1], (m, k), device)
-    embed_raw(tokens_ptr, m, *packed, _geom_of(n, k, bits), scale, extra_ptr if count else 0, count, out.data_ptr(),
+    embed_raw(tokens.data_ptr(), m, *packed, _geom_of(n, k, bits), scale, extra_ptr if count else 0, count, out.data_ptr(),
               _stream_handle(device))
     return out
 

@@ -338,8 +338,8 @@ __global__ __launch_bounds__(256) void scale_rows_kernel(const float *__restrict
 // +-kPlain has 0 in place of its R. The logits of trained models do, and then
 // all tiles of a row agree; another tile's reference is its largest l2 rounded
 // down, a whole number, so that bringing it to the row's reference later is an
-// exact product with a power of two. (2^60 times 2^22 entries stays far below
-// float32's and bf16's largest, 2^-60 above their smallest.)
+// exact product with a power of two. (2^60 times 2^22 entries and weights up to
+// 2^44 stays below float32's and bf16's largest, 2^-60 far above their smallest.)
 constexpr float kPlain = 60.f;
 
 struct Vocabulary {
@@ -792,7 +792,7 @@ VocabularyTile vocabulary_first(trellis_geom g, int64_t m, int64_t tiles, int64_
   return best;
 }
 struct LossShape {
-  int32_t rows;       // of a chunk: its operands of the second product take at most 1 GiB, or 256 rows
+  int32_t rows;       // of a chunk
   VocabularyTile fwd, back;
   int steps, back_steps, ptiles, blocks;
   int64_t tiles, slab, back_tiles, back_slab;  // operand tiles in all and per launch
@@ -806,8 +806,12 @@ LossShape loss_shape(trellis_geom g, int32_t m, bool keep, int cus) {
   s.back_tiles = g.k / 16;
   s.back_steps = (g.n + 63) / 64 * 2;
   const int64_t n_pad = (int64_t)s.back_steps * kDenseStep;
-  // (statistics: 8 bytes a row and 64 columns at the most, kept below 512 MiB)
-  int64_t rows = (keep ? kLogitBytes / (2 * n_pad) : ((int64_t)1 << 29) / (n_pad / 8)) / 256 * 256;
+  // A chunk's operands of the second product take at most 1 GiB, those of x too,
+  // and its statistics (8 bytes a row and 64 columns at the most) 512 MiB; 256
+  // rows in any case.
+  int64_t rows = keep ? kLogitBytes / (2 * n_pad) : ((int64_t)1 << 29) / (n_pad / 8);
+  if (rows > kLogitBytes / (2 * (int64_t)g.k)) rows = kLogitBytes / (2 * (int64_t)g.k);
+  rows = rows / 256 * 256;
   if (rows < 256) rows = 256;
   if (rows > m) rows = m;
   s.rows = (int32_t)rows;
