@@ -44,50 +44,44 @@ __device__ __forceinline__ f32x2 join_stats_wave(f32x2 a) {
   return a;
 }
 
-// Takes the listed entries out of a row's logits: l2 to `listed`, -infinity in
-// their place. One wave a row; all are read before any is replaced, as an entry
-// may be listed several times.
-__global__ __launch_bounds__(64) void pluck_kernel(Lists L, float *__restrict__ logits) {
-  const int64_t row = blockIdx.x;
-  float *const l = logits + row * L.n;
-  const int32_t *const index = L.index + row * L.top;
-  constexpr int kEach = kMaxTop / 64;
-  int at[kEach];
-  float v[kEach];
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int j = threadIdx.x + 64 * i;
-    at[i] = j < L.top ? index[j] : -1;
-    if (at[i] >= L.n) at[i] = -1;
-    v[i] = at[i] >= 0 ? l[at[i]] * L.scale2 : 0.f;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int j = threadIdx.x + 64 * i;
-    if (j < L.top) L.listed[row * L.top + j] = v[i];
-    if (at[i] >= 0) l[at[i]] = -__builtin_inff();
-  }
-}
-
 constexpr int kStatSpan = 4096;  // logits of a workgroup
 
-// Largest and sum of a span of a row.
-__global__ __launch_bounds__(256) void row_stats_kernel(const float *__restrict__ logits, int n, float scale2,
+// Largest and sum of a span of a row without the listed entries, whose l2 go to
+// `listed`: a bit map in LDS says which they are.
+__global__ __launch_bounds__(256) void row_stats_kernel(Lists L, const float *__restrict__ logits,
                                                         f32x2 *__restrict__ stats) {
   __shared__ f32x2 part[4];
+  __shared__ uint32_t listed[kStatSpan / 32];
   const int64_t row = blockIdx.x;  // (y and z of a grid are limited to 2^16)
-  const int c0 = blockIdx.y * kStatSpan + 4 * (int)threadIdx.x;
-  const float *const l = logits + row * n;
+  const int tid = threadIdx.x, first = blockIdx.y * kStatSpan;
+  const float *const l = logits + row * L.n;
+  const float inf = __builtin_inff();
   f32x4 v[kStatSpan / 1024];
+#pragma unroll
+  for (int i = 0; i < kStatSpan / 1024; ++i) {
+    const int c = first + 1024 * i + 4 * tid;
+    v[i] = f32x4{-inf, -inf, -inf, -inf};
+    if (c < L.n) v[i] = *reinterpret_cast<const f32x4 *>(l + c) * L.scale2;
+  }
+  if (tid < kStatSpan / 32) listed[tid] = 0u;
+  __syncthreads();
+  if (tid < L.top) {
+    const int at = L.index[row * L.top + tid];
+    if (at >= first && at < L.n && at - first < kStatSpan) {
+      L.listed[row * L.top + tid] = l[at] * L.scale2;
+      atomicOr(&listed[(at - first) >> 5], 1u << (at & 31));
+    }
+  }
+  __syncthreads();
   float r = kLowest;
 #pragma unroll
   for (int i = 0; i < kStatSpan / 1024; ++i) {
-    const int c = c0 + 1024 * i;
-    v[i] = f32x4{-__builtin_inff(), -__builtin_inff(), -__builtin_inff(), -__builtin_inff()};
-    if (c < n) v[i] = *reinterpret_cast<const f32x4 *>(l + c) * scale2;
+    const uint32_t out = listed[32 * i + (tid >> 3)] >> (4 * (tid & 7));
 #pragma unroll
-    for (int e = 0; e < 4; ++e) r = fmaxf(r, v[i][e]);
+    for (int e = 0; e < 4; ++e) {
+      if ((out >> e) & 1) v[i][e] = -inf;
+      r = fmaxf(r, v[i][e]);
+    }
   }
   float s = 0.f;
 #pragma unroll
@@ -95,10 +89,9 @@ __global__ __launch_bounds__(256) void row_stats_kernel(const float *__restrict_
 #pragma unroll
     for (int e = 0; e < 4; ++e) s += __builtin_amdgcn_exp2f(v[i][e] - r);
   const f32x2 a = join_stats_wave(f32x2{r, s});
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = a;
+  if ((tid & 63) == 0) part[tid >> 6] = a;
   __syncthreads();
-  if (threadIdx.x == 0)
-    stats[row * gridDim.y + blockIdx.y] = join_stats(join_stats(part[0], part[1]), join_stats(part[2], part[3]));
+  if (tid == 0) stats[row * gridDim.y + blockIdx.y] = join_stats(join_stats(part[0], part[1]), join_stats(part[2], part[3]));
 }
 
 // What a workgroup of 256 threads works out of a row's list and of its other
@@ -596,32 +589,34 @@ __global__ __launch_bounds__(kDenseThreads) void vocabulary_back_kernel(Dense D)
   }
 }
 
-// The only entry of each list, or -1: one wave a row.
-__global__ __launch_bounds__(64) void sole_kernel(Lists L, int32_t *__restrict__ sole) {
-  const int64_t row = blockIdx.x;
+// The only entry of a row's list, or -1: one wave.
+__device__ __forceinline__ int sole_entry(const Lists &L, int64_t row, int lane) {
   int one = -1;
   bool several = false;
   for (int j0 = 0; j0 < L.top; j0 += 64) {
-    const int j = j0 + (int)threadIdx.x;
-    const int at = j < L.top ? L.index[row * L.top + j] : -1;
+    const int at = j0 + lane < L.top ? L.index[row * L.top + j0 + lane] : -1;
     const uint64_t named = __ballot(at >= 0 && at < L.n);
     if (!named) continue;
     if (one < 0) one = __builtin_amdgcn_readlane(at, __builtin_ctzll(named));
     several = several || __any(at >= 0 && at < L.n && at != one);
   }
-  if (threadIdx.x == 0) sole[row] = several ? -1 : one;
+  return several ? -1 : one;
 }
 
-// l2 of the listed entries of lists with several: W's rows decoded where they
-// are named, one wave an entry. Bound by the decode's VALU work.
+// l2 of the listed entries: W's rows decoded where they are named, one wave an
+// entry; and each list's only entry. Bound by the decode's VALU work.
 template <int BITS>
-__global__ __launch_bounds__(256) void listed_kernel(Lists L, const int32_t *__restrict__ sole,
+__global__ __launch_bounds__(256) void listed_kernel(Lists L, int32_t *__restrict__ sole,
                                                      const uint16_t *__restrict__ x, const uint32_t *__restrict__ codes,
                                                      const uint16_t *__restrict__ scales, int blocks) {
   constexpr int wpb = 8 * BITS;
   const int64_t row = blockIdx.x;
   const int j = blockIdx.y * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  if (j >= L.top || sole[row] >= 0) return;
+  if (j == 0) {
+    const int one = sole_entry(L, row, lane);
+    if (lane == 0) sole[row] = one;
+  }
+  if (j >= L.top) return;
   const int at = __builtin_amdgcn_readfirstlane(L.index[row * L.top + j]);
   if (at < 0 || at >= L.n) return;
   const float s = bf16_bits_to_f32(scales[at]);
@@ -893,7 +888,6 @@ trellis_status loss_dense(const uint16_t *x, int32_t m, const uint32_t *codes, c
     L.lse = all.lse + m0;
     const uint16_t *const xc = x + (int64_t)m0 * g.k;
     if (L.top > 1) {
-      hipLaunchKernelGGL(sole_kernel, dim3((unsigned)mc), dim3(64), 0, stream, L, sole);
       const dim3 grid((unsigned)mc, (unsigned)((L.top + 3) / 4));
       const auto listed = g.bits == 2 ? &listed_kernel<2> : g.bits == 3 ? &listed_kernel<3> : &listed_kernel<4>;
       hipLaunchKernelGGL(listed, grid, dim3(256), 0, stream, L, sole, xc, codes, scales, g.k >> 8);
@@ -1039,9 +1033,7 @@ trellis_status loss_rows(const uint16_t *x, int32_t m, const uint32_t *codes, co
     if (g.n <= kWholeRow) {
       hipLaunchKernelGGL(whole_row_kernel, dim3((unsigned)mc), dim3(256), 0, stream, L, logits, dx ? d : nullptr);
     } else {
-      hipLaunchKernelGGL(pluck_kernel, dim3((unsigned)mc), dim3(64), 0, stream, L, logits);
-      hipLaunchKernelGGL(row_stats_kernel, dim3((unsigned)mc, (unsigned)spans), dim3(256), 0, stream, logits, g.n, L.scale2,
-                         stats);
+      hipLaunchKernelGGL(row_stats_kernel, dim3((unsigned)mc, (unsigned)spans), dim3(256), 0, stream, L, logits, stats);
       hipLaunchKernelGGL(row_loss_kernel, dim3((unsigned)mc, dx ? (unsigned)spans : 1u), dim3(256), 0, stream, L, logits,
                          stats, spans, dx ? d : nullptr);
     }
