@@ -40,21 +40,11 @@ struct Unpack {
   int32_t first, tiles;  // tiles of this launch: first, number (per matrix)
   int32_t matrices;
 };
-// Operands of a launch beyond what the Infinity Cache holds (256 MB) are stored
-// past the caches, which pass them on faster than they take them in: 671 MB in
-// 146 us instead of 190 (columns 142 instead of 183). Smaller ones are kept: the
-// product reads them from there.
-constexpr int64_t kFarBytes = (int64_t)256 << 20;
-template <bool FAR>
-__device__ __forceinline__ void store_operand(bf16x8 *p, bf16x8 v) {
-  if constexpr (FAR) __builtin_nontemporal_store(v, p);
-  else *p = v;
-}
 
 // Forward: one wave per 16 rows of W and 256-weight block, 8 operands. Bound by
 // its writes: K = 5120, N = 17408, k = 4 in 48 us, 223 MB at 4.6 TB/s (a plain
 // copy reaches 5.2).
-template <int BITS, bool FAR>
+template <int BITS>
 __global__ __launch_bounds__(256) void unpack_rows_kernel(Unpack U) {
   constexpr int wpb = 8 * BITS;
   const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
@@ -87,7 +77,7 @@ __global__ __launch_bounds__(256) void unpack_rows_kernel(Unpack U) {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         v[e] = (__bf16)window_weight((uint32_t)(f[st] >> ((7 - e) * BITS)) & 0xFFFu, s, q, kq, decltype(chained)::value);
-      store_operand<FAR>(out + st * stride, v);
+      out[st * stride] = v;
     }
   };
   if (chain) decode(std::true_type{});
@@ -101,7 +91,7 @@ __global__ __launch_bounds__(256) void unpack_rows_kernel(Unpack U) {
 // each of the four columns. K = 5120, N = 17408, k = 4 in 51 us, 224 MB at 4.4
 // TB/s (64 us with the words read by each lane, 87 us before the operands were
 // stored a kilobyte at a time).
-template <int BITS, bool FAR>
+template <int BITS>
 __global__ __launch_bounds__(256) void unpack_columns_kernel(Unpack U) {
   constexpr int wpb = 8 * BITS, kRow = wpb + 4;  // words of a row's block, and in LDS
   __shared__ __attribute__((aligned(16))) uint32_t words[4][32 * kRow];
@@ -157,7 +147,7 @@ __global__ __launch_bounds__(256) void unpack_columns_kernel(Unpack U) {
 #pragma unroll
       for (int c = 0; c < 4; ++c) mine[(j >> 2) * 64 + g * 16 + 4 * (j & 3) + c] = w[c];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) store_operand<FAR>(out + (4 * part + i) * 64, mine[i * 64 + lane]);
+      for (int i = 0; i < 4; ++i) out[(4 * part + i) * 64] = mine[i * 64 + lane];
     }
   };
   if (chain) decode(std::true_type{});
@@ -301,9 +291,9 @@ constexpr int dense_buffers(int nt, int rt = 4) {
 // ms. Tried and not kept: four waves of 128 x 128 (2.0 ms), a raised wave
 // priority around the MFMAs, the reads before the copies, the other order of
 // the accumulators (all within 1%).
-// Registers: forward with six to eight column tiles a wave, the adapters' term
-// does not fit beside the accumulators, and its operands go through 16, 176 and
-// 312 bytes of scratch memory a lane, in and around the term's loop (once per
+// Registers: forward with seven and eight column tiles a wave, the adapters'
+// term does not fit beside the accumulators, and its operands go through 104 and
+// 180 bytes of scratch memory a lane, in and around the term's loop (once per
 // named adapter and 32 rank columns); the steps use none.
 // Where a lane's sums lie: lane (j, g), accumulator (r, i): row row0 + 16 r + j,
 // operand tile tile0 + i, its columns 4 g .. +3.

@@ -27,7 +27,7 @@ struct Lists {
   const int32_t *index;
   const float *logits;
   float *listed;     // [m, top]: l2 of the listed entries
-  int32_t m, n, top;
+  int32_t n, top;
   float temperature, scale2;  // scale2: log2(e) / T
   float *loss, *lse;
 };
@@ -346,7 +346,11 @@ struct Vocabulary {
 
 // The product's tile in, 2^(l2 - reference) and its sums out. Beside the
 // product's steps (see dense_sums) a tile's end costs 4 operations and one
-// exponential (a quarter of the rate) for each of its sums.
+// exponential (a quarter of the rate) for each of its sums. 2048 rows, K = 5120, N
+// = 131072: 2.23 to 2.38 ms, 1.16 to 1.23 PFLOP/s (a library product of this size,
+// its logits in bf16: 1.21). The exponentials are rounded to bf16 because that is
+// what the matrix cores multiply at this rate: each of dx's terms is off by 2^-9 of
+// itself, of either sign.
 template <int NT, int RT>
 __device__ __forceinline__ void vocabulary_out(const Dense &D, const Vocabulary &V, const DenseAt &at, f32x4 (&acc)[RT][NT]) {
   const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
@@ -417,9 +421,12 @@ __global__ __launch_bounds__(kDenseThreads) void vocabulary_kernel(Dense D, Voca
 // memory is a copy to LDS, so that the waits are the kernel's own: a copy is
 // waited for by the number of P's copies issued after it, which the words'
 // copies between them only make stricter.
-// Bound by the LDS and the decode side by side: a step of 384 rows and 128
-// columns takes 768 clocks of MFMA, 640 of LDS reads and 256 of writes, and 450
-// of the decode's VALU work.
+// A step of 384 rows and 128 columns has 768 clocks of MFMA, 640 of LDS reads and
+// 256 of writes, and 500 of the decode's VALU work; it takes 1900 (0.78 us; 256
+// rows 0.6), as the workgroup's waves meet at every step and the three overlap
+// only in part: 0.64 us without the decode, 0.76 without the copies, 0.63 without
+// the MFMAs. 333 rows, K = 5120, N = 50004, k = 3 in 245 us; decoded beforehand 139
+// and a product of 192-row tiles 246; few rows' kernel, in three tiles, 310.
 struct Packed {
   const uint32_t *codes;
   const uint16_t *scales;
@@ -572,7 +579,8 @@ __global__ __launch_bounds__(kDenseThreads) void vocabulary_decode_kernel(Dense 
   vocabulary_out<NT, RT>(D, V, at, acc);
 }
 
-// The second product: float32 sums of every split.
+// The second product: float32 sums of every split. 2048 rows, K = 5120, N =
+// 131072: 2.24 to 2.30 ms, 1.2 PFLOP/s (a library product: 1.32).
 template <int NT, int RT>
 __global__ __launch_bounds__(kDenseThreads) void vocabulary_back_kernel(Dense D) {
   const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
@@ -755,7 +763,7 @@ constexpr int64_t kVocabularyBytes = (int64_t)1 << 31;  // decoded weights of a 
 struct VocabularyTile {
   int nt, rt, splits;
   bool decode;  // vocabulary_decode_kernel
-  double us;    // with unpacking
+  double us;
 };
 VocabularyTile vocabulary_tile(int64_t m, int64_t tiles, int64_t steps, bool back, int cus) {
   VocabularyTile best{};
@@ -881,7 +889,6 @@ trellis_status loss_dense(const uint16_t *x, int32_t m, const uint32_t *codes, c
   for (int32_t m0 = 0; m0 < m; m0 += s.rows) {
     const int32_t mc = m - m0 < s.rows ? m - m0 : s.rows;
     const int ptiles = (mc + 15) / 16;
-    L.m = mc;
     L.index = all.index + (int64_t)m0 * L.top;
     L.logits = all.logits ? all.logits + (int64_t)m0 * L.top : nullptr;
     L.loss = all.loss + m0;
@@ -956,13 +963,13 @@ Plan loss_back_plan(trellis_geom g, int32_t m, int cus) {
   }
   return p;
 }
-// Whether W is decoded once into operands for a loss (loss_dense), by what both
-// sides are reckoned to take in us: fitted to 34 sizes, 96 to 768 rows of five
-// matrices (N, K: 8192 2048 to 131072 5120), where the side taken is at most 6%
-// slower than the other. Measured, few rows' way against this: K = 5120, N =
-// 131072, losses 445 / 588 at 192 rows, 780 / 785 at 333, 1029 / 875 at 509; with
-// gradient 965 / 1184, 1783 / 1648, 2528 / 1887; K = 2048, N = 8192, losses 34 /
-// 54 at 256 rows, 62 / 54 at 640.
+// Whether a loss takes the many rows' way (loss_dense), by what both are reckoned
+// to take in us: fitted to 60 points, 96 to 1536 rows of five matrices (N, K: 8192
+// 2048 to 131072 5120), where the side taken is 0.2% slower than the other on
+// average and 9% at most. Measured, few rows' way against this: K = 5120, N =
+// 131072, losses 267 / 398 at 128 rows, 440 / 400 at 192, 774 / 530 at 333; with
+// gradient 947 / 1019 at 192, 1266 / 1081 at 256, 2521 / 1741 at 509; K = 2048, N =
+// 8192, losses 40 / 54 at 509 rows, 61 / 54 at 640.
 bool loss_by_operands(trellis_geom g, int32_t m, bool keep, int cus) {
   const int forced = g_path.load(std::memory_order_relaxed);
   if (forced >= 0) return forced == 1;
@@ -1014,7 +1021,6 @@ trellis_status loss_rows(const uint16_t *x, int32_t m, const uint32_t *codes, co
   for (int32_t m0 = 0; m0 < m; m0 += rows) {
     const int32_t mc = m - m0 < rows ? m - m0 : rows;
     const int which = m0 + mc == m;
-    L.m = mc;
     L.index = all.index + (int64_t)m0 * L.top;
     L.logits = all.logits ? all.logits + (int64_t)m0 * L.top : nullptr;
     L.loss = all.loss + m0;
@@ -1067,7 +1073,7 @@ trellis_status trellis_cross_entropy(const uint16_t *x, int32_t m, const uint32_
   if (!on(x, 16) || !on(codes, 16) || !on(scales, 2) || !on(target, 4) || !on(loss, 4) || !on(lse, 4) || !on(dx, 16))
     return TRELLIS_E_ALIGN;
   std::lock_guard<std::mutex> lock(g_lock);
-  const Lists l{target, nullptr, nullptr, m, g.n, 1, 1.f, kLog2E, loss, lse};
+  const Lists l{target, nullptr, nullptr, g.n, 1, 1.f, kLog2E, loss, lse};
   return loss_rows(x, m, codes, scales, g, l, dx, reinterpret_cast<hipStream_t>(hip_stream));
 }
 
@@ -1084,7 +1090,7 @@ trellis_status trellis_distill(const uint16_t *x, int32_t m, const uint32_t *cod
       !on(lse, 4) || !on(dx, 16))
     return TRELLIS_E_ALIGN;
   std::lock_guard<std::mutex> lock(g_lock);
-  const Lists l{index, logits, nullptr, m, g.n, top, temperature, kLog2E / temperature, loss, lse};
+  const Lists l{index, logits, nullptr, g.n, top, temperature, kLog2E / temperature, loss, lse};
   return loss_rows(x, m, codes, scales, g, l, dx, reinterpret_cast<hipStream_t>(hip_stream));
 }
 

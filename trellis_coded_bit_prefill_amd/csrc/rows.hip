@@ -1625,17 +1625,13 @@ struct GatedGrads {
 };
 
 typedef void (*UnpackFn)(Unpack);
-template <bool FAR>
 UnpackFn unpack_fn(bool columns, int bits) {
-  if (columns)
-    return bits == 2 ? &unpack_columns_kernel<2, FAR> : bits == 3 ? &unpack_columns_kernel<3, FAR> : &unpack_columns_kernel<4, FAR>;
-  return bits == 2 ? &unpack_rows_kernel<2, FAR> : bits == 3 ? &unpack_rows_kernel<3, FAR> : &unpack_rows_kernel<4, FAR>;
+  if (columns) return bits == 2 ? &unpack_columns_kernel<2> : bits == 3 ? &unpack_columns_kernel<3> : &unpack_columns_kernel<4>;
+  return bits == 2 ? &unpack_rows_kernel<2> : bits == 3 ? &unpack_rows_kernel<3> : &unpack_rows_kernel<4>;
 }
 trellis_status launch_unpack(bool columns, int bits, const Unpack &u, hipStream_t stream) {
   const int64_t waves = columns ? (int64_t)(u.tiles / 16) * (u.steps / u.matrices) : (int64_t)u.tiles * (u.k >> 8);
-  const int64_t bytes = (int64_t)u.tiles * (columns ? 1 : u.matrices) * u.steps * 1024;
-  const UnpackFn fn = bytes > kFarBytes ? unpack_fn<true>(columns, bits) : unpack_fn<false>(columns, bits);
-  hipLaunchKernelGGL(fn, dim3((unsigned)((waves + 3) / 4), (unsigned)u.matrices), dim3(256), 0, stream, u);
+  hipLaunchKernelGGL(unpack_fn(columns, bits), dim3((unsigned)((waves + 3) / 4), (unsigned)u.matrices), dim3(256), 0, stream, u);
   return hipGetLastError() == hipSuccess ? TRELLIS_OK : TRELLIS_E_HIP;
 }
 
