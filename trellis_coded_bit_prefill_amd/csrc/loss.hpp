@@ -788,8 +788,7 @@ VocabularyTile vocabulary_first(trellis_geom g, int64_t m, int64_t tiles, int64_
   if (g_tiles.load(std::memory_order_relaxed) > 0) return best;  // (launches of so many tiles: there are none here)
   for (int rt = 4; rt <= 6; rt += 2) {
     const int64_t wg = (m + 64 * rt - 1) / (64 * rt) * ((tiles + 7) / 8);
-    const double rounds = 0.5 * ((double)((wg + cus - 1) / cus) + (double)wg / cus);
-    const double us = (rounds < 1 ? 1 : rounds) * (steps * (0.09 * rt + 0.23) + 6);
+    const double us = (double)((wg + cus - 1) / cus) * (steps * (0.09 * rt + 0.23) + 6);  // (power does not bind it)
     if (us < best.us) best = VocabularyTile{4, rt, 1, true, us};
   }
   return best;
@@ -965,8 +964,8 @@ Plan loss_back_plan(trellis_geom g, int32_t m, int cus) {
 }
 // Whether a loss takes the many rows' way (loss_dense), by what both are reckoned
 // to take in us: fitted to 60 points, 96 to 1536 rows of five matrices (N, K: 8192
-// 2048 to 131072 5120), where the side taken is 0.2% slower than the other on
-// average and 9% at most. Measured, few rows' way against this: K = 5120, N =
+// 2048 to 131072 5120), where the side taken is 0.2% slower than the faster one on
+// average and 10% at most. Measured, few rows' way against this: K = 5120, N =
 // 131072, losses 267 / 398 at 128 rows, 440 / 400 at 192, 774 / 530 at 333; with
 // gradient 947 / 1019 at 192, 1266 / 1081 at 256, 2521 / 1741 at 509; K = 2048, N =
 // 8192, losses 40 / 54 at 509 rows, 61 / 54 at 640.
