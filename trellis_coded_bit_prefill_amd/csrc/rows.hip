@@ -1,6 +1,7 @@
 // Fine-tuned packed Trellis layers at any number of rows, gfx950: low-rank
 // adapters beside the shared projection, the gated block, and the backward
-// passes of both.
+// passes of both. The losses over a vocabulary matrix (loss.hpp) and the
+// embedding (embed.hpp) are parts of this file.
 //
 // Every entry point here contains one product of a dense bf16 matrix with a
 // packed matrix W[N, K], in one of two directions:
@@ -290,7 +291,7 @@ namespace {
 // tiles 229 us (VALU 42%, LDS 36%, MFMA 18%). Tried and slower: one column tile
 // per wave from four row tiles on (53 against 49 us at 64 rows), two up to two
 // (40 against 38.7 at 24), four waves per SIMD from four row tiles on (97
-// against 47 at 64: registers spill). Transposed with six row tiles 48 bytes a
+// against 47 at 64: registers spill). Transposed with six row tiles 44 bytes a
 // lane go through scratch memory outside the steps.
 // LOGITS: forward, float32 sums to P.logits, and no adapters.
 template <int BITS, int KIND, int MT, int NT, bool LOGITS>
