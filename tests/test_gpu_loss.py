@@ -67,7 +67,7 @@ def test_cross_entropy(path, m, n, k, bits):
     check_all("forward", tp.cross_entropy(x, *packed(d), dev(target)), want)
 
 
-@pytest.mark.parametrize("top,t", [(1, 1.0), (3, 2.0), (64, 0.5), (65, 1.0), (256, 4.0)])
+@pytest.mark.parametrize("top,t", [(1, 1.0), (3, 2.0), (5, 0.01), (64, 0.5), (65, 1.0), (256, 100.0)])
 @pytest.mark.parametrize("m,n,k,bits", [SIZES[1], SIZES[2], SIZES[4], SIZES[5], SIZES[7], SIZES[9]])
 def test_distill(path, m, n, k, bits, top, t):
     print(f"distill {m} {n} {k} {bits} top {top} T {t} {path}", flush=True)
@@ -148,6 +148,24 @@ def test_rows_do_not_meet(path):
     assert all(torch.equal(a[keep], b[keep]) for a, b in zip(got, clean))
     assert got[0][20].isnan() and got[1][20].isnan() and not got[0][7].isfinite()
     assert abs(float(got[0][30]) - np.log(516)) < 1e-5
+
+
+def test_a_teacher_that_is_not_a_number(path):
+    """A NaN or infinite logit of a valid entry reaches its row alone."""
+    import torch
+
+    print(f"teacher NaN {path}", flush=True)
+    d = ref.draw(np.random.default_rng(14), 40, 516, 256, 4, top=4)
+    x, index, z = to_dev_bf16(d["x_bits"]), dev(d["index"]), dev(d["logits"])
+    clean = tp.distill(x, *packed(d), index, z, keep=True)
+    z[3, 1], z[11, 2] = float("nan"), float("inf")
+    x[20, 7] = float("inf")
+    got = tp.distill(x, *packed(d), index, z, keep=True)
+    keep = torch.ones(40, dtype=torch.bool, device="cuda")
+    keep[[3, 11, 20]] = False
+    assert all(torch.equal(a[keep], b[keep]) for a, b in zip(got, clean))
+    assert got[0][[3, 11]].isnan().all() and torch.equal(got[1][[3, 11]], clean[1][[3, 11]])
+    assert got[2][3].isnan().any() and not got[0][20].isfinite()
 
 
 def test_several_slabs_and_chunks():

@@ -294,3 +294,26 @@ def test_offsets_past_32_bits():
         at = (t >= 0).nonzero()[:, 0]
         want.index_add_(0, t[at], dout[r0:r0 + (1 << 17)][at].double())
     assert torch.equal(got, want.bfloat16())
+
+
+def test_loss_offsets_past_32_bits():
+    """2^20 rows of 2304 columns in several chunks: more than 2^31 elements of x and of its gradient."""
+    import torch
+
+    print("loss offsets past 32 bits", flush=True)
+    m, k, n = 1 << 20, 2304, 64
+    g = torch.Generator(device="cuda").manual_seed(4)
+    codes = torch.randint(-2**31, 2**31, (n, k * 4 // 32), generator=g, device="cuda", dtype=torch.int32)
+    scales = (torch.rand(n, generator=g, device="cuda") * 0.015 + 0.005).bfloat16()
+    x = torch.randn(m, k, generator=g, device="cuda", dtype=torch.bfloat16)
+    target = torch.randint(-1, n, (m,), generator=g, device="cuda", dtype=torch.int32)
+    loss, lse, dx = tp.cross_entropy(x, codes, scales, 4, target, keep=True)
+    w = tp.decode(codes, scales, k, 4)
+    largest = w.double().abs().max()
+    for r in (slice(0, 500), slice(932000, 932500), slice(m - 500, m)):
+        want = plain_loss(x[r], w, target[r], torch.float64)
+        el = k * 2.0 ** -24 * x[r].double().abs().sum(1) * largest
+        bound = 2 * el + 2.0 ** -17
+        assert ((loss[r] - want[0]).abs() <= 2 * bound).all() and ((lse[r] - want[1]).abs() <= bound).all()
+        off = (dx[r].double() - want[2]).abs()
+        assert (off <= 2 * largest * (2 * 2.0 ** -8 + 2 * bound[:, None]) + 2.0 ** -8 * want[2].abs()).all()
