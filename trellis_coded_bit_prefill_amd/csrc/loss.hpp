@@ -950,11 +950,20 @@ trellis_status loss_dense(const uint16_t *x, int32_t m, const uint32_t *codes, c
   return TRELLIS_OK;
 }
 
-// The transposed product of few rows' gradients. Its operands in several
-// launches lose to decoding in the product (256 rows, K = 5120, N = 131072: the
-// whole call 1.51 ms against 1.28).
+// The transposed product of few rows' gradients. Up to two row tiles, two
+// workgroups share a CU where what that saves (a step takes 1.65 times as long
+// for two) is more than the joining of twice as many parts costs: K = 5120, N =
+// 65536, 1 row with gradient 140 us against 160; K = 1024, N = 32772 74 against 48.
+// Its operands in several launches lose to decoding in the product (256 rows, K =
+// 5120, N = 131072: the whole call 1.51 ms against 1.28).
 Plan loss_back_plan(trellis_geom g, int32_t m, int cus) {
-  Plan p = plan_of(kTransposed, g, m, 1, cus);
+  Shape fused = shape_of(kTransposed, g, m, 1, cus, true);
+  if (kRowTiles[fused.mt] <= 2) {
+    Shape two = shape_of(kTransposed, g, m, 1, cus, true, 2);
+    two.crowd = 1.65;
+    if (fused_us(two) < fused_us(fused)) fused = two;
+  }
+  Plan p = plan_of(kTransposed, g, m, 1, cus, &fused);
   if (p.dense && p.many.slab < p.many.tiles && p.fused.units < ((int64_t)1 << 30)) {
     p.dense = false;
     p.bytes = p.fused.partial_bytes;
@@ -972,7 +981,7 @@ Plan loss_back_plan(trellis_geom g, int32_t m, int cus) {
 bool loss_by_operands(trellis_geom g, int32_t m, bool keep, int cus) {
   const int forced = g_path.load(std::memory_order_relaxed);
   if (forced >= 0) return forced == 1;
-  const Shape f = shape_of(kForward, g, m, 1, cus);
+  const Shape f = shape_of(kForward, g, m, 1, cus, true);
   if (f.units >= ((int64_t)1 << 30)) return true;  // (the product kernel counts them in 32 bits)
   const double mn = 1e-6 * m * (double)g.n, mb = 2e-6 * g.n * (double)g.k;
   double rows = fused_us(f) + (keep ? 20 + 2.8 * mn : 13 + 1.4 * mn);
@@ -999,7 +1008,7 @@ trellis_status loss_rows(const uint16_t *x, int32_t m, const uint32_t *codes, co
   size_t parts = 0;
   int64_t counters = 0;
   for (int i = 0; i < 2; ++i) {
-    fwd[i] = shape_of(kForward, g, counts[i], 1, cus);
+    fwd[i] = shape_of(kForward, g, counts[i], 1, cus, true);
     if (dx) bwd[i] = loss_back_plan(g, counts[i], cus);
     if (parts < fwd[i].partial_bytes) parts = fwd[i].partial_bytes;
     if (parts < bwd[i].bytes) parts = bwd[i].bytes;

@@ -293,8 +293,8 @@ namespace {
 // (40 against 38.7 at 24), four waves per SIMD from four row tiles on (97
 // against 47 at 64: registers spill). Transposed with six row tiles 44 bytes a
 // lane go through scratch memory outside the steps.
-// LOGITS: forward, float32 sums to P.logits, and no adapters.
-template <int BITS, int KIND, int MT, int NT, bool LOGITS>
+// LOSS: no adapters, and forward float32 sums to P.logits.
+template <int BITS, int KIND, int MT, int NT, bool LOSS>
 __device__ __forceinline__ void product(const Product &P) {
   constexpr bool kT = KIND == kTransposed;
   static_assert(kT ? NT == 4 : KIND == kGated ? NT == 2 : NT <= 2, "tiles per wave");
@@ -401,7 +401,7 @@ __device__ __forceinline__ void product(const Product &P) {
     } else {
       const int width = kT ? P.k : P.n, n = agroup * BN + c;
       if (n >= width) return;
-      if constexpr (LOGITS) *reinterpret_cast<f32x4 *>(P.logits + (int64_t)mrow * width + n) = v;
+      if constexpr (LOSS && !kT) *reinterpret_cast<f32x4 *>(P.logits + (int64_t)mrow * width + n) = v;
       else store4(P.out + (int64_t)mrow * width + n, v);
     }
   };
@@ -435,7 +435,7 @@ __device__ __forceinline__ void product(const Product &P) {
           }
         // The adapters' term joins the sums of the wave that holds the tile's
         // last step, half of the row tiles in each wk.
-        if (KIND != kGated && !LOGITS && a1 == P.steps && P.low.rank > 0) {
+        if (KIND != kGated && !LOSS && a1 == P.steps && P.low.rank > 0) {
           // (one row tile: the first wk alone)
           // Transposed: one row tile at a time, as the sums of the second
           // round are still in registers.
@@ -865,6 +865,10 @@ __global__ __launch_bounds__(kThreads, OCC) void product_kernel(Product P) {
 template <int BITS, int MT, int NT, int OCC>
 __global__ __launch_bounds__(kThreads, OCC) void logits_kernel(Product P) {
   product<BITS, kForward, MT, NT, true>(P);
+}
+template <int BITS, int MT, int OCC>
+__global__ __launch_bounds__(kThreads, OCC) void logits_gradient_kernel(Product P) {
+  product<BITS, kTransposed, MT, 4, true>(P);
 }
 
 // ---------------------------------------------------------------------------
@@ -1460,8 +1464,16 @@ ProductFn logits_of(int i) {
     default: return &logits_kernel<BITS, 8, wave_tiles(kForward, 8), waves_per_simd(kForward, 8)>;
   }
 }
-ProductFn product_fn(int kind, int bits, int i, bool logits) {
-  if (logits) return bits == 2 ? logits_of<2>(i) : bits == 3 ? logits_of<3>(i) : logits_of<4>(i);
+// The transposed product of up to two row tiles without adapters: its registers
+// allow two workgroups a CU.
+template <int BITS>
+ProductFn logits_gradient_of(int i) {
+  return i == 0 ? &logits_gradient_kernel<BITS, 1, 4> : &logits_gradient_kernel<BITS, 2, 4>;
+}
+ProductFn product_fn(int kind, int bits, int i, bool loss) {
+  if (loss && kind == kTransposed && i < 2)
+    return bits == 2 ? logits_gradient_of<2>(i) : bits == 3 ? logits_gradient_of<3>(i) : logits_gradient_of<4>(i);
+  if (loss && kind == kForward) return bits == 2 ? logits_of<2>(i) : bits == 3 ? logits_of<3>(i) : logits_of<4>(i);
   return kind == kForward ? product_of<kForward>(bits, i) : kind == kGated ? product_of<kGated>(bits, i)
                                                                            : product_of<kTransposed>(bits, i);
 }
@@ -1472,11 +1484,17 @@ struct Shape {
   int64_t tiles, units;
   int groups, steps, steps1, grid, parts;
   size_t partial_bytes, lds;
+  bool loss;
+  double crowd;  // what a step takes beside another workgroup's, to one alone
 };
-Shape shape_of(int kind, trellis_geom g, int32_t m, int matrices, int cus) {
+// (loss: the kernels without adapters; wgs: workgroups a CU, 0 for as many as the
+// kernel's waves allow)
+Shape shape_of(int kind, trellis_geom g, int32_t m, int matrices, int cus, bool loss = false, int wgs = 0) {
   Shape s{};
   s.kind = kind;
   s.bits = g.bits;
+  s.loss = loss;
+  s.crowd = 1;
   // at most 128 rows a tile, transposed 96 (its waves hold four column tiles)
   const int most_rows = kind == kTransposed ? 96 : 128;
   const int64_t chunks = ((int64_t)m + most_rows - 1) / most_rows;
@@ -1491,7 +1509,7 @@ Shape shape_of(int kind, trellis_geom g, int32_t m, int matrices, int cus) {
   s.steps = kind == kTransposed ? s.steps1 * matrices : s.steps1;
   s.tiles = rows * s.groups;
   s.units = s.tiles * s.steps;
-  const int64_t room = (int64_t)cus * waves_per_simd(kind, mt) / 2;  // workgroups the card holds at once
+  const int64_t room = (int64_t)cus * (wgs ? wgs : waves_per_simd(kind, mt) / 2);  // workgroups the card holds at once
   s.grid = (int)(s.units < room ? s.units : room);
   // Tiles split over the same number of workgroups each, where that leaves at
   // most a tenth of the card idle: no workgroup then reduces two tiles' parts
@@ -1508,11 +1526,11 @@ Shape shape_of(int kind, trellis_geom g, int32_t m, int matrices, int cus) {
 }
 
 trellis_status launch(const Shape &s, Product p, hipStream_t stream) {
-  const ProductFn fn = product_fn(s.kind, s.bits, s.mt, p.logits != nullptr);
+  const ProductFn fn = product_fn(s.kind, s.bits, s.mt, s.loss);
   static bool ready[kMaxDevices][2][3][3][kMts];
   int dev = 0, cus = 0;
   if (device(dev, cus) != TRELLIS_OK) return TRELLIS_E_HIP;
-  bool &done = ready[dev][p.logits != nullptr][s.kind][s.bits - 2][s.mt];
+  bool &done = ready[dev][s.loss][s.kind][s.bits - 2][s.mt];
   if (!done) {
     if (!worked(hipFuncSetAttribute(reinterpret_cast<const void *>(fn), hipFuncAttributeMaxDynamicSharedMemorySize, (int)s.lds)))
       return TRELLIS_E_HIP;
@@ -1722,7 +1740,7 @@ double fused_us(const Shape &s) {
   const double part = (double)s.partial_bytes / 2 / s.grid;
   int64_t tiles = 1;
   if (!s.parts) tiles = s.units % s.grid == 0 && steps % s.steps == 0 ? steps / s.steps : (steps - 1) / s.steps + (s.steps > 1 ? 2 : 1);
-  double us = steps * (step[s.kind][s.mt] + (s.bits == 3 ? 0.42 : 0)) + tiles * (0.8 + 20e-6 * part);
+  double us = steps * (step[s.kind][s.mt] + (s.bits == 3 ? 0.42 : 0)) * s.crowd + tiles * (0.8 + 20e-6 * part);
   if (s.parts != 1) {
     double share = s.parts ? s.parts : (double)s.grid / s.tiles + 1;
     if (share > s.steps) share = s.steps;
@@ -1747,9 +1765,9 @@ double fused_us(const Shape &s) {
 // 1024, N = 4096: adapters 32 / 45 at 1024, 53 / 47 at 2048; gated 20 / 35 at
 // 449, 69 / 52 at 2048; adapters_backward 47 / 48 at 97, 66 / 60 at 449;
 // gated_backward 44 / 41 at 97, 50 / 45 at 449.
-Plan plan_of(int kind, trellis_geom g, int32_t m, int matrices, int cus) {
+Plan plan_of(int kind, trellis_geom g, int32_t m, int matrices, int cus, const Shape *fused = nullptr) {
   Plan p{};
-  p.fused = shape_of(kind, g, m, matrices, cus);
+  p.fused = fused ? *fused : shape_of(kind, g, m, matrices, cus);
   const int forced = g_path.load(std::memory_order_relaxed);
   p.dense = forced == 1 || p.fused.units >= ((int64_t)1 << 30);  // (the product kernel counts them in 32 bits)
   if (p.dense) {
