@@ -88,6 +88,30 @@ def test_embed_backward(m, k, count, kind):
         assert torch.equal(tp.embed_backward(*args), got)
 
 
+@pytest.mark.parametrize("m,count,kind", [(1024, 257, "any"), (1025, 257, "any"), (16384, 257, "skewed"), (1025, 16384, "sorted"),
+                                          (16384, 16385, "any"), (16384, 20000, "same"), (9000, 4097, "skewed"), (2047, 63 * 256 + 1, "none")])
+def test_gradient_of_rows_sorted_by_several_workgroups(m, count, kind):
+    test_embed_backward(m, 256, count, kind)
+
+
+@pytest.mark.parametrize("m", [1024, 1025, 16384, 16385])
+@pytest.mark.parametrize("count", [2**18, 2**18 + 1, 2**22])
+def test_gradient_of_the_most_trained_rows(m, count):
+    """Each token once: its row is dout's, all others are zero."""
+    import torch
+
+    print(f"embed_backward {m} rows of {count}", flush=True)
+    rng = np.random.default_rng(m + count)
+    tokens = rng.choice(count, m, replace=False)
+    tokens[:2] = [0, count - 1] if not np.isin([0, count - 1], tokens[2:]).any() else tokens[:2]
+    dout = torch.randn(m, 256, device="cuda").bfloat16()
+    at = torch.from_numpy(tokens).cuda()
+    want = torch.zeros(count, 256, dtype=torch.bfloat16, device="cuda")
+    want[at] = dout
+    got = tp.embed_backward(dout, (at + 77).int(), 77, count, dextra=torch.full_like(want, float("nan")))
+    assert torch.equal(got, want)
+
+
 def test_one_token_everywhere_and_infinities():
     """An infinity reaches its token's row alone; a rows' order decides nothing but the last digits."""
     import torch

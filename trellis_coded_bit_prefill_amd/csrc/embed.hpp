@@ -179,38 +179,92 @@ __global__ __launch_bounds__(256) void sort_place_kernel(Sort S, const uint32_t 
   }
 }
 
-// Up to 16384 rows in one workgroup and one launch: every lane keeps up to 16
-// pairs in registers, each wave's in a row of positions, and LDS takes them to
-// their next places, the last ones too (stored to memory as they come, four
-// bytes a line, they took 13 us of 32).
+// Up to 16384 rows in one launch. Each workgroup sorts the pairs of `width`
+// trained rows: it looks at every token, counts those before its own, which is
+// where its pairs begin, and no workgroup waits for another. 256 trained rows are
+// one pass. 16384 rows of 16384 trained ones take 16.2 us with 64 workgroups and
+// 28.6 with one; up to 1024 rows have only one (one pair a lane; at 509 rows of
+// 16384 the call takes 17.2 and 19.1). Every lane keeps up to 16 pairs in
+// registers, each wave's in a row of positions, and LDS takes them to their next
+// places, the last ones too (stored to memory as they come, four bytes a line,
+// they took 13 us of 32).
 constexpr int kSmallRows = 16384;
+constexpr int kSmallGroups = 64;   // workgroups at most
+constexpr int kSmallWidth = 256;   // trained rows of a workgroup at least
+constexpr int kRowBits = 14;
+static_assert(1 << kRowBits == kSmallRows, "a pair's row");
+constexpr int kMostWidth = 1 << (32 - kRowBits);
+static_assert(TRELLIS_MAX_TRAINED / kSmallGroups <= kMostWidth, "a pair's trained row");
 struct SmallSort {
-  int32_t key[kSmallRows];
-  uint16_t row[kSmallRows];
+  uint32_t pair[kSmallRows];  // trained row of the workgroup's << 14 | row of dout
   uint16_t counts[16][256];
   uint32_t waves[4];
   uint32_t total;
+  int32_t below[16], own[16];
 };
-__global__ __launch_bounds__(1024) void sort_small_kernel(Sort S, uint32_t *__restrict__ arrived, int counters) {
+__global__ __launch_bounds__(1024) void sort_small_kernel(Sort S, int width, uint32_t *__restrict__ arrived, int counters) {
   extern __shared__ __attribute__((aligned(16))) unsigned char small_space[];
   SmallSort &M = *reinterpret_cast<SmallSort *>(small_space);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  for (int i = tid; i < counters; i += 1024) arrived[i] = 0u;
+  for (int i = (int)blockIdx.x * 1024 + tid; i < counters; i += (int)gridDim.x * 1024) arrived[i] = 0u;
   constexpr int kEach = kSmallRows / 1024;
-  int key[kEach], row[kEach], rank[kEach];
-  uint32_t in = 0;  // bit i: pair i exists
-  const int each = (S.m + 1023) >> 10, i0 = wave * (64 * each) + lane;
+  uint32_t pair[kEach];
+  int rank[kEach];
+  uint32_t in = 0, under = 0;  // bit i: pair i exists, is another workgroup's before this one
+  const int low = (int)blockIdx.x * width, high = S.count - low < width ? S.count - low : width;
+  int each = (S.m + 1023) >> 10, i0 = wave * (64 * each) + lane, begin = 0;
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
     const int at = i0 + 64 * i, token = S.tokens[at < S.m ? at : S.m - 1];
-    const bool have = i < each && at < S.m && token >= S.first && token - S.first < S.count;
-    key[i] = have ? token - S.first : 0;
-    row[i] = at;
+    const bool there = i < each && at < S.m && token >= S.first && token - S.first < S.count;
+    const int mine = there ? token - S.first - low : -1;
+    const bool have = mine >= 0 && mine < high;
+    pair[i] = have ? (uint32_t)mine << kRowBits | (uint32_t)at : 0u;
     in |= (uint32_t)have << i;
+    under |= (uint32_t)(there && mine < 0) << i;
+  }
+  if (gridDim.x > 1) {
+    // The workgroup's own pairs move together, in order.
+    int own = 0, below = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      own += (int)__popcll(__ballot((in >> i) & 1));
+      below += (int)__popcll(__ballot((under >> i) & 1));
+    }
+    if (lane == 0) {
+      M.below[wave] = below;
+      M.own[wave] = own;
+    }
+    __syncthreads();
+    int at = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) {
+      begin += M.below[w];
+      at += w < wave ? M.own[w] : 0;
+      all += M.own[w];
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const bool have = (in >> i) & 1;
+      const uint64_t some = __ballot(have);
+      if (have) M.pair[at + (int)__popcll(some & ((1ull << lane) - 1ull))] = pair[i];
+      at += (int)__popcll(some);
+    }
+    __syncthreads();
+    each = (all + 1023) >> 10;
+    i0 = wave * (64 * each) + lane;
+    in = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int from = i0 + 64 * i;
+      in |= (uint32_t)(i < each && from < all) << i;
+      pair[i] = M.pair[from < kSmallRows ? from : 0];  // (past the last pair: not used)
+    }
+    __syncthreads();
   }
   // As few passes as 8 bits each allow, of as few bits as they need: every bit of
   // a digit costs six operations a pair.
-  const int all = 32 - __builtin_clz((S.count - 1) | 1), passes = (all + 7) >> 3, bits = (all + passes - 1) / passes;
+  const int all = 32 - __builtin_clz((width - 1) | 1), passes = (all + 7) >> 3, bits = (all + passes - 1) / passes;
   const uint32_t mask = (1u << bits) - 1u;
   for (int shift = 0;; shift += bits) {
     for (int i = tid; i < 16 * 256; i += 1024) (&M.counts[0][0])[i] = 0;
@@ -221,7 +275,7 @@ __global__ __launch_bounds__(1024) void sort_small_kernel(Sort S, uint32_t *__re
       uint64_t same = __ballot(have);
       int place = 0;
       if (same) {
-        const uint32_t digit = (uint32_t)(key[i] >> shift) & mask;
+        const uint32_t digit = pair[i] >> (kRowBits + shift) & mask;
 #pragma unroll
         for (int b = 0; b < 8; ++b)
           if (b < bits) {
@@ -266,11 +320,7 @@ __global__ __launch_bounds__(1024) void sort_small_kernel(Sort S, uint32_t *__re
     const bool last = shift + bits >= all;
 #pragma unroll
     for (int i = 0; i < kEach; ++i)
-      if ((in >> i) & 1) {
-        const int at = M.counts[wave][(uint32_t)(key[i] >> shift) & mask] + rank[i];
-        M.key[at] = key[i];
-        M.row[at] = (uint16_t)row[i];
-      }
+      if ((in >> i) & 1) M.pair[M.counts[wave][pair[i] >> (kRowBits + shift) & mask] + rank[i]] = pair[i];
     __syncthreads();
     if (last) break;
     in = 0;
@@ -278,16 +328,15 @@ __global__ __launch_bounds__(1024) void sort_small_kernel(Sort S, uint32_t *__re
     for (int i = 0; i < kEach; ++i) {
       const int at = i0 + 64 * i;
       in |= (uint32_t)(i < each && at < (int)M.total) << i;
-      key[i] = M.key[at < kSmallRows ? at : 0];  // (past the last pair: not used)
-      row[i] = M.row[at < kSmallRows ? at : 0];
+      pair[i] = M.pair[at < kSmallRows ? at : 0];
     }
     __syncthreads();
   }
   for (int i = tid; i < (int)M.total; i += 1024) {
-    S.key_out[i] = M.key[i];
-    S.row_out[i] = M.row[i];
+    S.key_out[begin + i] = low + (int)(M.pair[i] >> kRowBits);
+    S.row_out[begin + i] = (int)(M.pair[i] & (kSmallRows - 1));
   }
-  if (tid == 0) *S.total = M.total;
+  if (tid == 0 && blockIdx.x == gridDim.x - 1) *S.total = (uint32_t)begin + M.total;
 }
 
 // Sums of the sorted rows: a wave takes one chunk of pairs and 512 columns (8 a
@@ -512,7 +561,11 @@ trellis_status trellis_embed_backward(const uint16_t *dout, const int32_t *token
       return TRELLIS_E_HIP;
     ready[dev] = true;
     const Sort s{tokens, nullptr, nullptr, pairs[0], pairs[1], nullptr, total, m, first, count, 0, 0};
-    hipLaunchKernelGGL(sort_small_kernel, dim3(1), dim3(1024), sizeof(SmallSort), stream, s, arrived, chunks * columns);
+    int width = (count + kSmallGroups - 1) / kSmallGroups;
+    if (width < kSmallWidth) width = kSmallWidth;
+    if (count < width || (m <= 1024 && count <= kMostWidth)) width = count;
+    hipLaunchKernelGGL(sort_small_kernel, dim3((unsigned)((count + width - 1) / width)), dim3(1024), sizeof(SmallSort), stream, s,
+                       width, arrived, chunks * columns);
   } else {
     hipLaunchKernelGGL(clear_kernel, dim3((unsigned)((chunks * columns + 255) / 256)), dim3(256), 0, stream, arrived,
                        (int64_t)chunks * columns);
