@@ -94,6 +94,25 @@ def test_gradient_of_rows_sorted_by_several_workgroups(m, count, kind):
     test_embed_backward(m, 256, count, kind)
 
 
+# runs of 16-row chunks that begin and end inside and at the borders of 32 neighbouring chunks
+@pytest.mark.parametrize("m,runs", [(16384, [16384]), (16384, [512, 512, 15360]), (16384, [500, 40, 600, 4, 8192, 7000, 48]), (600, [30, 514, 56]),
+                                    (1040, [16, 1024]), (1056, [16, 1040]), (1024, [1008, 16]), (1040, [511, 2, 511, 16]), (40000, [9, 20000, 19000, 991])])
+@pytest.mark.parametrize("k", [256, 1280])
+def test_gradient_of_long_runs(m, runs, k):
+    import torch
+
+    print(f"embed_backward {m} {runs} {k}", flush=True)
+    rng = np.random.default_rng(m + len(runs))
+    tokens = np.repeat(np.arange(len(runs), dtype=np.int32), runs)
+    bits, dout = ref.bf16(rng.standard_normal((m, k)))
+    args = to_dev_bf16(bits), dev(tokens), 0, len(runs) + 1
+    got = tp.embed_backward(*args)
+    value, bound = ref.embed_gradient(dout, tokens, 0, len(runs) + 1, 1.0)
+    ref.check("dextra", bf16_bits_to_f32(from_dev_bf16(got)), value, bound)
+    for _ in range(3):
+        assert torch.equal(tp.embed_backward(*args), got)
+
+
 @pytest.mark.parametrize("m", [1024, 1025, 16384, 16385])
 @pytest.mark.parametrize("count", [2**18, 2**18 + 1, 2**22])
 def test_gradient_of_the_most_trained_rows(m, count):
