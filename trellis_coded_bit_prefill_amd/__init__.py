@@ -220,6 +220,19 @@ def _check_tensor(name, t, dtypes, ndim, device=None):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
+def _written(*outs):
+    """Tells autograd that the library has written these tensors of the caller's
+    (None: it allocated that one itself): they are written by their addresses,
+    which moves no version counter, and a graph that has saved one of them would
+    go on with what stands there now. With the counter moved, its backward pass
+    raises as after any operation in place."""
+    given = [t for t in outs if t is not None]
+    if given:
+        import torch
+
+        torch.autograd.graph.increment_version(given)
+
+
 def _dtypes():
     import torch
 
@@ -358,6 +371,7 @@ def decode(codes, scales, k: int, bits: int, out=None):
         raise ValueError(f"codes has {codes.shape[1]} words per row, expected K*bits/32 = {k * bits // 32}")
     if scales.shape[0] != n:
         raise ValueError("scales must have one entry per row")
+    given = out
     if out is None:
         out = torch.empty((n, k), dtype=torch.bfloat16, device=codes.device)
     _check_tensor("out", out, bf, 2, codes.device)
@@ -365,6 +379,7 @@ def decode(codes, scales, k: int, bits: int, out=None):
         raise ValueError("out must be [N, K]")
     decode_raw(codes.data_ptr(), scales.data_ptr(), geom(n, k, bits), out.data_ptr(),
                _stream_handle(codes.device))
+    _written(given)
     return out
 
 
@@ -399,6 +414,7 @@ def _linear(entry, x, codes, scales, bits: int, out=None):
         raise ValueError(f"codes has {codes.shape[1]} words per row, expected K*bits/32 = {k * bits // 32}")
     if scales.shape[0] != n:
         raise ValueError("scales must have one entry per row")
+    given = out
     if out is None:
         out = torch.empty((m, n), dtype=torch.bfloat16, device=x.device)
     _check_tensor("out", out, bf, 2, x.device)
@@ -406,6 +422,7 @@ def _linear(entry, x, codes, scales, bits: int, out=None):
         raise ValueError("out must be [M, N]")
     entry(x.data_ptr(), m, codes.data_ptr(), scales.data_ptr(), geom(n, k, bits), out.data_ptr(),
           _stream_handle(x.device))
+    _written(given)
     return out
 
 
@@ -432,6 +449,7 @@ def prefill_packed(xs, codes, scales, bits: int, outs=None):
             raise ValueError("every input must have the same K")
     if codes.shape[1] * 32 != k * bits:
         raise ValueError(f"codes has {codes.shape[1]} words per row, expected K*bits/32 = {k * bits // 32}")
+    given = () if outs is None else outs
     if outs is None:
         outs = [torch.empty((x.shape[0], n), dtype=torch.bfloat16, device=codes.device) for x in xs]
     if len(outs) != len(xs):
@@ -443,6 +461,7 @@ def prefill_packed(xs, codes, scales, bits: int, outs=None):
     prefill_packed_raw([x.data_ptr() if x.shape[0] else 0 for x in xs], [x.shape[0] for x in xs],
                        codes.data_ptr(), scales.data_ptr(), geom(n, k, bits),
                        [o.data_ptr() if o.shape[0] else 0 for o in outs], _stream_handle(codes.device))
+    _written(*given)
     return outs
 
 
@@ -464,6 +483,7 @@ def gate_up(x, codes_gate, scales_gate, codes_up, scales_up, bits: int, out=None
         raise ValueError(f"codes have {codes_gate.shape[1]} words per row, expected K*bits/32 = {k * bits // 32}")
     if scales_gate.shape[0] != n or scales_up.shape[0] != n:
         raise ValueError("scales must have one entry per row")
+    given = out
     if out is None:
         out = torch.empty((m, n), dtype=torch.bfloat16, device=x.device)
     _check_tensor("out", out, bf, 2, x.device)
@@ -471,6 +491,7 @@ def gate_up(x, codes_gate, scales_gate, codes_up, scales_up, bits: int, out=None
         raise ValueError("out must be [M, N]")
     gate_up_raw(x.data_ptr(), m, codes_gate.data_ptr(), scales_gate.data_ptr(), codes_up.data_ptr(),
                 scales_up.data_ptr(), geom(n, k, bits), out.data_ptr(), _stream_handle(x.device))
+    _written(given)
     return out
 
 
@@ -597,8 +618,9 @@ def adapters(x, codes, scales, bits: int, a, b, gain, index, out=None):
         from ._autograd import Adapters
 
         return Adapters.apply(x, codes, scales, bits, a, b, gain, index)
-    out = _output("out", out, (m, n), device)
+    given, out = out, _output("out", out, (m, n), device)
     adapters_raw(x.data_ptr(), m, *packed, geom(n, k, bits), *set_, out.data_ptr(), _stream_handle(device))
+    _written(given)
     return out
 
 
@@ -613,11 +635,13 @@ def adapters_backward(dout, x, codes, scales, bits: int, a, b, gain, index, dx=N
     dout_ptr = _address("dout", dout, _kinds()[1], (m, n), device)
     set_ = _adapter_addresses(a, b, gain, index, m, n, k, device)
     count, rank = set_[-2:]
+    given = dx, da, db
     dx = _output("dx", dx, (m, k), device)
     da = _output("da", da, (count, rank, k), device)
     db = _output("db", db, (count, n, rank), device)
     adapters_backward_raw(dout_ptr, x.data_ptr(), m, *packed, geom(n, k, bits), *set_, dx.data_ptr(), da.data_ptr(),
                           db.data_ptr(), _stream_handle(device))
+    _written(*given)
     return dx, da, db
 
 
@@ -639,11 +663,12 @@ def gated(x, codes_gate, scales_gate, codes_up, scales_up, bits: int, out=None, 
         from ._autograd import Gated
 
         return Gated.apply(x, codes_gate, scales_gate, codes_up, scales_up, bits, keep)
-    h = _output("out", out, (m, n), device)
+    given, h = out, _output("out", out, (m, n), device)
     gate = _output("gate", None, (m, n), device) if keep else None
     up = _output("up", None, (m, n), device) if keep else None
     gated_raw(x.data_ptr(), m, *packed, geom(n, k, bits), h.data_ptr(), gate.data_ptr() if keep else 0,
               up.data_ptr() if keep else 0, _stream_handle(device))
+    _written(given)
     return (h, gate, up) if keep else h
 
 
@@ -660,11 +685,13 @@ def gated_backward(dh, gate, up, codes_gate, scales_gate, codes_up, scales_up, b
     k = codes_gate.shape[1] * 32 // bits if bits in (2, 3, 4) else 0
     packed = (*_packed_address(codes_gate, scales_gate, n, k, bits, device, "_gate"),
               *_packed_address(codes_up, scales_up, n, k, bits, device, "_up"))
+    given = dx, dgate, dup
     dx = _output("dx", dx, (m, k), device)
     dgate = _output("dgate", dgate, (m, n), device)
     dup = _output("dup", dup, (m, n), device)
     gated_backward_raw(dh.data_ptr(), *kept, m, *packed, geom(n, k, bits), dx.data_ptr(), dgate.data_ptr(),
                        dup.data_ptr(), _stream_handle(device))
+    _written(*given)
     return dx, dgate, dup
 
 
@@ -763,12 +790,14 @@ def distill(x, codes, scales, bits: int, index, logits, temperature: float = 1.0
 def loss_backward(dloss, dx, out=None):
     """The gradient of x from the gradients dloss [M] (float32) of the rows'
     losses and the dx [M, K] that cross_entropy() or distill() kept: dloss[r]
-    dx[r], rounded once more. out may be dx. Not differentiated further:
+    dx[r], rounded once more. out may be dx, unless that is a recorded call's,
+    which keeps it: its backward pass then raises. Not differentiated further:
     autograd records nothing of this call."""
     m, k, device = _rows_of("dx", dx)
     dloss_ptr = _address("dloss", dloss, _kinds()[3], (m,), device)
-    out = _output("out", out, (m, k), device)
+    given, out = out, _output("out", out, (m, k), device)
     loss_backward_raw(dloss_ptr, dx.data_ptr(), m, k, out.data_ptr(), _stream_handle(device))
+    _written(given)
     return out
 
 
@@ -799,12 +828,14 @@ def embed(tokens, codes, scales, k: int, bits: int, scale: float = 1.0, extra=No
         from ._autograd import Embed
 
         return Embed.apply(tokens, codes, scales, k, bits, scale, extra)
+    given = out
     if out is None:
         out = _new((m, k), "bf16", device)
     else:
         _address("out", out, _kinds()[1], (m, k), device)
     embed_raw(tokens.data_ptr(), m, *packed, _geom_of(n, k, bits), scale, extra_ptr if count else 0, count, out.data_ptr(),
               _stream_handle(device))
+    _written(given)
     return out
 
 
@@ -818,6 +849,7 @@ def embed_backward(dout, tokens, first: int, count: int, scale: float = 1.0, dex
     tokens_ptr = _address("tokens", tokens, _kinds()[4], (m,), device)
     if not 1 <= count <= MAX_TRAINED:
         raise ValueError(f"count must be in [1, {MAX_TRAINED}], got {count}")
-    dextra = _output("dextra", dextra, (count, k), device)
+    given, dextra = dextra, _output("dextra", dextra, (count, k), device)
     embed_backward_raw(dout.data_ptr(), tokens_ptr, m, k, first, count, scale, dextra.data_ptr(), _stream_handle(device))
+    _written(given)
     return dextra
