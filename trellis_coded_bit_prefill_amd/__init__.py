@@ -188,7 +188,7 @@ def _stream_handle(device) -> int:
     """The current stream of `device`, which must be the current device (the
     library works on the current device)."""
     global _current_device, _raw_stream
-    if _current_device is None:
+    if _raw_stream is None:  # (the last one set: another thread's first call finds both or looks them up itself)
         import torch
 
         _current_device = torch.cuda.current_device
