@@ -53,3 +53,14 @@ def test_stream_handle(monkeypatch):
     got = interleaved(monkeypatch, ("_current_device", "_raw_stream"), tp._stream_handle,
                       lambda: tp._stream_handle(torch.device("cuda", 0)))
     assert len(got) > 20 and set(got) == {7}
+
+
+def test_new_tensors(monkeypatch):
+    got = interleaved(monkeypatch, ("_empty", "_f32", "_bf16"), tp._new, lambda: tp._new((2, 3), "bf16", "cpu"))
+    assert len(got) > 10 and all(getattr(t, "dtype", t) == torch.bfloat16 for t in got)
+
+
+def test_kinds(monkeypatch):
+    got = interleaved(monkeypatch, ("_types", "_grad_enabled", "_forward_ad"), tp._kinds,
+                      lambda: (tp._kinds()[3], tp._grad_enabled(), tp._forward_ad._current_level))
+    assert len(got) > 10 and set(got) == {((torch.float32,), True, -1)}

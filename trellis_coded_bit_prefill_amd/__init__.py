@@ -714,7 +714,8 @@ def _new(shape, dtype, device):
     if _empty is None:
         import torch
 
-        _empty, _f32, _bf16 = torch.empty, torch.float32, torch.bfloat16
+        _f32, _bf16 = torch.float32, torch.bfloat16
+        _empty = torch.empty  # (last: another thread's first call finds all three or looks them up itself)
     return _empty(shape, dtype=_f32 if dtype == "f32" else _bf16, device=device)
 
 
