@@ -140,3 +140,16 @@ def test_given_outputs_are_known_to_be_written(plain, monkeypatch):
     with torch.inference_mode():  # (such tensors have no counter)
         out = torch.empty(M, N, dtype=torch.bfloat16)
         assert tp.adapters(t["x"], *layer, *set_, out=out) is out
+
+
+@pytest.mark.parametrize("what", ["adapters", "gated", "cross_entropy", "distill", "embed"])
+def test_a_refused_capture_names_the_calls_to_make(monkeypatch, what):
+    import re
+
+    from trellis_coded_bit_prefill_amd import _autograd
+
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    with pytest.raises(ValueError, match=f"{what}.. is not differentiated") as refused:
+        _autograd.refuse_capture(what)
+    named = [f for f in re.findall(r"(\w+)\(\)", str(refused.value)) if f != "no_grad"]
+    assert what in named and any(f.endswith("_backward") for f in named) and all(hasattr(tp, f) for f in named)

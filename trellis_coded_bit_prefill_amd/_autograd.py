@@ -17,8 +17,9 @@ def refuse_capture(what):
     live, and a stream outside the capture that takes part ends the capture or
     the process. The calls themselves can be captured under torch.no_grad()."""
     if torch.cuda.is_current_stream_capturing():
+        gradients = "keep=True and loss_backward()" if what in ("cross_entropy", "distill") else f"{what}_backward()"
         raise ValueError(f"{what}() is not differentiated while its stream is captured: capture it under "
-                         f"torch.no_grad(), with {what}_backward() for the gradients")
+                         f"torch.no_grad(), with {gradients} for the gradients")
 
 
 def _rows(grad):
