@@ -153,3 +153,22 @@ def test_a_refused_capture_names_the_calls_to_make(monkeypatch, what):
         _autograd.refuse_capture(what)
     named = [f for f in re.findall(r"(\w+)\(\)", str(refused.value)) if f != "no_grad"]
     assert what in named and any(f.endswith("_backward") for f in named) and all(hasattr(tp, f) for f in named)
+
+
+def embed(t, extra, **kw):
+    return tp.embed(t["tokens"], t["codes"], t["scales"], K, BITS, extra=extra, **kw)
+
+
+def test_embedding_gradients(plain):
+    extra, dout = leaf(plain["extra"]), draw(M, K, seed=4)
+    embed(plain, extra, scale=3.0).backward(dout)
+    assert torch.equal(extra.grad, tp.embed_backward(dout, plain["tokens"], N, COUNT, scale=3.0))
+
+
+def test_the_gradient_of_no_trained_rows(plain):
+    """extra [0, K]: accepted forward, an empty gradient backward."""
+    extra = leaf(plain["extra"][:0])
+    out = embed(plain, extra)
+    assert torch.equal(out, embed(plain, None)) and out.requires_grad
+    out.sum().backward()
+    assert extra.grad.shape == (0, K) and extra.grad.dtype == torch.bfloat16

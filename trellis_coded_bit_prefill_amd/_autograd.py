@@ -124,4 +124,6 @@ class Embed(torch.autograd.Function):
     def backward(ctx, dout):
         refuse_capture("embed")
         tokens, = ctx.saved_tensors
+        if ctx.at[1] == 0:  # (no trained rows: embed_backward() takes one at least)
+            return (None,) * 6 + (dout.new_empty((0, dout.shape[1])),)
         return (None,) * 6 + (tp.embed_backward(_rows(dout), tokens, *ctx.at),)
