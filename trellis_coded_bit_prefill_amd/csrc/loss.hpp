@@ -314,16 +314,17 @@ __global__ __launch_bounds__(256) void whole_row_kernel(Lists L, const float *__
 // dx = dloss[row] * dx: a factor a row.
 __global__ __launch_bounds__(256) void scale_rows_kernel(const float *__restrict__ f, const uint16_t *__restrict__ src,
                                                          int64_t vectors, int per_row, uint16_t *__restrict__ dst) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= vectors) return;
-  const float s = f[i / per_row];
-  const u32x4 v = reinterpret_cast<const u32x4 *>(src)[i];
-  u32x4 o;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < vectors; i += (int64_t)gridDim.x * 256) {
+    const float s = f[i / per_row];
+    const u32x4 v = reinterpret_cast<const u32x4 *>(src)[i];
+    u32x4 o;
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    o[e] = (uint32_t)bf16_of(s * bf16_half(v[e], 0)) | ((uint32_t)bf16_of(s * bf16_half(v[e], 1)) << 16);
-  reinterpret_cast<u32x4 *>(dst)[i] = o;
+    for (int e = 0; e < 4; ++e)
+      o[e] = (uint32_t)bf16_of(s * bf16_half(v[e], 0)) | ((uint32_t)bf16_of(s * bf16_half(v[e], 1)) << 16);
+    reinterpret_cast<u32x4 *>(dst)[i] = o;
+  }
 }
+constexpr int64_t kScaleGroups = 1 << 22;  // workgroups at most (a launch has fewer than 2^32 threads); beyond, a thread takes several
 
 // ---- many rows ------------------------------------------------------------------
 
@@ -1110,7 +1111,8 @@ trellis_status trellis_loss_backward(const float *dloss, const uint16_t *dx, int
   if (!on(dloss, 4) || !on(dx, 16) || !on(out, 16)) return TRELLIS_E_ALIGN;
   const int64_t vectors = (int64_t)m * (k / 8);
   (void)hipGetLastError();
-  hipLaunchKernelGGL(scale_rows_kernel, dim3((unsigned)((vectors + 255) / 256)), dim3(256), 0,
+  const int64_t groups = (vectors + 255) / 256 < kScaleGroups ? (vectors + 255) / 256 : kScaleGroups;
+  hipLaunchKernelGGL(scale_rows_kernel, dim3((unsigned)groups), dim3(256), 0,
                      reinterpret_cast<hipStream_t>(hip_stream), dloss, dx, vectors, k / 8, out);
   return hipGetLastError() == hipSuccess ? TRELLIS_OK : TRELLIS_E_HIP;
 }
