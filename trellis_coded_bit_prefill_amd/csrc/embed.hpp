@@ -62,6 +62,8 @@ __global__ __launch_bounds__(256) void embed_kernel(const int32_t *__restrict__ 
   }
 }
 
+constexpr int64_t kEmbedWaves = 1 << 25;  // of a launch
+
 // ---- gradient: rows sorted by token -------------------------------------------
 // A stable radix sort of (trained row, row of dout), eight bits a pass, each
 // pass: digits counted by 2048 rows, the counts' running sums, the rows placed.
@@ -547,10 +549,12 @@ trellis_status trellis_embed(const int32_t *tokens, int32_t m, const uint32_t *c
   hipStream_t stream = reinterpret_cast<hipStream_t>(hip_stream);
   const int blocks = g.k >> 8;
   // One pair of blocks a wave until the card is full (8192 waves), then up to
-  // four, which share the token's and the scale's loads.
+  // four, which share the token's and the scale's loads; more only for outputs
+  // beyond 128 GiB (a launch has fewer than 2^32 threads).
   const int both = (blocks + 1) / 2;
   int pairs = (int)((int64_t)m * both / 8192);
   pairs = pairs < 1 ? 1 : pairs > 4 ? 4 : pairs;
+  while ((int64_t)m * ((both + pairs - 1) / pairs) > kEmbedWaves) pairs *= 2;
   const int per_row = (both + pairs - 1) / pairs;
   const int64_t waves = (int64_t)m * per_row;
   const dim3 grid((unsigned)((waves + 3) / 4));
