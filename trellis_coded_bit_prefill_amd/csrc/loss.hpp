@@ -311,9 +311,9 @@ __global__ __launch_bounds__(256) void whole_row_kernel(Lists L, const float *__
   if (S.first[tid] && alive) o[S.at[tid]] = bf16_of(L.temperature * S.add[tid]);
 }
 
-// dx = dloss[row] * dx: a factor a row.
-__global__ __launch_bounds__(256) void scale_rows_kernel(const float *__restrict__ f, const uint16_t *__restrict__ src,
-                                                         int64_t vectors, int per_row, uint16_t *__restrict__ dst) {
+// dst = dloss[row] * src: a factor a row. (dst may be src: neither is __restrict__.)
+__global__ __launch_bounds__(256) void scale_rows_kernel(const float *__restrict__ f, const uint16_t *src, int64_t vectors,
+                                                         int per_row, uint16_t *dst) {
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < vectors; i += (int64_t)gridDim.x * 256) {
     const float s = f[i / per_row];
     const u32x4 v = reinterpret_cast<const u32x4 *>(src)[i];
