@@ -129,7 +129,7 @@ typedef enum trellis_status {
     TRELLIS_E_HIP = -5,      /* the HIP runtime reported a launch error */
     TRELLIS_E_SCRATCH = -6,  /* trellis_prefill_noalloc: the call's workspace exceeds the fixed scratch */
     TRELLIS_E_ADAPTERS = -7, /* the number of adapters or their rank outside the accepted range */
-  TRELLIS_E_RANGE = -8     /* listed entries, temperature, trained rows or scale outside the accepted range */
+    TRELLIS_E_RANGE = -8     /* listed entries, temperature, trained rows or scale outside the accepted range */
 } trellis_status;
 
 /* 1 if (g, m) is inside the accepted domain of trellis_prefill, else 0.

@@ -1566,7 +1566,7 @@ struct DenseShape {
   double us;           // what the product's rounds are reckoned to take
   size_t operand_bytes, row_bytes, partial_bytes;
 };
-DenseShape dense_shape(int kind, trellis_geom g, int32_t m, int matrices, int cus, int64_t limit = kOperandBytes) {
+DenseShape dense_shape(int kind, trellis_geom g, int32_t m, int matrices, int cus) {
   DenseShape s{};
   s.matrices = matrices;
   const bool t = kind == kTransposed;
@@ -1585,7 +1585,7 @@ DenseShape dense_shape(int kind, trellis_geom g, int32_t m, int matrices, int cu
   // in seven).
   const int64_t mt = (m + kDenseRows - 1) / kDenseRows;
   const int64_t tile_bytes = (int64_t)s.steps * 1024;
-  const bool several = s.tiles > 16 && tile_bytes * s.tiles > limit;  // launches
+  const bool several = s.tiles > 16 && tile_bytes * s.tiles > kOperandBytes;  // launches
   double best = 0;
   for (int nt = 8; nt >= 4; --nt) {
     if (kind == kGated && nt % 2) continue;
@@ -1593,7 +1593,7 @@ DenseShape dense_shape(int kind, trellis_geom g, int32_t m, int matrices, int cu
     // go in slabs of 16 tiles and multiples of it: of whole workgroup tiles for
     // nt = 4 and 8 alone (the rest of a cut one would be stored over the next
     // slab's columns).
-    if (several && nt % 4 && tile_bytes * 16 * nt > limit) continue;
+    if (several && nt % 4 && tile_bytes * 16 * nt > kOperandBytes) continue;
     const int64_t wg = mt * ((s.tiles + 2 * nt - 1) / (2 * nt));
     for (int splits = 1; splits == 1 || (splits <= 8 && splits <= s.steps / 16); ++splits) {
       const double rounds = (double)((wg * splits + cus - 1) / cus);
@@ -1606,10 +1606,10 @@ DenseShape dense_shape(int kind, trellis_geom g, int32_t m, int matrices, int cu
       }
     }
   }
-  int64_t slab = limit / tile_bytes / (16 * s.nt) * (16 * s.nt);  // whole workgroup tiles, fours and pairs
+  int64_t slab = kOperandBytes / tile_bytes / (16 * s.nt) * (16 * s.nt);  // whole workgroup tiles, fours and pairs
   const int forced = g_tiles.load(std::memory_order_relaxed);
   if (forced > 0) slab = ((int64_t)forced + 16 * s.nt - 1) / (16 * s.nt) * (16 * s.nt);
-  if (slab == 0) slab = limit / tile_bytes / 16 * 16;  // long contractions: whole 256-column blocks,
+  if (slab == 0) slab = kOperandBytes / tile_bytes / 16 * 16;  // long contractions: whole 256-column blocks,
   if (slab == 0) slab = 16;                                    // one at least (512 bytes per row of W)
   if (slab > s.tiles) slab = s.tiles;
   s.slab = slab;
