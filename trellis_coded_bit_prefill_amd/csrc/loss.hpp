@@ -131,7 +131,7 @@ __device__ __forceinline__ bool row_single(const Lists &L, int64_t row, f32x2 re
   int at = L.index[row];
   if (at >= L.n) at = -1;
   const bool valid = at >= 0;
-  const float z = valid && L.logits ? L.logits[row] * L.scale2 : 0.f;
+  const float z = valid && L.logits ? L.logits[row] : 0.f;
   const bool alive = valid && z != -__builtin_inff();
   const float q = (z - z) + 1.f;  // softmax of one logit; NaN where it is not a number
   const float l2 = valid ? L.listed[row] : 0.f;
@@ -164,13 +164,15 @@ __device__ bool row_list(const Lists &L, int64_t row, f32x2 rest, bool whole, Ro
   if (at >= L.n) at = -1;
   float z = -inf, l2 = -inf;
   if (at >= 0) {
-    z = L.logits ? L.logits[row * L.top + j] * L.scale2 : 0.f;
+    z = L.logits ? L.logits[row * L.top + j] : 0.f;
     l2 = L.listed[row * L.top + j];
   }
   S.at[j] = at;
   // q: softmax of the list. A NaN among the teacher's logits is a NaN in the sum.
+  // The difference first: the lowest finite logit, a mask's, times log2(e) / T
+  // would be -inf, which is no entry, and the largest inf.
   const float zmax = fmaxf(max_256(z, S.red[0]), kLowest);
-  const float e = at >= 0 ? __builtin_amdgcn_exp2f(z - zmax) : 0.f;
+  const float z2 = (z - zmax) * L.scale2, e = at >= 0 ? __builtin_amdgcn_exp2f(z2) : 0.f;
   const float total = sum_256(e, S.red[1]);
   const bool alive = total != 0.f;
   const float q = alive ? e / total : 0.f;
@@ -195,7 +197,7 @@ __device__ bool row_list(const Lists &L, int64_t row, f32x2 rest, bool whole, Ro
   S.first[j] = first;
   S.qs[j] = qs;
   S.add[j] = !first ? 0.f : alone ? qs * (-others / sum) : here / sum - qs;
-  float term = q != 0.f ? q * (z - zmax - __builtin_amdgcn_logf(total)) * kLn2 : 0.f;  // q log q
+  float term = q != 0.f ? q * (z2 - __builtin_amdgcn_logf(total)) * kLn2 : 0.f;  // q log q
   if (!alone) {
     if (q != 0.f) term += q * (lse2 - l2) * kLn2;
   } else if (first) {
