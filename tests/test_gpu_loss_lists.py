@@ -45,3 +45,47 @@ def test_teachers_of_the_largest_and_lowest_logits(path, m, n, top, t):  # noqa:
     logits = d["logits"].copy()
     logits[:, 1::2] = LOWEST
     check("masked", d, t, distill(d, d["index"], logits, t), ref.loss(d, d["index"], logits, t))
+
+
+@pytest.mark.parametrize("top", [2, 5, 70])
+@pytest.mark.parametrize("m,n,t", [(5, 260, 1.0), (3, 20004, 2.0), (300, 260, 0.5), (70, 1028, 1.0)])
+def test_entries_of_no_logit_are_none(path, m, n, top, t):  # noqa: F811
+    """Bit for bit what the same list gives with those entries outside the vocabulary."""
+    import torch
+
+    print(f"-inf entries {m} {n} top {top} T {t} {path}", flush=True)
+    rng = np.random.default_rng(m * 3 + n + top)
+    d = ref.draw(rng, m, n, 256, 4, top=top)
+    index, logits = d["index"].copy(), d["logits"].copy()
+    index[:, -1] = index[:, 0]  # named twice, in some rows once with a logit and once without
+    gone = rng.random((m, top)) < 0.5
+    gone[::3, 1:] = True        # rows of one entry, or none
+    logits[gone] = -np.inf
+    hidden = np.where(gone, -1, index).astype(np.int32)
+    got, want = distill(d, index, logits, t), distill(d, hidden, logits, t)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    check("none", d, t, got, ref.loss(d, hidden, logits, t))
+
+
+@pytest.mark.parametrize("n", [64, 20004])
+@pytest.mark.parametrize("m", [3, 300])
+def test_a_certain_entry_beside_entries_of_no_logit(path, m, n):  # noqa: F811
+    """A list of one entry, padded with others whose logits are -inf: 1 - p and the loss far below float32's step at 1
+    come from the others' sum, as in a list of that entry alone."""
+    print(f"certain entry, padded list {m} {n} {path}", flush=True)
+    rng = np.random.default_rng(8 + n)
+    d = ref.draw(rng, m, n, 512, 4, top=4)
+    d["index"] = (d["index"][:, :1] + np.array([0, 1, 7, 0])) % n  # the last names the first again
+    w = d["w"][d["index"][:, 0]]
+    lean = np.linspace(15, 60, m)[:, None]
+    d["x_bits"], d["x"] = ref.bf16(0.1 * rng.standard_normal((m, 512)) + lean * w / (w ** 2).sum(1, keepdims=True))
+    logits = np.full((m, 4), -np.inf, np.float32)
+    logits[:, 0] = rng.standard_normal(m)
+    logits[::2, 3] = 0.5
+    got = distill(d, d["index"].astype(np.int32), logits, 1.0)
+    want = ref.loss(d, np.where(logits > -np.inf, d["index"], -1), logits, 1.0)
+    check("padded", d, 1.0, got, want)
+    alone = np.arange(m) % 2 == 1  # (an entry named twice has its q in two parts, whose logarithms are off by 2^-24)
+    small = alone & (want["loss"][0] < 1e-8)
+    assert small.any()
+    np.testing.assert_allclose(got[0].cpu().numpy()[small], want["loss"][0][small], rtol=1e-4)

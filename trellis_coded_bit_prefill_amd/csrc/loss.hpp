@@ -32,6 +32,16 @@ struct Lists {
   float *loss, *lse;
 };
 
+// The vocabulary entry at a place of the lists, -1 where there is none: an index
+// outside, or a teacher's logit of -inf. Such a place must not count, or a row of
+// one entry beside it would lose the digits of its 1 - p. (Lists of one place keep
+// it whatever its logit: row_single puts it back into the sum.)
+__device__ __forceinline__ int list_entry(const Lists &L, int64_t place) {
+  const int at = L.index[place];
+  if (at < 0 || at >= L.n) return -1;
+  return L.top > 1 && L.logits[place] == -__builtin_inff() ? -1 : at;
+}
+
 // (largest, sum of 2^(v - largest)) of two parts of a row; a part without finite
 // entries has kLowest and 0.
 __device__ __forceinline__ f32x2 join_stats(f32x2 a, f32x2 b) {
@@ -66,8 +76,8 @@ __global__ __launch_bounds__(256) void row_stats_kernel(Lists L, const float *__
   if (tid < kStatSpan / 32) listed[tid] = 0u;
   __syncthreads();
   if (tid < L.top) {
-    const int at = L.index[row * L.top + tid];
-    if (at >= first && at < L.n && at - first < kStatSpan) {
+    const int at = list_entry(L, row * L.top + tid);
+    if (at >= first && at - first < kStatSpan) {
       L.listed[row * L.top + tid] = l[at] * L.scale2;
       atomicOr(&listed[(at - first) >> 5], 1u << (at & 31));
     }
@@ -160,11 +170,10 @@ __device__ bool row_list(const Lists &L, int64_t row, f32x2 rest, bool whole, Ro
   const int j = threadIdx.x;
   const float inf = __builtin_inff();
   if (L.top == 1) return row_single(L, row, rest, whole, S, write);
-  int at = j < L.top ? L.index[row * L.top + j] : -1;
-  if (at >= L.n) at = -1;
+  const int at = j < L.top ? list_entry(L, row * L.top + j) : -1;
   float z = -inf, l2 = -inf;
   if (at >= 0) {
-    z = L.logits ? L.logits[row * L.top + j] : 0.f;
+    z = L.logits[row * L.top + j];
     l2 = L.listed[row * L.top + j];
   }
   S.at[j] = at;
@@ -266,8 +275,7 @@ __global__ __launch_bounds__(256) void whole_row_kernel(Lists L, const float *__
     v[i] = f32x4{-inf, -inf, -inf, -inf};
     if (c < L.n) v[i] = *reinterpret_cast<const f32x4 *>(l + c);
   }
-  int at = tid < L.top ? L.index[row * L.top + tid] : -1;
-  if (at >= L.n) at = -1;
+  const int at = tid < L.top ? list_entry(L, row * L.top + tid) : -1;
   if (tid < L.top) L.listed[row * L.top + tid] = at >= 0 ? l[at] * L.scale2 : 0.f;
   for (int i = tid; i < (L.n + 31) / 32; i += 256) listed[i] = 0u;
   __syncthreads();
@@ -605,11 +613,11 @@ __device__ __forceinline__ int sole_entry(const Lists &L, int64_t row, int lane)
   int one = -1;
   bool several = false;
   for (int j0 = 0; j0 < L.top; j0 += 64) {
-    const int at = j0 + lane < L.top ? L.index[row * L.top + j0 + lane] : -1;
-    const uint64_t named = __ballot(at >= 0 && at < L.n);
+    const int at = j0 + lane < L.top ? list_entry(L, row * L.top + j0 + lane) : -1;
+    const uint64_t named = __ballot(at >= 0);
     if (!named) continue;
     if (one < 0) one = __builtin_amdgcn_readlane(at, __builtin_ctzll(named));
-    several = several || __any(at >= 0 && at < L.n && at != one);
+    several = several || __any(at >= 0 && at != one);
   }
   return several ? -1 : one;
 }
@@ -628,8 +636,8 @@ __global__ __launch_bounds__(256) void listed_kernel(Lists L, int32_t *__restric
     if (lane == 0) sole[row] = one;
   }
   if (j >= L.top) return;
-  const int at = __builtin_amdgcn_readfirstlane(L.index[row * L.top + j]);
-  if (at < 0 || at >= L.n) return;
+  const int at = __builtin_amdgcn_readfirstlane(list_entry(L, row * L.top + j));
+  if (at < 0) return;
   const float s = bf16_bits_to_f32(scales[at]);
   float q, kq;
   alu_row_constants(s, q, kq);
