@@ -89,3 +89,58 @@ def test_a_certain_entry_beside_entries_of_no_logit(path, m, n):  # noqa: F811
     small = alone & (want["loss"][0] < 1e-8)
     assert small.any()
     np.testing.assert_allclose(got[0].cpu().numpy()[small], want["loss"][0][small], rtol=1e-4)
+
+
+@pytest.mark.parametrize("forced,chunk", [((False, 0), 256), ((True, 0), 512)], ids=["few", "many"])
+def test_lists_over_several_chunks_of_rows(forced, chunk):
+    """A vocabulary of 2^20 entries takes 256 or 512 rows at a time: ragged lists of every chunk, the last one short,
+    against the formula in float64 on the GPU, and the first chunk's rows as a call of their own. Bounds as in
+    test_chunks_of_rows (tests/test_gpu_vocabulary_run.py), in units of T; q is off by 2^-18 of itself."""
+    import torch
+
+    print(f"chunks of lists {forced}", flush=True)
+    m, n, k, bits, top, t = 600, 1 << 20, 256, 2, 7, 1.5
+    g = torch.Generator(device="cuda").manual_seed(21)
+    codes = torch.randint(-2**31, 2**31, (n, k * bits // 32), generator=g, device="cuda", dtype=torch.int32)
+    scales = (torch.rand(n, generator=g, device="cuda") * 0.015 + 0.005).bfloat16()
+    x = (torch.randn(m, k, generator=g, device="cuda") * 4).bfloat16()
+    index = torch.randint(0, n, (m, top), generator=g, device="cuda", dtype=torch.int32)
+    logits = torch.randn(m, top, generator=g, device="cuda") * 3
+    length = torch.randint(0, top + 1, (m, 1), generator=g, device="cuda")
+    index.masked_fill_(torch.arange(top, device="cuda") >= length, -1)  # lists of none to all
+    logits[::5, 1] = -float("inf")
+    try:
+        tp.force_path(*forced)
+        got = tp.distill(x, codes, scales, bits, index, logits, temperature=t, keep=True)
+        short = tp.distill(x, codes, scales, bits, index, logits, temperature=t)
+        first = tp.distill(x[:chunk], codes, scales, bits, index[:chunk], logits[:chunk], temperature=t, keep=True)
+    finally:
+        tp.force_path(None)
+    assert all(torch.equal(a[:chunk], b) for a, b in zip(got, first))
+    e24 = 2.0 ** -24
+    w = tp.decode(codes, scales, k, bits).double()
+    largest = w.abs().max()
+    for r0 in range(0, m, 100):
+        r = slice(r0, r0 + 100)
+        l = x[r].double() @ w.T / t
+        lse = torch.logsumexp(l, 1, keepdim=True)
+        there = (index[r] >= 0) & (logits[r] > -float("inf"))
+        z = torch.where(there, logits[r].double() / t, -float("inf"))
+        some = there.any(1, keepdim=True)
+        q = torch.where(some, torch.softmax(torch.where(some, z, 0.0), 1), 0.0)
+        log_q = torch.where(q > 0, q, 1.0).log()
+        at = index[r].clamp(0).long()
+        off = torch.where(q > 0, lse - l.gather(1, at), 0.0)
+        loss = t * t * (q * (log_q + off)).sum(1)
+        d = (l - lse).exp_() * some
+        d.scatter_add_(1, at, -q)
+        dx = t * (d @ w)
+        el = (k * e24 * (x[r].double().abs().sum(1) * largest) + 4 * e24 * 40) / t
+        bound = 2 * el + 2.0 ** -17 + 8 * e24 * lse[:, 0].abs()
+        worst = 2 * bound + 2.0 ** -18 * (1 + log_q.abs().amax(1) + off.abs().amax(1))
+        for o in (got, short):
+            assert ((o[0][r] - loss).abs() <= t * t * worst).all() and ((o[1][r] - lse[:, 0]).abs() <= bound).all()
+        err = (got[2][r].double() - dx).abs()
+        assert (err <= t * 2 * largest * (2 * 2.0 ** -8 + 2 * bound[:, None]) + 2.0 ** -8 * dx.abs()).all()
+        assert (err.norm(dim=1) <= 2.0 ** -7 * dx.norm(dim=1) + 1e-6).all()
+        assert not got[2][r][~some[:, 0]].any() and not got[0][r][~some[:, 0]].any()
