@@ -989,7 +989,13 @@ Plan loss_back_plan(trellis_geom g, int32_t m, int cus) {
 // 131072, losses 267 / 398 at 128 rows, 440 / 400 at 192, 774 / 530 at 333; with
 // gradient 947 / 1019 at 192, 1266 / 1081 at 256, 2521 / 1741 at 509; K = 2048, N =
 // 8192, losses 40 / 54 at 509 rows, 61 / 54 at 640.
-bool loss_by_operands(trellis_geom g, int32_t m, bool keep, int cus) {
+// Lists of several entries cost this way a row of W decoded for each (3.2 G
+// weights a ms), the few rows' way hardly anything, as it has their logits: K =
+// 2048, N = 8192, 1024 rows with lists of 16 69 / 69, of 64 73 / 101, of 256 84 /
+// 232; K = 5120, N = 131072, 1024 rows of 256 2070 / 1857. On five other matrices,
+// lists of 32 and 200 entries among them, the side taken is 0.2% slower than the
+// faster one on average and 8% at most.
+bool loss_by_operands(trellis_geom g, int32_t m, bool keep, int cus, int top = 1) {
   const int forced = g_path.load(std::memory_order_relaxed);
   if (forced >= 0) return forced == 1;
   const Shape f = shape_of(kForward, g, m, 1, cus, true);
@@ -1000,7 +1006,14 @@ bool loss_by_operands(trellis_geom g, int32_t m, bool keep, int cus) {
     const Plan b = loss_back_plan(g, m, cus);
     rows += b.dense ? b.many.us + 6.5 + 0.187 * mb + 0.56 * mn : fused_us(b.fused);
   }
-  return loss_shape(g, m, keep, cus).us + 10 < rows;
+  double many = loss_shape(g, m, keep, cus).us + 10;
+  if (top > 1) {
+    const double entries = (double)m * top;
+    many += 3 + entries * (0.16e-3 + 0.24e-6 * g.k);
+    // (with gradient each workgroup of row_loss_kernel goes through its row's list)
+    rows += entries * (0.055e-3 + (keep && g.n > kWholeRow ? 0.032e-3 * ((g.n + kStatSpan - 1) / kStatSpan) : 0));
+  }
+  return many < rows;
 }
 
 // The logits of a chunk of rows in float32, decoded in the product; then the
@@ -1009,7 +1022,7 @@ trellis_status loss_rows(const uint16_t *x, int32_t m, const uint32_t *codes, co
                          Lists L, uint16_t *dx, hipStream_t stream) {
   int dev = 0, cus = 0;
   TRELLIS_TRY(device(dev, cus));
-  if (loss_by_operands(g, m, dx != nullptr, cus)) return loss_dense(x, m, codes, scales, g, L, dx, stream);
+  if (loss_by_operands(g, m, dx != nullptr, cus, L.top)) return loss_dense(x, m, codes, scales, g, L, dx, stream);
   const int64_t most = kLogitBytes / (4 * (int64_t)g.n) / 16 * 16;  // 64 rows at least: n is at most 2^22
   const int32_t rows = m < most ? m : (int32_t)most;
   // Plans of the full chunks and of the last one; the workspace holds either.
