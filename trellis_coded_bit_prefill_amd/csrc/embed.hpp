@@ -71,6 +71,15 @@ constexpr int64_t kEmbedWaves = 1 << 25;  // of a launch
 constexpr int kSortRows = 2048;   // of a workgroup
 constexpr int kSortWave = kSortRows / 4;
 
+// The wave's LDS accesses before this come before those behind it, other lanes'
+// too. (LDS keeps a wave's accesses in order; the fence keeps the compiler's: a
+// wave barrier alone says nothing of memory.)
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+}
+
 struct Sort {
   const int32_t *tokens;          // the first pass's input, else null
   const int32_t *key, *row;       // the others': *total pairs
@@ -175,9 +184,9 @@ __global__ __launch_bounds__(256) void sort_place_kernel(Sort S, const uint32_t 
       S.row_out[at] = row;
     }
     // (the wave's reads of its counts come before these writes)
-    __builtin_amdgcn_wave_barrier();
+    wave_order();
     if (in && (same >> lane) == 1ull) counts[wave][digit] += (uint32_t)__popcll(same);
-    __builtin_amdgcn_wave_barrier();
+    wave_order();
   }
 }
 
@@ -286,9 +295,9 @@ __global__ __launch_bounds__(1024) void sort_small_kernel(Sort S, int width, uin
           }
         const int before = M.counts[wave][digit];
         place = before + (int)__popcll(same & ((1ull << lane) - 1ull));
-        __builtin_amdgcn_wave_barrier();
+        wave_order();
         if (have && (same >> lane) == 1ull) M.counts[wave][digit] = (uint16_t)(before + (int)__popcll(same));
-        __builtin_amdgcn_wave_barrier();
+        wave_order();
       }
       rank[i] = place;
     }
