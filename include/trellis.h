@@ -316,17 +316,19 @@ trellis_status trellis_gated_backward(const uint16_t *dh_bf16, const uint16_t *g
  *
  * The losses give no logits out and hold them for a chunk of rows at a time only.
  * Sums and softmax statistics are float32, and results do not depend on timing.
- * The factors of dx's product with W, the probabilities and p - q of the listed
- * entries, are bf16: each is off by up to 2^-8 of itself, and dx is rounded to bf16
- * once more. Their workspace, which the stream keeps (see above), holds for a chunk
- * of rows (256 rows at least)
+ * In dx's product with W the probabilities of the vocabulary are bf16 factors, each
+ * off by up to 2^-8 of itself; p - q of the listed entries is not rounded (but for
+ * entries of long lists that together are at most a sixteenth of the list's
+ * gradients, squared). Their workspace, which the stream keeps (see above), holds
+ * for a chunk of rows (256 rows at least)
  *   - for few rows the float32 logits (at most 1 GiB), with dx their bf16 gradients
  *     (half as much) and what the product of these with W takes (see above);
  *   - else the decoded weights of a launch (at most 2 GiB, but 512 bytes a row of W
  *     at least), a copy of x (at most 1 GiB), statistics (at most 512 MiB), and with
  *     dx the exponentials in bf16 (at most 1 GiB) and its float32 sums, 4 bytes per
  *     column, row and split (at most eight);
- *   - 4 bytes a place of the rows' lists.
+ *   - 4 bytes a place of the rows' lists, and with dx 4 bytes per column and row for
+ *     the rests of the listed entries.
  * 256 rows of 2^22 entries take twice these 1 GiB. 2048 rows with dx on 131072 rows
  * of 5120 (k = 4) take 1.9 GiB, of which the decoded weights are 1.25. */
 

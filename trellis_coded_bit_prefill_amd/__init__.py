@@ -735,7 +735,7 @@ def cross_entropy(x, codes, scales, bits: int, target, keep: bool = False):
     """Softmax cross entropy of the logits x . W^T over a packed vocabulary
     matrix, which stay in the workspace, a chunk of rows at a time: (loss [M],
     lse [M]) in float32 on the current stream, with keep (loss, lse, dx [M, K]
-    bf16, of bf16 probabilities):
+    bf16, from bf16 probabilities but for the target's 1 - p):
 
         lse[r] = log sum_v exp(W_v x[r]),  loss[r] = lse[r] - W_target x[r],
         dx[r]  = the gradient of loss[r] with respect to x[r]

@@ -113,6 +113,8 @@ struct RowList {
   uint8_t first[kMaxTop];
   float red[2][4];
   f32x2 total;           // R and S of the whole row
+  int rest_at[kMaxTop], rests;  // listed_rests()
+  float rest[kMaxTop], rest_scale[kMaxTop];
 };
 __device__ __forceinline__ float sum_256(float v, float *red) {
 #pragma unroll
@@ -221,16 +223,97 @@ __device__ bool row_list(const Lists &L, int64_t row, f32x2 rest, bool whole, Ro
   return alive;
 }
 
+// What the listed entries' gradients lose as operands: the logits' gradients are
+// bf16 in the product with W, because that is what the matrix cores multiply at
+// their rate, each off by up to 2^-8 of itself. Over the vocabulary these errors
+// have either sign and cancel for the most part. Those of the listed entries, which
+// are most of a row's gradient, do not (dx off by 0.0019 to 0.0029 relative, where
+// its own last rounding alone is 0.0017). So their rests x - bf16(x) are multiplied
+// with their rows of W here, in float32, and `add` [m, k] joins the product's sums:
+// 0.0017 then, but where an unlisted entry is most of a gradient. Left out are rests
+// of entries so small that, squared, all of them are at most a sixteenth of the
+// list's gradients (their error then at most a quarter of what it was).
+// It costs cross entropy 1.3 us of 18 at 5 rows and 15 to 20 of 5040 at 2048 (N =
+// 131072, K = 5120), 4 of 165 at 19 rows with lists of 8, 60 to 75 of 2640 at 2048
+// with lists of 64; at worst, lists of 256 entries of like gradients, as much as a
+// row of W decoded for each: 16384 x 4096, 192 rows, 141 to 225.
+// value: what the workgroup's thread j has rounded for its entry, 0 where it has
+// none; wave w of `waves` takes the 256-column blocks w, w + waves ..
+struct Rests {
+  const uint32_t *codes;
+  const uint16_t *scales;
+  float *add;
+  int32_t blocks;  // of 256 columns
+};
+template <int BITS>
+__device__ __forceinline__ void listed_rests(const Lists &L, const Rests &F, int64_t row, float value, int wave0, int waves,
+                                             RowList &S) {
+  constexpr int wpb = 8 * BITS;
+  const int j = threadIdx.x, lane = j & 63, wave = __builtin_amdgcn_readfirstlane(j >> 6);
+  const float rest = value - bf16_bits_to_f32(bf16_of(value)), part = value != 0.f ? S.add[j] : 0.f;
+  const float all = sum_256(part * part, S.red[0]);
+  // (an infinity or a NaN is the product's)
+  const bool keep = fabsf(rest) > 0.f && fabsf(rest) < __builtin_inff() && !(part * part * (16.f * (float)L.top) < all);
+  const uint64_t kept = __ballot(keep);
+  const float s = keep ? bf16_bits_to_f32(F.scales[S.at[j]]) : 1.f;
+  const bool odd = !__all(alu_scale_ok(s));
+  __syncthreads();
+  if (lane == 0) {
+    S.red[0][wave] = (float)__popcll(kept);
+    S.red[1][wave] = odd ? 1.f : 0.f;
+  }
+  __syncthreads();
+  int at = 0;
+  for (int w = 0; w < wave; ++w) at += (int)S.red[0][w];
+  const int count = __builtin_amdgcn_readfirstlane((int)((S.red[0][0] + S.red[0][1]) + (S.red[0][2] + S.red[0][3])));
+  const bool chain = __builtin_amdgcn_readfirstlane((S.red[1][0] + S.red[1][1]) + (S.red[1][2] + S.red[1][3]) != 0.f) != 0;
+  if (keep) {
+    const int to = at + (int)__popcll(kept & ((1ull << lane) - 1ull));
+    S.rest_at[to] = S.at[j];
+    S.rest[to] = rest;
+    S.rest_scale[to] = s;
+  }
+  __syncthreads();
+  const int pos = (252 - 4 * lane) * BITS, w0 = pos >> 5, w1 = w0 + 1 == wpb ? 0 : w0 + 1, sh = pos & 31;
+  auto columns = [&](auto chained) {
+    for (int b = __builtin_amdgcn_readfirstlane(wave0); b < F.blocks; b += waves) {
+      f32x4 v = {0.f, 0.f, 0.f, 0.f};
+      // `some` entries' words on their way at once: one after the other they would cost a memory latency each
+      auto take = [&](int i, auto some) {
+        constexpr int U = decltype(some)::value;
+        uint32_t f[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const uint32_t *const bw = F.codes + ((int64_t)__builtin_amdgcn_readfirstlane(S.rest_at[i + u]) * F.blocks + b) * wpb;
+          f[u] = __builtin_amdgcn_alignbit(bw[w1], bw[w0], sh);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const float r = S.rest[i + u], sc = S.rest_scale[i + u];
+          float q, kq;
+          alu_row_constants(sc, q, kq);
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            v[c] = __builtin_fmaf(r, (float)(__bf16)window_weight(__builtin_amdgcn_ubfe(f[u], (3 - c) * BITS, 12), sc, q, kq, decltype(chained)::value), v[c]);
+        }
+      };
+      int i = 0;
+      for (; i + 16 <= count; i += 16) take(i, std::integral_constant<int, 16>{});
+      for (; i + 4 <= count; i += 4) take(i, std::integral_constant<int, 4>{});
+      for (; i < count; ++i) take(i, std::integral_constant<int, 1>{});
+      *reinterpret_cast<f32x4 *>(F.add + (row * F.blocks + b) * 256 + 4 * lane) = v;
+    }
+  };
+  if (chain) columns(std::true_type{});
+  else columns(std::false_type{});
+}
+
 // Loss and lse of a row and, where d is not null, the gradient of its logits in
-// a span. d is bf16, as that is what the matrix cores multiply at their rate: each
-// is off by up to 2^-8 of itself. Over the vocabulary these errors have either
-// sign and cancel in part; a listed entry's does not, and where that is most of
-// the row's gradient (an unlikely entry), all of dx is off by its one factor, 1 -
-// 2^-8 to 1 + 2^-8. Over the measured cases dx is off by 0.0019 to 0.0025 relative,
-// where float32 gradients with the last rounding alone are by 0.0017.
-__global__ __launch_bounds__(256) void row_loss_kernel(Lists L, const float *__restrict__ logits,
+// a span, and the listed entries' rests in a part of the columns.
+template <int BITS>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 4))) void row_loss_kernel(Lists L, const float *__restrict__ logits,
                                                        const f32x2 *__restrict__ stats, int spans,
-                                                       uint16_t *__restrict__ d) {
+                                                       uint16_t *__restrict__ d, Rests F) {
   __shared__ RowList S;
   const int64_t row = blockIdx.x;
   // every wave joins the spans, in the same order
@@ -255,15 +338,17 @@ __global__ __launch_bounds__(256) void row_loss_kernel(Lists L, const float *__r
   }
   __syncthreads();
   const int at = S.at[threadIdx.x];
-  if (S.first[threadIdx.x] && at >= c0 && at < c0 + kStatSpan && alive)
-    o[at] = bf16_of(L.temperature * S.add[threadIdx.x]);
+  const float value = S.first[threadIdx.x] && alive ? L.temperature * S.add[threadIdx.x] : 0.f;
+  if (S.first[threadIdx.x] && at >= c0 && at < c0 + kStatSpan && alive) o[at] = bf16_of(value);
+  listed_rests<BITS>(L, F, row, value, (int)blockIdx.y * 4 + (int)(threadIdx.x >> 6), 4 * (int)gridDim.y, S);
 }
 
 // Rows of up to 16384 logits in one launch instead of three: the row stays in
 // registers, 64 logits a thread at most, and a bit map in LDS says which are listed.
 constexpr int kWholeRow = 16384;
+template <int BITS>
 __global__ __launch_bounds__(256) void whole_row_kernel(Lists L, const float *__restrict__ logits,
-                                                        uint16_t *__restrict__ d) {
+                                                        uint16_t *__restrict__ d, Rests F) {
   __shared__ RowList S;
   __shared__ uint32_t listed[kWholeRow / 32];
   __shared__ f32x2 part[4];
@@ -322,7 +407,9 @@ __global__ __launch_bounds__(256) void whole_row_kernel(Lists L, const float *__
     }
   }
   __syncthreads();
-  if (S.first[tid] && alive) o[S.at[tid]] = bf16_of(L.temperature * S.add[tid]);
+  const float value = S.first[tid] && alive ? L.temperature * S.add[tid] : 0.f;
+  if (S.first[tid] && alive) o[S.at[tid]] = bf16_of(value);
+  listed_rests<BITS>(L, F, row, value, tid >> 6, 4, S);
 }
 
 // dst = dloss[row] * src: a factor a row; dx, rounded once when it was kept, is
@@ -672,10 +759,11 @@ __global__ __launch_bounds__(256) void listed_kernel(Lists L, int32_t *__restric
 
 // A row's blocks joined: its loss, lse and the factor of its dx (T / S in the
 // operands' unit; 0 for a row without entries). Tiles whose reference is not the
-// row's are brought to it, and the listed entries' operands become (p - q) S, in
-// bf16 as the others (what that costs: see row_loss_kernel).
-__global__ __launch_bounds__(256) void row_join_kernel(Lists L, Vocabulary V, int ptiles, int block_columns,
-                                                       float *__restrict__ factor) {
+// row's are brought to it, and the listed entries' operands become (p - q) S, their
+// rests in `add` in the same unit.
+template <int BITS>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 4))) void row_join_kernel(Lists L, Vocabulary V, int ptiles, int block_columns,
+                                                       float *__restrict__ factor, Rests F) {
   __shared__ RowList S;
   const int64_t row = blockIdx.x;
   const f32x2 *const stats = V.stats + row * V.blocks;
@@ -718,22 +806,28 @@ __global__ __launch_bounds__(256) void row_join_kernel(Lists L, Vocabulary V, in
     }
     __syncthreads();
   }
-  if (S.first[threadIdx.x] && alive)
-    *place(S.at[threadIdx.x]) = bf16_of(whole ? S.add[threadIdx.x] * total : S.qs[threadIdx.x] * -sum);
+  float value = 0.f;
+  if (S.first[threadIdx.x] && alive) {
+    value = whole ? S.add[threadIdx.x] * total : S.qs[threadIdx.x] * -sum;
+    *place(S.at[threadIdx.x]) = bf16_of(value);
+  }
+  listed_rests<BITS>(L, F, row, value, (int)(threadIdx.x >> 6), 4, S);
 }
 
-// dx: the splits' sums in order, times the row's factor, rounded. Four columns a thread.
+// dx: the splits' sums in order and the rests', times the row's factor (null: 1),
+// rounded. Four columns a thread.
 __global__ __launch_bounds__(256) void loss_gradient_kernel(const float *__restrict__ partials, int splits, int64_t plane,
                                                             int columns, int width, const float *__restrict__ factor,
-                                                            int m, uint16_t *__restrict__ dx) {
+                                                            const float *__restrict__ add, int m, uint16_t *__restrict__ dx) {
   const int quads = columns >> 2;
   const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t row = id / quads;
   if (row >= m) return;
   const int c = (int)(id - row * quads) * 4;
-  const float f = factor[row];
+  const float f = factor ? factor[row] : 1.f;
   f32x4 v = {0.f, 0.f, 0.f, 0.f};
   if (f != 0.f) {
+    const f32x4 rests = *reinterpret_cast<const f32x4 *>(add + row * width + c);
     for (int s0 = 0; s0 < splits; s0 += 4) {
       f32x4 part[4];
 #pragma unroll
@@ -743,7 +837,7 @@ __global__ __launch_bounds__(256) void loss_gradient_kernel(const float *__restr
       for (int s = 0; s < 4; ++s)
         if (s0 + s < splits) v += part[s];
     }
-    v *= f;
+    v = (v + rests) * f;
   }
   store4(dx + row * width + c, v);
 }
@@ -818,13 +912,30 @@ struct LossShape {
   size_t operand_bytes, row_bytes, e_bytes, stat_bytes, partial_bytes;
   double us;
 };
+// The second product of a chunk of rows: its tile, operands and sums.
+void loss_back_shape(LossShape &s, trellis_geom g, int64_t rows, int cus) {
+  const int forced = g_tiles.load(std::memory_order_relaxed);
+  s.back_tiles = g.k / 16;
+  s.back_steps = (g.n + 63) / 64 * 2;
+  s.ptiles = (int)((rows + 15) / 16);
+  s.back = vocabulary_tile(rows, s.back_tiles, s.back_steps, true, cus);
+  const int64_t back_bytes = (int64_t)s.back_steps * 1024;
+  // Whole workgroup tiles a launch and whole 256-column blocks (a tile takes up to
+  // 128 MB: one block at least, whose last workgroup tile may be cut, as may every
+  // launch's last).
+  s.back_slab = (forced > 0 ? (int64_t)forced : kVocabularyBytes / back_bytes) / 16 * 16;
+  if (s.back_slab == 0) s.back_slab = 16;
+  if (s.back_slab > s.back_tiles) s.back_slab = s.back_tiles;
+  if (s.operand_bytes < (size_t)(s.back_slab * back_bytes)) s.operand_bytes = (size_t)(s.back_slab * back_bytes);
+  s.operand_bytes = up256(s.operand_bytes);
+  s.e_bytes = up256((size_t)s.ptiles * back_bytes);
+  s.partial_bytes = up256((size_t)s.back.splits * rows * s.back_slab * 16 * 4);
+}
 LossShape loss_shape(trellis_geom g, int32_t m, bool keep, int cus) {
   LossShape s{};
   s.tiles = ((int64_t)g.n + 15) / 16;
   s.steps = (g.k + 63) / 64 * 2;
-  s.back_tiles = g.k / 16;
-  s.back_steps = (g.n + 63) / 64 * 2;
-  const int64_t n_pad = (int64_t)s.back_steps * kDenseStep;
+  const int64_t n_pad = ((int64_t)g.n + 63) / 64 * 64;
   // A chunk's operands of the second product take at most 1 GiB, those of x too,
   // and its statistics (8 bytes a row and 64 columns at the most) 512 MiB; 256
   // rows in any case.
@@ -836,7 +947,7 @@ LossShape loss_shape(trellis_geom g, int32_t m, bool keep, int cus) {
   s.rows = (int32_t)rows;
   s.fwd = vocabulary_first(g, rows, s.tiles, s.steps, cus);
   s.blocks = (int)((s.tiles + s.fwd.nt - 1) / s.fwd.nt);
-  const int64_t tile_bytes = (int64_t)s.steps * 1024, back_bytes = (int64_t)s.back_steps * 1024;
+  const int64_t tile_bytes = (int64_t)s.steps * 1024;
   const int forced = g_tiles.load(std::memory_order_relaxed);
   // Whole workgroup tiles a launch (a tile takes 8 MB at most).
   const int unit = 2 * s.fwd.nt;
@@ -848,19 +959,60 @@ LossShape loss_shape(trellis_geom g, int32_t m, bool keep, int cus) {
   s.stat_bytes = up256((size_t)rows * s.blocks * 8);
   s.us = s.fwd.us;
   if (keep) {
-    s.back = vocabulary_tile(rows, s.back_tiles, s.back_steps, true, cus);
-    // Here whole 256-column blocks as well (a tile takes up to 128 MB: one block
-    // at least, whose last workgroup tile may be cut, as may every launch's last).
-    s.back_slab = (forced > 0 ? (int64_t)forced : kVocabularyBytes / back_bytes) / 16 * 16;
-    if (s.back_slab == 0) s.back_slab = 16;
-    if (s.back_slab > s.back_tiles) s.back_slab = s.back_tiles;
-    if (s.operand_bytes < (size_t)(s.back_slab * back_bytes)) s.operand_bytes = (size_t)(s.back_slab * back_bytes);
-    s.e_bytes = up256((size_t)s.ptiles * back_bytes);
-    s.partial_bytes = up256((size_t)s.back.splits * rows * s.back_slab * 16 * 4);
+    loss_back_shape(s, g, rows, cus);
     s.us += s.back.us + 4 + 0.46e-6 * g.n * (double)g.k;
   }
   s.operand_bytes = up256(s.operand_bytes);
   return s;
+}
+
+// A kernel's dynamic LDS; asked for once a device.
+bool lds_allowed(bool &done, const void *f, size_t bytes) {
+  done = done || worked(hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes));
+  return done;
+}
+size_t lds_of(const VocabularyTile &t) { return (size_t)dense_buffers(t.nt, t.rt) * dense_step_bytes(t.nt, t.rt); }
+
+// dx of a chunk of rows from the logits' gradients as operands e.
+struct LossBack {
+  const uint32_t *codes;
+  const uint16_t *scales, *e;
+  uint16_t *operands;
+  float *partials;
+  const float *factor, *add;  // factor: null for 1
+  int32_t m;
+  uint16_t *dx;
+};
+trellis_status loss_back(const LossShape &s, trellis_geom g, const LossBack &b, int dev, hipStream_t stream) {
+  static bool ready[kMaxDevices][2][9];
+  const DenseFn fn = vocabulary_back_fn(s.back.nt, s.back.rt);
+  const size_t lds = lds_of(s.back);
+  if (!lds_allowed(ready[dev][s.back.rt - 3][s.back.nt], reinterpret_cast<const void *>(fn), lds)) return TRELLIS_E_HIP;
+  Dense d{};
+  d.p = b.e;
+  d.w = b.operands;
+  d.m = b.m;
+  d.steps = s.back_steps;
+  d.splits = s.back.splits;
+  d.ptiles = (b.m + 15) / 16;
+  d.mtiles = (b.m + 64 * s.back.rt - 1) / (64 * s.back.rt);
+  d.partials = b.partials;
+  d.width = g.k;
+  (void)hipGetLastError();
+  for (int64_t first = 0; first < s.back_tiles; first += s.back_slab) {
+    d.wtiles = (int)(s.back_tiles - first < s.back_slab ? s.back_tiles - first : s.back_slab);
+    d.ntiles = (d.wtiles + 2 * s.back.nt - 1) / (2 * s.back.nt);
+    d.first = (int)first * 16;
+    const Unpack u{{b.codes, nullptr}, {b.scales, nullptr}, b.operands, g.n, g.k, s.back_steps, (int)first, d.wtiles, 1};
+    TRELLIS_TRY(launch_unpack(true, g.bits, u, stream));
+    hipLaunchKernelGGL(fn, dim3((unsigned)(d.mtiles * d.ntiles * d.splits)), dim3(kDenseThreads), lds, stream, d);
+    const int columns = 16 * d.wtiles;
+    const int64_t threads = (int64_t)b.m * (columns / 4);
+    hipLaunchKernelGGL(loss_gradient_kernel, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, stream, b.partials,
+                       d.splits, (int64_t)b.m * columns, columns, g.k, b.factor, b.add + d.first, b.m, b.dx + d.first);
+    if (hipGetLastError() != hipSuccess) return TRELLIS_E_HIP;
+  }
+  return TRELLIS_OK;
 }
 
 trellis_status loss_dense(const uint16_t *x, int32_t m, const uint32_t *codes, const uint16_t *scales, trellis_geom g,
@@ -868,10 +1020,11 @@ trellis_status loss_dense(const uint16_t *x, int32_t m, const uint32_t *codes, c
   int dev = 0, cus = 0;
   TRELLIS_TRY(device(dev, cus));
   const LossShape s = loss_shape(g, m, dx != nullptr, cus);
-  const size_t list_bytes = up256((size_t)s.rows * L.top * 4), word_bytes = up256((size_t)s.rows * 4);
+  const size_t list_bytes = up256((size_t)s.rows * L.top * 4), word_bytes = up256((size_t)s.rows * 4),
+               add_bytes = dx ? up256((size_t)s.rows * g.k * 4) : 0;
   Space *w = nullptr;
   TRELLIS_TRY(space(dev, stream,
-                    s.operand_bytes + s.row_bytes + s.e_bytes + s.stat_bytes + s.partial_bytes + list_bytes + 3 * word_bytes, 0, w));
+                    s.operand_bytes + s.row_bytes + s.e_bytes + s.stat_bytes + s.partial_bytes + add_bytes + list_bytes + 3 * word_bytes, 0, w));
   unsigned char *at = w->bytes;
   auto take = [&](size_t bytes) {
     unsigned char *const p = at;
@@ -882,24 +1035,18 @@ trellis_status loss_dense(const uint16_t *x, int32_t m, const uint32_t *codes, c
                  *const packed = reinterpret_cast<uint16_t *>(take(s.row_bytes)),
                  *const e = reinterpret_cast<uint16_t *>(take(s.e_bytes));
   f32x2 *const stats = reinterpret_cast<f32x2 *>(take(s.stat_bytes));
-  float *const partials = reinterpret_cast<float *>(take(s.partial_bytes));
+  float *const partials = reinterpret_cast<float *>(take(s.partial_bytes)), *const add = reinterpret_cast<float *>(take(add_bytes));
   L.listed = reinterpret_cast<float *>(take(list_bytes));
   int32_t *const sole = reinterpret_cast<int32_t *>(take(word_bytes));
   float *const sole_l2 = reinterpret_cast<float *>(take(word_bytes)), *const factor = reinterpret_cast<float *>(take(word_bytes));
-  static bool ready[kMaxDevices][2][2][9], decode_ready[kMaxDevices][3][7];
+  static bool ready[kMaxDevices][2][9], decode_ready[kMaxDevices][3][7];
   const VocabularyFn fn = s.fwd.decode ? nullptr : vocabulary_fn(s.fwd.nt, s.fwd.rt);
   const VocabularyDecodeFn decode_fn = s.fwd.decode ? vocabulary_decode_fn(g.bits, s.fwd.rt) : nullptr;
-  const DenseFn back = dx ? vocabulary_back_fn(s.back.nt, s.back.rt) : nullptr;
-  auto lds_of = [](const VocabularyTile &t) { return (size_t)dense_buffers(t.nt, t.rt) * dense_step_bytes(t.nt, t.rt); };
-  const size_t lds = s.fwd.decode ? (size_t)decode_lds(g.bits, s.fwd.rt) : lds_of(s.fwd), lds_back = dx ? lds_of(s.back) : 0;
-  auto allow = [&](bool &done, const void *f, size_t bytes) {
-    done = done || worked(hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes));
-    return done;
-  };
-  if (!(s.fwd.decode ? allow(decode_ready[dev][g.bits - 2][s.fwd.rt], reinterpret_cast<const void *>(decode_fn), lds)
-                     : allow(ready[dev][0][s.fwd.rt - 3][s.fwd.nt], reinterpret_cast<const void *>(fn), lds)) ||
-      (dx && !allow(ready[dev][1][s.back.rt - 3][s.back.nt], reinterpret_cast<const void *>(back), lds_back)))
+  const size_t lds = s.fwd.decode ? (size_t)decode_lds(g.bits, s.fwd.rt) : lds_of(s.fwd);
+  if (!(s.fwd.decode ? lds_allowed(decode_ready[dev][g.bits - 2][s.fwd.rt], reinterpret_cast<const void *>(decode_fn), lds)
+                     : lds_allowed(ready[dev][s.fwd.rt - 3][s.fwd.nt], reinterpret_cast<const void *>(fn), lds)))
     return TRELLIS_E_HIP;
+  const auto join = g.bits == 2 ? &row_join_kernel<2> : g.bits == 3 ? &row_join_kernel<3> : &row_join_kernel<4>;
   const Lists all = L;
   (void)hipGetLastError();
   for (int32_t m0 = 0; m0 < m; m0 += s.rows) {
@@ -941,28 +1088,12 @@ trellis_status loss_dense(const uint16_t *x, int32_t m, const uint32_t *codes, c
       TRELLIS_TRY(launch_unpack(false, g.bits, u, stream));
       hipLaunchKernelGGL(fn, dim3((unsigned)(d.mtiles * d.ntiles)), dim3(kDenseThreads), lds, stream, d, v);
     }
-    hipLaunchKernelGGL(row_join_kernel, dim3((unsigned)mc), dim3(256), 0, stream, L, v, ptiles, 16 * s.fwd.nt, factor);
+    hipLaunchKernelGGL(join, dim3((unsigned)mc), dim3(256), 0, stream, L, v, ptiles, 16 * s.fwd.nt, factor,
+                       Rests{codes, scales, add, g.k >> 8});
     if (hipGetLastError() != hipSuccess) return TRELLIS_E_HIP;
-    if (!dx) continue;
-    d.p = e;
-    d.steps = s.back_steps;
-    d.mtiles = (mc + 64 * s.back.rt - 1) / (64 * s.back.rt);
-    d.splits = s.back.splits;
-    d.partials = partials;
-    d.width = g.k;
-    for (int64_t first = 0; first < s.back_tiles; first += s.back_slab) {
-      d.wtiles = (int)(s.back_tiles - first < s.back_slab ? s.back_tiles - first : s.back_slab);
-      d.ntiles = (d.wtiles + 2 * s.back.nt - 1) / (2 * s.back.nt);
-      d.first = (int)first * 16;
-      const Unpack u{{codes, nullptr}, {scales, nullptr}, operands, g.n, g.k, s.back_steps, (int)first, d.wtiles, 1};
-      TRELLIS_TRY(launch_unpack(true, g.bits, u, stream));
-      hipLaunchKernelGGL(back, dim3((unsigned)(d.mtiles * d.ntiles * d.splits)), dim3(kDenseThreads), lds_back, stream, d);
-      const int columns = 16 * d.wtiles;
-      const int64_t threads = (int64_t)mc * (columns / 4);
-      hipLaunchKernelGGL(loss_gradient_kernel, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, stream, partials,
-                         d.splits, (int64_t)mc * columns, columns, g.k, factor, mc, dx + (int64_t)m0 * g.k + d.first);
-      if (hipGetLastError() != hipSuccess) return TRELLIS_E_HIP;
-    }
+    if (dx)
+      TRELLIS_TRY(loss_back(s, g, LossBack{codes, scales, e, operands, partials, factor, add, mc, dx + (int64_t)m0 * g.k},
+                            dev, stream));
   }
   return TRELLIS_OK;
 }
@@ -971,7 +1102,8 @@ trellis_status loss_dense(const uint16_t *x, int32_t m, const uint32_t *codes, c
 // workgroups share a CU where what that saves (a step takes 1.65 times as long
 // for two) is more than the joining of twice as many parts costs: K = 5120, N =
 // 65536, 1 row with gradient 140 us against 160; K = 1024, N = 32772 74 against 48.
-// Its operands in several launches lose to decoding in the product (256 rows, K =
+// With operands it is many rows' second product (loss_back); these in several
+// launches lose to decoding in the product (256 rows, K =
 // 5120, N = 131072: the whole call 1.51 ms against 1.28).
 Plan loss_back_plan(trellis_geom g, int32_t m, int cus) {
   Shape fused = shape_of(kTransposed, g, m, 1, cus, true);
@@ -1000,7 +1132,7 @@ Plan loss_back_plan(trellis_geom g, int32_t m, int cus) {
 // 2048, N = 8192, 1024 rows with lists of 16 69 / 69, of 64 73 / 101, of 256 84 /
 // 232; K = 5120, N = 131072, 1024 rows of 256 2070 / 1857. On five other matrices,
 // lists of 32 and 200 entries among them, the side taken is 0.2% slower than the
-// faster one on average and 8% at most.
+// faster one on average and 9% at most.
 bool loss_by_operands(trellis_geom g, int32_t m, bool keep, int cus, int top = 1) {
   const int forced = g_path.load(std::memory_order_relaxed);
   if (forced >= 0) return forced == 1;
@@ -1029,17 +1161,24 @@ trellis_status loss_rows(const uint16_t *x, int32_t m, const uint32_t *codes, co
   int dev = 0, cus = 0;
   TRELLIS_TRY(device(dev, cus));
   if (loss_by_operands(g, m, dx != nullptr, cus, L.top)) return loss_dense(x, m, codes, scales, g, L, dx, stream);
-  const int64_t most = kLogitBytes / (4 * (int64_t)g.n) / 16 * 16;  // 64 rows at least: n is at most 2^22
+  // (64 rows at least: n is at most 2^22; with dx the listed entries' rests too)
+  const int64_t most = kLogitBytes / (4 * (int64_t)(dx && g.k > g.n ? g.k : g.n)) / 16 * 16;
   const int32_t rows = m < most ? m : (int32_t)most;
   // Plans of the full chunks and of the last one; the workspace holds either.
+  // (Where the transposed product takes operands, it is that of many rows.)
   const int32_t counts[2] = {rows, (m - 1) % rows + 1};
   Shape fwd[2];
   Plan bwd[2] = {};
+  LossShape back[2] = {};
   size_t parts = 0;
   int64_t counters = 0;
   for (int i = 0; i < 2; ++i) {
     fwd[i] = shape_of(kForward, g, counts[i], 1, cus, true);
     if (dx) bwd[i] = loss_back_plan(g, counts[i], cus);
+    if (bwd[i].dense) {
+      loss_back_shape(back[i], g, counts[i], cus);
+      bwd[i].bytes = back[i].operand_bytes + back[i].e_bytes + back[i].partial_bytes;
+    }
     if (parts < fwd[i].partial_bytes) parts = fwd[i].partial_bytes;
     if (parts < bwd[i].bytes) parts = bwd[i].bytes;
     if (counters < fwd[i].tiles) counters = fwd[i].tiles;
@@ -1047,14 +1186,19 @@ trellis_status loss_rows(const uint16_t *x, int32_t m, const uint32_t *codes, co
   }
   const int spans = (g.n + kStatSpan - 1) / kStatSpan;
   const size_t logit_bytes = up256((size_t)rows * g.n * 4), d_bytes = dx ? up256((size_t)rows * g.n * 2) : 0,
-               stat_bytes = up256((size_t)rows * spans * 8), listed_bytes = up256((size_t)rows * L.top * 4);
+               stat_bytes = up256((size_t)rows * spans * 8), listed_bytes = up256((size_t)rows * L.top * 4),
+               add_bytes = dx ? up256((size_t)rows * g.k * 4) : 0;
   Space *w = nullptr;
-  TRELLIS_TRY(space(dev, stream, logit_bytes + d_bytes + stat_bytes + listed_bytes + parts, (size_t)counters, w));
+  TRELLIS_TRY(space(dev, stream, logit_bytes + d_bytes + stat_bytes + listed_bytes + add_bytes + parts, (size_t)counters, w));
   float *const logits = reinterpret_cast<float *>(w->bytes);
   uint16_t *const d = reinterpret_cast<uint16_t *>(w->bytes + logit_bytes);
   f32x2 *const stats = reinterpret_cast<f32x2 *>(w->bytes + logit_bytes + d_bytes);
   L.listed = reinterpret_cast<float *>(w->bytes + logit_bytes + d_bytes + stat_bytes);
-  unsigned char *const rest = w->bytes + logit_bytes + d_bytes + stat_bytes + listed_bytes;
+  float *const add = reinterpret_cast<float *>(w->bytes + logit_bytes + d_bytes + stat_bytes + listed_bytes);
+  unsigned char *const rest = w->bytes + logit_bytes + d_bytes + stat_bytes + listed_bytes + add_bytes;
+  const auto whole_row = g.bits == 2 ? &whole_row_kernel<2> : g.bits == 3 ? &whole_row_kernel<3> : &whole_row_kernel<4>;
+  const auto row_loss = g.bits == 2 ? &row_loss_kernel<2> : g.bits == 3 ? &row_loss_kernel<3> : &row_loss_kernel<4>;
+  const Rests rests{codes, scales, add, g.k >> 8};
   const Lists all = L;
   for (int32_t m0 = 0; m0 < m; m0 += rows) {
     const int32_t mc = m - m0 < rows ? m - m0 : rows;
@@ -1075,16 +1219,29 @@ trellis_status loss_rows(const uint16_t *x, int32_t m, const uint32_t *codes, co
     p.k = g.k;
     TRELLIS_TRY(launch(fwd[which], p, stream));
     if (g.n <= kWholeRow) {
-      hipLaunchKernelGGL(whole_row_kernel, dim3((unsigned)mc), dim3(256), 0, stream, L, logits, dx ? d : nullptr);
+      hipLaunchKernelGGL(whole_row, dim3((unsigned)mc), dim3(256), 0, stream, L, logits, dx ? d : nullptr, rests);
     } else {
       hipLaunchKernelGGL(row_stats_kernel, dim3((unsigned)mc, (unsigned)spans), dim3(256), 0, stream, L, logits, stats);
-      hipLaunchKernelGGL(row_loss_kernel, dim3((unsigned)mc, dx ? (unsigned)spans : 1u), dim3(256), 0, stream, L, logits,
-                         stats, spans, dx ? d : nullptr);
+      hipLaunchKernelGGL(row_loss, dim3((unsigned)mc, dx ? (unsigned)spans : 1u), dim3(256), 0, stream, L, logits,
+                         stats, spans, dx ? d : nullptr, rests);
     }
     if (hipGetLastError() != hipSuccess) return TRELLIS_E_HIP;
     if (!dx) continue;
+    if (bwd[which].dense) {
+      const LossShape &s = back[which];
+      uint16_t *const operands = reinterpret_cast<uint16_t *>(rest), *const e = reinterpret_cast<uint16_t *>(rest + s.operand_bytes);
+      float *const partials = reinterpret_cast<float *>(rest + s.operand_bytes + s.e_bytes);
+      hipLaunchKernelGGL(g.n % 8 ? pack_rows_kernel<false> : pack_rows_kernel<true>,
+                         dim3((unsigned)(((int64_t)s.ptiles * (s.back_steps / 2) + 3) / 4)), dim3(256), 0, stream, d, mc,
+                         g.n, s.ptiles, s.back_steps, e);
+      if (hipGetLastError() != hipSuccess) return TRELLIS_E_HIP;
+      TRELLIS_TRY(loss_back(s, g, LossBack{codes, scales, e, operands, partials, nullptr, add, mc, dx + (int64_t)m0 * g.k},
+                            dev, stream));
+      continue;
+    }
     Product t{};
     t.p = d;
+    t.add = add;
     t.codes = codes;
     t.scales = scales;
     t.out = dx + (int64_t)m0 * g.k;

@@ -69,6 +69,7 @@ struct Product {
   const uint16_t *scales, *scales2;
   uint16_t *out, *gate, *up;       // gate, up: gated only, null where they are not kept
   float *logits;                   // logits_kernel: float32 [m, n] in place of out
+  const float *add;                // logits_gradient_kernel: float32 [m, k], added to the sums
   float *partials;
   uint32_t *counters;
   int32_t units_q, units_r;  // units (tiles * steps) of a workgroup: units_q, the first units_r one more
@@ -293,7 +294,7 @@ namespace {
 // (40 against 38.7 at 24), four waves per SIMD from four row tiles on (97
 // against 47 at 64: registers spill). Transposed with six row tiles 44 bytes a
 // lane go through scratch memory outside the steps.
-// LOSS: no adapters, and forward float32 sums to P.logits.
+// LOSS: no adapters; forward float32 sums to P.logits, transposed P.add added.
 template <int BITS, int KIND, int MT, int NT, bool LOSS>
 __device__ __forceinline__ void product(const Product &P) {
   constexpr bool kT = KIND == kTransposed;
@@ -401,6 +402,7 @@ __device__ __forceinline__ void product(const Product &P) {
     } else {
       const int width = kT ? P.k : P.n, n = agroup * BN + c;
       if (n >= width) return;
+      if constexpr (LOSS && kT) v += *reinterpret_cast<const f32x4 *>(P.add + (int64_t)mrow * width + n);
       if constexpr (LOSS && !kT) *reinterpret_cast<f32x4 *>(P.logits + (int64_t)mrow * width + n) = v;
       else store4(P.out + (int64_t)mrow * width + n, v);
     }
@@ -1464,14 +1466,19 @@ ProductFn logits_of(int i) {
     default: return &logits_kernel<BITS, 8, wave_tiles(kForward, 8), waves_per_simd(kForward, 8)>;
   }
 }
-// The transposed product of up to two row tiles without adapters: its registers
+// The transposed product without adapters: with up to two row tiles its registers
 // allow two workgroups a CU.
 template <int BITS>
 ProductFn logits_gradient_of(int i) {
-  return i == 0 ? &logits_gradient_kernel<BITS, 1, 4> : &logits_gradient_kernel<BITS, 2, 4>;
+  switch (i) {
+    case 0: return &logits_gradient_kernel<BITS, 1, 4>;
+    case 1: return &logits_gradient_kernel<BITS, 2, 4>;
+    case 2: return &logits_gradient_kernel<BITS, 4, waves_per_simd(kTransposed, 4)>;
+    default: return &logits_gradient_kernel<BITS, 6, waves_per_simd(kTransposed, 6)>;
+  }
 }
 ProductFn product_fn(int kind, int bits, int i, bool loss) {
-  if (loss && kind == kTransposed && i < 2)
+  if (loss && kind == kTransposed)
     return bits == 2 ? logits_gradient_of<2>(i) : bits == 3 ? logits_gradient_of<3>(i) : logits_gradient_of<4>(i);
   if (loss && kind == kForward) return bits == 2 ? logits_of<2>(i) : bits == 3 ? logits_of<3>(i) : logits_of<4>(i);
   return kind == kForward ? product_of<kForward>(bits, i) : kind == kGated ? product_of<kGated>(bits, i)
