@@ -233,10 +233,10 @@ __device__ bool row_list(const Lists &L, int64_t row, f32x2 rest, bool whole, Ro
 // 0.0017 then, but where an unlisted entry is most of a gradient. Left out are rests
 // of entries so small that, squared, all of them are at most a sixteenth of the
 // list's gradients (their error then at most a quarter of what it was).
-// It costs cross entropy 1.3 us of 18 at 5 rows and 15 to 20 of 5040 at 2048 (N =
-// 131072, K = 5120), 4 of 165 at 19 rows with lists of 8, 60 to 75 of 2640 at 2048
-// with lists of 64; at worst, lists of 256 entries of like gradients, as much as a
-// row of W decoded for each: 16384 x 4096, 192 rows, 141 to 225.
+// It costs cross entropy 1.5 us of 18 at 5 rows and 25 of 5060 at 2048 (N = 131072,
+// K = 5120), 3 of 165 at 19 rows with lists of 8, 25 to 60 of 2650 at 2048 with
+// lists of 64; at worst, lists of 256 entries of like gradients, as much as a row of
+// W decoded for each: 16384 x 4096, 192 rows, 141 to 225.
 // value: what the workgroup's thread j has rounded for its entry, 0 where it has
 // none; wave w of `waves` takes the 256-column blocks w, w + waves ..
 struct Rests {
